@@ -21,11 +21,13 @@ __all__ = [
     "gdr_prefill_with_decode",
     "gdr_verify_block", "gdr_verify_commit",
     "gdr_state_snapshot", "gdr_state_restore", "gdr_device_error", "gdr_selftest_wait_timeout", "gdr_status_string",
-    "GDR_F32", "GDR_BF16", "GDR_FLAG_QK_L2NORM", "GDR_FLAG_BETA_LOGITS",
+    "gdr_attn_append", "gdr_attn_prefill", "gdr_attn_decode", "gdr_attn_decode_workspace_bytes",
+    "gdr_attn_dims", "gdr_rows", "gdr_kv_cache",
+    "GDR_F32", "GDR_BF16", "GDR_F16", "GDR_FLAG_QK_L2NORM", "GDR_FLAG_BETA_LOGITS",
 ]
 
 GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_CUDA, GDR_ERR_DEVICE_TIMEOUT = range(5)
-GDR_F32, GDR_BF16 = 0, 1
+GDR_F32, GDR_BF16, GDR_F16 = 0, 1, 2
 GDR_FLAG_QK_L2NORM, GDR_FLAG_BETA_LOGITS = 1, 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,7 +55,28 @@ class gdr_dims(ctypes.Structure):
     ]
 
 
+class gdr_attn_dims(ctypes.Structure):
+    _fields_ = [
+        ("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class gdr_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class gdr_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+    ]
+
+
 _P = ctypes.c_void_p
+_ROWS = ctypes.POINTER(gdr_rows)
 _SIGS = {
     "gdr_abi_version": ([], ctypes.c_int32),
     "gdr_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -86,6 +109,15 @@ _SIGS = {
                           ctypes.c_int),
     "gdr_state_snapshot": ([ctypes.POINTER(gdr_dims), ctypes.c_int32, _P, _P, _P], ctypes.c_int),
     "gdr_state_restore": ([ctypes.POINTER(gdr_dims), ctypes.c_int32, _P, _P, _P], ctypes.c_int),
+    "gdr_attn_append": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, _P, ctypes.c_int64, _ROWS, _ROWS, _ROWS, _ROWS,
+                         _ROWS, ctypes.POINTER(gdr_kv_cache), _P, _P, ctypes.c_int32, ctypes.c_int32, _P],
+                        ctypes.c_int),
+    "gdr_attn_prefill": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, _P, ctypes.c_int64, _ROWS, _ROWS, _ROWS,
+                          _ROWS, _P, _P], ctypes.c_int),
+    "gdr_attn_decode": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, ctypes.c_int32, _ROWS,
+                         ctypes.POINTER(gdr_kv_cache), _P, _ROWS, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "gdr_attn_decode_workspace_bytes": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, ctypes.c_int32],
+                                        ctypes.c_size_t),
     "gdr_device_error": ([_P, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "gdr_selftest_wait_timeout": ([ctypes.c_int64, _P], ctypes.c_int),
 }
@@ -396,3 +428,176 @@ def gdr_selftest_wait_timeout(limit_cycles: int, *, stream=None, device=None) ->
     on gives up after limit_cycles SM clocks and records GDR_ERR_DEVICE_TIMEOUT."""
     _check(lib().gdr_selftest_wait_timeout(int(limit_cycles), _stream_handle(stream, device)),
            "gdr_selftest_wait_timeout")
+
+
+# --- softmax attention beside the rule ------------------------------------------
+
+def _attn_dims(q_heads: int, k, scale) -> gdr_attn_dims:
+    """dims from the query head count and a [.., H_kv, d] tensor (k rows or a cache)."""
+    torch = _torch()
+    h_kv, d = k.shape[-2], k.shape[-1]
+    if k.dtype == torch.bfloat16:
+        code = GDR_BF16
+    elif k.dtype == torch.float16:
+        code = GDR_F16
+    elif k.dtype == torch.float32:
+        code = GDR_F32
+    else:
+        raise TypeError(f"unsupported dtype {k.dtype}")
+    return gdr_attn_dims(q_heads, h_kv, d, code, d ** -0.5 if scale is None else scale)
+
+
+def _rows(t, like, heads: int, tokens: int, name: str) -> gdr_rows:
+    """Strided rows of t, checked to be [tokens, heads, d] of like's dtype, device and head size."""
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must have dtype {like.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    d = like.shape[-1]
+    if t.dim() != 3 or t.shape != (tokens, heads, d):
+        raise ValueError(f"{name} must have shape {(tokens, heads, d)}, not {tuple(t.shape)}")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    # the stride of a dimension of one entry is never used, and may be anything
+    return gdr_rows(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0)
+
+
+def _ints(t, n: int, like, name: str) -> int:
+    torch = _torch()
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {(n,)}")
+    return t.data_ptr()
+
+
+def _cache(k_cache, v_cache, page_table, n_seqs: int) -> gdr_kv_cache:
+    torch = _torch()
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape [n_pages, page_size, H_kv, d]")
+    if k_cache.dtype != v_cache.dtype or k_cache.device != v_cache.device:
+        raise TypeError("k_cache and v_cache must have one dtype and device")
+    n_pages, page, heads, _ = k_cache.shape
+    strides = k_cache.stride()
+    if strides != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same strides")
+    if strides[3] != 1:
+        raise ValueError("the caches' last dimension must be contiguous")
+    if page_table.dtype != torch.int32:
+        raise TypeError("page_table must be int32")
+    if page_table.device != k_cache.device:
+        raise ValueError(f"page_table is on {page_table.device}, not {k_cache.device}")
+    if page_table.dim() != 2 or page_table.shape[0] != n_seqs:
+        raise ValueError(f"page_table must have shape ({n_seqs}, max_pages)")
+    width = page_table.shape[1]
+    rs, cs = page_table.stride()
+    if cs != 1 and width > 1:
+        raise ValueError("page_table's rows must be contiguous")
+    return gdr_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), strides[0] if n_pages > 1 else 0,
+                        strides[1] if page > 1 else 0, strides[2] if heads > 1 else 0, page_table.data_ptr(),
+                        rs if n_seqs > 1 else 0, n_pages, page, width)
+
+
+def _f32(t, shape, like, name: str) -> Optional[int]:
+    torch = _torch()
+    if t is None:
+        return None
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be fp32")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def gdr_attn_append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens, inv_freq, cu_seqlens=None, *,
+                    interleaved: bool = False, stream=None) -> None:
+    """Rotate new queries and keys by their positions and append keys and values to
+    the paged cache (see gdr_attn_append in include/gdr.h).
+
+    q, q_out [T, H_q, d] (both may be None); k, v [T, H_kv, d]; k_out like k, k itself
+    or None; k_cache, v_cache [n_pages, page_size, H_kv, d] with any strides (a
+    head-major cache is passed as cache.transpose(1, 2)); page_table int32 [n, max_pages];
+    kv_lens int32 [n], each sequence's tokens including the new ones; inv_freq fp32
+    [rot_dim / 2] (None: no rotation); cu_seqlens int32 [n + 1], or None when every
+    sequence has T / n new tokens."""
+    n = kv_lens.shape[0]
+    T = k.shape[0]
+    if k.dim() != 3:
+        raise ValueError("k must be [T, H_kv, d]")
+    h_q = k.shape[1] if q is None else q.shape[1]
+    dims = _attn_dims(h_q, k, 1.0)
+    if k_cache.dtype != k.dtype or k_cache.device != k.device:
+        raise TypeError("the caches must have k's dtype and device")
+    if k_cache.shape[2:] != k.shape[1:]:
+        raise ValueError("the caches must have k's heads and head size")
+    h_kv = k.shape[1]
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    qr = qo = ko = None
+    if q is not None:
+        qr, qo = _rows(q, k, h_q, T, "q"), _rows(q_out, k, h_q, T, "q_out")
+    if k_out is not None:
+        ko = _rows(k_out, k, h_kv, T, "k_out")
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    st = lib().gdr_attn_append(
+        dims, n, None if cu_seqlens is None else _ints(cu_seqlens, n + 1, k, "cu_seqlens"), T, qr,
+        _rows(k, k, h_kv, T, "k"), _rows(v, k, h_kv, T, "v"), qo, ko, _cache(k_cache, v_cache, page_table, n),
+        _ints(kv_lens, n, k, "kv_lens"), _f32(inv_freq, (rot // 2,), k, "inv_freq") if rot else None, rot,
+        1 if interleaved else 0, _stream_handle(stream, k.device))
+    _check(st, "gdr_attn_append")
+
+
+def gdr_attn_prefill(q, k, v, o, cu_seqlens, *, scale: Optional[float] = None, lse=None, stream=None) -> None:
+    """Causal attention over whole packed prompts (see gdr_attn_prefill in
+    include/gdr.h): q, o [T, H_q, d]; k, v [T, H_kv, d], strided rows; cu_seqlens int32
+    [n + 1] on the device; scale defaults to 1 / sqrt(d); lse fp32 [T, H_q] or None."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, H_q, d] and k [T, H_kv, d]")
+    T, h_q, _ = q.shape
+    h_kv = k.shape[1]
+    n = cu_seqlens.shape[0] - 1
+    st = lib().gdr_attn_prefill(
+        _attn_dims(h_q, k, scale), n, _ints(cu_seqlens, n + 1, q, "cu_seqlens"), T, _rows(q, k, h_q, T, "q"),
+        _rows(k, k, h_kv, T, "k"), _rows(v, k, h_kv, T, "v"), _rows(o, k, h_q, T, "o"),
+        _f32(lse, (T, h_q), k, "lse"), _stream_handle(stream, q.device))
+    _check(st, "gdr_attn_prefill")
+
+
+def gdr_attn_decode_workspace_bytes(q, k_cache, n_seqs: int, n_tok: int = 1) -> int:
+    """Device scratch bytes gdr_attn_decode needs."""
+    return int(lib().gdr_attn_decode_workspace_bytes(_attn_dims(q.shape[1], k_cache, None), int(n_seqs), int(n_tok)))
+
+
+def gdr_attn_decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok: int = 1, *, scale: Optional[float] = None,
+                    lse=None, workspace=None, stream=None) -> None:
+    """Attention of every sequence's last n_tok (1 .. 16) tokens over its paged cache
+    (see gdr_attn_decode in include/gdr.h): q, o [n * n_tok, H_q, d]; caches, page_table
+    and kv_lens as for gdr_attn_append; lse fp32 [n * n_tok, H_q] or None.  Without
+    ``workspace`` (a device tensor of gdr_attn_decode_workspace_bytes bytes) one is taken
+    from torch's allocator on the call's stream."""
+    torch = _torch()
+    if q.dim() != 3:
+        raise ValueError("q must be [n * n_tok, H_q, d]")
+    n, h_q = kv_lens.shape[0], q.shape[1]
+    rows = n * n_tok
+    dims = _attn_dims(h_q, k_cache, scale)
+    L = lib()
+    if workspace is None:
+        need = int(L.gdr_attn_decode_workspace_bytes(dims, n, n_tok))
+        if need > 0:
+            s = stream if stream is not None else torch.cuda.current_stream(q.device)
+            if isinstance(s, int):
+                s = torch.cuda.ExternalStream(s, device=q.device)
+            with torch.cuda.stream(s):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = L.gdr_attn_decode(
+        dims, n, n_tok, _rows(q, k_cache, h_q, rows, "q"), _cache(k_cache, v_cache, page_table, n),
+        _ints(kv_lens, n, q, "kv_lens"), _rows(o, k_cache, h_q, rows, "o"), _f32(lse, (rows, h_q), q, "lse"),
+        _ptr(workspace), ws_bytes, _stream_handle(stream, q.device))
+    _check(st, "gdr_attn_decode")

@@ -1,0 +1,51 @@
+// Internal launch interface of the attention operators.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gdr.h"
+
+namespace gdr {
+namespace attn {
+
+// Strided rows of heads: value x of head h of token t at p[t * ts + h * hs + x].
+struct Rows {
+    uint16_t *p;
+    int64_t ts, hs;
+};
+
+struct Cache {
+    uint16_t *k, *v;
+    int64_t page_stride, token_stride, head_stride;
+    const int32_t *table;
+    int64_t table_stride;
+    int32_t n_pages, page_size, max_pages;
+};
+
+// Everything one launch needs, already validated on the host.
+struct Args {
+    int h_q, h_kv, group, d;
+    int f16;  // 1: fp16, 0: bf16
+    float scale;
+    int n_seqs, n_tok;  // n_tok: decode's tokens per sequence
+    const int32_t *cu;  // packed sequences' starts; nullptr (append): t_total / n_seqs tokens each
+    int64_t t_total;
+    Rows q, k, v, o;
+    Rows q_out, k_out;  // append: p is nullptr where not wanted
+    Cache cache;
+    const int32_t *kv_lens;
+    float *lse;
+    const float *inv_freq;
+    int rot, interleaved;
+    void *ws;
+    int32_t *err;
+};
+
+cudaError_t launch_append(const Args &a, cudaStream_t s);
+cudaError_t launch_prefill(const Args &a, cudaStream_t s);
+cudaError_t launch_decode(const Args &a, cudaStream_t s);
+size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok);
+
+}  // namespace attn
+}  // namespace gdr

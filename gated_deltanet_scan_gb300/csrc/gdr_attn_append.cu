@@ -1,0 +1,234 @@
+// Position rotation of new queries and keys, and the append of keys and values to
+// the paged cache, in one pass.
+//
+// Math.  A token at position p turns pair i of every query and key head by the
+// angle a = p f_i:  (x, y) -> (x cos a - y sin a, x sin a + y cos a).  The angle is
+// reduced in 64-bit fixed point: f_i / 2 pi modulo one turn is held as a fraction
+// of 2^64 (off by at most 2^-53 of a turn), p times it wraps around exactly, and
+// the top 32 bits of the product are the signed fraction of a turn that cos and
+// sin take.  At p = 2^24 the angle is still good to 2^-29 turns; a 32-bit float
+// product would be off by whole radians.
+//
+// Bound by HBM for prompts (every row read once, every output written once) and by
+// latency for a few tokens.  One 16-byte vector (8 values) per lane, d / 8 lanes a
+// row: a lane keeps the same 8 values of every row it handles, so cos and sin are
+// computed once per token and lane and serve all of the token's heads; 64-bit
+// products are integer multiplies, the fp64 pipe is used once per lane.  A pair's
+// other half is in the same vector (interleaved), in another lane of the row
+// (halves a multiple of 8 apart: shuffles) or read again by value (other halves).
+// A row is read whole by its warp before any of it is written, so outputs may be
+// the inputs.
+#include "gdr_attn_common.cuh"
+#include "gdr_internal.h"
+
+namespace gdr {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kUnroll = 4;  // row vectors in flight per lane
+
+struct Split {
+    int tokens;  // consecutive tokens per warp
+    int parts;   // warps that share a token's rows
+};
+
+enum Pairing { kNone = 0, kInterleaved = 1, kShuffle = 2, kByValue = 3 };
+
+template <int D, bool F16, int PAIR>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Args a, const Split sp) {
+    constexpr int LPR = D / 8;    // lanes per row
+    constexpr int RPW = 32 / LPR;  // rows per warp and step
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t chunk = warp / sp.parts;
+    const int part = (int)(warp - chunk * sp.parts);
+    const int64_t first = chunk * sp.tokens;
+    if (first >= a.t_total) return;
+    const int64_t last = min(first + sp.tokens, a.t_total);
+    const int vec = lane % LPR, sub = lane / LPR;
+    const int e0 = vec * 8;
+    const int half = a.rot / 2;
+
+    // fractions of a turn per position, the rotation's signs and reach of this lane's 8 values
+    uint64_t turn[8];
+    if constexpr (PAIR != kNone) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int x = e0 + e;
+            turn[e] = 0;
+            if (x < a.rot) {
+                const int i = PAIR == kInterleaved ? x >> 1 : (x < half ? x : x - half);
+                const double t = (double)a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+                const double f = t - floor(t);
+                // f may round up to 1 for tiny negative t: that is 0 turns
+                turn[e] = f < 1.0 ? (uint64_t)(f * 18446744073709551616.0) : 0;
+            }
+        }
+    }
+
+    const int n_q = a.q.p ? a.h_q : 0;
+    const int rows = n_q + 2 * a.h_kv;
+    const int even = (int)(a.t_total / a.n_seqs);  // tokens per sequence without cu
+    int s = a.cu ? find_seq(a.cu, a.n_seqs, first) : (int)(first / even);
+
+    for (int64_t t = first; t < last; ++t) {
+        int64_t t0, t1;
+        if (a.cu) {
+            while (s + 1 < a.n_seqs && a.cu[s + 1] <= t) ++s;
+            t0 = a.cu[s];
+            t1 = a.cu[s + 1];
+            if (t0 < 0 || t < t0 || t1 <= t || t1 > a.t_total) {
+                record_invalid(a.err);
+                continue;
+            }
+        } else {
+            while (t >= (int64_t)(s + 1) * even) ++s;
+            t0 = (int64_t)s * even;
+            t1 = t0 + even;
+        }
+        const int64_t pos = (int64_t)a.kv_lens[s] - (t1 - t);
+        int64_t slot = -1;  // offset of the token's slot in the cache, in elements
+        if (pos >= 0 && pos < (int64_t)a.cache.max_pages * a.cache.page_size) {
+            const int pg = (int)pos / a.cache.page_size;
+            const int page = a.cache.table[(int64_t)s * a.cache.table_stride + pg];
+            if (page >= 0 && page < a.cache.n_pages)
+                slot = page * a.cache.page_stride +
+                       (int64_t)((int)pos - pg * a.cache.page_size) * a.cache.token_stride;
+        }
+        if (slot < 0) record_invalid(a.err);
+
+        float cs[8], sn[8];
+        if constexpr (PAIR != kNone) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int x = e0 + e;
+                if (PAIR == kInterleaved && (e & 1)) {
+                    cs[e] = cs[e - 1];
+                    sn[e] = -sn[e - 1];
+                } else {
+                    const int32_t w = (int32_t)(((uint64_t)pos * turn[e]) >> 32);
+                    sincospif((float)w * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31 half turns
+                    if (PAIR == kInterleaved || x < half) sn[e] = -sn[e];
+                }
+            }
+        }
+
+        for (int r0 = part * RPW; r0 < rows; r0 += sp.parts * RPW * kUnroll) {
+            uint4 w[kUnroll];
+            const uint16_t *src[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int r = min(r0 + u * sp.parts * RPW + sub, rows - 1);
+                src[u] = r < n_q ? a.q.p + t * a.q.ts + r * a.q.hs
+                         : r < n_q + a.h_kv ? a.k.p + t * a.k.ts + (r - n_q) * a.k.hs
+                                            : a.v.p + t * a.v.ts + (r - n_q - a.h_kv) * a.v.hs;
+                w[u] = *reinterpret_cast<const uint4 *>(src[u] + e0);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int r = r0 + u * sp.parts * RPW + sub;
+                if constexpr (PAIR != kNone) {
+                    const uint32_t own[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                    uint32_t oth[4];  // the pairs' other values
+                    if constexpr (PAIR == kInterleaved) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) oth[i] = __byte_perm(own[i], 0, 0x1032);
+                    } else if constexpr (PAIR == kShuffle) {
+                        const int h8 = half >> 3;
+                        const int from = vec < h8 ? lane + h8 : lane - h8;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) oth[i] = __shfl_sync(0xffffffffu, own[i], from & 31);
+                    } else {
+                        const int ru = min(r, rows - 1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t o2 = 0;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int x = e0 + 2 * i + j;
+                                if (x < a.rot && ru < n_q + a.h_kv)
+                                    o2 |= (uint32_t)src[u][x < half ? x + half : x - half] << (16 * j);
+                            }
+                            oth[i] = o2;
+                        }
+                    }
+                    if (r < n_q + a.h_kv && e0 < a.rot) {
+                        uint32_t res[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 x = unpack2<F16>(own[i]), y = unpack2<F16>(oth[i]);
+                            const float lo = x.x * cs[2 * i] + y.x * sn[2 * i];
+                            const float hi = x.y * cs[2 * i + 1] + y.y * sn[2 * i + 1];
+                            const uint32_t m = pack2<F16>(lo, hi);
+                            // values past the rotated part are copied bit for bit
+                            const int e = e0 + 2 * i;
+                            res[i] = (e < a.rot ? m & 0xFFFFu : own[i] & 0xFFFFu) |
+                                     (e + 1 < a.rot ? m & 0xFFFF0000u : own[i] & 0xFFFF0000u);
+                        }
+                        w[u] = make_uint4(res[0], res[1], res[2], res[3]);
+                    }
+                }
+            }
+            if constexpr (PAIR == kByValue) __syncwarp();  // every value read before any is written
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int r = r0 + u * sp.parts * RPW + sub;
+                if (r >= rows) continue;
+                if (r < n_q) {
+                    *reinterpret_cast<uint4 *>(a.q_out.p + t * a.q_out.ts + r * a.q_out.hs + e0) = w[u];
+                } else {
+                    const bool is_k = r < n_q + a.h_kv;
+                    const int h = is_k ? r - n_q : r - n_q - a.h_kv;
+                    if (is_k && a.k_out.p)
+                        *reinterpret_cast<uint4 *>(a.k_out.p + t * a.k_out.ts + h * a.k_out.hs + e0) = w[u];
+                    if (slot >= 0)
+                        *reinterpret_cast<uint4 *>((is_k ? a.cache.k : a.cache.v) + slot + h * a.cache.head_stride +
+                                                   e0) = w[u];
+                }
+            }
+        }
+    }
+}
+
+template <int D, bool F16>
+void launch(const Args &a, int pairing, const Split &sp, unsigned blocks, cudaStream_t s) {
+    switch (pairing) {
+        case kNone: append_kernel<D, F16, kNone><<<blocks, kThreads, 0, s>>>(a, sp); break;
+        case kInterleaved: append_kernel<D, F16, kInterleaved><<<blocks, kThreads, 0, s>>>(a, sp); break;
+        case kShuffle: append_kernel<D, F16, kShuffle><<<blocks, kThreads, 0, s>>>(a, sp); break;
+        default: append_kernel<D, F16, kByValue><<<blocks, kThreads, 0, s>>>(a, sp); break;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const Args &a, cudaStream_t s) {
+    const int rpw = 32 / (a.d / 8);
+    const int rows = (a.q.p ? a.h_q : 0) + 2 * a.h_kv;
+    // One warp per token and all its rows where there are tokens enough to fill the
+    // GPU (32 warps an SM), several tokens per warp beyond that; with fewer tokens a
+    // token's rows are shared out, down to one step of a warp each.
+    const int64_t want = 152 * 32;
+    Split sp{1, 1};
+    if (a.t_total >= want) {
+        sp.tokens = (int)((a.t_total + want - 1) / want);
+    } else {
+        const int64_t steps = (rows + rpw - 1) / rpw;
+        const int64_t parts = want / a.t_total;
+        sp.parts = (int)(parts < steps ? parts : steps);
+    }
+    const int64_t warps = (a.t_total + sp.tokens - 1) / sp.tokens * sp.parts;
+    const unsigned blocks = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
+    const int pairing = a.rot == 0 ? kNone : a.interleaved ? kInterleaved : (a.rot / 2) % 8 == 0 ? kShuffle : kByValue;
+    if (a.d == 64)
+        a.f16 ? launch<64, true>(a, pairing, sp, blocks, s) : launch<64, false>(a, pairing, sp, blocks, s);
+    else if (a.d == 128)
+        a.f16 ? launch<128, true>(a, pairing, sp, blocks, s) : launch<128, false>(a, pairing, sp, blocks, s);
+    else
+        a.f16 ? launch<256, true>(a, pairing, sp, blocks, s) : launch<256, false>(a, pairing, sp, blocks, s);
+    return cudaGetLastError();
+}
+
+}  // namespace attn
+}  // namespace gdr

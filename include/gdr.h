@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define GDR_ABI_VERSION 9
+#define GDR_ABI_VERSION 10
 
 /* Same object as cudaStream_t; declared here so callers need no CUDA header. */
 typedef struct CUstream_st *gdr_stream_t;
@@ -65,7 +65,8 @@ typedef enum gdr_status {
     GDR_ERR_DEVICE_TIMEOUT = 4
 } gdr_status;
 
-typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
+/* GDR_F16 is a type of the attention operators (gdr_attn_*) only. */
+typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1, GDR_F16 = 2 } gdr_dtype;
 
 typedef struct gdr_dims {
     int32_t h_qk;      /* QK heads */
@@ -420,6 +421,139 @@ gdr_status gdr_state_snapshot(const gdr_dims *dims, int32_t n_seqs, const float 
 /* Copy n_seqs states back from `snapshot` to `state` (undo a verify block). */
 gdr_status gdr_state_restore(const gdr_dims *dims, int32_t n_seqs, const float *snapshot,
                              float *state, gdr_stream_t stream);
+
+/*
+ * Softmax attention: the layers of a hybrid model that stand between the gated
+ * delta rule's (for Qwen3.5-9B every fourth: 16 query and 4 key/value heads of
+ * 256, rotation over 64 of them).  Three operators: gdr_attn_append rotates new
+ * queries and keys and stores keys and values in a paged cache, gdr_attn_prefill
+ * is causal attention over whole packed prompts, and gdr_attn_decode is attention
+ * of the last 1 to 16 tokens of every sequence over its pages.
+ *
+ * Types: q, k, v, o and the cache all have dims->dtype, GDR_BF16 or GDR_F16;
+ * scores, softmax statistics and sums are fp32, and each output is rounded once.
+ * Head sizes: d in {64, 128, 256}.  Query head h reads key/value head
+ * h / (h_q / h_kv); h_q / h_kv <= 128.
+ *
+ * Tensors of rows (q, k, v, o) may be strided, e.g. parts of one fused
+ * projection: value x of head h of token t is at
+ *     ptr[t * token_stride + h * head_stride + x],
+ * strides in elements.  ptr is 16-byte aligned and both strides are multiples of
+ * 8, not negative, and below 2^40 (GDR_ERR_INVALID_ARG otherwise).  Rows that are
+ * written must not overlap one another.
+ */
+typedef struct gdr_attn_dims {
+    int32_t h_q;   /* query heads; a multiple of h_kv */
+    int32_t h_kv;  /* key/value heads */
+    int32_t d;     /* head size: 64, 128 or 256 */
+    int32_t dtype; /* GDR_BF16 or GDR_F16 */
+    float scale;   /* multiplies q . k; finite; usually 1 / sqrt(d) */
+} gdr_attn_dims;
+
+typedef struct gdr_rows {
+    void *ptr; /* DEVICE; not written through where the argument is an input */
+    int64_t token_stride;
+    int64_t head_stride;
+} gdr_rows;
+
+/*
+ * A paged cache.  Token p of sequence s is slot p % page_size of page
+ * page_table[s * table_stride + p / page_size]; its key and value for head h are
+ * the d values from
+ *     k (v) + page * page_stride + slot * token_stride + h * head_stride,
+ * which covers token-major and head-major pages.  k and v: DEVICE, 16-byte
+ * aligned; strides in elements, multiples of 8, not negative, below 2^40; offsets are
+ * computed in 64 bits.  page_table: DEVICE int32, entries of pages a sequence
+ * does not reach yet are not read.  page_size and max_pages (pages a table row
+ * holds) are at least 1, and page_size * max_pages below 2^31.  A page id outside
+ * [0, n_pages) is never followed: the kernels record GDR_ERR_INVALID_ARG in the
+ * device error word and leave out its writes (append) or read zeros (decode: that
+ * sequence's results are then meaningless).
+ */
+typedef struct gdr_kv_cache {
+    void *k, *v;
+    int64_t page_stride, token_stride, head_stride;
+    const int32_t *page_table;
+    int64_t table_stride;
+    int32_t n_pages, page_size, max_pages;
+} gdr_kv_cache;
+
+/*
+ * Rotates the new tokens' queries and keys and appends keys and values to the cache.
+ *
+ * Sequence s has n new tokens: [cu_seqlens[s], cu_seqlens[s + 1]) of the packed
+ * rows, or, with cu_seqlens NULL, t_total / n_seqs rows each.  kv_lens[s] counts
+ * the sequence's tokens INCLUDING these (the same array gdr_attn_decode takes), so
+ * new token j has position p = kv_lens[s] - n + j.  The first rot_dim values of
+ * every query and key head are rot_dim / 2 pairs (x, y): values i and
+ * i + rot_dim / 2, or, interleaved, 2 i and 2 i + 1.  With a = p * inv_freq[i],
+ *     (x, y) -> (x cos a - y sin a, x sin a + y cos a),
+ * the angle reduced exactly enough (64-bit fixed point) that far positions lose
+ * nothing; the other values are copied.  q_out, k_out and the cached key are the
+ * rotated rows rounded once; values are copied.
+ *
+ *   q, q_out   [t_total][h_q][d]; q_out may be q (same strides).  Both NULL: no queries.
+ *   k, v       [t_total][h_kv][d]
+ *   k_out      as k, or k itself, or NULL: the rotated keys, packed (for gdr_attn_prefill)
+ *   kv_lens    DEVICE int32 [n_seqs]
+ *   inv_freq   DEVICE fp32 [rot_dim / 2], each value's magnitude below 2^20; NULL when rot_dim is 0
+ *   rot_dim    even, 0 .. d
+ * A sequence whose positions leave [0, max_pages * page_size) has the tokens outside
+ * left out of the cache, and GDR_ERR_INVALID_ARG recorded in the device error word;
+ * entries of cu_seqlens outside [0, t_total] likewise skip the sequence.  dims->scale
+ * is not used.  n_seqs = 0 or t_total = 0 is a no-op.
+ */
+gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, int64_t t_total,
+                           const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *q_out,
+                           const gdr_rows *k_out, const gdr_kv_cache *cache, const int32_t *kv_lens,
+                           const float *inv_freq, int32_t rot_dim, int32_t interleaved, gdr_stream_t stream);
+
+/*
+ * Causal attention over whole packed prompts:
+ *     o_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j
+ * within each sequence [cu_seqlens[s], cu_seqlens[s + 1]) (DEVICE int32
+ * [n_seqs + 1], non-decreasing from 0 to t_total; empty sequences allowed; entries
+ * outside [0, t_total] make the kernel skip the sequences that use them and record
+ * GDR_ERR_INVALID_ARG in the device error word).  A token never sees a later one's
+ * or another sequence's key or value, whatever these hold (NaN and infinities
+ * included).
+ *
+ *   q, o [t_total][h_q][d]; k, v [t_total][h_kv][d] (strided rows, dims->dtype)
+ *   lse  NULL, or DEVICE fp32 [t_total][h_q]: log sum_j exp(scale q_i . k_j)
+ * t_total below 2^31.  No workspace.
+ */
+gdr_status gdr_attn_prefill(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, int64_t t_total,
+                            const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *o, float *lse,
+                            gdr_stream_t stream);
+
+/*
+ * Attention of the last n_tok (1 .. 16) tokens of every sequence over its paged
+ * cache: a decode step (n_tok = 1) or the draft tokens of a speculative block.  The
+ * tokens' own keys and values are in the cache already (gdr_attn_append).  Query j
+ * of sequence s, row s * n_tok + j, has position kv_lens[s] - n_tok + j and sees
+ * the positions up to its own:
+ *     o = sum_{p <= kv_lens[s] - n_tok + j} softmax_p(scale q . k_p) v_p.
+ * A query that sees nothing (kv_lens[s] < n_tok - j, or 0) has o = 0 and lse =
+ * -infinity.  kv_lens[s] outside [0, max_pages * page_size] counts as 0 and records
+ * GDR_ERR_INVALID_ARG in the device error word.  What the cache holds past a
+ * sequence's tokens is never used, nor a later draft token's key or value.
+ *
+ * The work of all sequences is cut into equal parts, one per resident block,
+ * whatever the lengths; sequences that are cut have their parts joined by a second
+ * launch in a fixed order, so results do not change from run to run.
+ *
+ *   q, o       [n_seqs * n_tok][h_q][d]
+ *   kv_lens    DEVICE int32 [n_seqs]
+ *   lse        NULL, or DEVICE fp32 [n_seqs * n_tok][h_q]
+ *   workspace  DEVICE, 16-byte aligned, at least gdr_attn_decode_workspace_bytes();
+ *              holds nothing between calls; not to be used by other work at the same time
+ */
+gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const gdr_rows *q,
+                           const gdr_kv_cache *cache, const int32_t *kv_lens, const gdr_rows *o, float *lse,
+                           void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/* Bytes of workspace gdr_attn_decode needs (0 for invalid dims).  Depends on the shapes only. */
+size_t gdr_attn_decode_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
