@@ -1,95 +1,620 @@
 // Attention of the last few tokens of every sequence over its paged cache.
 //
-// One warp per query row: the running maximum m and sum l of the softmax and the
-// row's output in fp32, one token at a time.
+// Math.  For one key/value head the group's queries of the sequence's n_tok tokens
+// are rows r = j group + g of one small matrix Q (rows = n_tok group).  Over tiles
+// of 16 tokens, with x = scale log2(e) Q K^T and the running row maximum m,
+//     p = 2^(x - m),   l += sum p,   O += P V,
+// earlier sums rescaled by 2^(m_old - m) when m grows; o = O / l at the end.  Two
+// parts of a row's tokens join the same way from their (m, l, O).
+//
+// Bound by HBM: keys and values are read once (4 h_kv d bytes a token) and little
+// else moves.  The tiles of all (sequence, key/value head, row block) triples lie
+// on one line, cut into equal parts, one per worker, so every worker streams the
+// same number of tiles whatever the lengths are.  A worker is RW warps of 16 rows
+// each (rows <= 16 RW) with a ring of shared-memory slots of their own, filled by
+// 16-byte asynchronous copies several tiles ahead: no worker waits for another, and
+// while one starts or ends a sequence the others of its SM keep the memory busy.
+// Both products are warp-level m16n8k16 MMAs on the 16-bit rows with fp32 sums: at 4
+// flops a byte the tensor pipes are far from busy, so the extra rows they pad cost
+// nothing.  A sequence that one worker sees whole is written by it; the others leave
+// (m, l, O) in the workspace, and a second kernel joins them in the order of the
+// tokens.  That launch is a programmatic dependent of the first.
+//
+// P is rounded to the tensors' type for P V (its sum l is not): that is the only
+// rounding between the inputs and the output's own.
 #include "gdr_attn_common.cuh"
 #include "gdr_internal.h"
+#include "tc_ptx.cuh"
 
 namespace gdr {
 namespace attn {
 namespace {
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) decode_rows_kernel(const __grid_constant__ Args a) {
-    constexpr int W = D / 64;  // 32-bit words per lane
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= a.t_total * a.h_q) return;
-    const int64_t t = row / a.h_q;
-    const int h = (int)(row - t * a.h_q);
-    const int s = (int)(t / a.n_tok), j = (int)(t - (int64_t)s * a.n_tok);
-    int64_t len = a.kv_lens[s];
-    if (len < 0 || len > (int64_t)a.cache.max_pages * a.cache.page_size) {
-        record_invalid(a.err);
-        len = 0;
-    }
-    float2 q[W], o[W];
-    const uint32_t *qp = reinterpret_cast<const uint32_t *>(a.q.p + t * a.q.ts + h * a.q.hs);
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        q[i] = unpack2<F16>(qp[lane + 32 * i]);
-        o[i] = make_float2(0.f, 0.f);
-    }
-    float m = -CUDART_INF_F, l = 0.f;
-    const int64_t seen = len - a.n_tok + j + 1;
-    for (int64_t p = 0; p < seen; ++p) {
-        const int page = a.cache.table[s * a.cache.table_stride + p / a.cache.page_size];
-        if (page < 0 || page >= a.cache.n_pages) {
-            record_invalid(a.err);
-            continue;
-        }
-        const int64_t at = page * a.cache.page_stride + (p % a.cache.page_size) * a.cache.token_stride +
-                           (h / a.group) * a.cache.head_stride;
-        const uint32_t *kp = reinterpret_cast<const uint32_t *>(a.cache.k + at);
-        const uint32_t *vp = reinterpret_cast<const uint32_t *>(a.cache.v + at);
-        float x = 0.f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const float2 k = unpack2<F16>(kp[lane + 32 * i]);
-            x += q[i].x * k.x + q[i].y * k.y;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        x *= a.scale;
-        const float mn = fmaxf(m, x);
-        const float c = m == mn ? 1.f : __expf(m - mn), w = __expf(x - mn);
-        l = l * c + w;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const float2 v = unpack2<F16>(vp[lane + 32 * i]);
-            o[i].x = o[i].x * c + w * v.x;
-            o[i].y = o[i].y * c + w * v.y;
-        }
-    }
-    uint32_t *op = reinterpret_cast<uint32_t *>(a.o.p + t * a.o.ts + h * a.o.hs);
-    const float r = seen > 0 ? 1.f / l : 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) op[lane + 32 * i] = pack2<F16>(o[i].x * r, o[i].y * r);
-    if (a.lse && lane == 0) a.lse[row] = seen > 0 ? m + logf(l) : -CUDART_INF_F;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kBlocks = 152;  // one resident block per SM
+constexpr int kTile = 16;     // tokens per tile: the MMA's inner size in P V
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D, int RW>
+struct Shape {
+    static constexpr int WORKERS = kWarps / RW;  // per block
+    static constexpr uint32_t SLOT = kTile * D * 2;
+    // about 24 KiB of ring per warp, at most 8 slots
+    static constexpr int FIT = RW * 24576 / (int)SLOT;
+    static constexpr int SLOTS = FIT < 8 ? FIT : 8;
+    static constexpr uint32_t SMEM = WORKERS * SLOTS * SLOT;
+};
+
+// Row warps for this many rows of a key/value head.
+int row_warps(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
+
+// Workspace: first tile of every sequence on the line ([n_seqs + 1], the last one the
+// total), then per worker two parts (its first and its last, cut, triple): per row
+// m and l, then O.
+struct Layout {
+    int rows, rw, blocks_of_rows, part_rows, workers;
+    size_t ml, o, total;
+};
+__host__ __device__ inline Layout layout(int rows, int rw, int d, int n_seqs) {
+    Layout L;
+    L.rows = rows;
+    L.rw = rw;
+    L.blocks_of_rows = (rows + 16 * rw - 1) / (16 * rw);
+    L.part_rows = rows < 16 * rw ? rows : 16 * rw;
+    L.workers = kBlocks * (kWarps / rw);
+    const size_t parts = (size_t)L.workers * 2 * L.part_rows;
+    L.ml = ((size_t)(n_seqs + 1) * 8 + 15) / 16 * 16;
+    L.o = L.ml + (parts * 8 + 15) / 16 * 16;
+    L.total = L.o + parts * d * 4;
+    return L;
 }
 
-template <int D>
-void launch(const Args &a, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((a.t_total * a.h_q + 3) / 4);
-    if (a.f16)
-        decode_rows_kernel<D, true><<<blocks, 128, 0, s>>>(a);
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        decode_rows_kernel<D, false><<<blocks, 128, 0, s>>>(a);
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// True where a 16-bit value is an infinity or NaN.
+template <bool F16>
+__device__ __forceinline__ bool nonfinite(uint32_t half_word) {
+    constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+    return (half_word & e) == e;
+}
+
+// Tokens of sequence s; outside [0, limit] counts as none.
+__device__ __forceinline__ int64_t length_of(const Args &a, int s) {
+    const int64_t n = a.kv_lens[s];
+    return n < 0 || n > (int64_t)a.cache.max_pages * a.cache.page_size ? 0 : n;
+}
+// First tile of worker w's part of the line.
+__device__ __forceinline__ int64_t part_start(int64_t total, int workers, int w) { return total * w / workers; }
+
+template <int D, bool F16, int RW>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Args a) {
+    using Sh = Shape<D, RW>;
+    constexpr int KS = D / 16;   // inner steps of Q K^T
+    constexpr int NT = D / 8;    // output column tiles
+    constexpr int CPR = D / 8;   // 16-byte chunks of a row
+    constexpr int RPI = 32 / CPR < 1 ? 1 : 32 / CPR;  // rows one copy instruction of a warp covers
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ int64_t s_scan[kThreads + 1];
+    __shared__ int64_t s_warp[kWarps];
+    __shared__ int s_seq[Sh::WORKERS];
+    __shared__ int64_t s_base[Sh::WORKERS];
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wk = warp / RW, rw = warp % RW;  // worker in the block, row warp in the worker
+    const int rows = a.n_tok * a.group;
+    const Layout L = layout(rows, RW, D, a.n_seqs);
+    // workers next to each other on the line sit on different SMs, so few tiles spread over many
+    const int me = wk * kBlocks + blockIdx.x;
+    int64_t *const line = reinterpret_cast<int64_t *>(a.ws);
+    const int64_t per_seq = (int64_t)a.h_kv * L.blocks_of_rows;
+
+    // The line: 256 sequences at a time, an exclusive scan of their tiles; the first
+    // pass finds the total, the second each worker's first sequence (one pass does
+    // both where there are up to 256 sequences).
+    int64_t total = 0;
+    const int chunks = (a.n_seqs + kThreads - 1) / kThreads;
+    if (tid < Sh::WORKERS) s_seq[tid] = -1;
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t base = 0;
+        for (int c = 0; c < chunks; ++c) {
+            if (pass == 0 || chunks > 1) {
+                const int s = c * kThreads + tid;
+                int64_t n = 0;
+                if (s < a.n_seqs) {
+                    n = length_of(a, s);
+                    if (pass == 0 && blockIdx.x == 0 && n != a.kv_lens[s]) record_invalid(a.err);
+                    n = (n + kTile - 1) / kTile * per_seq;
+                }
+                int64_t x = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+                    if (lane >= d) x += y;
+                }
+                __syncthreads();
+                if (lane == 31) s_warp[warp] = x;
+                __syncthreads();
+                int64_t before = 0;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i)
+                    if (i < warp) before += s_warp[i];
+                s_scan[tid] = base + before + x - n;
+                if (tid == kThreads - 1) s_scan[kThreads] = base + before + x;
+                __syncthreads();
+            }
+            base = s_scan[kThreads];
+            if (pass == 1) {
+                const int s0 = c * kThreads, m = min(kThreads, a.n_seqs - s0);
+                if (tid < Sh::WORKERS) {  // the last sequence that starts at or before the worker's part
+                    const int64_t at = part_start(total, L.workers, tid * kBlocks + blockIdx.x);
+                    if (s_seq[tid] < 0 && at < base) {
+                        int lo = 0, hi = m - 1;
+                        while (lo < hi) {
+                            const int mid = (lo + hi + 1) >> 1;
+                            if (s_scan[mid] <= at)
+                                lo = mid;
+                            else
+                                hi = mid - 1;
+                        }
+                        s_seq[tid] = s0 + lo;
+                        s_base[tid] = s_scan[lo];
+                    }
+                }
+                if (blockIdx.x == 0) {
+                    if (tid < m) line[s0 + tid] = s_scan[tid];
+                    if (tid == 0 && c == chunks - 1) line[a.n_seqs] = base;
+                }
+            }
+        }
+        total = base;
+    }
+    __syncthreads();
+
+    int64_t at = part_start(total, L.workers, me);
+    const int64_t end = part_start(total, L.workers, me + 1);
+    if (at >= end) return;  // a whole worker; workers meet at no barrier from here on
+    int s = s_seq[wk];
+    int64_t base = s_base[wk];
+
+    const uint32_t slots = tc::smem_u32(ring) + wk * Sh::SLOTS * Sh::SLOT;
+    auto worker_sync = [&] {
+        if constexpr (RW == 1)
+            __syncwarp();
+        else
+            tc::named_sync(1 + wk, 32 * RW);
+    };
+    const float sc = a.scale * kLog2e;
+    const int r0 = lane >> 2, cq = lane & 3;  // the MMA's row (and row + 8) and column pair of this lane
+    bool first_part = true;
+
+    while (at < end) {
+        // the triple at `at`: sequence s (of `tiles` tiles), key/value head h, row block rb
+        int64_t len = length_of(a, s);
+        int64_t tiles = (len + kTile - 1) / kTile;
+        while (at >= base + tiles * per_seq) {
+            base += tiles * per_seq;
+            ++s;
+            len = length_of(a, s);
+            tiles = (len + kTile - 1) / kTile;
+        }
+        const int64_t hr = (at - base) / tiles;
+        const int h = (int)(hr / L.blocks_of_rows), rb = (int)(hr - (int64_t)h * L.blocks_of_rows);
+        const int64_t seg0 = base + hr * tiles;  // where the triple starts on the line
+        const int tile0 = (int)(at - seg0);
+        const int tile1 = (int)min(tiles, end - seg0);
+        const int steps = 2 * (tile1 - tile0);  // keys and values of a tile are a step each
+        const int32_t *const pages = a.cache.table + (int64_t)s * a.cache.table_stride;
+        const int64_t head = h * a.cache.head_stride;
+
+        // Copies: lane & 15 is a token of the tile; its offset serves keys and values.
+        int64_t off = 0;   // of the tile whose copies are being issued
+        bool there = false;
+        int page_next = 0, slot_next = 0;  // of the tile after it, its page id loaded a tile early
+        bool has_next = false;
+        auto look_up = [&](int tile) {
+            const int64_t p = (int64_t)tile * kTile + (lane & 15);
+            has_next = tile < tile1 && p < len;
+            if (has_next) {
+                const uint32_t pg = (uint32_t)p / (uint32_t)a.cache.page_size;
+                slot_next = (int)((uint32_t)p - pg * (uint32_t)a.cache.page_size);
+                page_next = pages[pg];
+            }
+        };
+        look_up(tile0);
+        auto issue = [&](int step) {
+            if (step < steps) {
+                if (!(step & 1)) {
+                    there = has_next;
+                    if (there && (page_next < 0 || page_next >= a.cache.n_pages)) {
+                        record_invalid(a.err);
+                        there = false;
+                    }
+                    off = there ? page_next * a.cache.page_stride + slot_next * a.cache.token_stride + head : 0;
+                    look_up(tile0 + (step >> 1) + 1);
+                }
+                const uint16_t *const from = (step & 1) ? a.cache.v : a.cache.k;
+                const uint32_t to = slots + (step % Sh::SLOTS) * Sh::SLOT;
+                // the worker's warps share the tile's rows
+#pragma unroll
+                for (int i = 0; i < kTile / RPI; ++i) {
+                    if (RW > 1 && i % RW != rw) continue;
+                    const int row = i * RPI + (RPI > 1 ? lane / CPR : 0);
+                    const int chunk = lane % CPR;
+                    const int64_t o = __shfl_sync(0xffffffffu, off, row);
+                    const bool ok = __shfl_sync(0xffffffffu, (int)there, row);
+                    // no token (past the end, or its page is out of range): zeros
+                    cp_async16(to + row * (D * 2) + ((chunk ^ (row & 7)) << 4), from + o + chunk * 8, ok ? 16u : 0u);
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < Sh::SLOTS - 1; ++i) issue(i);
+
+        // Q: rows lane / 4 and + 8 of this warp's 16, as MMA fragments
+        uint32_t qf[KS][4];
+        int64_t out_row[2];  // output row, or -1
+        int seen[2];         // tokens the row sees
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (rb * RW + rw) * 16 + r0 + 8 * i;
+            out_row[i] = -1;
+            seen[i] = 0;
+            const uint16_t *src = nullptr;
+            if (r < rows) {
+                const int j = r / a.group, g = r - j * a.group;
+                const int64_t t = (int64_t)s * a.n_tok + j;
+                out_row[i] = t * a.h_q + h * a.group + g;
+                seen[i] = (int)max((int64_t)0, len - a.n_tok + j + 1);
+                src = a.q.p + t * a.q.ts + (int64_t)(h * a.group + g) * a.q.hs;
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                qf[k][i] = src ? *reinterpret_cast<const uint32_t *>(src + k * 16 + cq * 2) : 0u;
+                qf[k][2 + i] = src ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 8 + cq * 2) : 0u;
+            }
+        }
+        const int64_t all_see = len - a.n_tok + 1;  // tokens every row sees
+
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+
+        for (int tile = tile0; tile < tile1; ++tile) {
+            const int step = 2 * (tile - tile0);
+            const int64_t p0 = (int64_t)tile * kTile;
+            const bool masked = p0 + kTile > all_see;  // some row does not see all of the tile
+
+            // --- keys: x = sc Q K^T
+            cp_async_wait<Sh::SLOTS - 2>();
+            worker_sync();
+            issue(step + Sh::SLOTS - 1);
+            float x[2][2][4];  // [chain][token half]: two accumulation chains hide the MMA's latency
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
+            {
+                const uint32_t kb = slots + (step % Sh::SLOTS) * Sh::SLOT;
+                const int row = (lane & 7) + ((lane >> 4) << 3);
+                const uint32_t rbase = kb + row * (D * 2);
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t b[4];
+                    ldsm4(rbase + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4), b);
+                    mma16816<F16>(x[k & 1][0], qf[k], b[0], b[1]);
+                    mma16816<F16>(x[k & 1][1], qf[k], b[2], b[3]);
+                }
+            }
+            uint32_t pf[4];  // P as an MMA operand
+            float c[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = sc * (x[0][e >> 1][2 * i + (e & 1)] + x[1][e >> 1][2 * i + (e & 1)]);
+                    if (masked && p0 + (e >> 1) * 8 + cq * 2 + (e & 1) >= seen[i]) v[e] = -CUDART_INF_F;
+                }
+                float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float mn = fmaxf(m[i], top);
+                const float ref = mn == -CUDART_INF_F ? 0.f : mn;  // nothing visible yet: p = 2^-inf
+                c[i] = m[i] == mn ? 1.f : tc::fast_exp2(m[i] - ref);
+                m[i] = mn;
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = tc::fast_exp2(v[e] - ref);
+                l[i] = l[i] * c[i] + ((p[0] + p[1]) + (p[2] + p[3]));
+                pf[i] = pack2<F16>(p[0], p[1]);
+                pf[2 + i] = pack2<F16>(p[2], p[3]);
+            }
+            if (__any_sync(0xffffffffu, c[0] != 1.f || c[1] != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    acc[n][0] *= c[0];
+                    acc[n][1] *= c[0];
+                    acc[n][2] *= c[1];
+                    acc[n][3] *= c[1];
+                }
+            }
+
+            // --- values: O += P V
+            cp_async_wait<Sh::SLOTS - 2>();
+            worker_sync();
+            issue(step + Sh::SLOTS);
+            const uint32_t vb = slots + ((step + 1) % Sh::SLOTS) * Sh::SLOT;
+            if (masked && a.n_tok > 1) {
+                // Rows that do not see a draft token have p = 0 for it, and 0 times an
+                // infinity or NaN would reach them: such values are added to the rows
+                // that see them (p > 0 leaves them as they are) and replaced by zeros.
+#pragma unroll 1
+                for (int t = 0; t < kTile; ++t) {
+                    const int64_t p = p0 + t;
+                    if (p >= len) break;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t w;
+                        asm volatile("ld.shared.b32 %0, [%1];"
+                                     : "=r"(w)
+                                     : "r"(vb + t * (D * 2) + ((n ^ (t & 7)) << 4) + cq * 4)
+                                     : "memory");
+                        if (nonfinite<F16>(w) || nonfinite<F16>(w >> 16)) {
+                            const float2 v = unpack2<F16>(w);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                if (p >= seen[i]) continue;
+                                if (nonfinite<F16>(w)) acc[n][2 * i] += v.x;
+                                if (nonfinite<F16>(w >> 16)) acc[n][2 * i + 1] += v.y;
+                            }
+                        }
+                    }
+                }
+                worker_sync();
+                for (int i = rw * 32 + lane; i < kTile * D / 2; i += 32 * RW) {
+                    uint32_t w;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vb + 4 * i) : "memory");
+                    uint32_t z = nonfinite<F16>(w) ? w & 0xFFFF0000u : w;
+                    z = nonfinite<F16>(w >> 16) ? z & 0xFFFFu : z;
+                    if (z != w) asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + 4 * i), "r"(z) : "memory");
+                }
+                worker_sync();
+            }
+            {
+                const int row = lane & 15;
+                const uint32_t rbase = vb + row * (D * 2);
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t b[4];
+                    ldsm4t(rbase + (((n + (lane >> 4)) ^ (row & 7)) << 4), b);
+                    mma16816<F16>(acc[n], pf, b[0], b[1]);
+                    mma16816<F16>(acc[n + 1], pf, b[2], b[3]);
+                }
+            }
+        }
+        cp_async_wait<0>();  // only empty groups are left
+        worker_sync();       // the ring is free for the next triple
+
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        }
+        if (tile0 == 0 && tile1 == tiles) {  // the worker saw the whole triple
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (out_row[i] < 0) continue;
+                const float inv = seen[i] > 0 ? 1.f / l[i] : 0.f;
+                const int64_t t = out_row[i] / a.h_q;
+                uint16_t *dst = a.o.p + t * a.o.ts + (out_row[i] - t * a.h_q) * a.o.hs;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    *reinterpret_cast<uint32_t *>(dst + n * 8 + cq * 2) =
+                        pack2<F16>(acc[n][2 * i] * inv, acc[n][2 * i + 1] * inv);
+                if (a.lse && cq == 0)
+                    a.lse[out_row[i]] = seen[i] > 0 ? kLn2 * (m[i] + log2f(l[i])) : -CUDART_INF_F;
+            }
+        } else {
+            const int64_t part = ((int64_t)me * 2 + (first_part ? 0 : 1)) * L.part_rows;
+            float2 *const ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + L.ml);
+            float *const po = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + L.o);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (out_row[i] < 0) continue;
+                const int64_t r = part + rw * 16 + r0 + 8 * i;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    *reinterpret_cast<float2 *>(po + r * D + n * 8 + cq * 2) =
+                        make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
+                if (cq == 0) ml[r] = make_float2(m[i], l[i]);
+            }
+        }
+        first_part = false;
+        at = seg0 + tile1;
+    }
+}
+
+// Joins the parts of every row that more than one worker saw, in the order of the
+// tokens, and writes the rows that see nothing.  WPR warps per row.
+template <int D, bool F16, int WPR>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, const int rw) {
+    constexpr int V = D / 32;  // values per lane
+    constexpr int RPB = 8 / WPR;
+    __shared__ float s_acc[WPR > 1 ? WPR : 1][WPR > 1 ? D : 1];
+    __shared__ float s_l[WPR];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % WPR;
+    const int64_t row = (int64_t)blockIdx.x * RPB + warp / WPR;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (row >= a.t_total * a.h_q) return;
+    const int64_t t = row / a.h_q;
+    const int hq = (int)(row - t * a.h_q);
+    const int s = (int)(t / a.n_tok), j = (int)(t - (int64_t)s * a.n_tok);
+    const int h = hq / a.group, g = hq - h * a.group;
+    const Layout L = layout(a.n_tok * a.group, rw, D, a.n_seqs);
+    const int r = j * a.group + g, rb = r / (16 * rw), lr = r - rb * 16 * rw;
+
+    uint16_t *const dst = a.o.p + t * a.o.ts + hq * a.o.hs;
+    const int64_t len = length_of(a, s);
+    if (len == 0) {
+        if (w == 0) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) reinterpret_cast<uint32_t *>(dst)[lane + 32 * i] = 0u;
+            if (a.lse && lane == 0) a.lse[row] = -CUDART_INF_F;
+        }
+        return;
+    }
+    const int64_t tiles = (len + kTile - 1) / kTile;
+    const int64_t *const line = reinterpret_cast<const int64_t *>(a.ws);
+    const int64_t total = line[a.n_seqs];
+    const int64_t first = line[s] + ((int64_t)h * L.blocks_of_rows + rb) * tiles;
+    // the worker of tile u is the last whose part starts at or before it
+    const int w0 = (int)(((first + 1) * L.workers - 1) / total);
+    const int w1 = (int)(((first + tiles) * L.workers - 1) / total);
+    if (w0 == w1) return;
+
+    const float2 *const ml = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.ml);
+    const float *const po = reinterpret_cast<const float *>(static_cast<const uint8_t *>(a.ws) + L.o);
+    // a worker's part is its first where its own start is not before the triple's
+    auto part_row = [&](int wk) {
+        const int64_t slot = part_start(total, L.workers, wk) >= first ? 0 : 1;
+        return ((int64_t)wk * 2 + slot) * L.part_rows + lr;
+    };
+    auto used = [&](int wk) {  // with fewer tiles than workers some have none
+        return part_start(total, L.workers, wk) < part_start(total, L.workers, wk + 1);
+    };
+    float top = -CUDART_INF_F;
+    for (int i = w0 + lane; i <= w1; i += 32)
+        if (used(i)) top = fmaxf(top, ml[part_row(i)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    float acc[V], l = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int i = w0 + w; i <= w1; i += WPR) {
+        if (!used(i)) continue;
+        const int64_t pr = part_row(i);
+        const float2 v = ml[pr];
+        const float c = tc::fast_exp2(v.x - ref);
+        l += c * v.y;
+        const float2 *const p = reinterpret_cast<const float2 *>(po + pr * D);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            const float2 x = p[lane + 32 * e];
+            acc[2 * e] += c * x.x;
+            acc[2 * e + 1] += c * x.y;
+        }
+    }
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            s_acc[w][2 * (lane + 32 * e)] = acc[2 * e];
+            s_acc[w][2 * (lane + 32 * e) + 1] = acc[2 * e + 1];
+        }
+        if (lane == 0) s_l[w] = l;
+        __syncthreads();  // the block is one row: its warps come here together
+        if (w != 0) return;
+#pragma unroll
+        for (int i = 1; i < WPR; ++i) {
+            l += s_l[i];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                acc[2 * e] += s_acc[i][2 * (lane + 32 * e)];
+                acc[2 * e + 1] += s_acc[i][2 * (lane + 32 * e) + 1];
+            }
+        }
+    }
+    const bool sees = len - a.n_tok + j + 1 > 0;
+    const float inv = sees ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e)
+        reinterpret_cast<uint32_t *>(dst)[lane + 32 * e] = pack2<F16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[row] = sees ? kLn2 * (top + log2f(l)) : -CUDART_INF_F;
+}
+
+template <int D, bool F16, int RW>
+cudaError_t launch(const Args &a, cudaStream_t s) {
+    using Sh = Shape<D, RW>;
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, F16, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Sh::SMEM);
+    if (e != cudaSuccess) return e;
+    decode_kernel<D, F16, RW><<<kBlocks, kThreads, Sh::SMEM, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // The join: a block of 8 warps per row while that is at most about two waves, so
+    // that a row of many parts is read by all of them; a warp per row beyond that.
+    const int64_t rows = a.t_total * a.h_q;
+    const bool wide = rows <= 2048;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 8>, a, RW)
+                : cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 1>, a, RW);
+}
+
+template <int D, bool F16>
+cudaError_t launch_rw(const Args &a, cudaStream_t s) {
+    switch (row_warps(a.n_tok * a.group)) {
+        case 1: return launch<D, F16, 1>(a, s);
+        case 2: return launch<D, F16, 2>(a, s);
+        case 4: return launch<D, F16, 4>(a, s);
+        default: return launch<D, F16, 8>(a, s);
+    }
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes(int, int, int, int, int) { return 0; }
+size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok) {
+    const int rows = n_tok * (h_q / h_kv);
+    return layout(rows, row_warps(rows), d, n_seqs).total;
+}
 
 cudaError_t launch_decode(const Args &a, cudaStream_t s) {
-    if (a.d == 64)
-        launch<64>(a, s);
-    else if (a.d == 128)
-        launch<128>(a, s);
-    else
-        launch<256>(a, s);
-    return cudaGetLastError();
+    if (a.d == 64) return a.f16 ? launch_rw<64, true>(a, s) : launch_rw<64, false>(a, s);
+    if (a.d == 128) return a.f16 ? launch_rw<128, true>(a, s) : launch_rw<128, false>(a, s);
+    return a.f16 ? launch_rw<256, true>(a, s) : launch_rw<256, false>(a, s);
 }
 
 }  // namespace attn
