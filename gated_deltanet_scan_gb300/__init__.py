@@ -431,87 +431,88 @@ def gdr_selftest_wait_timeout(limit_cycles: int, *, stream=None, device=None) ->
 
 
 # --- softmax attention beside the rule ------------------------------------------
+# A decode step's kernels take a few microseconds, so its call must not cost the
+# host more: every attribute of a tensor is read once.
 
-def _attn_dims(q_heads: int, k, scale) -> gdr_attn_dims:
-    """dims from the query head count and a [.., H_kv, d] tensor (k rows or a cache)."""
+_attn_types = None  # dtype -> code, int32, fp32, and the raw current stream of a device index
+
+
+def _attn_init():
+    global _attn_types
     torch = _torch()
-    h_kv, d = k.shape[-2], k.shape[-1]
-    if k.dtype == torch.bfloat16:
-        code = GDR_BF16
-    elif k.dtype == torch.float16:
-        code = GDR_F16
-    elif k.dtype == torch.float32:
-        code = GDR_F32
-    else:
-        raise TypeError(f"unsupported dtype {k.dtype}")
-    return gdr_attn_dims(q_heads, h_kv, d, code, d ** -0.5 if scale is None else scale)
+    _attn_types = ({torch.bfloat16: GDR_BF16, torch.float16: GDR_F16, torch.float32: GDR_F32}, torch.int32,
+                   torch.float32, getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    return _attn_types
 
 
-def _rows(t, like, heads: int, tokens: int, name: str) -> gdr_rows:
-    """Strided rows of t, checked to be [tokens, heads, d] of like's dtype, device and head size."""
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must have dtype {like.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    d = like.shape[-1]
-    if t.dim() != 3 or t.shape != (tokens, heads, d):
-        raise ValueError(f"{name} must have shape {(tokens, heads, d)}, not {tuple(t.shape)}")
+def _attn_dims(h_q: int, h_kv: int, d: int, dtype, scale) -> gdr_attn_dims:
+    code = (_attn_types or _attn_init())[0].get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return gdr_attn_dims(h_q, h_kv, d, code, d ** -0.5 if scale is None else scale)
+
+
+def _attn_stream(stream, dev: int):
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        raw = _attn_types[3]
+        return raw(dev) if raw is not None else _torch().cuda.current_stream(dev).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _rows(t, shape, dtype, dev: int, name: str) -> gdr_rows:
+    """Strided rows of t, checked to be of this shape [tokens, heads, d], dtype and device."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
     ts, hs, es = t.stride()
     if es != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # the stride of a dimension of one entry is never used, and may be anything
-    return gdr_rows(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0)
+    return gdr_rows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
 
 
-def _ints(t, n: int, like, name: str) -> int:
-    torch = _torch()
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {(n,)}")
-    return t.data_ptr()
-
-
-def _cache(k_cache, v_cache, page_table, n_seqs: int) -> gdr_kv_cache:
-    torch = _torch()
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape [n_pages, page_size, H_kv, d]")
-    if k_cache.dtype != v_cache.dtype or k_cache.device != v_cache.device:
-        raise TypeError("k_cache and v_cache must have one dtype and device")
-    n_pages, page, heads, _ = k_cache.shape
-    strides = k_cache.stride()
-    if strides != v_cache.stride():
-        raise ValueError("k_cache and v_cache must have the same strides")
-    if strides[3] != 1:
-        raise ValueError("the caches' last dimension must be contiguous")
-    if page_table.dtype != torch.int32:
-        raise TypeError("page_table must be int32")
-    if page_table.device != k_cache.device:
-        raise ValueError(f"page_table is on {page_table.device}, not {k_cache.device}")
-    if page_table.dim() != 2 or page_table.shape[0] != n_seqs:
-        raise ValueError(f"page_table must have shape ({n_seqs}, max_pages)")
-    width = page_table.shape[1]
-    rs, cs = page_table.stride()
-    if cs != 1 and width > 1:
-        raise ValueError("page_table's rows must be contiguous")
-    return gdr_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), strides[0] if n_pages > 1 else 0,
-                        strides[1] if page > 1 else 0, strides[2] if heads > 1 else 0, page_table.data_ptr(),
-                        rs if n_seqs > 1 else 0, n_pages, page, width)
-
-
-def _f32(t, shape, like, name: str) -> Optional[int]:
-    torch = _torch()
-    if t is None:
-        return None
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be fp32")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+def _plain(t, shape, dtype, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of this shape, dtype and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {shape}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
     return t.data_ptr()
+
+
+def _cache(k_cache, v_cache, page_table, n_seqs: int, heads: int, d: int, dtype, dev: int) -> gdr_kv_cache:
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[2] != heads or shape[3] != d:
+        raise ValueError(f"the caches must have shape (n_pages, page_size, {heads}, {d}), not {tuple(shape)}")
+    if v_cache.shape != shape or v_cache.stride() != strides:
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError(f"the caches must have dtype {dtype}")
+    if strides[3] != 1:
+        raise ValueError("the caches' last dimension must be contiguous")
+    if page_table.dtype != _attn_types[1]:
+        raise TypeError("page_table must be int32")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must have shape ({n_seqs}, max_pages)")
+    n, width = page_table.shape
+    rs, cs = page_table.stride()
+    if n != n_seqs:
+        raise ValueError(f"page_table must have shape ({n_seqs}, max_pages)")
+    if cs != 1 and width > 1:
+        raise ValueError("page_table's rows must be contiguous")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev or page_table.get_device() != dev:
+        raise ValueError(f"the caches and page_table must be on device {dev}")
+    n_pages, page = shape[0], shape[1]
+    return gdr_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), strides[0] if n_pages > 1 else 0,
+                        strides[1] if page > 1 else 0, strides[2] if heads > 1 else 0, page_table.data_ptr(),
+                        rs if n > 1 else 0, n_pages, page, width)
 
 
 def gdr_attn_append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens, inv_freq, cu_seqlens=None, *,
@@ -525,52 +526,59 @@ def gdr_attn_append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens
     kv_lens int32 [n], each sequence's tokens including the new ones; inv_freq fp32
     [rot_dim / 2] (None: no rotation); cu_seqlens int32 [n + 1], or None when every
     sequence has T / n new tokens."""
-    n = kv_lens.shape[0]
-    T = k.shape[0]
-    if k.dim() != 3:
+    kv = k.shape
+    if len(kv) != 3:
         raise ValueError("k must be [T, H_kv, d]")
-    h_q = k.shape[1] if q is None else q.shape[1]
-    dims = _attn_dims(h_q, k, 1.0)
-    if k_cache.dtype != k.dtype or k_cache.device != k.device:
-        raise TypeError("the caches must have k's dtype and device")
-    if k_cache.shape[2:] != k.shape[1:]:
-        raise ValueError("the caches must have k's heads and head size")
-    h_kv = k.shape[1]
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out come together")
+    T, h_kv, d = kv
+    n, dtype, dev = kv_lens.shape[0], k.dtype, k.get_device()
     qr = qo = ko = None
-    if q is not None:
-        qr, qo = _rows(q, k, h_q, T, "q"), _rows(q_out, k, h_q, T, "q_out")
+    h_q = h_kv
+    if q is not None and q_out is not None:
+        h_q = q.shape[1]
+        qs = (T, h_q, d)
+        dims = _attn_dims(h_q, h_kv, d, dtype, 1.0)
+        qr, qo = _rows(q, qs, dtype, dev, "q"), _rows(q_out, qs, dtype, dev, "q_out")
+    elif q is q_out:
+        dims = _attn_dims(h_kv, h_kv, d, dtype, 1.0)
+    else:
+        raise ValueError("q and q_out come together")
+    kr, vr = _rows(k, kv, dtype, dev, "k"), _rows(v, kv, dtype, dev, "v")
     if k_out is not None:
-        ko = _rows(k_out, k, h_kv, T, "k_out")
-    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    st = lib().gdr_attn_append(
-        dims, n, None if cu_seqlens is None else _ints(cu_seqlens, n + 1, k, "cu_seqlens"), T, qr,
-        _rows(k, k, h_kv, T, "k"), _rows(v, k, h_kv, T, "v"), qo, ko, _cache(k_cache, v_cache, page_table, n),
-        _ints(kv_lens, n, k, "kv_lens"), _f32(inv_freq, (rot // 2,), k, "inv_freq") if rot else None, rot,
-        1 if interleaved else 0, _stream_handle(stream, k.device))
-    _check(st, "gdr_attn_append")
+        ko = _rows(k_out, kv, dtype, dev, "k_out")
+    i32, f32 = _attn_types[1], _attn_types[2]
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    st = (_lib or lib()).gdr_attn_append(
+        dims, n, None if cu_seqlens is None else _plain(cu_seqlens, (n + 1,), i32, dev, "cu_seqlens"), T, qr, kr, vr,
+        qo, ko, _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
+        _plain(kv_lens, (n,), i32, dev, "kv_lens"), _plain(inv_freq, (half,), f32, dev, "inv_freq") if half else None,
+        2 * half, 1 if interleaved else 0, _attn_stream(stream, dev))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_attn_append")
 
 
 def gdr_attn_prefill(q, k, v, o, cu_seqlens, *, scale: Optional[float] = None, lse=None, stream=None) -> None:
     """Causal attention over whole packed prompts (see gdr_attn_prefill in
     include/gdr.h): q, o [T, H_q, d]; k, v [T, H_kv, d], strided rows; cu_seqlens int32
     [n + 1] on the device; scale defaults to 1 / sqrt(d); lse fp32 [T, H_q] or None."""
-    if q.dim() != 3 or k.dim() != 3:
+    qs, kv = q.shape, k.shape
+    if len(qs) != 3 or len(kv) != 3 or qs[0] != kv[0] or qs[2] != kv[2]:
         raise ValueError("q must be [T, H_q, d] and k [T, H_kv, d]")
-    T, h_q, _ = q.shape
-    h_kv = k.shape[1]
+    T, h_q, d = qs
+    dtype, dev = q.dtype, q.get_device()
+    dims = _attn_dims(h_q, kv[1], d, dtype, scale)
     n = cu_seqlens.shape[0] - 1
-    st = lib().gdr_attn_prefill(
-        _attn_dims(h_q, k, scale), n, _ints(cu_seqlens, n + 1, q, "cu_seqlens"), T, _rows(q, k, h_q, T, "q"),
-        _rows(k, k, h_kv, T, "k"), _rows(v, k, h_kv, T, "v"), _rows(o, k, h_q, T, "o"),
-        _f32(lse, (T, h_q), k, "lse"), _stream_handle(stream, q.device))
-    _check(st, "gdr_attn_prefill")
+    st = (_lib or lib()).gdr_attn_prefill(
+        dims, n, _plain(cu_seqlens, (n + 1,), _attn_types[1], dev, "cu_seqlens"), T, _rows(q, qs, dtype, dev, "q"),
+        _rows(k, kv, dtype, dev, "k"), _rows(v, kv, dtype, dev, "v"), _rows(o, qs, dtype, dev, "o"),
+        None if lse is None else _plain(lse, (T, h_q), _attn_types[2], dev, "lse"), _attn_stream(stream, dev))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_attn_prefill")
 
 
 def gdr_attn_decode_workspace_bytes(q, k_cache, n_seqs: int, n_tok: int = 1) -> int:
     """Device scratch bytes gdr_attn_decode needs."""
-    return int(lib().gdr_attn_decode_workspace_bytes(_attn_dims(q.shape[1], k_cache, None), int(n_seqs), int(n_tok)))
+    dims = _attn_dims(q.shape[1], k_cache.shape[2], k_cache.shape[3], q.dtype, None)
+    return int(lib().gdr_attn_decode_workspace_bytes(dims, int(n_seqs), int(n_tok)))
 
 
 def gdr_attn_decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok: int = 1, *, scale: Optional[float] = None,
@@ -580,14 +588,18 @@ def gdr_attn_decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok: int = 1,
     and kv_lens as for gdr_attn_append; lse fp32 [n * n_tok, H_q] or None.  Without
     ``workspace`` (a device tensor of gdr_attn_decode_workspace_bytes bytes) one is taken
     from torch's allocator on the call's stream."""
-    torch = _torch()
-    if q.dim() != 3:
-        raise ValueError("q must be [n * n_tok, H_q, d]")
-    n, h_q = kv_lens.shape[0], q.shape[1]
-    rows = n * n_tok
-    dims = _attn_dims(h_q, k_cache, scale)
-    L = lib()
+    qs = q.shape
+    if len(qs) != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [n * n_tok, H_q, d] and the caches [n_pages, page_size, H_kv, d]")
+    n, h_q, d = kv_lens.shape[0], qs[1], qs[2]
+    if qs[0] != n * n_tok:
+        raise ValueError(f"q must have n * n_tok = {n * n_tok} rows, not {qs[0]}")
+    h_kv = k_cache.shape[2]
+    dtype, dev = q.dtype, q.get_device()
+    dims = _attn_dims(h_q, h_kv, d, dtype, scale)
+    L = _lib or lib()
     if workspace is None:
+        torch = _torch()
         need = int(L.gdr_attn_decode_workspace_bytes(dims, n, n_tok))
         if need > 0:
             s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -595,9 +607,13 @@ def gdr_attn_decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok: int = 1,
                 s = torch.cuda.ExternalStream(s, device=q.device)
             with torch.cuda.stream(s):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace is not on device {dev}")
     st = L.gdr_attn_decode(
-        dims, n, n_tok, _rows(q, k_cache, h_q, rows, "q"), _cache(k_cache, v_cache, page_table, n),
-        _ints(kv_lens, n, q, "kv_lens"), _rows(o, k_cache, h_q, rows, "o"), _f32(lse, (rows, h_q), q, "lse"),
-        _ptr(workspace), ws_bytes, _stream_handle(stream, q.device))
-    _check(st, "gdr_attn_decode")
+        dims, n, n_tok, _rows(q, qs, dtype, dev, "q"),
+        _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
+        _plain(kv_lens, (n,), _attn_types[1], dev, "kv_lens"), _rows(o, qs, dtype, dev, "o"),
+        None if lse is None else _plain(lse, (qs[0], h_q), _attn_types[2], dev, "lse"), _ptr(workspace),
+        0 if workspace is None else workspace.nbytes, _attn_stream(stream, dev))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_attn_decode")

@@ -4,10 +4,28 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gdr.h"
 
 namespace gdr {
 namespace attn {
+
+// A kernel's opt-in to more than 48 KiB of dynamic shared memory, set once per
+// device (one bit each; setting it twice from two threads is harmless).
+struct SmemOptIn {
+    std::atomic<uint64_t> done{0};
+    cudaError_t set(const void *kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 // Strided rows of heads: value x of head h of token t at p[t * ts + h * hs + x].
 struct Rows {

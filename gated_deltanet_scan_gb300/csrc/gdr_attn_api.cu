@@ -150,6 +150,7 @@ gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_
     if (st != GDR_OK) return st;
     if (n_seqs == 0) return GDR_OK;
     if (!rows_ok(q) || !rows_ok(o) || !aligned(kv_lens, 4) || (lse && !aligned(lse, 4))) return GDR_ERR_INVALID_ARG;
+    if ((int64_t)n_seqs * n_tok > INT_MAX / dims->h_q) return GDR_ERR_UNSUPPORTED;
     const size_t need = decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);
     if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return GDR_ERR_INVALID_ARG;
     Args a = make_args(dims);

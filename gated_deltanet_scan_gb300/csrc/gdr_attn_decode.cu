@@ -34,6 +34,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlocks = 152;  // one resident block per SM
 constexpr int kTile = 16;     // tokens per tile: the MMA's inner size in P V
+// P may exceed 1 by up to 2^kSlack before sums are rescaled: rounding is relative, so
+// P keeps its accuracy in either type, and most tiles rescale nothing.
+constexpr float kSlack = 6.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, int RW>
@@ -49,9 +52,15 @@ struct Shape {
 // Row warps for this many rows of a key/value head.
 int row_warps(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
 
-// Workspace: first tile of every sequence on the line ([n_seqs + 1], the last one the
-// total), then per worker two parts (its first and its last, cut, triple): per row
-// m and l, then O.
+// On the line a triple takes its tiles and, before them, kLead<D> places for what
+// starting and ending it costs a worker (about 3 us, against 16 d 4 bytes a tile at a
+// worker's share of the bandwidth): a batch of many short sequences is cut evenly too.
+template <int D>
+constexpr int kLead = 512 / D;
+
+// Workspace: place of every sequence's first triple on the line ([n_seqs + 1], the last
+// one the total), then per worker two parts (its first and its last, cut, triple): per
+// row m and l, then O.
 struct Layout {
     int rows, rw, blocks_of_rows, part_rows, workers;
     size_t ml, o, total;
@@ -117,8 +126,25 @@ __device__ __forceinline__ int64_t length_of(const Args &a, int s) {
     const int64_t n = a.kv_lens[s];
     return n < 0 || n > (int64_t)a.cache.max_pages * a.cache.page_size ? 0 : n;
 }
-// First tile of worker w's part of the line.
-__device__ __forceinline__ int64_t part_start(int64_t total, int workers, int w) { return total * w / workers; }
+// The line of `total` places in equal parts, the first `rest` one longer; never more
+// parts than places.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // a, b >= 0; mostly 32-bit values
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+struct Cut {
+    int64_t total, each, rest;
+    int parts;
+    __device__ __forceinline__ Cut(int64_t total_, int workers) : total(total_) {
+        parts = total < workers ? (int)total : workers;
+        each = parts > 0 ? quotient(total, parts) : 0;
+        rest = total - each * parts;
+    }
+    __device__ __forceinline__ int64_t start(int w) const { return each * w + (w < rest ? w : rest); }
+    __device__ __forceinline__ int part_of(int64_t place) const {
+        const int64_t longer = rest * (each + 1);
+        return (int)(place < longer ? quotient(place, each + 1) : rest + quotient(place - longer, each));
+    }
+};
 
 template <int D, bool F16, int RW>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Args a) {
@@ -158,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 if (s < a.n_seqs) {
                     n = length_of(a, s);
                     if (pass == 0 && blockIdx.x == 0 && n != a.kv_lens[s]) record_invalid(a.err);
-                    n = (n + kTile - 1) / kTile * per_seq;
+                    if (n > 0) n = ((n + kTile - 1) / kTile + kLead<D>) * per_seq;
                 }
                 int64_t x = n;
 #pragma unroll
@@ -181,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             if (pass == 1) {
                 const int s0 = c * kThreads, m = min(kThreads, a.n_seqs - s0);
                 if (tid < Sh::WORKERS) {  // the last sequence that starts at or before the worker's part
-                    const int64_t at = part_start(total, L.workers, tid * kBlocks + blockIdx.x);
+                    const Cut cut(total, L.workers);
+                    const int64_t at = cut.start(min(tid * kBlocks + (int)blockIdx.x, cut.parts));
                     if (s_seq[tid] < 0 && at < base) {
                         int lo = 0, hi = m - 1;
                         while (lo < hi) {
@@ -205,9 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
     __syncthreads();
 
-    int64_t at = part_start(total, L.workers, me);
-    const int64_t end = part_start(total, L.workers, me + 1);
-    if (at >= end) return;  // a whole worker; workers meet at no barrier from here on
+    const Cut cut(total, L.workers);
+    if (me >= cut.parts) return;  // a whole worker; workers meet at no barrier from here on
+    int64_t at = cut.start(me);
+    const int64_t end = cut.start(me + 1);
     int s = s_seq[wk];
     int64_t base = s_base[wk];
 
@@ -220,23 +248,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     };
     const float sc = a.scale * kLog2e;
     const int r0 = lane >> 2, cq = lane & 3;  // the MMA's row (and row + 8) and column pair of this lane
-    bool first_part = true;
 
     while (at < end) {
         // the triple at `at`: sequence s (of `tiles` tiles), key/value head h, row block rb
-        int64_t len = length_of(a, s);
-        int64_t tiles = (len + kTile - 1) / kTile;
-        while (at >= base + tiles * per_seq) {
-            base += tiles * per_seq;
-            ++s;
+        int64_t len, tiles, places;
+        for (;;) {
             len = length_of(a, s);
             tiles = (len + kTile - 1) / kTile;
+            places = len > 0 ? tiles + kLead<D> : 0;
+            if (at < base + places * per_seq) break;
+            base += places * per_seq;
+            ++s;
         }
-        const int64_t hr = (at - base) / tiles;
-        const int h = (int)(hr / L.blocks_of_rows), rb = (int)(hr - (int64_t)h * L.blocks_of_rows);
-        const int64_t seg0 = base + hr * tiles;  // where the triple starts on the line
-        const int tile0 = (int)(at - seg0);
-        const int tile1 = (int)min(tiles, end - seg0);
+        const int hr = (int)quotient(at - base, places);
+        const int h = hr / L.blocks_of_rows, rb = hr - h * L.blocks_of_rows;
+        const int64_t seg0 = base + hr * places;  // where the triple starts on the line
+        const int tile0 = (int)max((int64_t)0, at - seg0 - kLead<D>);
+        const int tile1 = (int)min(tiles, end - seg0 - kLead<D>);
+        at = seg0 + places;
+        if (tile1 <= tile0) continue;  // only lead places: the next worker has the tiles
+        const int slot_of_part = cut.start(me) >= seg0 ? 0 : 1;
         const int steps = 2 * (tile1 - tile0);  // keys and values of a tile are a step each
         const int32_t *const pages = a.cache.table + (int64_t)s * a.cache.table_stride;
         const int64_t head = h * a.cache.head_stride;
@@ -353,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float mn = fmaxf(m[i], top);
+                // the reference m follows the maximum only when that is kSlack above it
+                const float mn = top > m[i] + kSlack || m[i] == -CUDART_INF_F ? fmaxf(m[i], top) : m[i];
                 const float ref = mn == -CUDART_INF_F ? 0.f : mn;  // nothing visible yet: p = 2^-inf
                 c[i] = m[i] == mn ? 1.f : tc::fast_exp2(m[i] - ref);
                 m[i] = mn;
@@ -383,18 +415,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 // Rows that do not see a draft token have p = 0 for it, and 0 times an
                 // infinity or NaN would reach them: such values are added to the rows
                 // that see them (p > 0 leaves them as they are) and replaced by zeros.
-#pragma unroll 1
-                for (int t = 0; t < kTile; ++t) {
-                    const int64_t p = p0 + t;
-                    if (p >= len) break;
+                bool found = false;
+                for (int i = lane; i < kTile * D / 8; i += 32) {
+                    uint32_t w[4];
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(vb + 16 * i)
+                                 : "memory");
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        uint32_t w;
-                        asm volatile("ld.shared.b32 %0, [%1];"
-                                     : "=r"(w)
-                                     : "r"(vb + t * (D * 2) + ((n ^ (t & 7)) << 4) + cq * 4)
-                                     : "memory");
-                        if (nonfinite<F16>(w) || nonfinite<F16>(w >> 16)) {
+                    for (int e = 0; e < 4; ++e) found = found || nonfinite<F16>(w[e]) || nonfinite<F16>(w[e] >> 16);
+                }
+                // every warp of the worker looked at the whole tile, so they agree
+                if (__any_sync(0xffffffffu, found)) {
+#pragma unroll 1
+                    for (int t = 0; t < kTile; ++t) {
+                        const int64_t p = p0 + t;
+                        if (p >= len) break;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t w;
+                            asm volatile("ld.shared.b32 %0, [%1];"
+                                         : "=r"(w)
+                                         : "r"(vb + t * (D * 2) + ((n ^ (t & 7)) << 4) + cq * 4)
+                                         : "memory");
+                            if (!nonfinite<F16>(w) && !nonfinite<F16>(w >> 16)) continue;
                             const float2 v = unpack2<F16>(w);
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
@@ -404,16 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                             }
                         }
                     }
+                    worker_sync();
+                    for (int i = rw * 32 + lane; i < kTile * D / 2; i += 32 * RW) {
+                        uint32_t w;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vb + 4 * i) : "memory");
+                        uint32_t z = nonfinite<F16>(w) ? w & 0xFFFF0000u : w;
+                        z = nonfinite<F16>(w >> 16) ? z & 0xFFFFu : z;
+                        if (z != w) asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + 4 * i), "r"(z) : "memory");
+                    }
+                    worker_sync();
                 }
-                worker_sync();
-                for (int i = rw * 32 + lane; i < kTile * D / 2; i += 32 * RW) {
-                    uint32_t w;
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vb + 4 * i) : "memory");
-                    uint32_t z = nonfinite<F16>(w) ? w & 0xFFFF0000u : w;
-                    z = nonfinite<F16>(w >> 16) ? z & 0xFFFFu : z;
-                    if (z != w) asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + 4 * i), "r"(z) : "memory");
-                }
-                worker_sync();
             }
             {
                 const int row = lane & 15;
@@ -440,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             for (int i = 0; i < 2; ++i) {
                 if (out_row[i] < 0) continue;
                 const float inv = seen[i] > 0 ? 1.f / l[i] : 0.f;
-                const int64_t t = out_row[i] / a.h_q;
+                const int64_t t = quotient(out_row[i], a.h_q);
                 uint16_t *dst = a.o.p + t * a.o.ts + (out_row[i] - t * a.h_q) * a.o.hs;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -450,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     a.lse[out_row[i]] = seen[i] > 0 ? kLn2 * (m[i] + log2f(l[i])) : -CUDART_INF_F;
             }
         } else {
-            const int64_t part = ((int64_t)me * 2 + (first_part ? 0 : 1)) * L.part_rows;
+            const int64_t part = ((int64_t)me * 2 + slot_of_part) * L.part_rows;
             float2 *const ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + L.ml);
             float *const po = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + L.o);
 #pragma unroll
@@ -464,128 +508,135 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 if (cq == 0) ml[r] = make_float2(m[i], l[i]);
             }
         }
-        first_part = false;
-        at = seg0 + tile1;
     }
 }
 
 // Joins the parts of every row that more than one worker saw, in the order of the
-// tokens, and writes the rows that see nothing.  WPR warps per row.
+// tokens, and writes the rows that see nothing.  With WPR > 1 a block is WPR warps on 64
+// columns of one row, which share the row's parts; else a warp is one row.
 template <int D, bool F16, int WPR>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, const int rw) {
-    constexpr int V = D / 32;  // values per lane
-    constexpr int RPB = 8 / WPR;
-    __shared__ float s_acc[WPR > 1 ? WPR : 1][WPR > 1 ? D : 1];
-    __shared__ float s_l[WPR];
+    constexpr int V = WPR > 1 ? 2 : D / 32;  // columns per lane
+    constexpr int RPB = 8 / WPR;             // rows per block
+    __shared__ float2 s_acc[WPR > 1 ? WPR : 1][32];
+    __shared__ float2 s_ml[WPR];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % WPR;
-    const int64_t row = (int64_t)blockIdx.x * RPB + warp / WPR;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t row = blockIdx.x * RPB + warp / WPR;
+    const int word0 = WPR > 1 ? blockIdx.y * 32 + lane : lane;  // this lane's first pair of columns
     if (row >= a.t_total * a.h_q) return;
-    const int64_t t = row / a.h_q;
+    const uint32_t t = row / (uint32_t)a.h_q;
     const int hq = (int)(row - t * a.h_q);
-    const int s = (int)(t / a.n_tok), j = (int)(t - (int64_t)s * a.n_tok);
+    const int s = (int)(t / (uint32_t)a.n_tok), j = (int)(t - (uint32_t)s * a.n_tok);
     const int h = hq / a.group, g = hq - h * a.group;
     const Layout L = layout(a.n_tok * a.group, rw, D, a.n_seqs);
     const int r = j * a.group + g, rb = r / (16 * rw), lr = r - rb * 16 * rw;
-
-    uint16_t *const dst = a.o.p + t * a.o.ts + hq * a.o.hs;
+    uint32_t *const dst = reinterpret_cast<uint32_t *>(a.o.p + t * a.o.ts + hq * a.o.hs);
+    const bool write_lse = a.lse && lane == 0 && blockIdx.y == 0;
     const int64_t len = length_of(a, s);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (len == 0) {
         if (w == 0) {
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) reinterpret_cast<uint32_t *>(dst)[lane + 32 * i] = 0u;
-            if (a.lse && lane == 0) a.lse[row] = -CUDART_INF_F;
+            for (int e = 0; e < V / 2; ++e) dst[word0 + 32 * e] = 0u;
+            if (write_lse) a.lse[row] = -CUDART_INF_F;
         }
         return;
     }
     const int64_t tiles = (len + kTile - 1) / kTile;
     const int64_t *const line = reinterpret_cast<const int64_t *>(a.ws);
-    const int64_t total = line[a.n_seqs];
-    const int64_t first = line[s] + ((int64_t)h * L.blocks_of_rows + rb) * tiles;
-    // the worker of tile u is the last whose part starts at or before it
-    const int w0 = (int)(((first + 1) * L.workers - 1) / total);
-    const int w1 = (int)(((first + tiles) * L.workers - 1) / total);
+    const int64_t seg0 = line[s] + ((int64_t)h * L.blocks_of_rows + rb) * (tiles + kLead<D>);
+    const Cut cut(line[a.n_seqs], L.workers);
+    const int w0 = cut.part_of(seg0 + kLead<D>), w1 = cut.part_of(seg0 + kLead<D> + tiles - 1);
     if (w0 == w1) return;
 
     const float2 *const ml = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.ml);
-    const float *const po = reinterpret_cast<const float *>(static_cast<const uint8_t *>(a.ws) + L.o);
-    // a worker's part is its first where its own start is not before the triple's
-    auto part_row = [&](int wk) {
-        const int64_t slot = part_start(total, L.workers, wk) >= first ? 0 : 1;
-        return ((int64_t)wk * 2 + slot) * L.part_rows + lr;
-    };
-    auto used = [&](int wk) {  // with fewer tiles than workers some have none
-        return part_start(total, L.workers, wk) < part_start(total, L.workers, wk + 1);
-    };
-    float top = -CUDART_INF_F;
-    for (int i = w0 + lane; i <= w1; i += 32)
-        if (used(i)) top = fmaxf(top, ml[part_row(i)].x);
+    const float2 *const po = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.o);
+    // a worker's part is its first where its own start is not before the triple's: so
+    // all parts but perhaps the first one's
+    auto part_row = [&](int wk) { return ((int64_t)wk * 2 + (wk > w0 || cut.start(wk) >= seg0 ? 0 : 1)) * L.part_rows + lr; };
+    float2 acc[V / 2];
+    float m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float ref = top == -CUDART_INF_F ? 0.f : top;
-    float acc[V], l = 0.f;
+    for (int e = 0; e < V / 2; ++e) acc[e] = make_float2(0.f, 0.f);
+    constexpr int U = WPR > 1 ? 8 : 4;  // parts in flight
+#pragma unroll 1
+    for (int i = w0 + w; i <= w1; i += WPR * U) {
+        float2 x[U][V / 2], v[U];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int i = w0 + w; i <= w1; i += WPR) {
-        if (!used(i)) continue;
-        const int64_t pr = part_row(i);
-        const float2 v = ml[pr];
-        const float c = tc::fast_exp2(v.x - ref);
-        l += c * v.y;
-        const float2 *const p = reinterpret_cast<const float2 *>(po + pr * D);
+        for (int u = 0; u < U; ++u) {
+            const int64_t pr = part_row(min(i + u * WPR, w1));
+            v[u] = ml[pr];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) x[u][e] = po[pr * (D / 2) + word0 + 32 * e];
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, i + u * WPR <= w1 ? v[u].x : top);
+        const float ref = top == -CUDART_INF_F ? 0.f : top;
+        const float c0 = m == top ? 1.f : tc::fast_exp2(m - ref);
+        m = top;
+        l *= c0;
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
-            const float2 x = p[lane + 32 * e];
-            acc[2 * e] += c * x.x;
-            acc[2 * e + 1] += c * x.y;
+            acc[e].x *= c0;
+            acc[e].y *= c0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u * WPR > w1) break;
+            const float c = tc::fast_exp2(v[u].x - ref);
+            l += c * v[u].y;
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                acc[e].x += c * x[u][e].x;
+                acc[e].y += c * x[u][e].y;
+            }
         }
     }
     if constexpr (WPR > 1) {
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-            s_acc[w][2 * (lane + 32 * e)] = acc[2 * e];
-            s_acc[w][2 * (lane + 32 * e) + 1] = acc[2 * e + 1];
-        }
-        if (lane == 0) s_l[w] = l;
+        s_acc[w][lane] = acc[0];
+        if (lane == 0) s_ml[w] = make_float2(m, l);
         __syncthreads();  // the block is one row: its warps come here together
         if (w != 0) return;
 #pragma unroll
-        for (int i = 1; i < WPR; ++i) {
-            l += s_l[i];
+        for (int i = 1; i < WPR; ++i) m = fmaxf(m, s_ml[i].x);
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        l = 0.f;
+        acc[0] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-                acc[2 * e] += s_acc[i][2 * (lane + 32 * e)];
-                acc[2 * e + 1] += s_acc[i][2 * (lane + 32 * e) + 1];
-            }
+        for (int i = 0; i < WPR; ++i) {
+            const float c = tc::fast_exp2(s_ml[i].x - ref);
+            l += c * s_ml[i].y;
+            acc[0].x += c * s_acc[i][lane].x;
+            acc[0].y += c * s_acc[i][lane].y;
         }
     }
     const bool sees = len - a.n_tok + j + 1 > 0;
     const float inv = sees ? 1.f / l : 0.f;
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e)
-        reinterpret_cast<uint32_t *>(dst)[lane + 32 * e] = pack2<F16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    if (a.lse && lane == 0) a.lse[row] = sees ? kLn2 * (top + log2f(l)) : -CUDART_INF_F;
+    for (int e = 0; e < V / 2; ++e) dst[word0 + 32 * e] = pack2<F16>(acc[e].x * inv, acc[e].y * inv);
+    if (write_lse) a.lse[row] = sees ? kLn2 * (m + log2f(l)) : -CUDART_INF_F;
 }
 
 template <int D, bool F16, int RW>
 cudaError_t launch(const Args &a, cudaStream_t s) {
     using Sh = Shape<D, RW>;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, F16, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Sh::SMEM);
+    static SmemOptIn opt_in;
+    cudaError_t e = opt_in.set(reinterpret_cast<const void *>(decode_kernel<D, F16, RW>), (int)Sh::SMEM);
     if (e != cudaSuccess) return e;
     decode_kernel<D, F16, RW><<<kBlocks, kThreads, Sh::SMEM, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // The join: a block of 8 warps per row while that is at most about two waves, so
-    // that a row of many parts is read by all of them; a warp per row beyond that.
+    // The join: 8 warps on every 64 columns of a row where a row has many parts (few
+    // triples for the workers), else a warp per row.
     const int64_t rows = a.t_total * a.h_q;
-    const bool wide = rows <= 2048;
+    const Layout L = layout(a.n_tok * a.group, RW, D, a.n_seqs);
+    const bool wide = L.workers >= (int64_t)16 * a.n_seqs * a.h_kv * L.blocks_of_rows;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
+    cfg.gridDim = wide ? dim3((unsigned)rows, D / 64) : dim3((unsigned)((rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = &attr;

@@ -542,7 +542,7 @@ gdr_status gdr_attn_prefill(const gdr_attn_dims *dims, int32_t n_seqs, const int
  * whatever the lengths; sequences that are cut have their parts joined by a second
  * launch in a fixed order, so results do not change from run to run.
  *
- *   q, o       [n_seqs * n_tok][h_q][d]
+ *   q, o       [n_seqs * n_tok][h_q][d]; n_seqs * n_tok * h_q below 2^31
  *   kv_lens    DEVICE int32 [n_seqs]
  *   lse        NULL, or DEVICE fp32 [n_seqs * n_tok][h_q]
  *   workspace  DEVICE, 16-byte aligned, at least gdr_attn_decode_workspace_bytes();

@@ -151,6 +151,6 @@ def test_binding_refuses(L):
                                 a["inv"], a["cu"])
     with pytest.raises(ValueError):
         gdr.gdr_attn_decode(q[:3], kc, kc.clone(), table, lens, q[:2])
-    with pytest.raises(gdr.GdrError):  # fp32 has no kernel
-        gdr.gdr_attn_prefill(q.float(), k.float(), k.float(), q.float(), cu, stream=0)
+    with pytest.raises(ValueError):  # host memory
+        gdr.gdr_attn_prefill(q, k, k.clone(), q.clone(), cu, stream=0)
     assert ctypes.sizeof(gdr.gdr_kv_cache) == 72
