@@ -10,7 +10,7 @@ namespace gdr {
 namespace attn {
 namespace {
 
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = (int64_t)1 << 38;
 
 bool aligned(const void *p, uintptr_t bytes) { return p && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool stride_ok(int64_t s) { return s >= 0 && s < kMaxStride && (s & 7) == 0; }

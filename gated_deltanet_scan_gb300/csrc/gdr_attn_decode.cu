@@ -553,21 +553,22 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     const float2 *const po = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.o);
     // a worker's part is its first where its own start is not before the triple's: so
     // all parts but perhaps the first one's
-    auto part_row = [&](int wk) { return ((int64_t)wk * 2 + (wk > w0 || cut.start(wk) >= seg0 ? 0 : 1)) * L.part_rows + lr; };
+    const int64_t row0 = cut.start(w0) >= seg0 ? 0 : L.part_rows;
+    auto part_row = [&](int wk) { return (int64_t)wk * 2 * L.part_rows + (wk == w0 ? row0 : 0) + lr; };
     float2 acc[V / 2];
     float m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) acc[e] = make_float2(0.f, 0.f);
-    constexpr int U = WPR > 1 ? 8 : 4;  // parts in flight
+    constexpr int U = WPR > 1 ? 16 : 4;  // parts in flight
 #pragma unroll 1
     for (int i = w0 + w; i <= w1; i += WPR * U) {
         float2 x[U][V / 2], v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t pr = part_row(min(i + u * WPR, w1));
-            v[u] = ml[pr];
+            v[u] = __ldcg(ml + pr);
 #pragma unroll
-            for (int e = 0; e < V / 2; ++e) x[u][e] = po[pr * (D / 2) + word0 + 32 * e];
+            for (int e = 0; e < V / 2; ++e) x[u][e] = __ldcg(po + pr * (D / 2) + word0 + 32 * e);
         }
         float top = m;
 #pragma unroll

@@ -1,85 +1,505 @@
-// Causal attention over whole packed prompts.
+// Causal attention over whole packed prompts, on tcgen05 tensor cores.
 //
-// One warp per query row: the running maximum m and sum l of the softmax and the
-// row's output in fp32, one token at a time.
+// Math.  For one key/value head the queries of the `group` heads that share it are
+// rows of one matrix, token by token: row r of a block of 128 is query head
+// r % group of its token r / group.  Over tiles of 128 tokens, with the running
+// reference m of each row,
+//     x = sc Q K^T  (sc = scale log2 e),   p = 2^(x - m),   l += sum p,   O += P V,
+// and o = O / l at the end.  m follows the row's maximum only when that is 2^8 above
+// it; O and l are then multiplied by 2^(m_old - m).
+//
+// Bound by the tensor cores: 4 d flops a visible (query, token) pair.  A pair of CTAs
+// (a cluster of two SMs) works on 256 rows with cta_group::2 MMAs: each CTA holds its
+// 128 rows of Q, S = Q K^T and O, and half of every key tile (64 tokens) and value
+// tile (half of the columns), so a tile crosses L2 once for 256 rows (32 bytes a clock
+// and SM at full MMA rate, against the 64 a single CTA of 128 rows would need).  O
+// (d columns) and two S tiles (128 each) fill TMEM at d = 256; P overwrites its S as
+// 16-bit pairs and is the second MMA's A operand from there.
+//
+// Twelve warps.  One thread loads K and V tiles by TMA into a ring, in the order the
+// MMAs take them: K0, K1, V0, K2, V1, ...  One thread of the leading CTA issues
+// S_{j+1} before P V_j, so the tensor pipe has work while P_j is made.  Two warpgroups
+// make P: one the even tiles, the other the odd ones, one row per thread.  Each hands
+// the row's reference m on to the other as soon as it has its tile's maximum, so they
+// work on two tiles at the same time; each keeps the sum l of its own tiles.  A
+// warpgroup that raises m rescales O itself, between the two MMAs.
+//
+// A token must not see what later tokens or other sequences hold, even a NaN, and 0
+// times NaN is NaN.  In S that is a select.  In the few tiles in which some row of the
+// pair does not see every token, two warps replace the value tile's infinities and
+// NaNs by zeros before the MMA reads it; where they found any, the rows that do see
+// them get them added at the end.
 #include "gdr_attn_common.cuh"
+#include "gdr_attn_ptx.cuh"
 #include "gdr_internal.h"
+#include "tc_ptx.cuh"
 
 namespace gdr {
 namespace attn {
 namespace {
 
+using namespace tc;
+
+constexpr int kThreads = 384;
+constexpr int kRows = 128;  // rows per CTA
+constexpr int kTile = 128;  // tokens per tile
+constexpr long long kWaitLimit = 4000000000LL;  // SM clocks (about 2 s)
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;
+
+template <int D>
+struct Shape {
+    static constexpr uint32_t Q_BLOCK = kRows * 128;       // 64 columns of Q
+    static constexpr uint32_t Q_BYTES = Q_BLOCK * (D / 64);
+    static constexpr int VC = D / 2 < 64 ? D / 2 : 64;     // columns of one value box
+    static constexpr int V_BOXES = D / 2 / VC;
+    static constexpr uint32_t V_BOX = kTile * VC * 2;
+    static constexpr uint32_t K_BOX = 64 * 128;            // 64 tokens, 64 columns
+    static constexpr uint32_t STAGE = 128 * D;             // half a key or value tile
+    static constexpr int STAGES = D == 256 ? 5 : 8;
+    static constexpr uint32_t OFF_RING = Q_BYTES;
+    static constexpr uint32_t OFF_M = OFF_RING + STAGES * STAGE;  // float [2][128]: m handed on
+    static constexpr uint32_t OFF_L = OFF_M + 1024;               // float [2][128]: the warpgroups' l
+    static constexpr uint32_t OFF_BAR = OFF_L + 1024;
+    static constexpr uint32_t OFF_WORDS = OFF_BAR + 64 * 8;       // TMEM address, patch flag, scan scratch
+    static constexpr uint32_t BYTES = OFF_WORDS + 128;
+    static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
+    static constexpr uint32_t COLS_S = 256;                // S tiles at columns 256 and 384, O at 0
+};
+
+// barriers, as 8-byte words from OFF_BAR
+enum Bar {
+    kQFull = 0,
+    kKvFull = 1,               // [stages], on the leading CTA
+    kKvEmpty = kKvFull + 8,    // [stages]
+    kSFull = kKvEmpty + 8,     // [2]
+    kPFull = kSFull + 2,       // [2], on the leading CTA
+    kPvDone = kPFull + 2,
+    kODone = kPvDone + 1,      // the last P V
+    kVLocal = kODone + 1,      // [3]: value tiles to be looked through
+    kMReady = kVLocal + 3,     // [2][4]: m of a warp's rows
+    kBars = kMReady + 8,
+};
+static_assert(kBars <= 64, "barrier words");
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+// Packed rows: tokens per CTA and per pair.
+__host__ __device__ inline int tokens_per_cta(int group) { return kRows / group; }
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(128) prefill_rows_kernel(const __grid_constant__ Args a) {
-    constexpr int W = D / 64;  // 32-bit words per lane
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= a.t_total * a.h_q) return;
-    const int64_t t = row / a.h_q;
-    const int h = (int)(row - t * a.h_q);
-    const int s = find_seq(a.cu, a.n_seqs, t);
-    const int64_t t0 = a.cu[s], t1 = a.cu[s + 1];
-    if (t0 < 0 || t < t0 || t1 <= t || t1 > a.t_total) {
-        record_invalid(a.err);
-        return;
-    }
-    float2 q[W], o[W];
-    const uint32_t *qp = reinterpret_cast<const uint32_t *>(a.q.p + t * a.q.ts + h * a.q.hs);
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
+    using Sh = Shape<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    float *const s_m = reinterpret_cast<float *>(smem + Sh::OFF_M);
+    float *const s_l = reinterpret_cast<float *>(smem + Sh::OFF_L);
+    const uint32_t bars = base + Sh::OFF_BAR;
+    uint32_t *const s_words = reinterpret_cast<uint32_t *>(smem + Sh::OFF_WORDS);
+    // s_words: 0 TMEM address, 1 patch flag, then the search's scratch
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = pair::cta_rank();
+    auto bar = [&](int i) { return bars + 8u * i; };
+
+    // --- which sequence, block of tokens and key/value head
+    const int per_cta = tokens_per_cta(a.group), per_pair = 2 * per_cta;
+    const int pair_id = blockIdx.x >> 1;
+    const int h = pair_id % a.h_kv;
+    const int64_t want = pair_id / a.h_kv;  // 0: the last block of the last sequence, whose row sees most
+    int64_t t0 = 0;  // the sequence's first token
+    int len = 0, block = -1;
+    {
+        // blocks of every sequence, 384 sequences at a time from the last
+        int *const s_warp = reinterpret_cast<int *>(s_words + 2);          // [12]
+        int *const s_hit = reinterpret_cast<int *>(s_words + 14);          // sequence, blocks after it
+        if (tid == 0) s_hit[0] = -1;
+        int64_t after = 0;
+        for (int hi = a.n_seqs; hi > 0 && after <= want; hi -= kThreads) {
+            const int s = hi - 1 - tid;
+            int n = 0;
+            if (s >= 0) {
+                const int64_t b = a.cu[s], e = a.cu[s + 1];
+                if (b < 0 || e < b || e > a.t_total) {
+                    record_invalid(a.err);
+                } else {
+                    n = (int)((e - b + per_pair - 1) / per_pair);
+                }
+            }
+            int x = n;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        q[i] = unpack2<F16>(qp[lane + 32 * i]);
-        o[i] = make_float2(0.f, 0.f);
-    }
-    float m = -CUDART_INF_F, l = 0.f;
-    for (int64_t p = t0; p <= t; ++p) {
-        const uint32_t *kp = reinterpret_cast<const uint32_t *>(a.k.p + p * a.k.ts + (h / a.group) * a.k.hs);
-        const uint32_t *vp = reinterpret_cast<const uint32_t *>(a.v.p + p * a.v.ts + (h / a.group) * a.v.hs);
-        float x = 0.f;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) s_warp[warp] = x;
+            __syncthreads();
+            int before = 0, all = 0;
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const float2 k = unpack2<F16>(kp[lane + 32 * i]);
-            x += q[i].x * k.x + q[i].y * k.y;
+            for (int i = 0; i < kThreads / 32; ++i) {
+                if (i < warp) before += s_warp[i];
+                all += s_warp[i];
+            }
+            const int64_t end = after + before + x;
+            if (want >= end - n && want < end) {
+                s_hit[0] = s;
+                s_hit[1] = (int)(end - 1 - want);  // blocks of s before this one
+            }
+            after += all;
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        x *= a.scale;
-        const float mn = fmaxf(m, x);
-        const float c = m == mn ? 1.f : __expf(m - mn), w = __expf(x - mn);
-        l = l * c + w;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const float2 v = unpack2<F16>(vp[lane + 32 * i]);
-            o[i].x = o[i].x * c + w * v.x;
-            o[i].y = o[i].y * c + w * v.y;
+        __syncthreads();
+        const int s = s_hit[0];
+        if (s >= 0) {
+            t0 = a.cu[s];
+            len = (int)(a.cu[s + 1] - t0);
+            block = s_hit[1];
         }
     }
-    uint32_t *op = reinterpret_cast<uint32_t *>(a.o.p + t * a.o.ts + h * a.o.hs);
-    const float r = 1.f / l;
+    if (block < 0) return;  // both CTAs of the pair: more pairs were launched than there are blocks
+
+    const int first = block * per_pair;              // the pair's first token in the sequence
+    const int mine = first + (int)rank * per_cta;    // this CTA's
+    const int n = (min(len, first + per_pair) + kTile - 1) / kTile;  // tiles
+    const int j_clean = (first + 1) >> 7;            // the first tile some row sees only in part
+
+    // --- barriers and TMEM
+    if (tid == 0) {
+        mbar_init(bar(kQFull), 2);
+        for (int i = 0; i < Sh::STAGES; ++i) {
+            mbar_init(bar(kKvFull + i), 2);
+            mbar_init(bar(kKvEmpty + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kPFull + i), 8);
+            for (int w = 0; w < 4; ++w) mbar_init(bar(kMReady + 4 * i + w), 1);
+        }
+        mbar_init(bar(kPvDone), 1);
+        mbar_init(bar(kODone), 1);
+        for (int i = 0; i < 3; ++i) mbar_init(bar(kVLocal + i), 1);
+        s_words[1] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        pair::tmem_alloc(smem_u32(s_words), 512);
+        pair::tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    pair::cluster_sync();
+    tc_fence_after_sync();
+    const uint32_t tmem = s_words[0];
+    bool ok = true;
+
+    // Order of the ring: K0, K1, V0, K2, V1, ..., V of the last tile at the end.
+    auto k_index = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
+    auto v_index = [&](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
+
+    if (warp == 8 && lane == 0) {
+        // ---- loads (both CTAs: own halves)
+        const uint32_t q_bar = pair::map_to(bar(kQFull), 0);
+        const uint32_t q_bytes = (uint32_t)(D / 64) * 128u * (uint32_t)(per_cta * a.group);
+        pair::arrive_expect_remote(q_bar, q_bytes);
+        for (int c = 0; c < D / 64; ++c)
+            pair::tma_load_3d_pair(base + c * Sh::Q_BLOCK, &maps.q, q_bar, c * 64, h * a.group, (int)t0 + mine);
+        for (int i = 0; i < 2 * n && ok; ++i) {
+            const int st = i % Sh::STAGES, use = i / Sh::STAGES;
+            if (use > 0) ok = mbar_wait_bounded(bar(kKvEmpty + st), (use - 1) & 1, kWaitLimit);
+            if (!ok) break;
+            const uint32_t dst = base + Sh::OFF_RING + st * Sh::STAGE;
+            const uint32_t full = pair::map_to(bar(kKvFull + st), 0);
+            const bool is_k = i == 0 || ((i & 1) && i != 2 * n - 1);
+            if (is_k) {
+                const int j = i == 0 ? 0 : (i + 1) / 2;
+                pair::arrive_expect_remote(full, Sh::STAGE);
+                for (int c = 0; c < D / 64; ++c)
+                    pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, h,
+                                           (int)t0 + j * kTile + (int)rank * 64);
+            } else {
+                const int j = i == 2 * n - 1 ? n - 1 : i / 2 - 1;
+                if (j >= j_clean) {  // looked through by warps 10 and 11, which then report the stage full
+                    const uint32_t b = bar(kVLocal + j - j_clean);
+                    mbar_arrive_expect_tx(b, Sh::STAGE);
+                    for (int c = 0; c < Sh::V_BOXES; ++c)
+                        tma_load_3d(dst + c * Sh::V_BOX, &maps.v, b, (int)rank * (D / 2) + c * Sh::VC, h,
+                                    (int)t0 + j * kTile);
+                } else {
+                    pair::arrive_expect_remote(full, Sh::STAGE);
+                    for (int c = 0; c < Sh::V_BOXES; ++c)
+                        pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full, (int)rank * (D / 2) + c * Sh::VC,
+                                               h, (int)t0 + j * kTile);
+                }
+            }
+        }
+    } else if (warp == 9 && lane == 0 && rank == 0) {
+        // ---- MMAs
+        const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // x = |sc| (-Q) K^T
+        const uint32_t id_s = (F16 ? idesc_f16_f32(256, kTile, 0, 0) : idesc_bf16_f32(256, kTile, 0, 0)) | negate;
+        const uint32_t id_o = F16 ? idesc_f16_f32(256, D, 0, 1) : idesc_bf16_f32(256, D, 0, 1);
+        ok = pair::wait_cluster(bar(kQFull), 0, kWaitLimit);
+        auto full = [&](int i) {
+            return pair::wait_cluster(bar(kKvFull + i % Sh::STAGES), (i / Sh::STAGES) & 1, kWaitLimit);
+        };
+        auto score = [&](int j) {
+            const int i = k_index(j), st = i % Sh::STAGES;
+            if (!full(i)) return false;
+            tc_fence_after_sync();
+            const uint32_t kb = base + Sh::OFF_RING + st * Sh::STAGE;
+            const uint32_t d = tmem + Sh::COLS_S + (j & 1) * kTile;
 #pragma unroll
-    for (int i = 0; i < W; ++i) op[lane + 32 * i] = pack2<F16>(o[i].x * r, o[i].y * r);
-    if (a.lse && lane == 0) a.lse[row] = m + logf(l);
+            for (int k = 0; k < D / 16; ++k) {
+                const uint64_t qa = smem_desc_sw128(base + (k >> 2) * Sh::Q_BLOCK + (k & 3) * 32, 0, 1024);
+                const uint64_t kd = smem_desc_sw128(kb + (k >> 2) * Sh::K_BOX + (k & 3) * 32, 0, 1024);
+                pair::mma_ss(d, qa, kd, id_s, k > 0);
+            }
+            pair::commit_both(bar(kKvEmpty + st));
+            pair::commit_both(bar(kSFull + (j & 1)));
+            return true;
+        };
+        ok = ok && score(0);
+        for (int j = 0; j < n && ok; ++j) {
+            if (j + 1 < n) ok = score(j + 1);
+            const int i = v_index(j), st = i % Sh::STAGES;
+            ok = ok && full(i);
+            ok = ok && pair::wait_cluster(bar(kPFull + (j & 1)), (j >> 1) & 1, kWaitLimit);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t vb = base + Sh::OFF_RING + st * Sh::STAGE;
+            const uint32_t p = tmem + Sh::COLS_S + (j & 1) * kTile;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k) {
+                const uint32_t at = vb + k * 16 * (Sh::VC * 2);
+                const uint64_t vd = Sh::VC == 64 ? smem_desc(at, Sh::V_BOX, 1024, kSwizzle128)
+                                                 : smem_desc(at, Sh::V_BOX, 512, kSwizzle64);
+                pair::mma_ts(tmem, p + k * 8, vd, id_o, j > 0 || k > 0);
+            }
+            pair::commit_both(bar(kKvEmpty + st));
+            pair::commit_both(bar(kPvDone));
+        }
+        if (ok) pair::commit_both(bar(kODone));
+    } else if (warp >= 10) {
+        // ---- value tiles that some row sees only in part (both CTAs: own halves)
+        bool found = false;
+        for (int j = j_clean; j < n; ++j) {  // every tile even after a timeout: the two warps meet in each
+            const int i = v_index(j), st = i % Sh::STAGES;
+            ok = ok && mbar_wait_bounded(bar(kVLocal + j - j_clean), 0, kWaitLimit);
+            uint4 *const tile = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE);
+            constexpr uint32_t e = F16 ? 0x7C007C00u : 0x7F807F80u;
+#pragma unroll 4
+            for (int x = tid - 320; ok && x < (int)Sh::STAGE / 16; x += 64) {
+                uint4 w = tile[x];
+                uint32_t *const p = &w.x;
+                bool bad = false;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const bool lo = (p[y] & e & 0xFFFFu) == (e & 0xFFFFu);
+                    const bool hi = (p[y] & e & 0xFFFF0000u) == (e & 0xFFFF0000u);
+                    bad = bad || lo || hi;
+                    p[y] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
+                }
+                if (bad) {
+                    tile[x] = w;
+                    found = true;
+                }
+            }
+            fence_proxy_async_smem();
+            named_sync(1, 64);
+            if (tid == 320 && ok) pair::arrive_remote(pair::map_to(bar(kKvFull + st), 0));
+        }
+        if (found) s_words[1] = 1;
+    } else if (warp < 8) {
+        // ---- softmax: warpgroup wg takes tiles wg, wg + 2, ...; a thread is a row
+        const int wg = warp >> 2, row = tid & 127, wq = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+        // a scale of 0 still has to leave a masked score at minus infinity
+        const float sc = fmaxf(fabsf(a.scale), 1e-30f) * kLog2e;
+        const int token = mine + row / a.group;  // in the sequence
+        const uint32_t p_bar = pair::map_to(bar(kPFull + wg), 0);
+        float m_own = -CUDART_INF_F, l = 0.f;
+        for (int j = wg; j < n && ok; j += 2) {
+            ok = mbar_wait_bounded(bar(kSFull + wg), (j >> 1) & 1, kWaitLimit);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t s_at = lanes + Sh::COLS_S + wg * kTile;
+            uint32_t r[128];
+            pair::tmem_load128(s_at, r);
+            if (j * kTile + kTile - 1 > mine) {  // some row of this CTA sees only part of the tile
+                const int seen = token - j * kTile;  // columns 0 .. seen
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (c > seen) r[c] = 0xFF800000u;
+            }
+            float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top[e] = fmaxf(top[e], fmaxf(__uint_as_float(r[c + e]), __uint_as_float(r[c + 4 + e])));
+            }
+            const float x_top = sc * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            // the reference after the tile before, from the other warpgroup
+            float m_prev = -CUDART_INF_F;
+            if (j > 0) {
+                ok = mbar_wait_bounded(bar(kMReady + 4 * (wg ^ 1) + wq), ((j - 1) >> 1) & 1, kWaitLimit);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                m_prev = s_m[(wg ^ 1) * 128 + row];
+            }
+            const bool raise = j == 0 || x_top > m_prev + kSlack;
+            const float m = raise ? x_top : m_prev;
+            s_m[wg * 128 + row] = m;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kMReady + 4 * wg + wq));
+
+            if (j > 0 && __any_sync(0xffffffffu, raise)) {
+                // O so far is that of tiles 0 .. j - 1: P V of tile j waits for this warp's P
+                ok = mbar_wait_bounded(bar(kPvDone), (j - 1) & 1, kWaitLimit);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const float f = raise ? fast_exp2(m_prev - m) : 1.f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    pair::tmem_load32(lanes + c, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    pair::tmem_store32(lanes + c, o);
+                }
+            }
+            l *= m_own == m ? 1.f : fast_exp2(m_own - m);
+            m_own = m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t p[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const int i = half * 64 + 2 * c;
+                    const float x = fast_exp2(fmaf(__uint_as_float(r[i]), sc, -m));
+                    const float y = fast_exp2(fmaf(__uint_as_float(r[i + 1]), sc, -m));
+                    sum[c & 1] += x;
+                    sum[2 + (c & 1)] += y;
+                    p[c] = pack2<F16>(x, y);
+                }
+                pair::tmem_store32(s_at + half * 32, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            pair::tmem_store_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) pair::arrive_remote(p_bar);
+        }
+        s_l[wg * 128 + row] = l;
+        if (wg >= n) s_m[wg * 128 + row] = -CUDART_INF_F;  // no tile was this warpgroup's
+        ok = ok && mbar_wait_bounded(bar(kODone), 0, kWaitLimit);
+    }
+    if (!ok) {
+        // a wait gave up: leave the copies and MMAs in flight time to end before shared
+        // memory and TMEM go (they wait for nothing themselves)
+        atomicCAS(a.err, 0, (int32_t)GDR_ERR_DEVICE_TIMEOUT);
+        const long long t_end = clock64() + 4000000;
+        while (clock64() < t_end) {}
+    }
+    __syncwarp();
+    pair::cluster_sync();
+    tc_fence_after_sync();
+
+    if (warp < 8) {
+        // ---- o = O / l: warpgroup wg writes half of the columns
+        const int wg = warp >> 2, row = tid & 127, wq = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+        const int tok = row / a.group, token = mine + tok;
+        const bool live = tok < per_cta && token < len;
+        const int64_t t = t0 + token;
+        const int hq = h * a.group + row - tok * a.group;
+        const float2 e0 = make_float2(s_m[row], s_l[row]), e1 = make_float2(s_m[128 + row], s_l[128 + row]);
+        const float m = ((n - 1) & 1) ? e1.x : e0.x;
+        const float l = (e0.x == m ? e0.y : e0.y * fast_exp2(e0.x - m)) +
+                        (e1.x == m ? e1.y : e1.y * fast_exp2(e1.x - m));
+        const float inv = 1.f / l;
+        const bool patch = s_words[1] | pair::load_remote(pair::map_to(smem_u32(s_words + 1), rank ^ 1u));
+        const int c0 = wg * (D / 2);
+        uint16_t *const dst = a.o.p + t * a.o.ts + (int64_t)hq * a.o.hs + c0;
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+            uint32_t o[32];
+            pair::tmem_load32(lanes + c0 + c, o);
+            if (live && patch) {
+                for (int p = j_clean * kTile; p <= token; ++p) {
+                    const uint16_t *const v = a.v.p + (t0 + p) * a.v.ts + (int64_t)h * a.v.hs + c0 + c;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float x = unpack1<F16>(v[e]);
+                        if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                    }
+                }
+            }
+            if (live) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 w;
+                    w.x = pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                    w.y = pack2<F16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                    w.z = pack2<F16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                    w.w = pack2<F16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                    *reinterpret_cast<uint4 *>(dst + c + e) = w;
+                }
+            }
+            __syncwarp();
+        }
+        if (wg == 0 && live && a.lse) a.lse[t * a.h_q + hq] = kLn2 * (m + log2f(l));
+        tc_fence_before_sync();
+    }
+    __syncwarp();
+    pair::cluster_sync();  // both CTAs are done with TMEM and with each other's flags
+    if (warp == 9) pair::tmem_dealloc(tmem, 512);
 }
 
 template <int D>
-void launch(const Args &a, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((a.t_total * a.h_q + 3) / 4);
-    if (a.f16)
-        prefill_rows_kernel<D, true><<<blocks, 128, 0, s>>>(a);
-    else
-        prefill_rows_kernel<D, false><<<blocks, 128, 0, s>>>(a);
+constexpr uint32_t smem_bytes() {
+    // at least 116 KiB, so that one CTA has the SM (and its TMEM) to itself
+    return Shape<D>::BYTES < 116u * 1024 ? 116u * 1024 : Shape<D>::BYTES;
+}
+
+template <int D, bool F16>
+cudaError_t launch(const Args &a, cudaStream_t s) {
+    using Sh = Shape<D>;
+    Maps m;
+    const int per_cta = tokens_per_cta(a.group);
+    if (!encode_heads_3d(&m.q, a.q.p, F16, D, a.h_q, a.t_total, a.q.hs, a.q.ts, 64, a.group, per_cta,
+                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_heads_3d(&m.k, a.k.p, F16, D, a.h_kv, a.t_total, a.k.hs, a.k.ts, 64, 1, 64,
+                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_heads_3d(&m.v, a.v.p, F16, D, a.h_kv, a.t_total, a.v.hs, a.v.ts, Sh::VC, 1, kTile,
+                         Sh::VC == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    static SmemOptIn opt_in;
+    cudaError_t e = opt_in.set(reinterpret_cast<const void *>(prefill_kernel<D, F16>), (int)smem_bytes<D>());
+    if (e != cudaSuccess) return e;
+    // every sequence has at most one block that is not full
+    const int64_t pairs = (a.t_total / (2 * per_cta) + a.n_seqs) * a.h_kv;
+    if (2 * pairs > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    prefill_kernel<D, F16><<<(unsigned)(2 * pairs), kThreads, smem_bytes<D>(), s>>>(a, m);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const Args &a, cudaStream_t s) {
-    if (a.d == 64)
-        launch<64>(a, s);
-    else if (a.d == 128)
-        launch<128>(a, s);
-    else
-        launch<256>(a, s);
-    return cudaGetLastError();
+    if (a.d == 64) return a.f16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    if (a.d == 128) return a.f16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    return a.f16 ? launch<256, true>(a, s) : launch<256, false>(a, s);
 }
 
 }  // namespace attn

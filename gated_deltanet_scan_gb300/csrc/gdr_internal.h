@@ -94,6 +94,12 @@ cudaError_t launch_commit(const Args &a, int32_t *err, cudaStream_t s);
 bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
                     CUtensorMapSwizzle swizzle);
 
+// Strided 16-bit rows [tokens][heads][d] (strides in elements) as a TMA map with box
+// {box_d, box_heads, box_tokens}.
+bool encode_heads_3d(CUtensorMap *m, const void *base, bool f16, int d, int heads, int64_t tokens, int64_t head_stride,
+                     int64_t token_stride, uint32_t box_d, uint32_t box_heads, uint32_t box_tokens,
+                     CUtensorMapSwizzle swizzle);
+
 // Device address of the error word (nullptr if it cannot be resolved).
 int32_t *device_error_word();
 

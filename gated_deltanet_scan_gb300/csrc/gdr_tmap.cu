@@ -34,4 +34,21 @@ bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_heads_3d(CUtensorMap *m, const void *base, bool f16, int d, int heads, int64_t tokens, int64_t head_stride,
+                     int64_t token_stride, uint32_t box_d, uint32_t box_heads, uint32_t box_tokens,
+                     CUtensorMapSwizzle swizzle) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    // the stride of a dimension of one entry is never used, but has to be a valid one
+    if (heads == 1) head_stride = d;
+    if (tokens == 1) token_stride = d;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
+    cuuint32_t box[3] = {box_d, box_heads, box_tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace gdr

@@ -439,7 +439,7 @@ gdr_status gdr_state_restore(const gdr_dims *dims, int32_t n_seqs, const float *
  * projection: value x of head h of token t is at
  *     ptr[t * token_stride + h * head_stride + x],
  * strides in elements.  ptr is 16-byte aligned and both strides are multiples of
- * 8, not negative, and below 2^40 (GDR_ERR_INVALID_ARG otherwise).  Rows that are
+ * 8, not negative, and below 2^38 (GDR_ERR_INVALID_ARG otherwise).  Rows that are
  * written must not overlap one another.
  */
 typedef struct gdr_attn_dims {
@@ -462,7 +462,7 @@ typedef struct gdr_rows {
  * the d values from
  *     k (v) + page * page_stride + slot * token_stride + h * head_stride,
  * which covers token-major and head-major pages.  k and v: DEVICE, 16-byte
- * aligned; strides in elements, multiples of 8, not negative, below 2^40; offsets are
+ * aligned; strides in elements, multiples of 8, not negative, below 2^38; offsets are
  * computed in 64 bits.  page_table: DEVICE int32, entries of pages a sequence
  * does not reach yet are not read.  page_size and max_pages (pages a table row
  * holds) are at least 1, and page_size * max_pages below 2^31.  A page id outside
