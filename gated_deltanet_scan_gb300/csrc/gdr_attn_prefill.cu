@@ -194,123 +194,140 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = s_words[0];
     bool ok = true;
 
+    auto gave_up = [&] {
+        // a wait gave up: leave the copies and MMAs in flight time to end before shared
+        // memory and TMEM go (they wait for nothing themselves)
+        atomicCAS(a.err, 0, (int32_t)GDR_ERR_DEVICE_TIMEOUT);
+        const long long t_end = clock64() + 4000000;
+        while (clock64() < t_end) {}
+    };
+
     // Order of the ring: K0, K1, V0, K2, V1, ..., V of the last tile at the end.
     auto k_index = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
     auto v_index = [&](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
 
-    if (warp == 8 && lane == 0) {
-        // ---- loads (both CTAs: own halves)
-        const uint32_t q_bar = pair::map_to(bar(kQFull), 0);
-        const uint32_t q_bytes = (uint32_t)(D / 64) * 128u * (uint32_t)(per_cta * a.group);
-        pair::arrive_expect_remote(q_bar, q_bytes);
-        for (int c = 0; c < D / 64; ++c)
-            pair::tma_load_3d_pair(base + c * Sh::Q_BLOCK, &maps.q, q_bar, c * 64, h * a.group, (int)t0 + mine);
-        for (int i = 0; i < 2 * n && ok; ++i) {
-            const int st = i % Sh::STAGES, use = i / Sh::STAGES;
-            if (use > 0) ok = mbar_wait_bounded(bar(kKvEmpty + st), (use - 1) & 1, kWaitLimit);
-            if (!ok) break;
-            const uint32_t dst = base + Sh::OFF_RING + st * Sh::STAGE;
-            const uint32_t full = pair::map_to(bar(kKvFull + st), 0);
-            const bool is_k = i == 0 || ((i & 1) && i != 2 * n - 1);
-            if (is_k) {
-                const int j = i == 0 ? 0 : (i + 1) / 2;
-                pair::arrive_expect_remote(full, Sh::STAGE);
-                for (int c = 0; c < D / 64; ++c)
-                    pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, h,
-                                           (int)t0 + j * kTile + (int)rank * 64);
-            } else {
-                const int j = i == 2 * n - 1 ? n - 1 : i / 2 - 1;
-                if (j >= j_clean) {  // looked through by warps 10 and 11, which then report the stage full
-                    const uint32_t b = bar(kVLocal + j - j_clean);
-                    mbar_arrive_expect_tx(b, Sh::STAGE);
-                    for (int c = 0; c < Sh::V_BOXES; ++c)
-                        tma_load_3d(dst + c * Sh::V_BOX, &maps.v, b, (int)rank * (D / 2) + c * Sh::VC, h,
-                                    (int)t0 + j * kTile);
-                } else {
+    // the launch's 384 x 168 registers become 128 x 56 and 256 x 224
+    if (warp >= 8) {
+        pair::fewer_registers<56>();
+        if (warp == 8 && lane == 0) {
+            // ---- loads (both CTAs: own halves)
+            const uint32_t q_bar = pair::map_to(bar(kQFull), 0);
+            const uint32_t q_bytes = (uint32_t)(D / 64) * 128u * (uint32_t)(per_cta * a.group);
+            pair::arrive_expect_remote(q_bar, q_bytes);
+            for (int c = 0; c < D / 64; ++c)
+                pair::tma_load_3d_pair(base + c * Sh::Q_BLOCK, &maps.q, q_bar, c * 64, h * a.group, (int)t0 + mine);
+            for (int i = 0; i < 2 * n && ok; ++i) {
+                const int st = i % Sh::STAGES, use = i / Sh::STAGES;
+                if (use > 0) ok = mbar_wait_bounded(bar(kKvEmpty + st), (use - 1) & 1, kWaitLimit);
+                if (!ok) break;
+                const uint32_t dst = base + Sh::OFF_RING + st * Sh::STAGE;
+                const uint32_t full = pair::map_to(bar(kKvFull + st), 0);
+                const bool is_k = i == 0 || ((i & 1) && i != 2 * n - 1);
+                if (is_k) {
+                    const int j = i == 0 ? 0 : (i + 1) / 2;
                     pair::arrive_expect_remote(full, Sh::STAGE);
-                    for (int c = 0; c < Sh::V_BOXES; ++c)
-                        pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full, (int)rank * (D / 2) + c * Sh::VC,
-                                               h, (int)t0 + j * kTile);
+                    for (int c = 0; c < D / 64; ++c)
+                        pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, h,
+                                               (int)t0 + j * kTile + (int)rank * 64);
+                } else {
+                    const int j = i == 2 * n - 1 ? n - 1 : i / 2 - 1;
+                    if (j >= j_clean) {  // looked through by warps 10 and 11, which then report the stage full
+                        const uint32_t b = bar(kVLocal + j - j_clean);
+                        mbar_arrive_expect_tx(b, Sh::STAGE);
+                        for (int c = 0; c < Sh::V_BOXES; ++c)
+                            tma_load_3d(dst + c * Sh::V_BOX, &maps.v, b, (int)rank * (D / 2) + c * Sh::VC, h,
+                                        (int)t0 + j * kTile);
+                    } else {
+                        pair::arrive_expect_remote(full, Sh::STAGE);
+                        for (int c = 0; c < Sh::V_BOXES; ++c)
+                            pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full, (int)rank * (D / 2) + c * Sh::VC,
+                                                   h, (int)t0 + j * kTile);
+                    }
                 }
             }
-        }
-    } else if (warp == 9 && lane == 0 && rank == 0) {
-        // ---- MMAs
-        const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // x = |sc| (-Q) K^T
-        const uint32_t id_s = (F16 ? idesc_f16_f32(256, kTile, 0, 0) : idesc_bf16_f32(256, kTile, 0, 0)) | negate;
-        const uint32_t id_o = F16 ? idesc_f16_f32(256, D, 0, 1) : idesc_bf16_f32(256, D, 0, 1);
-        ok = pair::wait_cluster(bar(kQFull), 0, kWaitLimit);
-        auto full = [&](int i) {
-            return pair::wait_cluster(bar(kKvFull + i % Sh::STAGES), (i / Sh::STAGES) & 1, kWaitLimit);
-        };
-        auto score = [&](int j) {
-            const int i = k_index(j), st = i % Sh::STAGES;
-            if (!full(i)) return false;
-            tc_fence_after_sync();
-            const uint32_t kb = base + Sh::OFF_RING + st * Sh::STAGE;
-            const uint32_t d = tmem + Sh::COLS_S + (j & 1) * kTile;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint64_t qa = smem_desc_sw128(base + (k >> 2) * Sh::Q_BLOCK + (k & 3) * 32, 0, 1024);
-                const uint64_t kd = smem_desc_sw128(kb + (k >> 2) * Sh::K_BOX + (k & 3) * 32, 0, 1024);
-                pair::mma_ss(d, qa, kd, id_s, k > 0);
-            }
-            pair::commit_both(bar(kKvEmpty + st));
-            pair::commit_both(bar(kSFull + (j & 1)));
-            return true;
-        };
-        ok = ok && score(0);
-        for (int j = 0; j < n && ok; ++j) {
-            if (j + 1 < n) ok = score(j + 1);
-            const int i = v_index(j), st = i % Sh::STAGES;
-            ok = ok && full(i);
-            ok = ok && pair::wait_cluster(bar(kPFull + (j & 1)), (j >> 1) & 1, kWaitLimit);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t vb = base + Sh::OFF_RING + st * Sh::STAGE;
-            const uint32_t p = tmem + Sh::COLS_S + (j & 1) * kTile;
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) {
-                const uint32_t at = vb + k * 16 * (Sh::VC * 2);
-                const uint64_t vd = Sh::VC == 64 ? smem_desc(at, Sh::V_BOX, 1024, kSwizzle128)
-                                                 : smem_desc(at, Sh::V_BOX, 512, kSwizzle64);
-                pair::mma_ts(tmem, p + k * 8, vd, id_o, j > 0 || k > 0);
-            }
-            pair::commit_both(bar(kKvEmpty + st));
-            pair::commit_both(bar(kPvDone));
-        }
-        if (ok) pair::commit_both(bar(kODone));
-    } else if (warp >= 10) {
-        // ---- value tiles that some row sees only in part (both CTAs: own halves)
-        bool found = false;
-        for (int j = j_clean; j < n; ++j) {  // every tile even after a timeout: the two warps meet in each
-            const int i = v_index(j), st = i % Sh::STAGES;
-            ok = ok && mbar_wait_bounded(bar(kVLocal + j - j_clean), 0, kWaitLimit);
-            uint4 *const tile = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE);
-            constexpr uint32_t e = F16 ? 0x7C007C00u : 0x7F807F80u;
-#pragma unroll 4
-            for (int x = tid - 320; ok && x < (int)Sh::STAGE / 16; x += 64) {
-                uint4 w = tile[x];
-                uint32_t *const p = &w.x;
-                bool bad = false;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const bool lo = (p[y] & e & 0xFFFFu) == (e & 0xFFFFu);
-                    const bool hi = (p[y] & e & 0xFFFF0000u) == (e & 0xFFFF0000u);
-                    bad = bad || lo || hi;
-                    p[y] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
+        } else if (warp == 9 && lane == 0 && rank == 0) {
+            // ---- MMAs
+            const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // x = |sc| (-Q) K^T
+            const uint32_t id_s = (F16 ? idesc_f16_f32(256, kTile, 0, 0) : idesc_bf16_f32(256, kTile, 0, 0)) | negate;
+            const uint32_t id_o = F16 ? idesc_f16_f32(256, D, 0, 1) : idesc_bf16_f32(256, D, 0, 1);
+            ok = mbar_wait_bounded(bar(kQFull), 0, kWaitLimit);
+            auto full = [&](int i) {
+                return mbar_wait_bounded(bar(kKvFull + i % Sh::STAGES), (i / Sh::STAGES) & 1, kWaitLimit);
+            };
+            auto score = [&](int j) {
+                const int i = k_index(j), st = i % Sh::STAGES;
+                if (!full(i)) return false;
+                tc_fence_after_sync();
+                const uint32_t kb = base + Sh::OFF_RING + st * Sh::STAGE;
+                const uint32_t d = tmem + Sh::COLS_S + (j & 1) * kTile;
+    #pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t qa = smem_desc_sw128(base + (k >> 2) * Sh::Q_BLOCK + (k & 3) * 32, 0, 1024);
+                    const uint64_t kd = smem_desc_sw128(kb + (k >> 2) * Sh::K_BOX + (k & 3) * 32, 0, 1024);
+                    pair::mma_ss(d, qa, kd, id_s, k > 0);
                 }
-                if (bad) {
-                    tile[x] = w;
-                    found = true;
+                pair::commit_both(bar(kKvEmpty + st));
+                pair::commit_both(bar(kSFull + (j & 1)));
+                return true;
+            };
+            ok = ok && score(0);
+            for (int j = 0; j < n && ok; ++j) {
+                if (j + 1 < n) ok = score(j + 1);
+                const int i = v_index(j), st = i % Sh::STAGES;
+                ok = ok && (j < j_clean ? full(i)
+                                        : pair::wait_cluster(bar(kKvFull + st), (i / Sh::STAGES) & 1, kWaitLimit));
+                ok = ok && mbar_wait_bounded(bar(kPFull + (j & 1)), (j >> 1) & 1, kWaitLimit);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t vb = base + Sh::OFF_RING + st * Sh::STAGE;
+                const uint32_t p = tmem + Sh::COLS_S + (j & 1) * kTile;
+    #pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) {
+                    const uint32_t at = vb + k * 16 * (Sh::VC * 2);
+                    const uint64_t vd = Sh::VC == 64 ? smem_desc(at, Sh::V_BOX, 1024, kSwizzle128)
+                                                     : smem_desc(at, Sh::V_BOX, 512, kSwizzle64);
+                    pair::mma_ts(tmem, p + k * 8, vd, id_o, j > 0 || k > 0);
                 }
+                pair::commit_both(bar(kKvEmpty + st));
+                pair::commit_both(bar(kPvDone));
             }
-            fence_proxy_async_smem();
-            named_sync(1, 64);
-            if (tid == 320 && ok) pair::arrive_remote(pair::map_to(bar(kKvFull + st), 0));
+            if (ok) pair::commit_both(bar(kODone));
+        } else if (warp >= 10) {
+            // ---- value tiles that some row sees only in part (both CTAs: own halves)
+            bool found = false;
+            for (int j = j_clean; j < n; ++j) {  // every tile even after a timeout: the two warps meet in each
+                const int i = v_index(j), st = i % Sh::STAGES;
+                ok = ok && mbar_wait_bounded(bar(kVLocal + j - j_clean), 0, kWaitLimit);
+                uint4 *const tile = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE);
+                constexpr uint32_t e = F16 ? 0x7C007C00u : 0x7F807F80u;
+    #pragma unroll 4
+                for (int x = tid - 320; ok && x < (int)Sh::STAGE / 16; x += 64) {
+                    uint4 w = tile[x];
+                    uint32_t *const p = &w.x;
+                    bool bad = false;
+    #pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const bool lo = (p[y] & e & 0xFFFFu) == (e & 0xFFFFu);
+                        const bool hi = (p[y] & e & 0xFFFF0000u) == (e & 0xFFFF0000u);
+                        bad = bad || lo || hi;
+                        p[y] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
+                    }
+                    if (bad) {
+                        tile[x] = w;
+                        found = true;
+                    }
+                }
+                fence_proxy_async_smem();
+                named_sync(1, 64);
+                if (tid == 320 && ok) pair::arrive_remote_release(pair::map_to(bar(kKvFull + st), 0));
+            }
+            if (found) s_words[1] = 1;
         }
-        if (found) s_words[1] = 1;
-    } else if (warp < 8) {
+        if (!ok) gave_up();
+        __syncwarp();
+        pair::cluster_sync();
+    } else {
+        pair::more_registers<224>();
         // ---- softmax: warpgroup wg takes tiles wg, wg + 2, ...; a thread is a row
         const int wg = warp >> 2, row = tid & 127, wq = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
@@ -328,7 +345,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             const uint32_t s_at = lanes + Sh::COLS_S + wg * kTile;
             uint32_t r[128];
-            pair::tmem_load128(s_at, r);
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) pair::tmem_load32_start(s_at + c, r + c);
+            pair::tmem_load_wait(r);
             if (j * kTile + kTile - 1 > mine) {  // some row of this CTA sees only part of the tile
                 const int seen = token - j * kTile;  // columns 0 .. seen
 #pragma unroll
@@ -403,31 +422,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         s_l[wg * 128 + row] = l;
         if (wg >= n) s_m[wg * 128 + row] = -CUDART_INF_F;  // no tile was this warpgroup's
         ok = ok && mbar_wait_bounded(bar(kODone), 0, kWaitLimit);
-    }
-    if (!ok) {
-        // a wait gave up: leave the copies and MMAs in flight time to end before shared
-        // memory and TMEM go (they wait for nothing themselves)
-        atomicCAS(a.err, 0, (int32_t)GDR_ERR_DEVICE_TIMEOUT);
-        const long long t_end = clock64() + 4000000;
-        while (clock64() < t_end) {}
-    }
-    __syncwarp();
-    pair::cluster_sync();
-    tc_fence_after_sync();
+        if (!ok) gave_up();
+        __syncwarp();
+        pair::cluster_sync();
+        tc_fence_after_sync();
 
-    if (warp < 8) {
         // ---- o = O / l: warpgroup wg writes half of the columns
-        const int wg = warp >> 2, row = tid & 127, wq = warp & 3;
-        const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-        const int tok = row / a.group, token = mine + tok;
+        const int tok = token - mine;
         const bool live = tok < per_cta && token < len;
         const int64_t t = t0 + token;
         const int hq = h * a.group + row - tok * a.group;
         const float2 e0 = make_float2(s_m[row], s_l[row]), e1 = make_float2(s_m[128 + row], s_l[128 + row]);
         const float m = ((n - 1) & 1) ? e1.x : e0.x;
-        const float l = (e0.x == m ? e0.y : e0.y * fast_exp2(e0.x - m)) +
+        const float l_all = (e0.x == m ? e0.y : e0.y * fast_exp2(e0.x - m)) +
                         (e1.x == m ? e1.y : e1.y * fast_exp2(e1.x - m));
-        const float inv = 1.f / l;
+        const float inv = 1.f / l_all;
         const bool patch = s_words[1] | pair::load_remote(pair::map_to(smem_u32(s_words + 1), rank ^ 1u));
         const int c0 = wg * (D / 2);
         uint16_t *const dst = a.o.p + t * a.o.ts + (int64_t)hq * a.o.hs + c0;
@@ -458,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
-        if (wg == 0 && live && a.lse) a.lse[t * a.h_q + hq] = kLn2 * (m + log2f(l));
+        if (wg == 0 && live && a.lse) a.lse[t * a.h_q + hq] = kLn2 * (m + log2f(l_all));
         tc_fence_before_sync();
     }
     __syncwarp();
