@@ -64,7 +64,11 @@ struct Shape {
     static constexpr uint32_t OFF_WORDS = OFF_BAR + 64 * 8;       // TMEM address, patch flag, scan scratch
     static constexpr uint32_t BYTES = OFF_WORDS + 128;
     static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
-    static constexpr uint32_t COLS_S = 256;                // S tiles at columns 256 and 384, O at 0
+    // TMEM columns: O at 0, S tiles from here on.  With three of them (d <= 128) the
+    // MMAs of two more tiles' S run while a tile's P is made; at d = 256 two fit.
+    static constexpr int S_TILES = D == 256 ? 2 : 3;
+    static constexpr uint32_t COLS_S = 512 - S_TILES * kTile;
+    static constexpr int AHEAD = S_TILES - 1;              // tiles by which S runs ahead of P V
 };
 
 // barriers, as 8-byte words from OFF_BAR
@@ -72,10 +76,10 @@ enum Bar {
     kQFull = 0,
     kKvFull = 1,               // [stages], on the leading CTA
     kKvEmpty = kKvFull + 8,    // [stages]
-    kSFull = kKvEmpty + 8,     // [2]
-    kPFull = kSFull + 2,       // [2], on the leading CTA
-    kPvDone = kPFull + 2,
-    kODone = kPvDone + 1,      // the last P V
+    kSFull = kKvEmpty + 8,     // [S tiles]
+    kPFull = kSFull + 3,       // [S tiles], on the leading CTA
+    kPvDone = kPFull + 3,      // [2]: P V of even and odd tiles
+    kODone = kPvDone + 2,      // the last P V
     kVLocal = kODone + 1,      // [3]: value tiles to be looked through
     kMReady = kVLocal + 3,     // [2][4]: m of a warp's rows
     kBars = kMReady + 8,
@@ -172,12 +176,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(bar(kKvFull + i), 2);
             mbar_init(bar(kKvEmpty + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < Sh::S_TILES; ++i) {
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), 8);
-            for (int w = 0; w < 4; ++w) mbar_init(bar(kMReady + 4 * i + w), 1);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(bar(kMReady + i), 1);
         mbar_init(bar(kPvDone), 1);
+        mbar_init(bar(kPvDone + 1), 1);
         mbar_init(bar(kODone), 1);
         for (int i = 0; i < 3; ++i) mbar_init(bar(kVLocal + i), 1);
         s_words[1] = 0;
@@ -202,9 +207,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         while (clock64() < t_end) {}
     };
 
-    // Order of the ring: K0, K1, V0, K2, V1, ..., V of the last tile at the end.
-    auto k_index = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
-    auto v_index = [&](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
+    // Order of the ring: K0 .. K_AHEAD, V0, K_{AHEAD + 1}, V1, ..., the last values at the end.
+    constexpr int A = Sh::AHEAD;
+    auto k_index = [&](int j) { return j <= A ? j : 2 * j - A; };
+    auto v_index = [&](int j) { return j <= n - 1 - A ? A + 1 + 2 * j : n + j; };
 
     // the launch's 384 x 168 registers become 128 x 56 and 256 x 224
     if (warp >= 8) {
@@ -216,33 +222,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             pair::arrive_expect_remote(q_bar, q_bytes);
             for (int c = 0; c < D / 64; ++c)
                 pair::tma_load_3d_pair(base + c * Sh::Q_BLOCK, &maps.q, q_bar, c * 64, h * a.group, (int)t0 + mine);
-            for (int i = 0; i < 2 * n && ok; ++i) {
-                const int st = i % Sh::STAGES, use = i / Sh::STAGES;
-                if (use > 0) ok = mbar_wait_bounded(bar(kKvEmpty + st), (use - 1) & 1, kWaitLimit);
+            auto slot = [&](int i) {  // a free stage of the ring
+                const int use = i / Sh::STAGES;
+                if (use > 0) ok = ok && mbar_wait_bounded(bar(kKvEmpty + i % Sh::STAGES), (use - 1) & 1, kWaitLimit);
+                return base + Sh::OFF_RING + (i % Sh::STAGES) * Sh::STAGE;
+            };
+            auto load_k = [&](int j) {
+                const int i = k_index(j);
+                const uint32_t dst = slot(i);
+                if (!ok) return;
+                const uint32_t full = pair::map_to(bar(kKvFull + i % Sh::STAGES), 0);
+                pair::arrive_expect_remote(full, Sh::STAGE);
+                for (int c = 0; c < D / 64; ++c)
+                    pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, h,
+                                           (int)t0 + j * kTile + (int)rank * 64);
+            };
+            for (int j = 0; j <= A && j < n; ++j) load_k(j);
+            for (int j = 0; j < n && ok; ++j) {
+                if (j > 0 && j + A < n) load_k(j + A);
+                const int i = v_index(j);
+                const uint32_t dst = slot(i);
                 if (!ok) break;
-                const uint32_t dst = base + Sh::OFF_RING + st * Sh::STAGE;
-                const uint32_t full = pair::map_to(bar(kKvFull + st), 0);
-                const bool is_k = i == 0 || ((i & 1) && i != 2 * n - 1);
-                if (is_k) {
-                    const int j = i == 0 ? 0 : (i + 1) / 2;
-                    pair::arrive_expect_remote(full, Sh::STAGE);
-                    for (int c = 0; c < D / 64; ++c)
-                        pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, h,
-                                               (int)t0 + j * kTile + (int)rank * 64);
+                if (j >= j_clean) {  // looked through by warps 10 and 11, which then report the stage full
+                    const uint32_t b = bar(kVLocal + j - j_clean);
+                    mbar_arrive_expect_tx(b, Sh::STAGE);
+                    for (int c = 0; c < Sh::V_BOXES; ++c)
+                        tma_load_3d(dst + c * Sh::V_BOX, &maps.v, b, (int)rank * (D / 2) + c * Sh::VC, h,
+                                    (int)t0 + j * kTile);
                 } else {
-                    const int j = i == 2 * n - 1 ? n - 1 : i / 2 - 1;
-                    if (j >= j_clean) {  // looked through by warps 10 and 11, which then report the stage full
-                        const uint32_t b = bar(kVLocal + j - j_clean);
-                        mbar_arrive_expect_tx(b, Sh::STAGE);
-                        for (int c = 0; c < Sh::V_BOXES; ++c)
-                            tma_load_3d(dst + c * Sh::V_BOX, &maps.v, b, (int)rank * (D / 2) + c * Sh::VC, h,
-                                        (int)t0 + j * kTile);
-                    } else {
-                        pair::arrive_expect_remote(full, Sh::STAGE);
-                        for (int c = 0; c < Sh::V_BOXES; ++c)
-                            pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full, (int)rank * (D / 2) + c * Sh::VC,
-                                                   h, (int)t0 + j * kTile);
-                    }
+                    const uint32_t full = pair::map_to(bar(kKvFull + i % Sh::STAGES), 0);
+                    pair::arrive_expect_remote(full, Sh::STAGE);
+                    for (int c = 0; c < Sh::V_BOXES; ++c)
+                        pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full, (int)rank * (D / 2) + c * Sh::VC,
+                                               h, (int)t0 + j * kTile);
                 }
             }
         } else if (warp == 9 && lane == 0 && rank == 0) {
@@ -259,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!full(i)) return false;
                 tc_fence_after_sync();
                 const uint32_t kb = base + Sh::OFF_RING + st * Sh::STAGE;
-                const uint32_t d = tmem + Sh::COLS_S + (j & 1) * kTile;
+                const uint32_t d = tmem + Sh::COLS_S + (j % Sh::S_TILES) * kTile;
     #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t qa = smem_desc_sw128(base + (k >> 2) * Sh::Q_BLOCK + (k & 3) * 32, 0, 1024);
@@ -267,20 +279,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     pair::mma_ss(d, qa, kd, id_s, k > 0);
                 }
                 pair::commit_both(bar(kKvEmpty + st));
-                pair::commit_both(bar(kSFull + (j & 1)));
+                pair::commit_both(bar(kSFull + j % Sh::S_TILES));
                 return true;
             };
-            ok = ok && score(0);
+            for (int j = 0; j <= A && j < n; ++j) ok = ok && score(j);
             for (int j = 0; j < n && ok; ++j) {
-                if (j + 1 < n) ok = score(j + 1);
+                if (j > 0 && j + A < n) ok = score(j + A);  // over P of tile j - 1, whose P V is issued
                 const int i = v_index(j), st = i % Sh::STAGES;
                 ok = ok && (j < j_clean ? full(i)
                                         : pair::wait_cluster(bar(kKvFull + st), (i / Sh::STAGES) & 1, kWaitLimit));
-                ok = ok && mbar_wait_bounded(bar(kPFull + (j & 1)), (j >> 1) & 1, kWaitLimit);
+                ok = ok && mbar_wait_bounded(bar(kPFull + j % Sh::S_TILES), (j / Sh::S_TILES) & 1, kWaitLimit);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t vb = base + Sh::OFF_RING + st * Sh::STAGE;
-                const uint32_t p = tmem + Sh::COLS_S + (j & 1) * kTile;
+                const uint32_t p = tmem + Sh::COLS_S + (j % Sh::S_TILES) * kTile;
     #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k) {
                     const uint32_t at = vb + k * 16 * (Sh::VC * 2);
@@ -289,7 +301,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     pair::mma_ts(tmem, p + k * 8, vd, id_o, j > 0 || k > 0);
                 }
                 pair::commit_both(bar(kKvEmpty + st));
-                pair::commit_both(bar(kPvDone));
+                pair::commit_both(bar(kPvDone + (j & 1)));
             }
             if (ok) pair::commit_both(bar(kODone));
         } else if (warp >= 10) {
@@ -334,16 +346,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // a scale of 0 still has to leave a masked score at minus infinity
         const float sc = fmaxf(fabsf(a.scale), 1e-30f) * kLog2e;
         const int token = mine + row / a.group;  // in the sequence
-        const uint32_t p_bar = pair::map_to(bar(kPFull + wg), 0);
+        const uint32_t p_bars = pair::map_to(bar(kPFull), 0);
         float m_own = -CUDART_INF_F, l = 0.f;
         for (int j = wg; j < n && ok; j += 2) {
-            ok = mbar_wait_bounded(bar(kSFull + wg), (j >> 1) & 1, kWaitLimit);
+            const int st = j % Sh::S_TILES;
+            ok = mbar_wait_bounded(bar(kSFull + st), (j / Sh::S_TILES) & 1, kWaitLimit);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after_sync();
-            const uint32_t s_at = lanes + Sh::COLS_S + wg * kTile;
+            const uint32_t s_at = lanes + Sh::COLS_S + st * kTile;
             uint32_t r[128];
 #pragma unroll
             for (int c = 0; c < 128; c += 32) pair::tmem_load32_start(s_at + c, r + c);
@@ -354,14 +367,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 128; ++c)
                     if (c > seen) r[c] = 0xFF800000u;
             }
-            float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+            float top[4];
 #pragma unroll
-            for (int c = 0; c < 128; c += 8) {
+            for (int e = 0; e < 4; ++e) top[e] = __uint_as_float(r[e]);
+#pragma unroll
+            for (int c = 4; c < 124; c += 8) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    top[e] = fmaxf(top[e], fmaxf(__uint_as_float(r[c + e]), __uint_as_float(r[c + 4 + e])));
+                    top[e] = pair::max3(top[e], __uint_as_float(r[c + e]), __uint_as_float(r[c + 4 + e]));
             }
-            const float x_top = sc * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(r[124 + e]));
+            const float x_top = sc * fmaxf(pair::max3(top[0], top[1], top[2]), top[3]);
             // the reference after the tile before, from the other warpgroup
             float m_prev = -CUDART_INF_F;
             if (j > 0) {
@@ -379,8 +396,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(kMReady + 4 * wg + wq));
 
             if (j > 0 && __any_sync(0xffffffffu, raise)) {
-                // O so far is that of tiles 0 .. j - 1: P V of tile j waits for this warp's P
-                ok = mbar_wait_bounded(bar(kPvDone), (j - 1) & 1, kWaitLimit);
+                // O is that of tiles 0 .. j - 1 then: P V of tile j waits for this warp's P.  (S of
+                // tile j is complete, so P V of tile j - 3 is: this barrier's phase is unambiguous.)
+                ok = mbar_wait_bounded(bar(kPvDone + ((j - 1) & 1)), ((j - 1) >> 1) & 1, kWaitLimit);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -398,26 +416,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             l *= m_own == m ? 1.f : fast_exp2(m_own - m);
             m_own = m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint64_t sum[2] = {0, 0};
+            const uint64_t sc2 = pair::pack_f32x2(sc, sc), m2 = pair::pack_f32x2(-m, -m);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t p[32];
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const int i = half * 64 + 2 * c;
-                    const float x = fast_exp2(fmaf(__uint_as_float(r[i]), sc, -m));
-                    const float y = fast_exp2(fmaf(__uint_as_float(r[i + 1]), sc, -m));
-                    sum[c & 1] += x;
-                    sum[2 + (c & 1)] += y;
+                    float x, y;
+                    pair::unpack_f32x2(
+                        pair::fma_f32x2(pair::pack_f32x2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sc2, m2), x,
+                        y);
+                    x = fast_exp2(x);
+                    y = fast_exp2(y);
+                    sum[c & 1] = pair::add_f32x2(sum[c & 1], pair::pack_f32x2(x, y));
                     p[c] = pack2<F16>(x, y);
                 }
                 pair::tmem_store32(s_at + half * 32, p);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            {
+                float x, y;
+                pair::unpack_f32x2(pair::add_f32x2(sum[0], sum[1]), x, y);
+                l += x + y;
+            }
             pair::tmem_store_wait();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) pair::arrive_remote(p_bar);
+            if (lane == 0) pair::arrive_remote(p_bars + 8u * st);
         }
         s_l[wg * 128 + row] = l;
         if (wg >= n) s_m[wg * 128 + row] = -CUDART_INF_F;  // no tile was this warpgroup's
