@@ -104,7 +104,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t bars = base + Sh::OFF_BAR;
     uint32_t *const s_words = reinterpret_cast<uint32_t *>(smem + Sh::OFF_WORDS);
     // s_words: 0 TMEM address, 1 patch flag, then the search's scratch
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform for the compiler, too
     const uint32_t rank = pair::cta_rank();
     auto bar = [&](int i) { return bars + 8u * i; };
 
@@ -215,95 +216,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the launch's 384 x 168 registers become 128 x 56 and 256 x 224
     if (warp >= 8) {
         pair::fewer_registers<56>();
-        if (warp == 8 && lane == 0) {
+        if (warp == 8) {
             // ---- loads (both CTAs: own halves)
-            const uint32_t q_bar = pair::map_to(bar(kQFull), 0);
-            const uint32_t q_bytes = (uint32_t)(D / 64) * 128u * (uint32_t)(per_cta * a.group);
-            pair::arrive_expect_remote(q_bar, q_bytes);
-            for (int c = 0; c < D / 64; ++c)
-                pair::tma_load_3d_pair(base + c * Sh::Q_BLOCK, &maps.q, q_bar, c * 64, h * a.group, (int)t0 + mine);
-            auto slot = [&](int i) {  // a free stage of the ring
+            const bool issue = elect_one();
+            const uint32_t q_bar = pair::map_to(bar(kQFull), 0), full0 = pair::map_to(bar(kKvFull), 0);
+            if (issue) {
+                pair::arrive_expect_remote(q_bar, (uint32_t)(D / 64) * 128u * (uint32_t)(per_cta * a.group));
+                for (int c = 0; c < D / 64; ++c)
+                    pair::tma_load_3d_pair(base + c * Sh::Q_BLOCK, &maps.q, q_bar, c * 64, h * a.group,
+                                           (int)t0 + mine);
+            }
+            __syncwarp();
+            auto free_stage = [&](int i) {
                 const int use = i / Sh::STAGES;
-                if (use > 0) ok = ok && mbar_wait_bounded(bar(kKvEmpty + i % Sh::STAGES), (use - 1) & 1, kWaitLimit);
+                if (use > 0)
+                    ok = ok && mbar_wait_bounded(bar(kKvEmpty + i % Sh::STAGES), (use - 1) & 1, kWaitLimit);
+                ok = __all_sync(0xffffffffu, ok);
                 return base + Sh::OFF_RING + (i % Sh::STAGES) * Sh::STAGE;
             };
             auto load_k = [&](int j) {
                 const int i = k_index(j);
-                const uint32_t dst = slot(i);
-                if (!ok) return;
-                const uint32_t full = pair::map_to(bar(kKvFull + i % Sh::STAGES), 0);
-                pair::arrive_expect_remote(full, Sh::STAGE);
-                for (int c = 0; c < D / 64; ++c)
-                    pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, h,
-                                           (int)t0 + j * kTile + (int)rank * 64);
+                const uint32_t dst = free_stage(i);
+                if (ok && issue) {
+                    const uint32_t full = full0 + 8u * (i % Sh::STAGES);
+                    pair::arrive_expect_remote(full, Sh::STAGE);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, h,
+                                               (int)t0 + j * kTile + (int)rank * 64);
+                }
+                __syncwarp();
             };
             for (int j = 0; j <= A && j < n; ++j) load_k(j);
             for (int j = 0; j < n && ok; ++j) {
                 if (j > 0 && j + A < n) load_k(j + A);
                 const int i = v_index(j);
-                const uint32_t dst = slot(i);
-                if (!ok) break;
-                if (j >= j_clean) {  // looked through by warps 10 and 11, which then report the stage full
-                    const uint32_t b = bar(kVLocal + j - j_clean);
-                    mbar_arrive_expect_tx(b, Sh::STAGE);
-                    for (int c = 0; c < Sh::V_BOXES; ++c)
-                        tma_load_3d(dst + c * Sh::V_BOX, &maps.v, b, (int)rank * (D / 2) + c * Sh::VC, h,
-                                    (int)t0 + j * kTile);
-                } else {
-                    const uint32_t full = pair::map_to(bar(kKvFull + i % Sh::STAGES), 0);
-                    pair::arrive_expect_remote(full, Sh::STAGE);
-                    for (int c = 0; c < Sh::V_BOXES; ++c)
-                        pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full, (int)rank * (D / 2) + c * Sh::VC,
-                                               h, (int)t0 + j * kTile);
+                const uint32_t dst = free_stage(i);
+                if (ok && issue) {
+                    if (j >= j_clean) {  // looked through by warps 10 and 11, which then report the stage full
+                        const uint32_t b = bar(kVLocal + j - j_clean);
+                        mbar_arrive_expect_tx(b, Sh::STAGE);
+#pragma unroll
+                        for (int c = 0; c < Sh::V_BOXES; ++c)
+                            tma_load_3d(dst + c * Sh::V_BOX, &maps.v, b, (int)rank * (D / 2) + c * Sh::VC, h,
+                                        (int)t0 + j * kTile);
+                    } else {
+                        const uint32_t full = full0 + 8u * (i % Sh::STAGES);
+                        pair::arrive_expect_remote(full, Sh::STAGE);
+#pragma unroll
+                        for (int c = 0; c < Sh::V_BOXES; ++c)
+                            pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full,
+                                                   (int)rank * (D / 2) + c * Sh::VC, h, (int)t0 + j * kTile);
+                    }
                 }
+                __syncwarp();
             }
-        } else if (warp == 9 && lane == 0 && rank == 0) {
-            // ---- MMAs
+        } else if (warp == 9 && rank == 0) {
+            // ---- MMAs.  The whole warp walks the tiles and one elected lane issues, so that
+            // descriptors are made in uniform registers (one lane in a branch of its own took
+            // 1500 clocks a tile, more than the MMAs): a tile's are one base plus constants.
+            const bool issue = elect_one();
             const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // x = |sc| (-Q) K^T
             const uint32_t id_s = (F16 ? idesc_f16_f32(256, kTile, 0, 0) : idesc_bf16_f32(256, kTile, 0, 0)) | negate;
             const uint32_t id_o = F16 ? idesc_f16_f32(256, D, 0, 1) : idesc_bf16_f32(256, D, 0, 1);
-            ok = mbar_wait_bounded(bar(kQFull), 0, kWaitLimit);
+            const uint64_t q0 = smem_desc_sw128(base, 0, 1024);
+            const uint64_t k0 = smem_desc_sw128(base + Sh::OFF_RING, 0, 1024);
+            const uint64_t v0 = Sh::VC == 64 ? smem_desc(base + Sh::OFF_RING, Sh::V_BOX, 1024, kSwizzle128)
+                                             : smem_desc(base + Sh::OFF_RING, Sh::V_BOX, 512, kSwizzle64);
+            auto all_ok = [&](bool mine_ok) { return __all_sync(0xffffffffu, mine_ok) != 0; };
+            ok = all_ok(mbar_wait_bounded(bar(kQFull), 0, kWaitLimit));
             auto full = [&](int i) {
-                return mbar_wait_bounded(bar(kKvFull + i % Sh::STAGES), (i / Sh::STAGES) & 1, kWaitLimit);
+                return all_ok(mbar_wait_bounded(bar(kKvFull + i % Sh::STAGES), (i / Sh::STAGES) & 1, kWaitLimit));
             };
             auto score = [&](int j) {
-                const int i = k_index(j), st = i % Sh::STAGES;
+                const int i = k_index(j), st = i % Sh::STAGES, s_tile = j % Sh::S_TILES;
                 if (!full(i)) return false;
                 tc_fence_after_sync();
-                const uint32_t kb = base + Sh::OFF_RING + st * Sh::STAGE;
-                const uint32_t d = tmem + Sh::COLS_S + (j % Sh::S_TILES) * kTile;
-    #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t qa = smem_desc_sw128(base + (k >> 2) * Sh::Q_BLOCK + (k & 3) * 32, 0, 1024);
-                    const uint64_t kd = smem_desc_sw128(kb + (k >> 2) * Sh::K_BOX + (k & 3) * 32, 0, 1024);
-                    pair::mma_ss(d, qa, kd, id_s, k > 0);
+                const uint64_t kd = k0 + (uint64_t)(st * (Sh::STAGE >> 4));
+                const uint32_t d = tmem + Sh::COLS_S + s_tile * kTile;
+                if (issue) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        pair::mma_ss(d, q0 + (((k >> 2) * Sh::Q_BLOCK + (k & 3) * 32) >> 4),
+                                     kd + (((k >> 2) * Sh::K_BOX + (k & 3) * 32) >> 4), id_s, k > 0);
+                    pair::commit_both(bar(kKvEmpty + st));
+                    pair::commit_both(bar(kSFull + s_tile));
                 }
-                pair::commit_both(bar(kKvEmpty + st));
-                pair::commit_both(bar(kSFull + j % Sh::S_TILES));
+                __syncwarp();
                 return true;
             };
             for (int j = 0; j <= A && j < n; ++j) ok = ok && score(j);
             for (int j = 0; j < n && ok; ++j) {
                 if (j > 0 && j + A < n) ok = score(j + A);  // over P of tile j - 1, whose P V is issued
-                const int i = v_index(j), st = i % Sh::STAGES;
+                const int i = v_index(j), st = i % Sh::STAGES, s_tile = j % Sh::S_TILES;
                 ok = ok && (j < j_clean ? full(i)
-                                        : pair::wait_cluster(bar(kKvFull + st), (i / Sh::STAGES) & 1, kWaitLimit));
-                ok = ok && mbar_wait_bounded(bar(kPFull + j % Sh::S_TILES), (j / Sh::S_TILES) & 1, kWaitLimit);
+                                        : all_ok(pair::wait_cluster(bar(kKvFull + st), (i / Sh::STAGES) & 1, kWaitLimit)));
+                ok = ok && all_ok(mbar_wait_bounded(bar(kPFull + s_tile), (j / Sh::S_TILES) & 1, kWaitLimit));
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t vb = base + Sh::OFF_RING + st * Sh::STAGE;
-                const uint32_t p = tmem + Sh::COLS_S + (j % Sh::S_TILES) * kTile;
-    #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k) {
-                    const uint32_t at = vb + k * 16 * (Sh::VC * 2);
-                    const uint64_t vd = Sh::VC == 64 ? smem_desc(at, Sh::V_BOX, 1024, kSwizzle128)
-                                                     : smem_desc(at, Sh::V_BOX, 512, kSwizzle64);
-                    pair::mma_ts(tmem, p + k * 8, vd, id_o, j > 0 || k > 0);
+                const uint64_t vd = v0 + (uint64_t)(st * (Sh::STAGE >> 4));
+                const uint32_t p = tmem + Sh::COLS_S + s_tile * kTile;
+                if (issue) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        pair::mma_ts(tmem, p + k * 8, vd + ((k * 16 * (Sh::VC * 2)) >> 4), id_o, j > 0 || k > 0);
+                    pair::commit_both(bar(kKvEmpty + st));
+                    pair::commit_both(bar(kPvDone + (j & 1)));
                 }
-                pair::commit_both(bar(kKvEmpty + st));
-                pair::commit_both(bar(kPvDone + (j & 1)));
+                __syncwarp();
             }
-            if (ok) pair::commit_both(bar(kODone));
+            if (ok && issue) pair::commit_both(bar(kODone));
         } else if (warp >= 10) {
             // ---- value tiles that some row sees only in part (both CTAs: own halves)
             bool found = false;

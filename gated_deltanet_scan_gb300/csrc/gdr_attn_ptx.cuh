@@ -35,10 +35,10 @@ __device__ __forceinline__ uint32_t load_remote(uint32_t cluster_addr) {
 // what TMEM fences and the copies' own transaction counts order: a release at cluster
 // scope also waits for this thread's global writes, hundreds of cycles each time.
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 __device__ __forceinline__ void arrive_expect_remote(uint32_t cluster_bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
                  : "memory");
 }
 // With the release: after writes to shared memory that the other CTA's MMA reads.
