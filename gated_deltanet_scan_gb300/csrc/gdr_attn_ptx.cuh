@@ -26,10 +26,19 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
     return a;
 }
-__device__ __forceinline__ uint32_t load_remote(uint32_t cluster_addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
-    return v;
+__device__ __forceinline__ void store_remote(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+// Barrier among `count` threads of the CTA; true if `v` is true in any of them.
+__device__ __forceinline__ bool named_or(uint32_t id, uint32_t count, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(count), "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
 }
 // Arrivals on a barrier of either CTA (cluster address).  The plain forms order only
 // what TMEM fences and the copies' own transaction counts order: a release at cluster
