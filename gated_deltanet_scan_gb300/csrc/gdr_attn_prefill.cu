@@ -118,7 +118,8 @@ struct Cursor {
         // pairs take the blocks of a round in turn, back and forth: the sizes even out
         const int64_t number = (int64_t)item * pairs + ((item & 1) ? pairs - 1 - pair_id : pair_id);
         ++item;
-        const int64_t want = number / a.h_kv;
+        const int64_t want =
+            number >> 31 ? number / a.h_kv : (int64_t)((uint32_t)number / (uint32_t)a.h_kv);
         const int per_pair = 2 * tokens_per_cta(a.group);
         while (hi > 0) {
             const int s = hi - 1 - lane;
@@ -131,7 +132,7 @@ struct Cursor {
                     t0 = t1 = 0;
                 }
             }
-            const int n = (int)((t1 - t0 + per_pair - 1) / per_pair);
+            const int n = (int)((uint32_t)(t1 - t0 + per_pair - 1) / (uint32_t)per_pair);
             int x = n;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -304,7 +305,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t v0 = Sh::VC == 64 ? smem_desc(base + Sh::OFF_RING, Sh::V_BOX, 1024, kSwizzle128)
                                              : smem_desc(base + Sh::OFF_RING, Sh::V_BOX, 512, kSwizzle64);
             uint32_t i0 = 0, g0 = 0;  // stages and tiles before this block's
-            for (int it = 0; ok && cursor.next(a, pair_id, pairs, lane, b); ++it) {
+            Block ahead;
+            bool more = cursor.next(a, pair_id, pairs, lane, ahead);
+            for (int it = 0; ok && more; ++it) {
+                b = ahead;
                 auto score = [&](int j) {
                     const uint32_t i = i0 + k_index(j), st = i % Sh::STAGES, s_tile = (g0 + j) % Sh::S_TILES;
                     ok = all_ok(ok && mbar_wait_bounded(bar(kKvFull + st), (i / Sh::STAGES) & 1, kWaitLimit));
@@ -326,6 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = all_ok(mbar_wait_bounded(bar(kQFull), it & 1, kWaitLimit));
                 // the S tiles are free: the P V that read them are issued
                 for (int j = 0; j <= A && j < b.n; ++j) score(j);
+                more = cursor.next(a, pair_id, pairs, lane, ahead);  // while P of the first tile is made
                 if (it > 0) ok = all_ok(ok && mbar_wait_bounded(bar(kOFree), (it - 1) & 1, kWaitLimit));
                 for (int j = 0; j < b.n && ok; ++j) {
                     if (j > 0 && j + A < b.n) score(j + A);  // over P of tile j - 1, whose P V is issued
@@ -413,7 +418,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t p_bars = pair::map_to(bar(kPFull), 0), o_free = pair::map_to(bar(kOFree), 0);
         uint32_t g0 = 0;              // tiles before this block's
         uint32_t turn[2] = {0, 0};    // tiles of either warpgroup before this block's
-        for (int it = 0; cursor.next(a, pair_id, pairs, lane, b); ++it) {
+        Block ahead;
+        bool more = cursor.next(a, pair_id, pairs, lane, ahead);
+        for (int it = 0; more; ++it) {
+            b = ahead;
             const int n = b.n, mine = b.first + (int)rank * per_cta;
             const int token = mine + tok;  // in the sequence
             float m_own = -CUDART_INF_F, l = 0.f;
@@ -507,6 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) pair::arrive_remote(p_bars + 8u * st);
             }
+            more = cursor.next(a, pair_id, pairs, lane, ahead);  // while the last P V runs
             s_l[wg * 128 + row] = l;
             if (wg >= n) s_m[wg * 128 + row] = -CUDART_INF_F;  // no tile was this warpgroup's
             named_sync(3, 256);
