@@ -2,7 +2,7 @@
 //
 // Math.  For one key/value head the group's queries of the sequence's n_tok tokens
 // are rows r = j group + g of one small matrix Q (rows = n_tok group).  Over tiles
-// of 16 tokens, with x = scale log2(e) Q K^T and the running row maximum m,
+// of 16 or 32 tokens, with x = scale log2(e) Q K^T and the running row maximum m,
 //     p = 2^(x - m),   l += sum p,   O += P V,
 // earlier sums rescaled by 2^(m_old - m) when m grows; o = O / l at the end.  Two
 // parts of a row's tokens join the same way from their (m, l, O).
@@ -33,16 +33,20 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlocks = 152;  // one resident block per SM
-constexpr int kTile = 16;     // tokens per tile: the MMA's inner size in P V
 // P may exceed 1 by up to 2^kSlack before sums are rescaled: rounding is relative, so
 // P keeps its accuracy in either type, and most tiles rescale nothing.
 constexpr float kSlack = 6.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// Tokens per tile.  A worker of one warp takes 16 (the MMA's inner size in P V; its ring
+// is 24 KiB).  Several warps meet once per step, so they take twice as many.
+__host__ __device__ constexpr int tile_of(int rw) { return rw == 1 ? 16 : 32; }
+
 template <int D, int RW>
 struct Shape {
+    static constexpr int TILE = tile_of(RW);
     static constexpr int WORKERS = kWarps / RW;  // per block
-    static constexpr uint32_t SLOT = kTile * D * 2;
+    static constexpr uint32_t SLOT = TILE * D * 2;
     // about 24 KiB of ring per warp, at most 8 slots
     static constexpr int FIT = RW * 24576 / (int)SLOT;
     static constexpr int SLOTS = FIT < 8 ? FIT : 8;
@@ -53,7 +57,7 @@ struct Shape {
 int row_warps(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
 
 // On the line a triple takes its tiles and, before them, kLead<D> places for what
-// starting and ending it costs a worker (about 3 us, against 16 d 4 bytes a tile at a
+// starting and ending it costs a worker (about 3 us, against 4 d bytes a token at a
 // worker's share of the bandwidth): a batch of many short sequences is cut evenly too.
 template <int D>
 constexpr int kLead = 512 / D;
@@ -149,6 +153,8 @@ struct Cut {
 template <int D, bool F16, int RW>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Args a) {
     using Sh = Shape<D, RW>;
+    constexpr int kTile = Sh::TILE;
+    constexpr int TT = kTile / 8;  // 8-token column tiles of S
     constexpr int KS = D / 16;   // inner steps of Q K^T
     constexpr int NT = D / 8;    // output column tiles
     constexpr int CPR = D / 8;   // 16-byte chunks of a row
@@ -272,13 +278,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         const int32_t *const pages = a.cache.table + (int64_t)s * a.cache.table_stride;
         const int64_t head = h * a.cache.head_stride;
 
-        // Copies: lane & 15 is a token of the tile; its offset serves keys and values.
+        // Copies: lane % kTile is a token of the tile; its offset serves keys and values.
         int64_t off = 0;   // of the tile whose copies are being issued
         bool there = false;
         int page_next = 0, slot_next = 0;  // of the tile after it, its page id loaded a tile early
         bool has_next = false;
         auto look_up = [&](int tile) {
-            const int64_t p = (int64_t)tile * kTile + (lane & 15);
+            const int64_t p = (int64_t)tile * kTile + lane % kTile;
             has_next = tile < tile1 && p < len;
             if (has_next) {
                 const uint32_t pg = (uint32_t)p / (uint32_t)a.cache.page_size;
@@ -356,32 +362,46 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             cp_async_wait<Sh::SLOTS - 2>();
             worker_sync();
             issue(step + Sh::SLOTS - 1);
-            float x[2][2][4];  // [chain][token half]: two accumulation chains hide the MMA's latency
+            // S in TT column tiles; with two of them each is summed in two chains, which hides
+            // the MMA's latency as four column tiles do
+            constexpr int CH = TT == 2 ? 2 : 1;
+            float x[CH][TT][4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i >> 3][(i >> 2) & 1][i & 3] = 0.f;
+            for (int i = 0; i < CH * TT * 4; ++i) x[i / (TT * 4)][i / 4 % TT][i % 4] = 0.f;
             {
                 const uint32_t kb = slots + (step % Sh::SLOTS) * Sh::SLOT;
                 const int row = (lane & 7) + ((lane >> 4) << 3);
-                const uint32_t rbase = kb + row * (D * 2);
+                // chunk (2 k + b) ^ (row & 7), b = (lane >> 3) & 1: four lane offsets and constants
+                uint32_t at[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    at[i] = kb + row * (D * 2) + (((2 * i) ^ ((lane >> 3) & 1) ^ (row & 7)) << 4);
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    uint32_t b[4];
-                    ldsm4(rbase + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4), b);
-                    mma16816<F16>(x[k & 1][0], qf[k], b[0], b[1]);
-                    mma16816<F16>(x[k & 1][1], qf[k], b[2], b[3]);
+#pragma unroll
+                    for (int t = 0; t < TT; t += 2) {
+                        uint32_t b[4];
+                        ldsm4(at[k & 3] + t * 8 * D * 2 + (k >> 2) * 128, b);
+                        mma16816<F16>(x[k % CH][t], qf[k], b[0], b[1]);
+                        mma16816<F16>(x[k % CH][t + 1], qf[k], b[2], b[3]);
+                    }
                 }
             }
-            uint32_t pf[4];  // P as an MMA operand
+            uint32_t pf[TT / 2][4];  // P as MMA operands
             float c[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float v[4];
+                float v[2 * TT];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = sc * (x[0][e >> 1][2 * i + (e & 1)] + x[1][e >> 1][2 * i + (e & 1)]);
+                for (int e = 0; e < 2 * TT; ++e) {
+                    v[e] = x[0][e >> 1][2 * i + (e & 1)];
+                    if (CH == 2) v[e] += x[CH - 1][e >> 1][2 * i + (e & 1)];
+                    v[e] *= sc;
                     if (masked && p0 + (e >> 1) * 8 + cq * 2 + (e & 1) >= seen[i]) v[e] = -CUDART_INF_F;
                 }
-                float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+                float top = v[0];
+#pragma unroll
+                for (int e = 1; e < 2 * TT; ++e) top = fmaxf(top, v[e]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // the reference m follows the maximum only when that is kSlack above it
@@ -389,12 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 const float ref = mn == -CUDART_INF_F ? 0.f : mn;  // nothing visible yet: p = 2^-inf
                 c[i] = m[i] == mn ? 1.f : tc::fast_exp2(m[i] - ref);
                 m[i] = mn;
-                float p[4];
+                l[i] *= c[i];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = tc::fast_exp2(v[e] - ref);
-                l[i] = l[i] * c[i] + ((p[0] + p[1]) + (p[2] + p[3]));
-                pf[i] = pack2<F16>(p[0], p[1]);
-                pf[2 + i] = pack2<F16>(p[2], p[3]);
+                for (int e = 0; e < TT; ++e) {
+                    const float p = tc::fast_exp2(v[2 * e] - ref), q = tc::fast_exp2(v[2 * e + 1] - ref);
+                    l[i] += p + q;
+                    pf[e >> 1][(e & 1) * 2 + i] = pack2<F16>(p, q);
+                }
             }
             if (__any_sync(0xffffffffu, c[0] != 1.f || c[1] != 1.f)) {
 #pragma unroll
@@ -461,13 +482,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             }
             {
                 const int row = lane & 15;
-                const uint32_t rbase = vb + row * (D * 2);
+                uint32_t at[4];  // as for the keys: chunk (n + (lane >> 4)) ^ (row & 7)
 #pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t b[4];
-                    ldsm4t(rbase + (((n + (lane >> 4)) ^ (row & 7)) << 4), b);
-                    mma16816<F16>(acc[n], pf, b[0], b[1]);
-                    mma16816<F16>(acc[n + 1], pf, b[2], b[3]);
+                for (int i = 0; i < 4; ++i)
+                    at[i] = vb + row * (D * 2) + (((2 * i) ^ (lane >> 4) ^ (row & 7)) << 4);
+#pragma unroll
+                for (int t = 0; t < TT / 2; ++t) {
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t b[4];
+                        ldsm4t(at[(n >> 1) & 3] + t * 16 * D * 2 + (n >> 3) * 128, b);
+                        mma16816<F16>(acc[n], pf[t], b[0], b[1]);
+                        mma16816<F16>(acc[n + 1], pf[t], b[2], b[3]);
+                    }
                 }
             }
         }
@@ -542,7 +569,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         }
         return;
     }
-    const int64_t tiles = (len + kTile - 1) / kTile;
+    const int tile = tile_of(rw);
+    const int64_t tiles = (len + tile - 1) / tile;
     const int64_t *const line = reinterpret_cast<const int64_t *>(a.ws);
     const int64_t seg0 = line[s] + ((int64_t)h * L.blocks_of_rows + rb) * (tiles + kLead<D>);
     const Cut cut(line[a.n_seqs], L.workers);
