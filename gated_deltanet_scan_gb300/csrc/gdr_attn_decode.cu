@@ -17,8 +17,9 @@
 // Both products are warp-level m16n8k16 MMAs on the 16-bit rows with fp32 sums: at 4
 // flops a byte the tensor pipes are far from busy, so the extra rows they pad cost
 // nothing.  A sequence that one worker sees whole is written by it; the others leave
-// (m, l, O) in the workspace, and a second kernel joins them in the order of the
-// tokens.  That launch is a programmatic dependent of the first.
+// (m, l, O): the workers of a block, next to each other on the line, join what they can
+// among themselves, and a second kernel, a programmatic dependent launch, joins the
+// blocks' parts from the workspace; always in the order of the tokens.
 //
 // P is rounded to the tensors' type for P V (its sum l is not): that is the only
 // rounding between the inputs and the output's own.
@@ -46,11 +47,14 @@ template <int D, int RW>
 struct Shape {
     static constexpr int TILE = tile_of(RW);
     static constexpr int WORKERS = kWarps / RW;  // per block
+    // with two workers, joining their parts here costs more than the join kernel saves
+    static constexpr bool MERGE = WORKERS > 2;
     static constexpr uint32_t SLOT = TILE * D * 2;
     // about 24 KiB of ring per warp, at most 8 slots
     static constexpr int FIT = RW * 24576 / (int)SLOT;
     static constexpr int SLOTS = FIT < 8 ? FIT : 8;
     static constexpr uint32_t SMEM = WORKERS * SLOTS * SLOT;
+    static_assert(SLOTS * SLOT >= RW * 16 * D * 4, "a ring holds its worker's part");
 };
 
 // Row warps for this many rows of a key/value head.
@@ -136,10 +140,12 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // a, b >= 
     return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 struct Cut {
-    int64_t total, each, rest;
-    int parts;
-    __device__ __forceinline__ Cut(int64_t total_, int workers) : total(total_) {
-        parts = total < workers ? (int)total : workers;
+    int64_t each, rest;
+    int parts, per_block;  // workers in use, and of each block: few places spread over many blocks
+    __device__ __forceinline__ Cut(int64_t total, int workers_per_block) {
+        per_block = total >= (int64_t)kBlocks * workers_per_block ? workers_per_block
+                                                                  : max(1, (int)((uint32_t)total / kBlocks));
+        parts = total < kBlocks * per_block ? (int)total : kBlocks * per_block;
         each = parts > 0 ? quotient(total, parts) : 0;
         rest = total - each * parts;
     }
@@ -164,14 +170,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     __shared__ int64_t s_warp[kWarps];
     __shared__ int s_seq[Sh::WORKERS];
     __shared__ int64_t s_base[Sh::WORKERS];
+    __shared__ int64_t s_cut[Sh::WORKERS];    // the triple a worker's part ends in, or -1
+    __shared__ float2 s_ml[kWarps * 16];      // m and l of its rows
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wk = warp / RW, rw = warp % RW;  // worker in the block, row warp in the worker
     const int rows = a.n_tok * a.group;
     const Layout L = layout(rows, RW, D, a.n_seqs);
-    // workers next to each other on the line sit on different SMs, so few tiles spread over many
-    const int me = wk * kBlocks + blockIdx.x;
     int64_t *const line = reinterpret_cast<int64_t *>(a.ws);
     const int64_t per_seq = (int64_t)a.h_kv * L.blocks_of_rows;
 
@@ -213,9 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             if (pass == 1) {
                 const int s0 = c * kThreads, m = min(kThreads, a.n_seqs - s0);
                 if (tid < Sh::WORKERS) {  // the last sequence that starts at or before the worker's part
-                    const Cut cut(total, L.workers);
-                    const int64_t at = cut.start(min(tid * kBlocks + (int)blockIdx.x, cut.parts));
-                    if (s_seq[tid] < 0 && at < base) {
+                    const Cut cut(total, Sh::WORKERS);
+                    const int64_t at = cut.start(min((int)blockIdx.x * cut.per_block + tid, cut.parts));
+                    if (tid < cut.per_block && s_seq[tid] < 0 && at < base) {
                         int lo = 0, hi = m - 1;
                         while (lo < hi) {
                             const int mid = (lo + hi + 1) >> 1;
@@ -238,10 +244,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
     __syncthreads();
 
-    const Cut cut(total, L.workers);
-    if (me >= cut.parts) return;  // a whole worker; workers meet at no barrier from here on
-    int64_t at = cut.start(me);
-    const int64_t end = cut.start(me + 1);
+    const Cut cut(total, Sh::WORKERS);
+    const int me = blockIdx.x * cut.per_block + wk;  // a block's workers are next to each other on the line
+    int64_t at = cut.start(min(me, cut.parts));      // beyond the parts: nothing to do
+    const int64_t end = wk < cut.per_block ? cut.start(min(me + 1, cut.parts)) : at;
+    if (lane == 0 && rw == 0) s_cut[wk] = -1;
     int s = s_seq[wk];
     int64_t base = s_base[wk];
 
@@ -252,6 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         else
             tc::named_sync(1 + wk, 32 * RW);
     };
+    float2 *const ml_parts = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + L.ml);
+    float *const o_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + L.o);
     const float sc = a.scale * kLog2e;
     const int r0 = lane >> 2, cq = lane & 3;  // the MMA's row (and row + 8) and column pair of this lane
 
@@ -521,19 +530,55 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     a.lse[out_row[i]] = seen[i] > 0 ? kLn2 * (m[i] + log2f(l[i])) : -CUDART_INF_F;
             }
         } else {
+            // the part goes to the workspace, or, where the triple goes on in the next worker, to
+            // the ring, which this worker has no more use for
+            const bool goes_on = Sh::MERGE && tile1 < tiles;
             const int64_t part = ((int64_t)me * 2 + slot_of_part) * L.part_rows;
-            float2 *const ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + L.ml);
-            float *const po = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + L.o);
+            float2 *const ml = goes_on ? s_ml + (warp - rw) * 16 : ml_parts + part;
+            float *const po = goes_on ? reinterpret_cast<float *>(ring + wk * Sh::SLOTS * Sh::SLOT) : o_parts + part * D;
+            if (goes_on && lane == 0 && rw == 0) s_cut[wk] = seg0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (out_row[i] < 0) continue;
-                const int64_t r = part + rw * 16 + r0 + 8 * i;
+                const int r = rw * 16 + r0 + 8 * i;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     *reinterpret_cast<float2 *>(po + r * D + n * 8 + cq * 2) =
                         make_float2(acc[n][2 * i], acc[n][2 * i + 1]);
                 if (cq == 0) ml[r] = make_float2(m[i], l[i]);
             }
+        }
+    }
+
+    // Parts of one triple that end with their workers are joined here, in the order of the
+    // tokens, into the first of these workers' part.
+    if constexpr (!Sh::MERGE) return;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < Sh::WORKERS; ++w) {
+        const int64_t seg0 = s_cut[w];
+        if (seg0 < 0 || (w > 0 && s_cut[w - 1] == seg0)) continue;
+        int last = w;
+        while (last + 1 < Sh::WORKERS && s_cut[last + 1] == seg0) ++last;
+        const int worker = blockIdx.x * cut.per_block + w;
+        const int64_t part = ((int64_t)worker * 2 + (cut.start(worker) >= seg0 ? 0 : 1)) * L.part_rows;
+        for (int x = tid; x < L.part_rows * (D / 2); x += kThreads) {
+            const int r = x / (D / 2), c = x % (D / 2);
+            float top = -CUDART_INF_F;
+            for (int i = w; i <= last; ++i) top = fmaxf(top, s_ml[i * RW * 16 + r].x);
+            const float ref = top == -CUDART_INF_F ? 0.f : top;
+            float2 o = make_float2(0.f, 0.f);
+            float l = 0.f;
+            for (int i = w; i <= last; ++i) {
+                const float2 v = s_ml[i * RW * 16 + r];
+                const float f = tc::fast_exp2(v.x - ref);
+                const float2 y = reinterpret_cast<const float2 *>(ring + i * Sh::SLOTS * Sh::SLOT)[r * (D / 2) + c];
+                l += f * v.y;
+                o.x += f * y.x;
+                o.y += f * y.y;
+            }
+            reinterpret_cast<float2 *>(o_parts)[(part + r) * (D / 2) + c] = o;
+            if (c == 0) ml_parts[part + r] = make_float2(top, l);
         }
     }
 }
@@ -573,7 +618,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     const int64_t tiles = (len + tile - 1) / tile;
     const int64_t *const line = reinterpret_cast<const int64_t *>(a.ws);
     const int64_t seg0 = line[s] + ((int64_t)h * L.blocks_of_rows + rb) * (tiles + kLead<D>);
-    const Cut cut(line[a.n_seqs], L.workers);
+    const Cut cut(line[a.n_seqs], 8 / rw);
     const int w0 = cut.part_of(seg0 + kLead<D>), w1 = cut.part_of(seg0 + kLead<D> + tiles - 1);
     if (w0 == w1) return;
 
@@ -581,26 +626,33 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     const float2 *const po = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.o);
     // a worker's part is its first where its own start is not before the triple's: so
     // all parts but perhaps the first one's
+    // all but the last worker's part are joined within their blocks (where these do): the parts
+    // are those of the first such worker of every block, and the last worker's
+    const int per_block = 8 / rw > 2 ? cut.per_block : 1, b0 = w0 / per_block;
+    const int n_parts = (w1 - 1) / per_block - b0 + 2;
     const int64_t row0 = cut.start(w0) >= seg0 ? 0 : L.part_rows;
-    auto part_row = [&](int wk) { return (int64_t)wk * 2 * L.part_rows + (wk == w0 ? row0 : 0) + lr; };
+    auto part_row = [&](int i) {
+        const int wk = i == 0 ? w0 : i == n_parts - 1 ? w1 : (b0 + i) * per_block;
+        return (int64_t)wk * 2 * L.part_rows + (i == 0 ? row0 : 0) + lr;
+    };
     float2 acc[V / 2];
     float m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) acc[e] = make_float2(0.f, 0.f);
-    constexpr int U = WPR > 1 ? 16 : 4;  // parts in flight
+    constexpr int U = 4;  // parts in flight
 #pragma unroll 1
-    for (int i = w0 + w; i <= w1; i += WPR * U) {
+    for (int i = w; i < n_parts; i += WPR * U) {
         float2 x[U][V / 2], v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t pr = part_row(min(i + u * WPR, w1));
+            const int64_t pr = part_row(min(i + u * WPR, n_parts - 1));
             v[u] = __ldcg(ml + pr);
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) x[u][e] = __ldcg(po + pr * (D / 2) + word0 + 32 * e);
         }
         float top = m;
 #pragma unroll
-        for (int u = 0; u < U; ++u) top = fmaxf(top, i + u * WPR <= w1 ? v[u].x : top);
+        for (int u = 0; u < U; ++u) top = fmaxf(top, i + u * WPR < n_parts ? v[u].x : top);
         const float ref = top == -CUDART_INF_F ? 0.f : top;
         const float c0 = m == top ? 1.f : tc::fast_exp2(m - ref);
         m = top;
@@ -612,7 +664,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i + u * WPR > w1) break;
+            if (i + u * WPR >= n_parts) break;
             const float c = tc::fast_exp2(v[u].x - ref);
             l += c * v[u].y;
 #pragma unroll
@@ -660,7 +712,8 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     // triples for the workers), else a warp per row.
     const int64_t rows = a.t_total * a.h_q;
     const Layout L = layout(a.n_tok * a.group, RW, D, a.n_seqs);
-    const bool wide = L.workers >= (int64_t)16 * a.n_seqs * a.h_kv * L.blocks_of_rows;
+    const int64_t parts = Sh::MERGE ? kBlocks : L.workers;
+    const bool wide = parts >= (int64_t)16 * a.n_seqs * a.h_kv * L.blocks_of_rows;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
