@@ -4,20 +4,20 @@
 // Math.  A token at position p turns pair i of every query and key head by the
 // angle a = p f_i:  (x, y) -> (x cos a - y sin a, x sin a + y cos a).  The angle is
 // reduced in 64-bit fixed point: f_i / 2 pi modulo one turn is held as a fraction
-// of 2^64 (off by at most 2^-53 of a turn), p times it wraps around exactly, and
-// the top 32 bits of the product are the signed fraction of a turn that cos and
-// sin take.  At p = 2^24 the angle is still good to 2^-29 turns; a 32-bit float
-// product would be off by whole radians.
+// of 2^64 (from the float's bits and the 64 leading bits of 1 / 2 pi: off by 2^-62 of
+// itself), p times it wraps around exactly, and the top 32 bits of the product are
+// the signed fraction of a turn that cos and sin take.  At p = 2^24 the angle is still
+// good to 2^-32 turns; a 32-bit float product would be off by whole radians.
 //
 // Bound by HBM for prompts (every row read once, every output written once) and by
 // latency for a few tokens.  One 16-byte vector (8 values) per lane, d / 8 lanes a
 // row: a lane keeps the same 8 values of every row it handles, so cos and sin are
-// computed once per token and lane and serve all of the token's heads; 64-bit
-// products are integer multiplies, the fp64 pipe is used once per lane.  A pair's
-// other half is in the same vector (interleaved), in another lane of the row
-// (halves a multiple of 8 apart: shuffles) or read again by value (other halves).
-// A row is read whole by its warp before any of it is written, so outputs may be
-// the inputs.
+// computed once per token and lane and serve all of the token's heads.  A step's
+// vectors are loaded a step ahead, the first ones before the token's position is
+// known.  A pair's other half is in the same vector (interleaved), in another lane of
+// the row (halves a multiple of 8 apart: shuffles) or read again by value (other
+// halves).  A row is read whole by its warp before any of it is written, so outputs
+// may be the inputs.
 #include "gdr_attn_common.cuh"
 #include "gdr_internal.h"
 
@@ -35,6 +35,19 @@ struct Split {
 
 enum Pairing { kNone = 0, kInterleaved = 1, kShuffle = 2, kByValue = 3 };
 
+// f / 2 pi modulo 1, as a fraction of 2^64: f = +-M 2^E exactly, and M times the 64
+// leading bits of 1 / 2 pi is an integer of 88 bits.
+__device__ __forceinline__ uint64_t turn_of(float f) {
+    constexpr uint64_t kInvTwoPi = 0x28BE60DB9391054Aull;  // floor(2^64 / (2 pi))
+    const uint32_t u = __float_as_uint(f);
+    const int e = (u >> 23) & 0xFF;
+    const uint64_t m = (u & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+    const int down = 150 - (e ? e : 1);  // -E: at least 7 below 2^20
+    const uint64_t lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+    const uint64_t t = down <= 0 ? lo : down < 64 ? (lo >> down) | (hi << (64 - down)) : down < 128 ? hi >> (down - 64) : 0;
+    return u >> 31 ? 0 - t : t;
+}
+
 template <int D, bool F16, int PAIR>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Args a, const Split sp) {
     constexpr int LPR = D / 8;    // lanes per row
@@ -50,44 +63,52 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int e0 = vec * 8;
     const int half = a.rot / 2;
 
-    // fractions of a turn per position, the rotation's signs and reach of this lane's 8 values
-    uint64_t turn[8];
-    if constexpr (PAIR != kNone) {
+    const int n_q = a.q.p ? a.h_q : 0;
+    const int rows = n_q + 2 * a.h_kv;
+    const int stride = sp.parts * RPW;  // between a lane's rows
+    uint4 next[kUnroll];                // vectors of the step to come
+    auto row_of = [&](int64_t t, int r) -> const uint16_t * {
+        r = min(r, rows - 1);
+        return r < n_q ? a.q.p + t * a.q.ts + r * a.q.hs
+               : r < n_q + a.h_kv ? a.k.p + t * a.k.ts + (r - n_q) * a.k.hs
+                                  : a.v.p + t * a.v.ts + (r - n_q - a.h_kv) * a.v.hs;
+    };
+    auto load = [&](int64_t t, int r0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int x = e0 + e;
-            turn[e] = 0;
-            if (x < a.rot) {
-                const int i = PAIR == kInterleaved ? x >> 1 : (x < half ? x : x - half);
-                const double t = (double)a.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-                const double f = t - floor(t);
-                // f may round up to 1 for tiny negative t: that is 0 turns
-                turn[e] = f < 1.0 ? (uint64_t)(f * 18446744073709551616.0) : 0;
-            }
+        for (int u = 0; u < kUnroll; ++u)
+            next[u] = *reinterpret_cast<const uint4 *>(row_of(t, r0 + u * stride + sub) + e0);
+    };
+    load(first, part * RPW);
+
+    // fractions of a turn per position of this lane's 8 values
+    uint64_t turn[PAIR == kInterleaved ? 4 : 8];
+    if constexpr (PAIR != kNone) {
+        constexpr int N = PAIR == kInterleaved ? 4 : 8;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int x = PAIR == kInterleaved ? e0 / 2 + e : e0 + e;  // pair, or value
+            const int i = PAIR == kInterleaved ? x : (x < half ? x : x - half);
+            turn[e] = i < half ? turn_of(a.inv_freq[i]) : 0;
         }
     }
 
-    const int n_q = a.q.p ? a.h_q : 0;
-    const int rows = n_q + 2 * a.h_kv;
     const int even = (int)(a.t_total / a.n_seqs);  // tokens per sequence without cu
-    int s = a.cu ? find_seq(a.cu, a.n_seqs, first) : (int)(first / even);
+    int s = a.cu ? find_seq_warp(a.cu, a.n_seqs, first, lane) : (int)(first / even);
 
     for (int64_t t = first; t < last; ++t) {
         int64_t t0, t1;
+        bool known = true;
         if (a.cu) {
             while (s + 1 < a.n_seqs && a.cu[s + 1] <= t) ++s;
             t0 = a.cu[s];
             t1 = a.cu[s + 1];
-            if (t0 < 0 || t < t0 || t1 <= t || t1 > a.t_total) {
-                record_invalid(a.err);
-                continue;
-            }
+            known = t0 >= 0 && t0 <= t && t < t1 && t1 <= a.t_total;
         } else {
             while (t >= (int64_t)(s + 1) * even) ++s;
             t0 = (int64_t)s * even;
             t1 = t0 + even;
         }
-        const int64_t pos = (int64_t)a.kv_lens[s] - (t1 - t);
+        const int64_t pos = known ? (int64_t)a.kv_lens[s] - (t1 - t) : -1;
         int64_t slot = -1;  // offset of the token's slot in the cache, in elements
         if (pos >= 0 && pos < (int64_t)a.cache.max_pages * a.cache.page_size) {
             const int pg = (int)pos / a.cache.page_size;
@@ -102,32 +123,29 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         if constexpr (PAIR != kNone) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int x = e0 + e;
                 if (PAIR == kInterleaved && (e & 1)) {
                     cs[e] = cs[e - 1];
                     sn[e] = -sn[e - 1];
                 } else {
-                    const int32_t w = (int32_t)(((uint64_t)pos * turn[e]) >> 32);
+                    const int32_t w =
+                        (int32_t)(((uint64_t)pos * turn[PAIR == kInterleaved ? e / 2 : e]) >> 32);
                     sincospif((float)w * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31 half turns
-                    if (PAIR == kInterleaved || x < half) sn[e] = -sn[e];
+                    if (PAIR == kInterleaved || e0 + e < half) sn[e] = -sn[e];
                 }
             }
         }
 
-        for (int r0 = part * RPW; r0 < rows; r0 += sp.parts * RPW * kUnroll) {
+        for (int r0 = part * RPW; r0 < rows; r0 += stride * kUnroll) {
             uint4 w[kUnroll];
-            const uint16_t *src[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) w[u] = next[u];
+            if (r0 + stride * kUnroll < rows)
+                load(t, r0 + stride * kUnroll);
+            else if (t + 1 < last)
+                load(t + 1, part * RPW);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int r = min(r0 + u * sp.parts * RPW + sub, rows - 1);
-                src[u] = r < n_q ? a.q.p + t * a.q.ts + r * a.q.hs
-                         : r < n_q + a.h_kv ? a.k.p + t * a.k.ts + (r - n_q) * a.k.hs
-                                            : a.v.p + t * a.v.ts + (r - n_q - a.h_kv) * a.v.hs;
-                w[u] = *reinterpret_cast<const uint4 *>(src[u] + e0);
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int r = r0 + u * sp.parts * RPW + sub;
+                const int r = r0 + u * stride + sub;
                 if constexpr (PAIR != kNone) {
                     const uint32_t own[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
                     uint32_t oth[4];  // the pairs' other values
@@ -140,15 +158,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < 4; ++i) oth[i] = __shfl_sync(0xffffffffu, own[i], from & 31);
                     } else {
-                        const int ru = min(r, rows - 1);
+                        const uint16_t *const src = row_of(t, r);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t o2 = 0;
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const int x = e0 + 2 * i + j;
-                                if (x < a.rot && ru < n_q + a.h_kv)
-                                    o2 |= (uint32_t)src[u][x < half ? x + half : x - half] << (16 * j);
+                                if (x < a.rot && r < n_q + a.h_kv)
+                                    o2 |= (uint32_t)src[x < half ? x + half : x - half] << (16 * j);
                             }
                             oth[i] = o2;
                         }
@@ -171,9 +189,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                 }
             }
             if constexpr (PAIR == kByValue) __syncwarp();  // every value read before any is written
+            if (!known) continue;
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int r = r0 + u * sp.parts * RPW + sub;
+                const int r = r0 + u * stride + sub;
                 if (r >= rows) continue;
                 if (r < n_q) {
                     *reinterpret_cast<uint4 *>(a.q_out.p + t * a.q_out.ts + r * a.q_out.hs + e0) = w[u];

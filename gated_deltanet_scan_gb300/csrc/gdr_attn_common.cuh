@@ -41,15 +41,17 @@ __device__ __forceinline__ float unpack1(uint16_t w) {
         return __uint_as_float((uint32_t)w << 16);
 }
 
-// Sequence of token t among packed starts cu[0 .. n]: the last s with cu[s] <= t.
-__device__ __forceinline__ int find_seq(const int32_t *cu, int n, int64_t t) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] <= t)
-            lo = mid;
-        else
-            hi = mid - 1;
+// Sequence of token t among packed starts cu[0 .. n]: the last s < n with cu[s] <= t (or
+// 0).  The whole warp looks, 32 places at a time: two rounds of loads for a thousand.
+__device__ __forceinline__ int find_seq_warp(const int32_t *cu, int n, int64_t t, int lane) {
+    int lo = 0, hi = n;  // the answer is in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const uint32_t below = __ballot_sync(0xffffffffu, at < hi && cu[at] <= t);
+        const int k = below ? 31 - __clz(below) : 0;
+        lo += k * step;
+        hi = min(hi, lo + step);
     }
     return lo;
 }
