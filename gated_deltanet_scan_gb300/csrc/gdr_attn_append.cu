@@ -33,7 +33,11 @@ struct Split {
     int parts;   // warps that share a token's rows
 };
 
-enum Pairing { kNone = 0, kInterleaved = 1, kShuffle = 2, kByValue = 3 };
+// kInterleaved and kShuffle: a lane's 8 values are all rotated or all copied.  kRagged:
+// interleaved, the rotated part ends inside a vector.
+enum Pairing { kNone, kInterleaved, kRagged, kShuffle, kByValue };
+
+__host__ __device__ constexpr int blocks_per_sm(int pairing) { return pairing == kRagged || pairing == kByValue ? 3 : 5; }
 
 // f / 2 pi modulo 1, as a fraction of 2^64: f = +-M 2^E exactly, and M times the 64
 // leading bits of 1 / 2 pi is an integer of 88 bits.
@@ -49,7 +53,10 @@ __device__ __forceinline__ uint64_t turn_of(float f) {
 }
 
 template <int D, bool F16, int PAIR>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Args a, const Split sp) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
+    append_kernel(const __grid_constant__ Args a, const Split sp) {
+    constexpr bool kPaired = PAIR == kInterleaved || PAIR == kRagged;
+    constexpr bool kWhole = PAIR == kInterleaved || PAIR == kShuffle;
     constexpr int LPR = D / 8;    // lanes per row
     constexpr int RPW = 32 / LPR;  // rows per warp and step
     const int lane = threadIdx.x & 31;
@@ -69,9 +76,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     uint4 next[kUnroll];                // vectors of the step to come
     auto row_of = [&](int64_t t, int r) -> const uint16_t * {
         r = min(r, rows - 1);
-        return r < n_q ? a.q.p + t * a.q.ts + r * a.q.hs
-               : r < n_q + a.h_kv ? a.k.p + t * a.k.ts + (r - n_q) * a.k.hs
-                                  : a.v.p + t * a.v.ts + (r - n_q - a.h_kv) * a.v.hs;
+        const Rows &x = r < n_q ? a.q : r < n_q + a.h_kv ? a.k : a.v;
+        const int h = r < n_q ? r : r < n_q + a.h_kv ? r - n_q : r - n_q - a.h_kv;
+        return x.p + t * x.ts + h * x.hs;
     };
     auto load = [&](int64_t t, int r0) {
 #pragma unroll
@@ -81,13 +88,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     load(first, part * RPW);
 
     // fractions of a turn per position of this lane's 8 values
-    uint64_t turn[PAIR == kInterleaved ? 4 : 8];
+    uint64_t turn[kPaired ? 4 : 8];
     if constexpr (PAIR != kNone) {
-        constexpr int N = PAIR == kInterleaved ? 4 : 8;
+        constexpr int N = kPaired ? 4 : 8;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            const int x = PAIR == kInterleaved ? e0 / 2 + e : e0 + e;  // pair, or value
-            const int i = PAIR == kInterleaved ? x : (x < half ? x : x - half);
+            const int x = kPaired ? e0 / 2 + e : e0 + e;  // pair, or value
+            const int i = kPaired ? x : (x < half ? x : x - half);
             turn[e] = i < half ? turn_of(a.inv_freq[i]) : 0;
         }
     }
@@ -123,14 +130,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         if constexpr (PAIR != kNone) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (PAIR == kInterleaved && (e & 1)) {
+                if (kPaired && (e & 1)) {
                     cs[e] = cs[e - 1];
                     sn[e] = -sn[e - 1];
                 } else {
                     const int32_t w =
-                        (int32_t)(((uint64_t)pos * turn[PAIR == kInterleaved ? e / 2 : e]) >> 32);
+                        (int32_t)(((uint64_t)pos * turn[kPaired ? e / 2 : e]) >> 32);
                     sincospif((float)w * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31 half turns
-                    if (PAIR == kInterleaved || e0 + e < half) sn[e] = -sn[e];
+                    if (kPaired || e0 + e < half) sn[e] = -sn[e];
                 }
             }
         }
@@ -149,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                 if constexpr (PAIR != kNone) {
                     const uint32_t own[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
                     uint32_t oth[4];  // the pairs' other values
-                    if constexpr (PAIR == kInterleaved) {
+                    if constexpr (kPaired) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) oth[i] = __byte_perm(own[i], 0, 0x1032);
                     } else if constexpr (PAIR == kShuffle) {
@@ -178,11 +185,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                             const float2 x = unpack2<F16>(own[i]), y = unpack2<F16>(oth[i]);
                             const float lo = x.x * cs[2 * i] + y.x * sn[2 * i];
                             const float hi = x.y * cs[2 * i + 1] + y.y * sn[2 * i + 1];
-                            const uint32_t m = pack2<F16>(lo, hi);
-                            // values past the rotated part are copied bit for bit
-                            const int e = e0 + 2 * i;
-                            res[i] = (e < a.rot ? m & 0xFFFFu : own[i] & 0xFFFFu) |
-                                     (e + 1 < a.rot ? m & 0xFFFF0000u : own[i] & 0xFFFF0000u);
+                            res[i] = pack2<F16>(lo, hi);
+                            if constexpr (!kWhole) {  // values past the rotated part are copied bit for bit
+                                const int e = e0 + 2 * i;
+                                res[i] = (e < a.rot ? res[i] & 0xFFFFu : own[i] & 0xFFFFu) |
+                                         (e + 1 < a.rot ? res[i] & 0xFFFF0000u : own[i] & 0xFFFF0000u);
+                            }
                         }
                         w[u] = make_uint4(res[0], res[1], res[2], res[3]);
                     }
@@ -215,6 +223,7 @@ void launch(const Args &a, int pairing, const Split &sp, unsigned blocks, cudaSt
     switch (pairing) {
         case kNone: append_kernel<D, F16, kNone><<<blocks, kThreads, 0, s>>>(a, sp); break;
         case kInterleaved: append_kernel<D, F16, kInterleaved><<<blocks, kThreads, 0, s>>>(a, sp); break;
+        case kRagged: append_kernel<D, F16, kRagged><<<blocks, kThreads, 0, s>>>(a, sp); break;
         case kShuffle: append_kernel<D, F16, kShuffle><<<blocks, kThreads, 0, s>>>(a, sp); break;
         default: append_kernel<D, F16, kByValue><<<blocks, kThreads, 0, s>>>(a, sp); break;
     }
@@ -225,10 +234,15 @@ void launch(const Args &a, int pairing, const Split &sp, unsigned blocks, cudaSt
 cudaError_t launch_append(const Args &a, cudaStream_t s) {
     const int rpw = 32 / (a.d / 8);
     const int rows = (a.q.p ? a.h_q : 0) + 2 * a.h_kv;
-    // One warp per token and all its rows where there are tokens enough to fill the
-    // GPU (32 warps an SM), several tokens per warp beyond that; with fewer tokens a
-    // token's rows are shared out, down to one step of a warp each.
-    const int64_t want = 152 * 32;
+    const int pairing = a.rot == 0                ? kNone
+                        : a.interleaved         ? (a.rot % 8 == 0 ? kInterleaved : kRagged)
+                        : (a.rot / 2) % 8 == 0 ? kShuffle
+                                               : kByValue;
+    // One warp per token and all its rows where there are tokens enough for the warps the
+    // GPU holds at once, several tokens per warp beyond that (one wave: 32 warps an SM in
+    // one and a half waves took 147 us where one wave takes 124 us, at 29204 tokens); with
+    // fewer tokens a token's rows are shared out, down to one step of a warp each.
+    const int64_t want = 152 * (kThreads / 32) * blocks_per_sm(pairing);
     Split sp{1, 1};
     if (a.t_total >= want) {
         sp.tokens = (int)((a.t_total + want - 1) / want);
@@ -239,7 +253,6 @@ cudaError_t launch_append(const Args &a, cudaStream_t s) {
     }
     const int64_t warps = (a.t_total + sp.tokens - 1) / sp.tokens * sp.parts;
     const unsigned blocks = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
-    const int pairing = a.rot == 0 ? kNone : a.interleaved ? kInterleaved : (a.rot / 2) % 8 == 0 ? kShuffle : kByValue;
     if (a.d == 64)
         a.f16 ? launch<64, true>(a, pairing, sp, blocks, s) : launch<64, false>(a, pairing, sp, blocks, s);
     else if (a.d == 128)
