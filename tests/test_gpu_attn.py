@@ -473,3 +473,38 @@ def test_bad_lengths_and_pages_are_recorded_and_nothing_is_touched():
         gdr.gdr_device_error(device="cuda")
     torch.cuda.synchronize()
     assert ctypes.sizeof(gdr.gdr_rows) == 24
+
+
+# --- together, as they are used -----------------------------------------------------------------------------
+
+def test_example_decodes_step_by_step_what_one_prefill_gives():
+    """The hybrid example: prompt, single tokens and a draft block through append, prefill and decode, against
+    one prefill of the whole sequences.  Both sides round q and k alike; o differs by the weights' rounding and
+    its own (2 x 2^-8 of o's terms), which the output projection (rows of unit norm) sums over 4096 inputs."""
+    import importlib.util
+    import os
+
+    torch = gu.require_gpu()
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_decode.py")
+    spec = importlib.util.spec_from_file_location("hybrid_decode", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    got, whole = mod.run(lengths=(130, 1, 77), steps=5, draft=3)
+    no_error()
+    assert torch.isfinite(got).all()
+    # per row: errors of at most 2^-6 of each |o| term reach the row's entries as 2^-6 of their rms; entries
+    # are sums of x (|x| a few) and the projection, rounded to 2^-8 of themselves on both sides
+    err = (got.float() - whole.float()).abs()
+    bound = 2.0 ** -7 * whole.float().abs() + 2.0 ** -4
+    assert torch.all(err <= bound), float((err - bound).max())
+
+
+def test_prefill_inputs_may_be_expanded():
+    """Keys and values shared by all heads or all queries alike: zero strides."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(50)
+    q = randn(rng, (150, 4, 64), "bf16")
+    k = randn(rng, (150, 1, 64), "bf16").expand(150, 2, 64)
+    v = randn(rng, (1, 2, 64), "bf16").expand(150, 2, 64)
+    check_prefill(q, k, v, [150], "bf16")
+    check_prefill(q[:1].expand(150, 4, 64), k, v, [100, 50], "bf16")
