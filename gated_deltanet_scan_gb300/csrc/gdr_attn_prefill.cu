@@ -16,13 +16,19 @@
 // (d columns) and two S tiles (128 each) fill TMEM at d = 256; P overwrites its S as
 // 16-bit pairs and is the second MMA's A operand from there.
 //
-// Twelve warps.  One thread loads K and V tiles by TMA into a ring, in the order the
-// MMAs take them: K0, K1, V0, K2, V1, ...  One thread of the leading CTA issues
-// S_{j+1} before P V_j, so the tensor pipe has work while P_j is made.  Two warpgroups
-// make P: one the even tiles, the other the odd ones, one row per thread.  Each hands
-// the row's reference m on to the other as soon as it has its tile's maximum, so they
-// work on two tiles at the same time; each keeps the sum l of its own tiles.  A
-// warpgroup that raises m rescales O itself, between the two MMAs.
+// Sixteen warps, persistent: every pair walks its blocks of 256 rows, and all roles run
+// over the blocks' ends, so that a block's start and end hide behind its neighbours'.
+//   loads   one warp; K and V tiles by TMA into a ring, in the order the MMAs take them:
+//           K runs AHEAD tiles ahead of V, over the blocks' ends too.  It also finds the
+//           blocks and tells the other roles (entries of four blocks in shared memory).
+//   MMAs    one warp of the leading CTA; S of the tile AHEAD comes before P V of this one,
+//           so the tensor pipe has work while P is made.
+//   P       two warpgroups, one the even tiles, the other the odd ones, one row per thread.
+//           Each hands the row's reference m on to the other as soon as it has its tile's
+//           maximum, so they work on two tiles at the same time; each keeps the sum l of its
+//           own tiles.  A warpgroup that raises m rescales O itself, between the two MMAs.
+//   O / l   a warpgroup reads O when a block's last P V is done, and stores the result while
+//           the next block's first tiles are already in work.
 //
 // A token must not see what later tokens or other sequences hold, even a NaN, and 0
 // times NaN is NaN.  In S that is a select.  In the few tiles in which some row of the
@@ -40,7 +46,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kPairs = 76;   // CTA pairs on 152 SMs
 constexpr int kRows = 128;  // rows per CTA
 constexpr int kTile = 128;  // tokens per tile
@@ -58,12 +64,16 @@ struct Shape {
     static constexpr uint32_t K_BOX = 64 * 128;            // 64 tokens, 64 columns
     static constexpr uint32_t STAGE = 128 * D;             // half a key or value tile
     static constexpr int STAGES = D == 256 ? 5 : 8;
-    static constexpr uint32_t OFF_RING = Q_BYTES;
-    static constexpr uint32_t OFF_M = OFF_RING + STAGES * STAGE;  // float [2][128]: m handed on
-    static constexpr uint32_t OFF_L = OFF_M + 1024;               // float [2][128]: the warpgroups' l
-    static constexpr uint32_t OFF_BAR = OFF_L + 1024;
-    static constexpr uint32_t OFF_WORDS = OFF_BAR + 56 * 8;       // TMEM address, flags
-    static constexpr uint32_t BYTES = OFF_WORDS + 128;
+    static constexpr int Q_TILES = D == 256 ? 1 : 2;       // the next block's Q loads beside this one's
+    static constexpr uint32_t OFF_RING = Q_TILES * Q_BYTES;
+    static constexpr uint32_t OFF_M = OFF_RING + STAGES * STAGE;  // float [128]: m handed on
+    static constexpr uint32_t OFF_L = OFF_M + 512;                // float [2][128]: l of a block's other warpgroup
+    static constexpr uint32_t OFF_INV = OFF_L + 1024;             // float [2][128]: a block's 1 / l
+    static constexpr uint32_t OFF_ENTRY = OFF_INV + 1024;         // int4 [4]: blocks
+    static constexpr uint32_t OFF_WORDS = OFF_ENTRY + 64;         // TMEM address; flags [4][2]
+    static constexpr uint32_t OFF_BAR = OFF_WORDS + 48;
+    static constexpr int BARS = 3 * STAGES + 2 * (D == 256 ? 2 : 3) + 28;
+    static constexpr uint32_t BYTES = OFF_BAR + 8 * BARS;
     static_assert(BYTES <= 227 * 1024, "shared memory of one CTA");
     // TMEM columns: O at 0, S tiles from here on.  With three of them (d <= 128) the
     // MMAs of two more tiles' S run while a tile's P is made; at d = 256 two fit.
@@ -73,22 +83,27 @@ struct Shape {
 };
 
 // barriers, as 8-byte words from OFF_BAR
-enum Bar {
-    kQFull = 0,                // on the leading CTA
-    kQEmpty = kQFull + 1,
-    kKvFull = kQEmpty + 1,     // [stages], on the leading CTA
-    kKvEmpty = kKvFull + 8,    // [stages]
-    kVLocal = kKvEmpty + 8,    // [stages]: a value tile to be looked through
-    kSFull = kVLocal + 8,      // [S tiles]
-    kPFull = kSFull + 3,       // [S tiles], on the leading CTA
-    kPvDone = kPFull + 3,      // [2]: P V of even and odd tiles
-    kODone = kPvDone + 2,      // a block's last P V
-    kOFree = kODone + 1,       // O is read, on the leading CTA
-    kMReady = kOFree + 1,      // [2][4]: m of a warp's rows
-    kPatch = kMReady + 8,      // [8]: a block's flags
-    kBars = kPatch + 8,
+template <int D>
+struct Bar {
+    static constexpr int N = Shape<D>::STAGES, S = Shape<D>::S_TILES;
+    static constexpr int QFull = 0;              // [Q tiles], on the leading CTA
+    static constexpr int QEmpty = QFull + 2;     // [Q tiles]
+    static constexpr int KvFull = QEmpty + 2;    // [stages], on the leading CTA
+    static constexpr int KvEmpty = KvFull + N;   // [stages]
+    static constexpr int VLocal = KvEmpty + N;   // [stages]: a value tile to be looked through
+    static constexpr int SFull = VLocal + N;     // [S tiles]
+    static constexpr int PFull = SFull + S;      // [S tiles], on the leading CTA
+    static constexpr int PvDone = PFull + S;     // [2]: P V of even and odd tiles
+    static constexpr int ODone = PvDone + 2;     // a block's last P V
+    static constexpr int OFree = ODone + 1;      // O is read, on the leading CTA
+    static constexpr int MReady = OFree + 1;     // [4]: m of a warp's rows
+    static constexpr int Patch = MReady + 4;     // [4 blocks]: flags
+    static constexpr int Block = Patch + 4;      // [4 blocks]: entries
+    static constexpr int Read = Block + 4;       // [4 blocks]: entry, flags and 1 / l are read (P: 8 warps, O: 4)
+    static constexpr int LOther = Read + 4;      // [2 blocks]: l of the warpgroup that has not the last tile
+    static constexpr int Inv = LOther + 2;       // [2 blocks]: 1 / l
+    static constexpr int COUNT = Inv + 2;
 };
-static_assert(kBars <= 56, "barrier words");
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -162,40 +177,49 @@ template <int D, bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     using Sh = Shape<D>;
+    using Bar = Bar<D>;
+    static_assert(Bar::COUNT == Sh::BARS, "barrier words");
+    constexpr int A = Sh::AHEAD, N = Sh::STAGES, S = Sh::S_TILES, QT = Sh::Q_TILES;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     float *const s_m = reinterpret_cast<float *>(smem + Sh::OFF_M);
     float *const s_l = reinterpret_cast<float *>(smem + Sh::OFF_L);
-    const uint32_t bars = base + Sh::OFF_BAR;
+    float *const s_inv = reinterpret_cast<float *>(smem + Sh::OFF_INV);
+    int4 *const s_entry = reinterpret_cast<int4 *>(smem + Sh::OFF_ENTRY);
     uint32_t *const s_tmem = reinterpret_cast<uint32_t *>(smem + Sh::OFF_WORDS);
-    uint32_t *const s_flags = s_tmem + 1;  // [8 blocks][2 CTAs]: values to be added at the end
+    uint32_t *const s_flags = s_tmem + 1;  // [4 blocks][2 CTAs]: values to be added at the end
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform for the compiler, too
     const uint32_t rank = pair::cta_rank();
     const int per_cta = tokens_per_cta(a.group);
-    const int pair_id = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    auto bar = [&](int i) { return bars + 8u * i; };
+    auto bar = [&](int i) { return base + Sh::OFF_BAR + 8u * i; };
 
     // --- barriers and TMEM
+    if (tid < 8) s_flags[tid] = 0;
     if (tid == 0) {
-        mbar_init(bar(kQFull), 2);
-        mbar_init(bar(kQEmpty), 1);
-        for (int i = 0; i < Sh::STAGES; ++i) {
-            mbar_init(bar(kKvFull + i), 2);
-            mbar_init(bar(kKvEmpty + i), 1);
-            mbar_init(bar(kVLocal + i), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(Bar::QFull + i), 2);
+            mbar_init(bar(Bar::QEmpty + i), 1);
+            mbar_init(bar(Bar::PvDone + i), 1);
+            mbar_init(bar(Bar::LOther + i), 4);
+            mbar_init(bar(Bar::Inv + i), 4);
         }
-        for (int i = 0; i < Sh::S_TILES; ++i) {
-            mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kPFull + i), 8);
+        for (int i = 0; i < N; ++i) {
+            mbar_init(bar(Bar::KvFull + i), 2);
+            mbar_init(bar(Bar::KvEmpty + i), 1);
+            mbar_init(bar(Bar::VLocal + i), 1);
         }
-        mbar_init(bar(kPvDone), 1);
-        mbar_init(bar(kPvDone + 1), 1);
-        mbar_init(bar(kODone), 1);
-        mbar_init(bar(kOFree), 16);
-        for (int i = 0; i < 8; ++i) {
-            mbar_init(bar(kMReady + i), 1);
-            mbar_init(bar(kPatch + i), 2);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(bar(Bar::SFull + i), 1);
+            mbar_init(bar(Bar::PFull + i), 8);
+        }
+        mbar_init(bar(Bar::ODone), 1);
+        mbar_init(bar(Bar::OFree), 8);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(Bar::MReady + i), 1);
+            mbar_init(bar(Bar::Patch + i), 2);
+            mbar_init(bar(Bar::Block + i), 1);
+            mbar_init(bar(Bar::Read + i), 12);
         }
         fence_mbar_init();
     }
@@ -216,82 +240,141 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const long long t_end = clock64() + 4000000;
         while (clock64() < t_end) {}
     };
-    auto all_ok = [&](bool mine_ok) { return __all_sync(0xffffffffu, mine_ok) != 0; };
+    // every lane of the warp waits, and all of them go on or give up
+    auto wait = [&](int i, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(bar(i), parity & 1, kWaitLimit)) != 0;
+        return ok;
+    };
+    // Block number `it` of this pair, from the entry the loading warp left; n = 0: there is none.
+    auto fetch = [&](int it, Block &b) {
+        if (!wait(Bar::Block + (it & 3), it >> 2)) return false;
+        const int4 e = s_entry[it & 3];
+        b.t0 = e.x;
+        b.len = e.y;
+        b.first = e.z;
+        b.h = e.w;
+        b.n = (min(b.len, b.first + 2 * per_cta) + kTile - 1) / kTile;
+        b.j_clean = (b.first + 1) >> 7;
+        return b.n > 0;
+    };
 
-    // The ring takes a block's tiles in the order K0 .. K_AHEAD, V0, K_{AHEAD + 1}, V1, ...,
-    // the last values at the end, and blocks one after the other.  Every role walks the same
-    // blocks and counts stages, tiles and blocks through all of them: the counts give stages,
-    // S tiles and barrier phases.
-    constexpr int A = Sh::AHEAD;
-    auto k_index = [](int j) { return j <= A ? j : 2 * j - A; };
-    auto v_index = [](int j, int n) { return j <= n - 1 - A ? A + 1 + 2 * j : n + j; };
-    Cursor cursor{a.n_seqs, 0, 0};
-    Block b;
+    // Roles count stages (i), tiles (g) and blocks (it) through all of a pair's blocks: the
+    // counts give stages, S tiles and barrier phases.  Stage order: K of tiles 0 .. A, V of
+    // tile 0, K of tile A + 1, V of tile 1, ..., at the very end the last values.
 
-    // the launch's 384 x 168 registers become 128 x 56 and 256 x 224
-    if (warp >= 8) {
+    // the launch's 512 x 128 registers become 128 x 56, 128 x 104 and 256 x 176
+    if (warp >= 8 && warp < 12) {
         pair::fewer_registers<56>();
         if (warp == 8) {
             // ---- loads (both CTAs: own halves)
             const bool issue = elect_one();
-            const uint32_t q_bar = pair::map_to(bar(kQFull), 0), full0 = pair::map_to(bar(kKvFull), 0);
-            uint32_t i0 = 0;  // stages before this block's
-            for (int it = 0; ok && cursor.next(a, pair_id, pairs, lane, b); ++it) {
-                const int t_kv = (int)b.t0;
-                auto free_stage = [&](uint32_t i) {
-                    const uint32_t use = i / Sh::STAGES;
-                    if (use > 0)
-                        ok = ok && mbar_wait_bounded(bar(kKvEmpty + i % Sh::STAGES), (use - 1) & 1, kWaitLimit);
-                    ok = all_ok(ok);
-                    return base + Sh::OFF_RING + (i % Sh::STAGES) * Sh::STAGE;
-                };
-                auto load_k = [&](int j) {
-                    const uint32_t i = i0 + k_index(j), dst = free_stage(i);
-                    if (ok && issue) {
-                        const uint32_t full = full0 + 8u * (i % Sh::STAGES);
-                        pair::arrive_expect_remote(full, Sh::STAGE);
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c)
-                            pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, b.h,
-                                                   t_kv + j * kTile + (int)rank * 64);
-                    }
-                    __syncwarp();
-                };
-                load_k(0);
-                if (it > 0) ok = all_ok(ok && mbar_wait_bounded(bar(kQEmpty), (it - 1) & 1, kWaitLimit));
+            const uint32_t q_full = pair::map_to(bar(Bar::QFull), 0), kv_full = pair::map_to(bar(Bar::KvFull), 0);
+            Cursor cursor{a.n_seqs, 0, 0};
+            uint32_t i = 0;
+            // Q of block q_it is still to be loaded, when its place is free
+            int q_it = 0, q_token = 0, q_head = 0;
+            bool q_waits = false;
+            auto load_q = [&](bool block) {
+                if (!q_waits) return;
+                const int slot = q_it % QT, use = q_it / QT;
+                if (use > 0) {
+                    if (block)
+                        wait(Bar::QEmpty + slot, use - 1);
+                    else if (!__all_sync(0xffffffffu, mbar_test_wait(bar(Bar::QEmpty + slot), (use - 1) & 1)))
+                        return;
+                }
                 if (ok && issue) {
-                    pair::arrive_expect_remote(q_bar, (uint32_t)(D / 64) * 128u * (uint32_t)(per_cta * a.group));
+                    const uint32_t full = q_full + 8u * slot;
+                    pair::arrive_expect_remote(full, (uint32_t)(D / 64) * 128u * (uint32_t)(per_cta * a.group));
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c)
-                        pair::tma_load_3d_pair(base + c * Sh::Q_BLOCK, &maps.q, q_bar, c * 64, b.h * a.group,
-                                               t_kv + b.first + (int)rank * per_cta);
+                        pair::tma_load_3d_pair(base + slot * Sh::Q_BYTES + c * Sh::Q_BLOCK, &maps.q, full, c * 64,
+                                               q_head * a.group, q_token);
                 }
                 __syncwarp();
-                for (int j = 1; j <= A && j < b.n; ++j) load_k(j);
-                for (int j = 0; j < b.n && ok; ++j) {
-                    if (j > 0 && j + A < b.n) load_k(j + A);
-                    const uint32_t i = i0 + v_index(j, b.n), st = i % Sh::STAGES, dst = free_stage(i);
+                q_waits = false;
+            };
+            auto free_stage = [&] {  // of the ring; Q's place may become free first
+                const int st = i % N, use = i / N;
+                if (use > 0 && q_waits) {
+                    const long long t_end = clock64() + kWaitLimit;
+                    while (ok && q_waits &&
+                           !__all_sync(0xffffffffu, mbar_test_wait(bar(Bar::KvEmpty + st), (use - 1) & 1))) {
+                        load_q(false);
+                        if (clock64() > t_end) ok = false;
+                        ok = __all_sync(0xffffffffu, ok);
+                    }
+                }
+                if (use > 0) wait(Bar::KvEmpty + st, use - 1);
+                return base + Sh::OFF_RING + st * Sh::STAGE;
+            };
+            Block kb, vb;
+            int k_it = -1, kj = 0, v_it = 0, vj = 0;
+            kb.n = 0;
+            bool k_more = true;
+            auto load_k = [&] {
+                if (kj == kb.n) {  // the next block
+                    load_q(true);
+                    ++k_it;
+                    kj = 0;
+                    k_more = cursor.next(a, blockIdx.x >> 1, gridDim.x >> 1, lane, kb);
+                    if (!k_more) kb = Block{};
+                    if (k_it >= 4) wait(Bar::Read + (k_it & 3), (k_it >> 2) - 1);
                     if (ok && issue) {
-                        const int x = (int)rank * (D / 2);
-                        if (j >= b.j_clean) {  // looked through by warps 10 and 11, which then report the stage full
-                            mbar_arrive_expect_tx(bar(kVLocal + st), Sh::STAGE);
-#pragma unroll
-                            for (int c = 0; c < Sh::V_BOXES; ++c)
-                                tma_load_3d(dst + c * Sh::V_BOX, &maps.v, bar(kVLocal + st), x + c * Sh::VC, b.h,
-                                            t_kv + j * kTile);
-                        } else {
-                            const uint32_t full = full0 + 8u * st;
-                            pair::arrive_expect_remote(full, Sh::STAGE);
-#pragma unroll
-                            for (int c = 0; c < Sh::V_BOXES; ++c)
-                                pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full, x + c * Sh::VC, b.h,
-                                                       t_kv + j * kTile);
-                        }
+                        s_entry[k_it & 3] = make_int4((int)kb.t0, kb.len, kb.first, kb.h);
+                        mbar_arrive(bar(Bar::Block + (k_it & 3)));
                     }
                     __syncwarp();
+                    if (!k_more || !ok) return;
+                    q_it = k_it;
+                    q_token = (int)kb.t0 + kb.first + (int)rank * per_cta;
+                    q_head = kb.h;
+                    q_waits = true;
+                    load_q(false);
                 }
-                i0 += 2 * b.n;
+                const uint32_t dst = free_stage();
+                if (ok && issue) {
+                    const uint32_t full = kv_full + 8u * (i % N);
+                    pair::arrive_expect_remote(full, Sh::STAGE);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        pair::tma_load_3d_pair(dst + c * Sh::K_BOX, &maps.k, full, c * 64, kb.h,
+                                               (int)kb.t0 + kj * kTile + (int)rank * 64);
+                }
+                __syncwarp();
+                ++kj;
+                ++i;
+            };
+            for (int j = 0; j <= A && k_more && ok; ++j) load_k();
+            bool more = ok && fetch(0, vb);
+            for (bool start = true; more; start = false) {
+                if (!start && k_more) load_k();
+                const uint32_t dst = free_stage();
+                if (ok && issue) {
+                    const int x = (int)rank * (D / 2), y = (int)vb.t0 + vj * kTile, st = i % N;
+                    if (vj >= vb.j_clean) {  // looked through by warps 10 and 11, which then report the stage full
+                        mbar_arrive_expect_tx(bar(Bar::VLocal + st), Sh::STAGE);
+#pragma unroll
+                        for (int c = 0; c < Sh::V_BOXES; ++c)
+                            tma_load_3d(dst + c * Sh::V_BOX, &maps.v, bar(Bar::VLocal + st), x + c * Sh::VC, vb.h, y);
+                    } else {
+                        const uint32_t full = kv_full + 8u * st;
+                        pair::arrive_expect_remote(full, Sh::STAGE);
+#pragma unroll
+                        for (int c = 0; c < Sh::V_BOXES; ++c)
+                            pair::tma_load_3d_pair(dst + c * Sh::V_BOX, &maps.v, full, x + c * Sh::VC, vb.h, y);
+                    }
+                }
+                __syncwarp();
+                ++i;
+                if (++vj == vb.n) {
+                    vj = 0;
+                    more = fetch(++v_it, vb);
+                }
+                load_q(false);
+                more = more && ok;
             }
+            load_q(true);
         } else if (warp == 9 && rank == 0) {
             // ---- MMAs.  The whole warp walks the tiles and one elected lane issues, so that
             // descriptors are made in uniform registers (one lane in a branch of its own took
@@ -304,69 +387,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t k0 = smem_desc_sw128(base + Sh::OFF_RING, 0, 1024);
             const uint64_t v0 = Sh::VC == 64 ? smem_desc(base + Sh::OFF_RING, Sh::V_BOX, 1024, kSwizzle128)
                                              : smem_desc(base + Sh::OFF_RING, Sh::V_BOX, 512, kSwizzle64);
-            uint32_t i0 = 0, g0 = 0;  // stages and tiles before this block's
-            Block ahead;
-            bool more = cursor.next(a, pair_id, pairs, lane, ahead);
-            for (int it = 0; ok && more; ++it) {
-                b = ahead;
-                auto score = [&](int j) {
-                    const uint32_t i = i0 + k_index(j), st = i % Sh::STAGES, s_tile = (g0 + j) % Sh::S_TILES;
-                    ok = all_ok(ok && mbar_wait_bounded(bar(kKvFull + st), (i / Sh::STAGES) & 1, kWaitLimit));
-                    if (!ok) return;
-                    tc_fence_after_sync();
-                    const uint64_t kd = k0 + (uint64_t)(st * (Sh::STAGE >> 4));
-                    const uint32_t d = tmem + Sh::COLS_S + s_tile * kTile;
-                    if (issue) {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            pair::mma_ss(d, q0 + (((k >> 2) * Sh::Q_BLOCK + (k & 3) * 32) >> 4),
-                                         kd + (((k >> 2) * Sh::K_BOX + (k & 3) * 32) >> 4), id_s, k > 0);
-                        pair::commit_both(bar(kKvEmpty + st));
-                        pair::commit_both(bar(kSFull + s_tile));
-                        if (j == b.n - 1) pair::commit_both(bar(kQEmpty));
-                    }
-                    __syncwarp();
-                };
-                ok = all_ok(mbar_wait_bounded(bar(kQFull), it & 1, kWaitLimit));
-                // the S tiles are free: the P V that read them are issued
-                for (int j = 0; j <= A && j < b.n; ++j) score(j);
-                more = cursor.next(a, pair_id, pairs, lane, ahead);  // while P of the first tile is made
-                if (it > 0) ok = all_ok(ok && mbar_wait_bounded(bar(kOFree), (it - 1) & 1, kWaitLimit));
-                for (int j = 0; j < b.n && ok; ++j) {
-                    if (j > 0 && j + A < b.n) score(j + A);  // over P of tile j - 1, whose P V is issued
-                    const uint32_t i = i0 + v_index(j, b.n), st = i % Sh::STAGES;
-                    const uint32_t g = g0 + j, s_tile = g % Sh::S_TILES;
-                    ok = ok && (j < b.j_clean
-                                    ? mbar_wait_bounded(bar(kKvFull + st), (i / Sh::STAGES) & 1, kWaitLimit)
-                                    : pair::wait_cluster(bar(kKvFull + st), (i / Sh::STAGES) & 1, kWaitLimit));
-                    ok = ok && mbar_wait_bounded(bar(kPFull + s_tile), (g / Sh::S_TILES) & 1, kWaitLimit);
-                    ok = all_ok(ok);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint64_t vd = v0 + (uint64_t)(st * (Sh::STAGE >> 4));
-                    const uint32_t p = tmem + Sh::COLS_S + s_tile * kTile;
-                    if (issue) {
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            pair::mma_ts(tmem, p + k * 8, vd + ((k * 16 * (Sh::VC * 2)) >> 4), id_o, j > 0 || k > 0);
-                        pair::commit_both(bar(kKvEmpty + st));
-                        pair::commit_both(bar(kPvDone + (g & 1)));
-                        if (j == b.n - 1) pair::commit_both(bar(kODone));
-                    }
-                    __syncwarp();
+            uint32_t i = 0, gs = 0, g = 0;  // stage; tiles of S and of P V so far
+            int k_it = -1, kj = 0, kn = 0, v_it = 0, vj = 0;
+            bool k_more = true;
+            Block b;
+            auto score = [&] {
+                if (kj == kn) {
+                    ++k_it;
+                    kj = 0;
+                    k_more = fetch(k_it, b);
+                    kn = b.n;
+                    if (!k_more || !wait(Bar::QFull + k_it % QT, k_it / QT)) return;
                 }
-                i0 += 2 * b.n;
-                g0 += b.n;
+                const uint32_t st = i % N, s_tile = gs % S;
+                if (!wait(Bar::KvFull + st, i / N)) return;
+                tc_fence_after_sync();
+                const uint64_t qd = q0 + (uint64_t)((k_it % QT) * (Sh::Q_BYTES >> 4));
+                const uint64_t kd = k0 + (uint64_t)(st * (Sh::STAGE >> 4));
+                const uint32_t d = tmem + Sh::COLS_S + s_tile * kTile;
+                if (issue) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        pair::mma_ss(d, qd + (((k >> 2) * Sh::Q_BLOCK + (k & 3) * 32) >> 4),
+                                     kd + (((k >> 2) * Sh::K_BOX + (k & 3) * 32) >> 4), id_s, k > 0);
+                    pair::commit_both(bar(Bar::KvEmpty + st));
+                    pair::commit_both(bar(Bar::SFull + s_tile));
+                    if (kj == kn - 1) pair::commit_both(bar(Bar::QEmpty + k_it % QT));
+                }
+                __syncwarp();
+                ++kj;
+                ++gs;
+                ++i;
+            };
+            for (int j = 0; j <= A && k_more && ok; ++j) score();
+            Block vb;
+            bool more = ok && fetch(0, vb);
+            while (more && ok) {
+                if (g > 0 && k_more) score();  // over P of the tile before, whose P V is issued
+                if (!ok) break;
+                const uint32_t st = i % N, s_tile = g % S;
+                if (vj == 0 && v_it > 0 && !wait(Bar::OFree, v_it - 1)) break;
+                if (vj < vb.j_clean)
+                    wait(Bar::KvFull + st, i / N);
+                else
+                    ok = __all_sync(0xffffffffu, pair::wait_cluster(bar(Bar::KvFull + st), (i / N) & 1, kWaitLimit));
+                if (!ok || !wait(Bar::PFull + s_tile, g / S)) break;
+                tc_fence_after_sync();
+                const uint64_t vd = v0 + (uint64_t)(st * (Sh::STAGE >> 4));
+                const uint32_t p = tmem + Sh::COLS_S + s_tile * kTile;
+                if (issue) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        pair::mma_ts(tmem, p + k * 8, vd + ((k * 16 * (Sh::VC * 2)) >> 4), id_o, vj > 0 || k > 0);
+                    pair::commit_both(bar(Bar::KvEmpty + st));
+                    pair::commit_both(bar(Bar::PvDone + (g & 1)));
+                    if (vj == vb.n - 1) pair::commit_both(bar(Bar::ODone));
+                }
+                __syncwarp();
+                ++i;
+                ++g;
+                if (++vj == vb.n) {
+                    vj = 0;
+                    more = fetch(++v_it, vb);
+                }
             }
         } else if (warp >= 10) {
             // ---- value tiles that some row sees only in part (both CTAs: own halves)
-            uint32_t i0 = 0, turns = 0;  // stages before this block's; per stage, phase of its barrier
-            for (int it = 0; cursor.next(a, pair_id, pairs, lane, b); ++it) {
+            uint32_t g = 0, k_count = 0, turns = 0;  // V tiles so far; K tiles known of; per stage, its barrier's phase
+            int k_it = 0;
+            bool k_more = true;
+            Block b, kb;
+            for (int it = 0;; ++it) {
+                const bool more = fetch(it, b);
+                ok = !pair::named_or(2, 64, !ok);  // the two warps leave together
+                if (!more || !ok) break;
                 bool found = false;
-                for (int j = b.j_clean; j < b.n; ++j) {  // even after a timeout: the two warps meet in each
-                    const uint32_t st = (i0 + v_index(j, b.n)) % Sh::STAGES;
-                    ok = ok && mbar_wait_bounded(bar(kVLocal + st), (turns >> st) & 1, kWaitLimit);
+                for (int j = 0; j < b.n; ++j, ++g) {
+                    if (j < b.j_clean) continue;
+                    // stages before this one: V of g tiles, and K of those up to A tiles ahead
+                    while (ok && k_more && k_count < g + A + 1) {
+                        k_more = fetch(k_it++, kb);
+                        k_count += kb.n;
+                    }
+                    const uint32_t st = (g + min(g + A + 1, k_count)) % N;
+                    ok = ok && mbar_wait_bounded(bar(Bar::VLocal + st), (turns >> st) & 1, kWaitLimit);
                     turns ^= 1u << st;
+                    bool here = false;
                     uint4 *const tile = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE);
                     constexpr uint32_t e = F16 ? 0x7C007C00u : 0x7F807F80u;
 #pragma unroll 4
@@ -383,52 +489,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         if (bad) {
                             tile[x] = w;
-                            found = true;
+                            here = true;
                         }
                     }
-                    fence_proxy_async_smem();
-                    named_sync(1, 64);
-                    if (tid == 320 && ok) pair::arrive_remote_release(pair::map_to(bar(kKvFull + st), 0));
+                    if (here) fence_proxy_async_smem();
+                    here = pair::named_or(1, 64, here);
+                    found = found || here;
+                    if (tid == 320 && ok) {
+                        const uint32_t full = pair::map_to(bar(Bar::KvFull + st), 0);
+                        if (here)  // written: a release, which costs a thousand clocks, only then
+                            pair::arrive_remote_release(full);
+                        else
+                            pair::arrive_remote(full);
+                    }
+                    __syncwarp();
                 }
-                // the block's flag, to both CTAs.  Its slot is used again eight blocks on, when this
-                // block's last stages have left the ring of at most eight
-                const int slot = it & 7;
-                found = pair::named_or(2, 64, found);
-                if (tid == 320) {
+                // both CTAs look for values to add where a flag is set.  Flags are never reset: a later
+                // block of the slot looks in vain
+                if (tid == 320 && ok) {
 #pragma unroll
                     for (uint32_t r = 0; r < 2; ++r) {
-                        pair::store_remote(pair::map_to(smem_u32(s_flags + slot * 2 + rank), r), found);
-                        pair::arrive_remote_release(pair::map_to(bar(kPatch + slot), r));
+                        const uint32_t told = pair::map_to(bar(Bar::Patch + (it & 3)), r);
+                        if (found) {
+                            pair::store_remote(pair::map_to(smem_u32(s_flags + (it & 3) * 2 + rank), r), 1);
+                            pair::arrive_remote_release(told);
+                        } else {
+                            pair::arrive_remote(told);
+                        }
                     }
                 }
-                i0 += 2 * b.n;
+                __syncwarp();
             }
         }
         if (!ok) gave_up();
         __syncwarp();
         pair::cluster_sync();
-    } else {
-        pair::more_registers<224>();
-        // ---- softmax: warpgroup wg takes a block's tiles wg, wg + 2, ...; a thread is a row
+    } else if (warp < 8) {
+        pair::more_registers<176>();
+        // ---- P: warpgroup wg takes the tiles with g % 2 == wg; a thread is a row
         const int wg = warp >> 2, row = tid & 127, wq = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
         // a scale of 0 still has to leave a masked score at minus infinity
         const float sc = fmaxf(fabsf(a.scale), 1e-30f) * kLog2e;
         const int tok = row / a.group, head_in_group = row - tok * a.group;
-        const uint32_t p_bars = pair::map_to(bar(kPFull), 0), o_free = pair::map_to(bar(kOFree), 0);
+        const uint32_t p_bars = pair::map_to(bar(Bar::PFull), 0);
         uint32_t g0 = 0;              // tiles before this block's
-        uint32_t turn[2] = {0, 0};    // tiles of either warpgroup before this block's
-        Block ahead;
-        bool more = cursor.next(a, pair_id, pairs, lane, ahead);
-        for (int it = 0; more; ++it) {
-            b = ahead;
+        uint32_t others = 0;          // per block slot, phase of LOther: blocks of two tiles or more
+        Block b;
+        for (int it = 0; fetch(it, b); ++it) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Bar::Read + (it & 3)));
             const int n = b.n, mine = b.first + (int)rank * per_cta;
             const int token = mine + tok;  // in the sequence
             float m_own = -CUDART_INF_F, l = 0.f;
-            for (int j = wg; ok && j < n; j += 2) {
-                const uint32_t g = g0 + j, st = g % Sh::S_TILES;
-                ok = all_ok(mbar_wait_bounded(bar(kSFull + st), (g / Sh::S_TILES) & 1, kWaitLimit));
-                if (!ok) break;
+            for (int j = (g0 ^ wg) & 1; j < n; j += 2) {
+                const uint32_t g = g0 + j, st = g % S;
+                if (!wait(Bar::SFull + st, g / S)) break;
                 tc_fence_after_sync();
                 const uint32_t s_at = lanes + Sh::COLS_S + st * kTile;
                 uint32_t r[128];
@@ -453,34 +569,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(r[124 + e]));
                 const float x_top = sc * fmaxf(pair::max3(top[0], top[1], top[2]), top[3]);
-                // the reference after the tile before, from the other warpgroup
-                float m_prev = -CUDART_INF_F;
-                if (j > 0) {
-                    const uint32_t turn_prev = turn[wg ^ 1] + ((j - 1) >> 1);
-                    ok = all_ok(mbar_wait_bounded(bar(kMReady + 4 * (wg ^ 1) + wq), turn_prev & 1, kWaitLimit));
-                    if (!ok) break;
-                    m_prev = s_m[(wg ^ 1) * 128 + row];
-                }
+                // the reference after the tile before, from the other warpgroup; its place is
+                // written again only after this wait, also between two blocks' tiles
+                if (g > 0 && !wait(Bar::MReady + wq, g - 1)) break;
+                const float m_prev = j > 0 ? s_m[row] : -CUDART_INF_F;
                 const bool raise = j == 0 || x_top > m_prev + kSlack;
                 const float m = raise ? x_top : m_prev;
-                s_m[wg * 128 + row] = m;
+                s_m[row] = m;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kMReady + 4 * wg + wq));
+                if (lane == 0) mbar_arrive(bar(Bar::MReady + wq));
 
                 if (j > 0 && __any_sync(0xffffffffu, raise)) {
                     // O is that of tiles 0 .. j - 1 then: P V of tile j waits for this warp's P.  (S of
-                    // tile j is complete, so P V of tile j - 3 is: this barrier's phase is unambiguous.)
-                    ok = all_ok(mbar_wait_bounded(bar(kPvDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1, kWaitLimit));
-                    if (!ok) break;
+                    // tile g is complete, so P V of tile g - 3 is: this barrier's phase is unambiguous.)
+                    if (!wait(Bar::PvDone + ((g - 1) & 1), (g - 1) >> 1)) break;
                     tc_fence_after_sync();
                     const float f = raise ? fast_exp2(m_prev - m) : 1.f;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        pair::tmem_load32(lanes + c, o);
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        pair::tmem_load16(lanes + c, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        pair::tmem_store32(lanes + c, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        pair::tmem_store16(lanes + c, o);
                     }
                 }
                 l *= m_own == m ? 1.f : fast_exp2(m_own - m);
@@ -488,11 +599,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint64_t sum[2] = {0, 0};
                 const uint64_t sc2 = pair::pack_f32x2(sc, sc), m2 = pair::pack_f32x2(-m, -m);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t p[32];
+                for (int quarter = 0; quarter < 4; ++quarter) {
+                    uint32_t p[16];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int i = half * 64 + 2 * c;
+                    for (int c = 0; c < 16; ++c) {
+                        const int i = quarter * 32 + 2 * c;
                         float x, y;
                         pair::unpack_f32x2(
                             pair::fma_f32x2(pair::pack_f32x2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), sc2,
@@ -503,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         sum[c & 1] = pair::add_f32x2(sum[c & 1], pair::pack_f32x2(x, y));
                         p[c] = pack2<F16>(x, y);
                     }
-                    pair::tmem_store32(s_at + half * 32, p);
+                    pair::tmem_store16(s_at + quarter * 16, p);
                 }
                 {
                     float x, y;
@@ -514,68 +625,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) pair::arrive_remote(p_bars + 8u * st);
-            }
-            more = cursor.next(a, pair_id, pairs, lane, ahead);  // while the last P V runs
-            s_l[wg * 128 + row] = l;
-            if (wg >= n) s_m[wg * 128 + row] = -CUDART_INF_F;  // no tile was this warpgroup's
-            named_sync(3, 256);
-            const float2 e0 = make_float2(s_m[row], s_l[row]), e1 = make_float2(s_m[128 + row], s_l[128 + row]);
-            // read: the next block may write them.  A warp whose wait gave up comes here, too: all leave.
-            ok = !pair::named_or(4, 256, !ok);
-            if (!ok) break;
-            ok = all_ok(mbar_wait_bounded(bar(kODone), it & 1, kWaitLimit) &&
-                        pair::wait_cluster(bar(kPatch + (it & 7)), (it >> 3) & 1, kWaitLimit));
-            if (ok) {
-                // ---- o = O / l: warpgroup wg writes half of the columns
-                tc_fence_after_sync();
-                const bool live = tok < per_cta && token < b.len;
-                const int64_t t = b.t0 + token;
-                const int hq = b.h * a.group + head_in_group;
-                const float m = ((n - 1) & 1) ? e1.x : e0.x;
-                const float l_all = (e0.x == m ? e0.y : e0.y * fast_exp2(e0.x - m)) +
-                                    (e1.x == m ? e1.y : e1.y * fast_exp2(e1.x - m));
-                const float inv = 1.f / l_all;
-                volatile uint32_t *const flags = s_flags + (it & 7) * 2;
-                const bool patch = flags[0] | flags[1];
-                const int c0 = wg * (D / 2);
-                uint16_t *const dst = a.o.p + t * a.o.ts + (int64_t)hq * a.o.hs + c0;
-#pragma unroll 1
-                for (int c = 0; c < D / 2; c += 32) {
-                    uint32_t o[32];
-                    pair::tmem_load32(lanes + c0 + c, o);
-                    if (c + 32 >= D / 2) {  // this warp has read its part of O
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) pair::arrive_remote(o_free);
+
+                const int slot = it & 1;
+                if (j == n - 2) {  // the other warpgroup has the last tile
+                    s_l[slot * 128 + row] = l;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(Bar::LOther + slot));
+                } else if (j == n - 1) {
+                    if (n > 1) {  // the other sum is relative to its last tile's m, handed on to this one
+                        if (!wait(Bar::LOther + slot, others >> slot)) break;
+                        l += s_l[slot * 128 + row] * (m_prev == m ? 1.f : fast_exp2(m_prev - m));
                     }
+                    // the place of 1 / l: read for the block before last
+                    if (it >= 2 && !wait(Bar::Read + ((it - 2) & 3), (it - 2) >> 2)) break;
+                    s_inv[slot * 128 + row] = 1.f / l;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(Bar::Inv + slot));
+                    if (a.lse && tok < per_cta && token < b.len)
+                        a.lse[(b.t0 + token) * a.h_q + b.h * a.group + head_in_group] = kLn2 * (m + log2f(l));
+                }
+            }
+            if (!ok) break;
+            g0 += n;
+            if (n > 1) others ^= 1u << (it & 1);
+        }
+        if (!ok) gave_up();
+        __syncwarp();
+        pair::cluster_sync();
+    } else {
+        pair::fewer_registers<104>();
+        // ---- o = O / l; a thread is a row
+        const int row = tid & 127;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int tok = row / a.group, head_in_group = row - tok * a.group;
+        const uint32_t o_free = pair::map_to(bar(Bar::OFree), 0);
+        Block b;
+        for (int it = 0; fetch(it, b); ++it) {
+            const int token = b.first + (int)rank * per_cta + tok;
+            const bool live = tok < per_cta && token < b.len;
+            uint16_t *dst = live ? a.o.p + (b.t0 + token) * a.o.ts + (int64_t)(b.h * a.group + head_in_group) * a.o.hs
+                                 : nullptr;
+            if (!wait(Bar::Inv + (it & 1), it >> 1)) break;
+            const float inv = s_inv[(it & 1) * 128 + row];
+            ok = __all_sync(0xffffffffu, pair::wait_cluster(bar(Bar::Patch + (it & 3)), (it >> 2) & 1, kWaitLimit));
+            if (!ok) break;
+            volatile uint32_t *const flags = s_flags + (it & 3) * 2;
+            const bool patch = flags[0] | flags[1];
+            __syncwarp();
+            if (!wait(Bar::ODone, it)) break;
+            tc_fence_after_sync();
+            // Four lanes write a row's 64 bytes together, eight rows an instruction: a lane storing
+            // its own row touches 32 lines an instruction, which held O for 4400 clocks a block.
+            uint16_t *quad[4];  // rows of this lane's four, at this lane's 8 columns
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                quad[e] = reinterpret_cast<uint16_t *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), (lane & ~3) | e));
+                if (quad[e]) quad[e] += (lane & 3) * 8;
+            }
+            constexpr int COLS = D < 128 ? D : 128;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += COLS) {
+                uint32_t w[COLS / 2];
+#pragma unroll
+                for (int c = 0; c < COLS; c += 16) {
+                    uint32_t o[16];
+                    pair::tmem_load16(lanes + c0 + c, o);
                     if (live && patch) {
                         for (int p = b.j_clean * kTile; p <= token; ++p) {
                             const uint16_t *const v = a.v.p + (b.t0 + p) * a.v.ts + (int64_t)b.h * a.v.hs + c0 + c;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
+                            for (int e = 0; e < 16; ++e) {
                                 const float x = unpack1<F16>(v[e]);
                                 if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
                             }
                         }
                     }
-                    if (live) {
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 w;
-                            w.x = pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                            w.y = pack2<F16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                            w.z = pack2<F16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                            w.w = pack2<F16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                            *reinterpret_cast<uint4 *>(dst + c + e) = w;
-                        }
+                    for (int e = 0; e < 16; e += 2)
+                        w[(c + e) / 2] = pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                }
+                if (c0 + COLS == D) {  // this warp has read its part of O
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        pair::arrive_remote(o_free);
+                        mbar_arrive(bar(Bar::Read + (it & 3)));
                     }
                     __syncwarp();
                 }
-                if (wg == 0 && live && a.lse) a.lse[t * a.h_q + hq] = kLn2 * (m + log2f(l_all));
+#pragma unroll
+                for (int c = 0; c < COLS / 2; c += 16) {  // 32 columns: 16-byte pieces transposed among four lanes
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                        for (int p = 0; p < 4; p += 2) {
+                            uint32_t &x = w[c + p * 4 + e], &y = w[c + p * 4 + 4 + e];
+                            const uint32_t z = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
+                            ((lane & 1) ? x : y) = z;
+                        }
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            uint32_t &x = w[c + p * 4 + e], &y = w[c + p * 4 + 8 + e];
+                            const uint32_t z = __shfl_xor_sync(0xffffffffu, (lane & 2) ? x : y, 2);
+                            ((lane & 2) ? x : y) = z;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (quad[e])
+                            *reinterpret_cast<uint4 *>(quad[e] + c0 + 2 * c) =
+                                make_uint4(w[c + 4 * e], w[c + 4 * e + 1], w[c + 4 * e + 2], w[c + 4 * e + 3]);
+                }
+                __syncwarp();
             }
-            g0 += n;
-            turn[0] += (n + 1) >> 1;
-            turn[1] += n >> 1;
         }
         if (!ok) gave_up();
         __syncwarp();
