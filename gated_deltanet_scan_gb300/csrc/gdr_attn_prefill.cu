@@ -146,6 +146,7 @@ struct Cursor {
                     record_invalid(a.err);
                     t0 = t1 = 0;
                 }
+                if (t1 - t0 <= short_tokens(a.group)) t1 = t0;  // the short kernel's
             }
             const int n = (int)((uint32_t)(t1 - t0 + per_pair - 1) / (uint32_t)per_pair);
             int x = n;
@@ -193,6 +194,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t rank = pair::cta_rank();
     const int per_cta = tokens_per_cta(a.group);
     auto bar = [&](int i) { return base + Sh::OFF_BAR + 8u * i; };
+
+    // the short kernel may start beside this one: neither reads what the other writes
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 8 && elect_one()) {
+        pair::prefetch_map(&maps.q);
+        pair::prefetch_map(&maps.k);
+        pair::prefetch_map(&maps.v);
+    }
+    Cursor cursor{a.n_seqs, 0, 0};
+    Block kb;  // the loading warp goes on with these
+    if (!cursor.next(a, blockIdx.x >> 1, gridDim.x >> 1, lane, kb)) return;  // no block: both CTAs leave
 
     // --- barriers and TMEM
     if (tid < 8) s_flags[tid] = 0;
@@ -269,7 +281,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // ---- loads (both CTAs: own halves)
             const bool issue = elect_one();
             const uint32_t q_full = pair::map_to(bar(Bar::QFull), 0), kv_full = pair::map_to(bar(Bar::KvFull), 0);
-            Cursor cursor{a.n_seqs, 0, 0};
             uint32_t i = 0;
             // Q of block q_it is still to be loaded, when its place is free
             int q_it = 0, q_token = 0, q_head = 0;
@@ -308,16 +319,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (use > 0) wait(Bar::KvEmpty + st, use - 1);
                 return base + Sh::OFF_RING + st * Sh::STAGE;
             };
-            Block kb, vb;
-            int k_it = -1, kj = 0, v_it = 0, vj = 0;
-            kb.n = 0;
+            Block vb;
+            int k_it = -1, kj = kb.n, v_it = 0, vj = 0;
             bool k_more = true;
             auto load_k = [&] {
                 if (kj == kb.n) {  // the next block
                     load_q(true);
                     ++k_it;
                     kj = 0;
-                    k_more = cursor.next(a, blockIdx.x >> 1, gridDim.x >> 1, lane, kb);
+                    if (k_it > 0) k_more = cursor.next(a, blockIdx.x >> 1, gridDim.x >> 1, lane, kb);
                     if (!k_more) kb = Block{};
                     if (k_it >= 4) wait(Bar::Read + (k_it & 3), (k_it >> 2) - 1);
                     if (ok && issue) {
@@ -456,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t g = 0, k_count = 0, turns = 0;  // V tiles so far; K tiles known of; per stage, its barrier's phase
             int k_it = 0;
             bool k_more = true;
-            Block b, kb;
+            Block b;
             for (int it = 0;; ++it) {
                 const bool more = fetch(it, b);
                 ok = !pair::named_or(2, 64, !ok);  // the two warps leave together
@@ -779,10 +789,20 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_prefill(const Args &a, cudaStream_t s) {
+static cudaError_t launch_long(const Args &a, cudaStream_t s) {
     if (a.d == 64) return a.f16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
     if (a.d == 128) return a.f16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
     return a.f16 ? launch<256, true>(a, s) : launch<256, false>(a, s);
+}
+
+cudaError_t launch_prefill(const Args &a, cudaStream_t s) {
+    // The lengths are on the device; the totals say when one of the kernels has nothing to do.
+    const bool some_long = a.t_total > short_tokens(a.group), some_short = !some_long || a.n_seqs > 1;
+    if (some_long) {
+        const cudaError_t e = launch_long(a, s);
+        if (e != cudaSuccess) return e;
+    }
+    return some_short ? launch_prefill_short(a, some_long, s) : cudaSuccess;
 }
 
 }  // namespace attn

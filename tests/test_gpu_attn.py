@@ -81,6 +81,15 @@ PREFILL = [
 ]
 
 
+# the two-SM kernel's blocks (sequences over 256 tokens): groups that do not divide 128, a
+# group as large as a block, several blocks per pair, short sequences between long ones
+PREFILL += [
+    (128, 33, 1, [300]), (64, 100, 1, [270, 3]), (256, 128, 1, [259]), (128, 5, 1, [601, 258]),
+    (64, 3, 3, [257, 384, 385]), (256, 14, 2, [300, 20, 511]), (128, 24, 8, [513, 400, 256, 300]),
+    (64, 12, 12, [640, 641]),
+]
+
+
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("d,h_q,h_kv,lens", PREFILL)
 def test_prefill(d, h_q, h_kv, lens, dtype):
