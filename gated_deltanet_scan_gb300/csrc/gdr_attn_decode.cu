@@ -2,28 +2,29 @@
 //
 // Math.  For one key/value head the group's queries of the sequence's n_tok tokens
 // are rows r = j group + g of one small matrix Q (rows = n_tok group).  Over tiles
-// of 16 or 32 tokens, with x = scale log2(e) Q K^T and the running row maximum m,
+// of 16 tokens, with x = scale log2(e) Q K^T and the running row maximum m,
 //     p = 2^(x - m),   l += sum p,   O += P V,
 // earlier sums rescaled by 2^(m_old - m) when m grows; o = O / l at the end.  Two
 // parts of a row's tokens join the same way from their (m, l, O).
 //
 // Bound by HBM: keys and values are read once (4 h_kv d bytes a token) and little
-// else moves.  The tiles of all (sequence, key/value head, row block) triples lie
-// on one line, cut into equal parts, one per worker, so every worker streams the
-// same number of tiles whatever the lengths are.  A worker is RW warps of 16 rows
-// each (rows <= 16 RW) with a ring of shared-memory slots of their own, filled by
-// 16-byte asynchronous copies several tiles ahead: no worker waits for another, and
-// while one starts or ends a sequence the others of its SM keep the memory busy.
-// Both products are warp-level m16n8k16 MMAs on the 16-bit rows with fp32 sums: at 4
-// flops a byte the tensor pipes are far from busy, so the extra rows they pad cost
-// nothing.  A sequence that one worker sees whole is written by it; the others leave
-// (m, l, O): the workers of a block, next to each other on the line, join what they can
-// among themselves, and a second kernel, a programmatic dependent launch, joins the
-// blocks' parts from the workspace; always in the order of the tokens.
+// else moves.  Two kernels: this file's, for up to 16 rows (a decode step, a few draft
+// tokens), and gdr_attn_wide.cu's for more.  The tiles of all (sequence, key/value head,
+// row block) triples lie on one line, cut into equal parts, one per worker, so every
+// worker streams the same number of tiles whatever the lengths are.  Here a worker is
+// one warp with a ring of shared-memory slots of its own, filled by 16-byte asynchronous
+// copies several tiles ahead: no warp waits for another, and while one starts or ends a
+// sequence the others of its SM keep the memory busy.  Both products are warp-level
+// m16n8k16 MMAs on the 16-bit rows with fp32 sums: at 4 flops a byte the tensor pipes are
+// far from busy (17%), so the rows they pad cost nothing.  A sequence that one worker sees
+// whole is written by it; the others leave (m, l, O): the workers of a block, next to
+// each other on the line, join what they can among themselves, and a second kernel, a
+// programmatic dependent launch, joins the blocks' parts from the workspace; always in
+// the order of the tokens.
 //
 // P is rounded to the tensors' type for P V (its sum l is not): that is the only
 // rounding between the inputs and the output's own.
-#include "gdr_attn_common.cuh"
+#include "gdr_attn_line.cuh"
 #include "gdr_attn_mma.cuh"
 #include "gdr_internal.h"
 #include "tc_ptx.cuh"
@@ -34,213 +35,54 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kBlocks = 152;  // one resident block per SM
+constexpr int kTile = 16;  // tokens: the MMA's inner size in P V
 // P may exceed 1 by up to 2^kSlack before sums are rescaled: rounding is relative, so
 // P keeps its accuracy in either type, and most tiles rescale nothing.
 constexpr float kSlack = 6.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Tokens per tile.  A worker of one warp takes 16 (the MMA's inner size in P V; its ring
-// is 24 KiB).  Several warps meet once per step, so they take twice as many.
-__host__ __device__ constexpr int tile_of(int rw) { return rw == 1 ? 16 : 32; }
-
-template <int D, int RW>
-struct Shape {
-    static constexpr int TILE = tile_of(RW);
-    static constexpr int WORKERS = kWarps / RW;  // per block
-    // with two workers, joining their parts here costs more than the join kernel saves
-    static constexpr bool MERGE = WORKERS > 2;
-    static constexpr uint32_t SLOT = TILE * D * 2;
-    // about 24 KiB of ring per warp, at most 8 slots
-    static constexpr int FIT = RW * 24576 / (int)SLOT;
-    static constexpr int SLOTS = FIT < 8 ? FIT : 8;
-    static constexpr uint32_t SMEM = WORKERS * SLOTS * SLOT;
-    static_assert(SLOTS * SLOT >= RW * 16 * D * 4, "a ring holds its worker's part");
-};
-
-// Row warps for this many rows of a key/value head.
-int row_warps(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
-
-// On the line a triple takes its tiles and, before them, kLead<D> places for what
-// starting and ending it costs a worker (about 3 us, against 4 d bytes a token at a
-// worker's share of the bandwidth): a batch of many short sequences is cut evenly too.
 template <int D>
-constexpr int kLead = 512 / D;
-
-// Workspace: place of every sequence's first triple on the line ([n_seqs + 1], the last
-// one the total), then per worker two parts (its first and its last, cut, triple): per
-// row m and l, then O.
-struct Layout {
-    int rows, rw, blocks_of_rows, part_rows, workers;
-    size_t ml, o, total;
-};
-__host__ __device__ inline Layout layout(int rows, int rw, int d, int n_seqs) {
-    Layout L;
-    L.rows = rows;
-    L.rw = rw;
-    L.blocks_of_rows = (rows + 16 * rw - 1) / (16 * rw);
-    L.part_rows = rows < 16 * rw ? rows : 16 * rw;
-    L.workers = kBlocks * (kWarps / rw);
-    const size_t parts = (size_t)L.workers * 2 * L.part_rows;
-    L.ml = ((size_t)(n_seqs + 1) * 8 + 15) / 16 * 16;
-    L.o = L.ml + (parts * 8 + 15) / 16 * 16;
-    L.total = L.o + parts * d * 4;
-    return L;
-}
-
-// Tokens of sequence s; outside [0, limit] counts as none.
-__device__ __forceinline__ int64_t length_of(const Args &a, int s) {
-    const int64_t n = a.kv_lens[s];
-    return n < 0 || n > (int64_t)a.cache.max_pages * a.cache.page_size ? 0 : n;
-}
-// The line of `total` places in equal parts, the first `rest` one longer; never more
-// parts than places.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // a, b >= 0; mostly 32-bit values
-    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-struct Cut {
-    int64_t each, rest;
-    int parts, per_block;  // workers in use, and of each block: few places spread over many blocks
-    __device__ __forceinline__ Cut(int64_t total, int workers_per_block) {
-        per_block = total >= (int64_t)kBlocks * workers_per_block ? workers_per_block
-                                                                  : max(1, (int)((uint32_t)total / kBlocks));
-        parts = total < kBlocks * per_block ? (int)total : kBlocks * per_block;
-        each = parts > 0 ? quotient(total, parts) : 0;
-        rest = total - each * parts;
-    }
-    __device__ __forceinline__ int64_t start(int w) const { return each * w + (w < rest ? w : rest); }
-    __device__ __forceinline__ int part_of(int64_t place) const {
-        const int64_t longer = rest * (each + 1);
-        return (int)(place < longer ? quotient(place, each + 1) : rest + quotient(place - longer, each));
-    }
+struct Shape {
+    static constexpr uint32_t SLOT = kTile * D * 2;
+    static constexpr int FIT = 24576 / (int)SLOT;  // 24 KiB of ring per warp, at most 8 slots
+    static constexpr int SLOTS = FIT < 8 ? FIT : 8;
+    static constexpr uint32_t SMEM = kWarps * SLOTS * SLOT;
+    static_assert(SLOTS * SLOT >= 16 * D * 4, "a ring holds its worker's part");
 };
 
-template <int D, bool F16, int RW>
+template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Args a) {
-    using Sh = Shape<D, RW>;
-    constexpr int kTile = Sh::TILE;
+    using Sh = Shape<D>;
+    constexpr Spec sp = spec(false, D);
     constexpr int TT = kTile / 8;  // 8-token column tiles of S
     constexpr int KS = D / 16;   // inner steps of Q K^T
     constexpr int NT = D / 8;    // output column tiles
     constexpr int CPR = D / 8;   // 16-byte chunks of a row
-    constexpr int RPI = 32 / CPR < 1 ? 1 : 32 / CPR;  // rows one copy instruction of a warp covers
+    constexpr int RPI = 32 / CPR;  // rows one copy instruction of a warp covers
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ int64_t s_scan[kThreads + 1];
-    __shared__ int64_t s_warp[kWarps];
-    __shared__ int s_seq[Sh::WORKERS];
-    __shared__ int64_t s_base[Sh::WORKERS];
-    __shared__ int64_t s_cut[Sh::WORKERS];    // the triple a worker's part ends in, or -1
-    __shared__ float2 s_ml[kWarps * 16];      // m and l of its rows
+    __shared__ Line<kThreads, kWarps> s_line;
+    __shared__ int64_t s_cut[kWarps];     // the triple a worker's part ends in, or -1
+    __shared__ float2 s_ml[kWarps * 16];  // m and l of its rows
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int wk = warp / RW, rw = warp % RW;  // worker in the block, row warp in the worker
+    const int tid = threadIdx.x, wk = tid >> 5, lane = tid & 31;
     const int rows = a.n_tok * a.group;
-    const Layout L = layout(rows, RW, D, a.n_seqs);
-    int64_t *const line = reinterpret_cast<int64_t *>(a.ws);
-    const int64_t per_seq = (int64_t)a.h_kv * L.blocks_of_rows;
-
-    // The line: 256 sequences at a time, an exclusive scan of their tiles; the first
-    // pass finds the total, the second each worker's first sequence (one pass does
-    // both where there are up to 256 sequences).
-    int64_t total = 0;
-    const int chunks = (a.n_seqs + kThreads - 1) / kThreads;
-    if (tid < Sh::WORKERS) s_seq[tid] = -1;
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t base = 0;
-        for (int c = 0; c < chunks; ++c) {
-            if (pass == 0 || chunks > 1) {
-                const int s = c * kThreads + tid;
-                int64_t n = 0;
-                if (s < a.n_seqs) {
-                    n = length_of(a, s);
-                    if (pass == 0 && blockIdx.x == 0 && n != a.kv_lens[s]) record_invalid(a.err);
-                    if (n > 0) n = ((n + kTile - 1) / kTile + kLead<D>) * per_seq;
-                }
-                int64_t x = n;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-                    if (lane >= d) x += y;
-                }
-                __syncthreads();
-                if (lane == 31) s_warp[warp] = x;
-                __syncthreads();
-                int64_t before = 0;
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i)
-                    if (i < warp) before += s_warp[i];
-                s_scan[tid] = base + before + x - n;
-                if (tid == kThreads - 1) s_scan[kThreads] = base + before + x;
-                __syncthreads();
-            }
-            base = s_scan[kThreads];
-            if (pass == 1) {
-                const int s0 = c * kThreads, m = min(kThreads, a.n_seqs - s0);
-                if (tid < Sh::WORKERS) {  // the last sequence that starts at or before the worker's part
-                    const Cut cut(total, Sh::WORKERS);
-                    const int64_t at = cut.start(min((int)blockIdx.x * cut.per_block + tid, cut.parts));
-                    if (tid < cut.per_block && s_seq[tid] < 0 && at < base) {
-                        int lo = 0, hi = m - 1;
-                        while (lo < hi) {
-                            const int mid = (lo + hi + 1) >> 1;
-                            if (s_scan[mid] <= at)
-                                lo = mid;
-                            else
-                                hi = mid - 1;
-                        }
-                        s_seq[tid] = s0 + lo;
-                        s_base[tid] = s_scan[lo];
-                    }
-                }
-                if (blockIdx.x == 0) {
-                    if (tid < m) line[s0 + tid] = s_scan[tid];
-                    if (tid == 0 && c == chunks - 1) line[a.n_seqs] = base;
-                }
-            }
-        }
-        total = base;
-    }
-    __syncthreads();
-
-    const Cut cut(total, Sh::WORKERS);
-    const int me = blockIdx.x * cut.per_block + wk;  // a block's workers are next to each other on the line
-    int64_t at = cut.start(min(me, cut.parts));      // beyond the parts: nothing to do
-    const int64_t end = wk < cut.per_block ? cut.start(min(me + 1, cut.parts)) : at;
-    if (lane == 0 && rw == 0) s_cut[wk] = -1;
-    int s = s_seq[wk];
-    int64_t base = s_base[wk];
+    const Layout L = layout(rows, sp, D, a.n_seqs);
+    const Cut cut(s_line.place(a, sp, L.blocks_of_rows), kWarps);
+    int me;
+    Walk walk = s_line.walk(cut, wk, me);
+    if (lane == 0) s_cut[wk] = -1;
 
     const uint32_t slots = tc::smem_u32(ring) + wk * Sh::SLOTS * Sh::SLOT;
-    auto worker_sync = [&] {
-        if constexpr (RW == 1)
-            __syncwarp();
-        else
-            tc::named_sync(1 + wk, 32 * RW);
-    };
     float2 *const ml_parts = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + L.ml);
     float *const o_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + L.o);
     const float sc = a.scale * kLog2e;
     const int r0 = lane >> 2, cq = lane & 3;  // the MMA's row (and row + 8) and column pair of this lane
 
-    while (at < end) {
-        // the triple at `at`: sequence s (of `tiles` tiles), key/value head h, row block rb
-        int64_t len, tiles, places;
-        for (;;) {
-            len = length_of(a, s);
-            tiles = (len + kTile - 1) / kTile;
-            places = len > 0 ? tiles + kLead<D> : 0;
-            if (at < base + places * per_seq) break;
-            base += places * per_seq;
-            ++s;
-        }
-        const int hr = (int)quotient(at - base, places);
-        const int h = hr / L.blocks_of_rows, rb = hr - h * L.blocks_of_rows;
-        const int64_t seg0 = base + hr * places;  // where the triple starts on the line
-        const int tile0 = (int)max((int64_t)0, at - seg0 - kLead<D>);
-        const int tile1 = (int)min(tiles, end - seg0 - kLead<D>);
-        at = seg0 + places;
-        if (tile1 <= tile0) continue;  // only lead places: the next worker has the tiles
+    Triple tr;
+    while (walk.next(a, sp, L.blocks_of_rows, tr)) {
+        const int s = tr.s, h = tr.h, len = tr.len, tiles = tr.tiles, tile0 = tr.tile0, tile1 = tr.tile1;
+        const int64_t seg0 = tr.seg0;
         const int slot_of_part = cut.start(me) >= seg0 ? 0 : 1;
         const int steps = 2 * (tile1 - tile0);  // keys and values of a tile are a step each
         const int32_t *const pages = a.cache.table + (int64_t)s * a.cache.table_stride;
@@ -274,11 +116,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 }
                 const uint16_t *const from = (step & 1) ? a.cache.v : a.cache.k;
                 const uint32_t to = slots + (step % Sh::SLOTS) * Sh::SLOT;
-                // the worker's warps share the tile's rows
 #pragma unroll
                 for (int i = 0; i < kTile / RPI; ++i) {
-                    if (RW > 1 && i % RW != rw) continue;
-                    const int row = i * RPI + (RPI > 1 ? lane / CPR : 0);
+                    const int row = i * RPI + lane / CPR;
                     const int chunk = lane % CPR;
                     const int64_t o = __shfl_sync(0xffffffffu, off, row);
                     const bool ok = __shfl_sync(0xffffffffu, (int)there, row);
@@ -297,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         int seen[2];         // tokens the row sees
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = (rb * RW + rw) * 16 + r0 + 8 * i;
+            const int r = tr.rb * 16 + r0 + 8 * i;
             out_row[i] = -1;
             seen[i] = 0;
             const uint16_t *src = nullptr;
@@ -305,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 const int j = r / a.group, g = r - j * a.group;
                 const int64_t t = (int64_t)s * a.n_tok + j;
                 out_row[i] = t * a.h_q + h * a.group + g;
-                seen[i] = (int)max((int64_t)0, len - a.n_tok + j + 1);
+                seen[i] = max(0, len - a.n_tok + j + 1);
                 src = a.q.p + t * a.q.ts + (int64_t)(h * a.group + g) * a.q.hs;
             }
 #pragma unroll
@@ -314,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 qf[k][2 + i] = src ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 8 + cq * 2) : 0u;
             }
         }
-        const int64_t all_see = len - a.n_tok + 1;  // tokens every row sees
+        const int all_see = len - a.n_tok + 1;  // tokens every row sees
 
         float acc[NT][4];
 #pragma unroll
@@ -328,14 +168,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
             // --- keys: x = sc Q K^T
             cp_async_wait<Sh::SLOTS - 2>();
-            worker_sync();
+            __syncwarp();
             issue(step + Sh::SLOTS - 1);
-            // S in TT column tiles; with two of them each is summed in two chains, which hides
-            // the MMA's latency as four column tiles do
-            constexpr int CH = TT == 2 ? 2 : 1;
-            float x[CH][TT][4];
+            // two column tiles of 8 tokens, each summed in two chains, which hides the MMA's latency
+            float x[2][TT][4];
 #pragma unroll
-            for (int i = 0; i < CH * TT * 4; ++i) x[i / (TT * 4)][i / 4 % TT][i % 4] = 0.f;
+            for (int i = 0; i < 2 * TT * 4; ++i) x[i / (TT * 4)][i / 4 % TT][i % 4] = 0.f;
             {
                 const uint32_t kb = slots + (step % Sh::SLOTS) * Sh::SLOT;
                 const int row = (lane & 7) + ((lane >> 4) << 3);
@@ -350,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     for (int t = 0; t < TT; t += 2) {
                         uint32_t b[4];
                         ldsm4(at[k & 3] + t * 8 * D * 2 + (k >> 2) * 128, b);
-                        mma16816<F16>(x[k % CH][t], qf[k], b[0], b[1]);
-                        mma16816<F16>(x[k % CH][t + 1], qf[k], b[2], b[3]);
+                        mma16816<F16>(x[k & 1][t], qf[k], b[0], b[1]);
+                        mma16816<F16>(x[k & 1][t + 1], qf[k], b[2], b[3]);
                     }
                 }
             }
@@ -362,9 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 float v[2 * TT];
 #pragma unroll
                 for (int e = 0; e < 2 * TT; ++e) {
-                    v[e] = x[0][e >> 1][2 * i + (e & 1)];
-                    if (CH == 2) v[e] += x[CH - 1][e >> 1][2 * i + (e & 1)];
-                    v[e] *= sc;
+                    v[e] = sc * (x[0][e >> 1][2 * i + (e & 1)] + x[1][e >> 1][2 * i + (e & 1)]);
                     if (masked && p0 + (e >> 1) * 8 + cq * 2 + (e & 1) >= seen[i]) v[e] = -CUDART_INF_F;
                 }
                 float top = v[0];
@@ -397,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
             // --- values: O += P V
             cp_async_wait<Sh::SLOTS - 2>();
-            worker_sync();
+            __syncwarp();
             issue(step + Sh::SLOTS);
             const uint32_t vb = slots + ((step + 1) % Sh::SLOTS) * Sh::SLOT;
             if (masked && a.n_tok > 1) {
@@ -414,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 4; ++e) found = found || nonfinite<F16>(w[e]) || nonfinite<F16>(w[e] >> 16);
                 }
-                // every warp of the worker looked at the whole tile, so they agree
                 if (__any_sync(0xffffffffu, found)) {
 #pragma unroll 1
                     for (int t = 0; t < kTile; ++t) {
@@ -437,15 +272,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                             }
                         }
                     }
-                    worker_sync();
-                    for (int i = rw * 32 + lane; i < kTile * D / 2; i += 32 * RW) {
+                    __syncwarp();
+                    for (int i = lane; i < kTile * D / 2; i += 32) {
                         uint32_t w;
                         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vb + 4 * i) : "memory");
                         uint32_t z = nonfinite<F16>(w) ? w & 0xFFFF0000u : w;
                         z = nonfinite<F16>(w >> 16) ? z & 0xFFFFu : z;
                         if (z != w) asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + 4 * i), "r"(z) : "memory");
                     }
-                    worker_sync();
+                    __syncwarp();
                 }
             }
             {
@@ -467,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             }
         }
         cp_async_wait<0>();  // only empty groups are left
-        worker_sync();       // the ring is free for the next triple
+        __syncwarp();       // the ring is free for the next triple
 
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -491,15 +326,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         } else {
             // the part goes to the workspace, or, where the triple goes on in the next worker, to
             // the ring, which this worker has no more use for
-            const bool goes_on = Sh::MERGE && tile1 < tiles;
+            const bool goes_on = tile1 < tiles;
             const int64_t part = ((int64_t)me * 2 + slot_of_part) * L.part_rows;
-            float2 *const ml = goes_on ? s_ml + (warp - rw) * 16 : ml_parts + part;
+            float2 *const ml = goes_on ? s_ml + wk * 16 : ml_parts + part;
             float *const po = goes_on ? reinterpret_cast<float *>(ring + wk * Sh::SLOTS * Sh::SLOT) : o_parts + part * D;
-            if (goes_on && lane == 0 && rw == 0) s_cut[wk] = seg0;
+            if (goes_on && lane == 0) s_cut[wk] = seg0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (out_row[i] < 0) continue;
-                const int r = rw * 16 + r0 + 8 * i;
+                const int r = r0 + 8 * i;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     *reinterpret_cast<float2 *>(po + r * D + n * 8 + cq * 2) =
@@ -511,25 +346,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 
     // Parts of one triple that end with their workers are joined here, in the order of the
     // tokens, into the first of these workers' part.
-    if constexpr (!Sh::MERGE) return;
     __syncthreads();
 #pragma unroll 1
-    for (int w = 0; w < Sh::WORKERS; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         const int64_t seg0 = s_cut[w];
         if (seg0 < 0 || (w > 0 && s_cut[w - 1] == seg0)) continue;
         int last = w;
-        while (last + 1 < Sh::WORKERS && s_cut[last + 1] == seg0) ++last;
+        while (last + 1 < kWarps && s_cut[last + 1] == seg0) ++last;
         const int worker = blockIdx.x * cut.per_block + w;
         const int64_t part = ((int64_t)worker * 2 + (cut.start(worker) >= seg0 ? 0 : 1)) * L.part_rows;
         for (int x = tid; x < L.part_rows * (D / 2); x += kThreads) {
             const int r = x / (D / 2), c = x % (D / 2);
             float top = -CUDART_INF_F;
-            for (int i = w; i <= last; ++i) top = fmaxf(top, s_ml[i * RW * 16 + r].x);
+            for (int i = w; i <= last; ++i) top = fmaxf(top, s_ml[i * 16 + r].x);
             const float ref = top == -CUDART_INF_F ? 0.f : top;
             float2 o = make_float2(0.f, 0.f);
             float l = 0.f;
             for (int i = w; i <= last; ++i) {
-                const float2 v = s_ml[i * RW * 16 + r];
+                const float2 v = s_ml[i * 16 + r];
                 const float f = tc::fast_exp2(v.x - ref);
                 const float2 y = reinterpret_cast<const float2 *>(ring + i * Sh::SLOTS * Sh::SLOT)[r * (D / 2) + c];
                 l += f * v.y;
@@ -546,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 // tokens, and writes the rows that see nothing.  With WPR > 1 a block is WPR warps on 64
 // columns of one row, which share the row's parts; else a warp is one row.
 template <int D, bool F16, int WPR>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, const int rw) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, const bool wide) {
     constexpr int V = WPR > 1 ? 2 : D / 32;  // columns per lane
     constexpr int RPB = 8 / WPR;             // rows per block
     __shared__ float2 s_acc[WPR > 1 ? WPR : 1][32];
@@ -559,8 +393,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     const int hq = (int)(row - t * a.h_q);
     const int s = (int)(t / (uint32_t)a.n_tok), j = (int)(t - (uint32_t)s * a.n_tok);
     const int h = hq / a.group, g = hq - h * a.group;
-    const Layout L = layout(a.n_tok * a.group, rw, D, a.n_seqs);
-    const int r = j * a.group + g, rb = r / (16 * rw), lr = r - rb * 16 * rw;
+    const Spec sp = spec(wide, D);
+    const Layout L = layout(a.n_tok * a.group, sp, D, a.n_seqs);
+    const int r = j * a.group + g, rb = r / sp.block_rows, lr = r - rb * sp.block_rows;
     uint32_t *const dst = reinterpret_cast<uint32_t *>(a.o.p + t * a.o.ts + hq * a.o.hs);
     const bool write_lse = a.lse && lane == 0 && blockIdx.y == 0;
     const int64_t len = length_of(a, s);
@@ -573,21 +408,20 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         }
         return;
     }
-    const int tile = tile_of(rw);
-    const int64_t tiles = (len + tile - 1) / tile;
+    const int64_t tiles = (len + sp.tile - 1) / sp.tile;
     const int64_t *const line = reinterpret_cast<const int64_t *>(a.ws);
-    const int64_t seg0 = line[s] + ((int64_t)h * L.blocks_of_rows + rb) * (tiles + kLead<D>);
-    const Cut cut(line[a.n_seqs], 8 / rw);
-    const int w0 = cut.part_of(seg0 + kLead<D>), w1 = cut.part_of(seg0 + kLead<D> + tiles - 1);
+    const int64_t seg0 = line[s] + ((int64_t)h * L.blocks_of_rows + rb) * (tiles + sp.lead);
+    const Cut cut(line[a.n_seqs], sp.workers);
+    const int w0 = cut.part_of(seg0 + sp.lead), w1 = cut.part_of(seg0 + sp.lead + tiles - 1);
     if (w0 == w1) return;
 
     const float2 *const ml = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.ml);
     const float2 *const po = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.o);
     // a worker's part is its first where its own start is not before the triple's: so
     // all parts but perhaps the first one's
-    // all but the last worker's part are joined within their blocks (where these do): the parts
-    // are those of the first such worker of every block, and the last worker's
-    const int per_block = 8 / rw > 2 ? cut.per_block : 1, b0 = w0 / per_block;
+    // all but the last worker's part are joined within their blocks: the parts are those of the
+    // first such worker of every block, and the last worker's
+    const int per_block = cut.per_block, b0 = w0 / per_block;
     const int n_parts = (w1 - 1) / per_block - b0 + 2;
     const int64_t row0 = cut.start(w0) >= seg0 ? 0 : L.part_rows;
     auto part_row = [&](int i) {
@@ -658,55 +492,49 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     if (write_lse) a.lse[row] = sees ? kLn2 * (m + log2f(l)) : -CUDART_INF_F;
 }
 
-template <int D, bool F16, int RW>
-cudaError_t launch(const Args &a, cudaStream_t s) {
-    using Sh = Shape<D, RW>;
+template <int D, bool F16>
+cudaError_t launch_warps(const Args &a, cudaStream_t s) {
     static SmemOptIn opt_in;
-    cudaError_t e = opt_in.set(reinterpret_cast<const void *>(decode_kernel<D, F16, RW>), (int)Sh::SMEM);
+    const cudaError_t e = opt_in.set(reinterpret_cast<const void *>(decode_kernel<D, F16>), (int)Shape<D>::SMEM);
     if (e != cudaSuccess) return e;
-    decode_kernel<D, F16, RW><<<kBlocks, kThreads, Sh::SMEM, s>>>(a);
-    e = cudaGetLastError();
+    decode_kernel<D, F16><<<kBlocks, kThreads, Shape<D>::SMEM, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D, bool F16>
+cudaError_t launch(const Args &a, cudaStream_t s) {
+    const bool wide = is_wide(a.n_tok * a.group);
+    const cudaError_t e = wide ? launch_decode_wide(a, s) : launch_warps<D, F16>(a, s);
     if (e != cudaSuccess) return e;
     // The join: 8 warps on every 64 columns of a row where a row has many parts (few
-    // triples for the workers), else a warp per row.
+    // triples for the blocks), else a warp per row.
     const int64_t rows = a.t_total * a.h_q;
-    const Layout L = layout(a.n_tok * a.group, RW, D, a.n_seqs);
-    const int64_t parts = Sh::MERGE ? kBlocks : L.workers;
-    const bool wide = parts >= (int64_t)16 * a.n_seqs * a.h_kv * L.blocks_of_rows;
+    const Layout L = layout(a.n_tok * a.group, spec(wide, D), D, a.n_seqs);
+    const bool many = kBlocks >= (int64_t)16 * a.n_seqs * a.h_kv * L.blocks_of_rows;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = wide ? dim3((unsigned)rows, D / 64) : dim3((unsigned)((rows + 7) / 8));
+    cfg.gridDim = many ? dim3((unsigned)rows, D / 64) : dim3((unsigned)((rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 8>, a, RW)
-                : cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 1>, a, RW);
-}
-
-template <int D, bool F16>
-cudaError_t launch_rw(const Args &a, cudaStream_t s) {
-    switch (row_warps(a.n_tok * a.group)) {
-        case 1: return launch<D, F16, 1>(a, s);
-        case 2: return launch<D, F16, 2>(a, s);
-        case 4: return launch<D, F16, 4>(a, s);
-        default: return launch<D, F16, 8>(a, s);
-    }
+    return many ? cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 8>, a, wide)
+                : cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 1>, a, wide);
 }
 
 }  // namespace
 
 size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok) {
     const int rows = n_tok * (h_q / h_kv);
-    return layout(rows, row_warps(rows), d, n_seqs).total;
+    return layout(rows, spec(is_wide(rows), d), d, n_seqs).total;
 }
 
 cudaError_t launch_decode(const Args &a, cudaStream_t s) {
-    if (a.d == 64) return a.f16 ? launch_rw<64, true>(a, s) : launch_rw<64, false>(a, s);
-    if (a.d == 128) return a.f16 ? launch_rw<128, true>(a, s) : launch_rw<128, false>(a, s);
-    return a.f16 ? launch_rw<256, true>(a, s) : launch_rw<256, false>(a, s);
+    if (a.d == 64) return a.f16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    if (a.d == 128) return a.f16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    return a.f16 ? launch<256, true>(a, s) : launch<256, false>(a, s);
 }
 
 }  // namespace attn

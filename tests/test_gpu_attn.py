@@ -258,7 +258,20 @@ DECODE = [
     (64, 6, 2, 5, 16, False, [5, 4, 200]), (256, 4, 1, 2, 128, False, [2, 129, 1]), (128, 3, 3, 9, 7, True, [64, 10]),
     (256, 8, 8, 4, 256, False, [600]), (128, 24, 1, 8, 64, False, [130, 41]), (64, 128, 1, 16, 16, False, [37]),
     (256, 20, 1, 16, 16, False, [85]), (128, 16, 1, 3, 64, False, [260, 2]),
+    # 17 rows and more at other tile ends, many triples per worker
+    (256, 17, 1, 1, 64, False, [64, 63, 65, 128, 1]), (128, 9, 1, 2, 16, True, [700, 1, 2, 3]),
+    (64, 2, 1, 9, 48, False, [513, 8, 9, 10, 1000]), (256, 16, 4, 12, 33, True, [12, 2500, 11, 640]),
 ]
+
+
+@pytest.mark.parametrize("n_tok,h_q", [(16, 8), (1, 40)])
+def test_decode_wide_rows_many_sequences(n_tok, h_q):
+    gu.require_gpu()
+    rng = np.random.default_rng(26)
+    lens = [int(x) for x in rng.integers(0, 140, 230)]
+    c = Paged(rng, lens, 16, 2, 64, "bf16", stale=float("nan"))
+    check_decode(c, randn(rng, (230 * n_tok, h_q, 64), "bf16", 2.0), n_tok, "bf16")
+
 
 
 @pytest.mark.parametrize("dtype", DT)
@@ -295,14 +308,15 @@ def test_decode_more_heads_and_sequences_than_blocks():
     check_decode(c, randn(rng, (1500, 4, 64), "bf16"), 1, "bf16")
 
 
+@pytest.mark.parametrize("heads", [4, 1])  # 64 rows and 16: either kernel
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_decode_draft_tokens_never_see_later_ones(d, bad):
+def test_decode_draft_tokens_never_see_later_ones(d, bad, heads):
     torch = gu.require_gpu()
     rng = np.random.default_rng(23)
     n, n_tok = 203, 16
     c = Paged(rng, [n], 32, 1, d, "bf16")
-    q = randn(rng, (n_tok, 4, d), "bf16")
+    q = randn(rng, (n_tok, heads, d), "bf16")
     clean, _ = run_decode(c, q, n_tok)
     for j in (0, 5, 15):
         p = n - n_tok + j
