@@ -122,15 +122,17 @@ struct Block {
     int j_clean;  // the first of them that some row sees only in part
 };
 
-// A pair's blocks, found by one warp: block number `want` counts from the last block of
-// the last sequence, the one whose rows see most.  Numbers only grow, so the sequences
-// behind the cursor are not looked at again.
+// A pair's blocks, found by one warp.  Sequences are taken 32 at a time from the last, and
+// the blocks of such a group by their index in the sequence, the largest first: so the
+// longest blocks come first, and the pairs, which take a round's blocks in turn, back and
+// forth, come out even (8 prompts of 512 to 8192 tokens, sequence by sequence: the last
+// pair 6% over the mean).  Numbers only grow, so groups behind the cursor are not looked
+// at again.
 struct Cursor {
     int hi;         // sequences below this one are still to come
-    int64_t after;  // blocks (of one head) of the others
+    int64_t after;  // blocks (of one head) of the groups behind
     int item;       // round of this pair
     __device__ __forceinline__ bool next(const Args &a, int pair_id, int pairs, int lane, Block &b) {
-        // pairs take the blocks of a round in turn, back and forth: the sizes even out
         const int64_t number = (int64_t)item * pairs + ((item & 1) ? pairs - 1 - pair_id : pair_id);
         ++item;
         const int64_t want =
@@ -149,25 +151,34 @@ struct Cursor {
                 if (t1 - t0 <= short_tokens(a.group)) t1 = t0;  // the short kernel's
             }
             const int n = (int)((uint32_t)(t1 - t0 + per_pair - 1) / (uint32_t)per_pair);
-            int x = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
-            }
-            const int64_t end = after + x;
-            const uint32_t hit = __ballot_sync(0xffffffffu, want >= end - n && want < end);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
+            auto from = [&](int level) {  // blocks of this index or above in the group
+                return (int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)max(0, n - level));
+            };
+            const int64_t all = from(0), u = want - after;
+            if (u < all) {
+                int lo = 0, up = __reduce_max_sync(0xffffffffu, n);  // from(lo) > u >= from(up)
+                while (up - lo > 1) {
+                    const int mid = (lo + up) >> 1;
+                    if (from(mid) > u)
+                        lo = mid;
+                    else
+                        up = mid;
+                }
+                // the sequences that have a block `lo`, the last one first
+                const uint32_t have = __ballot_sync(0xffffffffu, n > lo);
+                const int rank = (int)(u - from(up));
+                const uint32_t me = __ballot_sync(
+                    0xffffffffu, n > lo && __popc(have & ((1u << lane) - 1u)) == rank);
+                const int src = __ffs(me) - 1;
                 b.t0 = __shfl_sync(0xffffffffu, t0, src);
                 b.len = (int)(__shfl_sync(0xffffffffu, t1, src) - b.t0);
                 b.h = (int)(number - want * a.h_kv);
-                b.first = (int)(__shfl_sync(0xffffffffu, end, src) - 1 - want) * per_pair;
+                b.first = lo * per_pair;
                 b.n = (min(b.len, b.first + per_pair) + kTile - 1) / kTile;
                 b.j_clean = (b.first + 1) >> 7;
                 return true;
             }
-            after += __shfl_sync(0xffffffffu, x, 31);
+            after += all;
             hi -= 32;
         }
         return false;
@@ -274,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // counts give stages, S tiles and barrier phases.  Stage order: K of tiles 0 .. A, V of
     // tile 0, K of tile A + 1, V of tile 1, ..., at the very end the last values.
 
-    // the launch's 512 x 128 registers become 128 x 56, 128 x 104 and 256 x 176
+    // the launch's 512 x 128 registers become 128 x 56, 128 x 120 and 256 x 168
     if (warp >= 8 && warp < 12) {
         pair::fewer_registers<56>();
         if (warp == 8) {
@@ -437,11 +448,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const uint32_t st = i % N, s_tile = g % S;
                 if (vj == 0 && v_it > 0 && !wait(Bar::OFree, v_it - 1)) break;
-                if (vj < vb.j_clean)
-                    wait(Bar::KvFull + st, i / N);
-                else
-                    ok = __all_sync(0xffffffffu, pair::wait_cluster(bar(Bar::KvFull + st), (i / N) & 1, kWaitLimit));
-                if (!ok || !wait(Bar::PFull + s_tile, g / S)) break;
+                // a looked-through tile that was written was released at cluster scope before this barrier
+                // was told; an acquire at that scope (2000 clocks a block) would be for this warp's own reads
+                if (!wait(Bar::KvFull + st, i / N) || !wait(Bar::PFull + s_tile, g / S)) break;
                 tc_fence_after_sync();
                 const uint64_t vd = v0 + (uint64_t)(st * (Sh::STAGE >> 4));
                 const uint32_t p = tmem + Sh::COLS_S + s_tile * kTile;
@@ -535,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         pair::cluster_sync();
     } else if (warp < 8) {
-        pair::more_registers<176>();
+        pair::more_registers<168>();
         // ---- P: warpgroup wg takes the tiles with g % 2 == wg; a thread is a row
         const int wg = warp >> 2, row = tid & 127, wq = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
@@ -663,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         pair::cluster_sync();
     } else {
-        pair::fewer_registers<104>();
+        pair::fewer_registers<120>();
         // ---- o = O / l; a thread is a row
         const int row = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -698,14 +707,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c0 = 0; c0 < D; c0 += COLS) {
                 uint32_t w[COLS / 2];
 #pragma unroll
-                for (int c = 0; c < COLS; c += 16) {
-                    uint32_t o[16];
-                    pair::tmem_load16(lanes + c0 + c, o);
+                for (int c = 0; c < COLS; c += 32) {
+                    uint32_t o[32];
+                    pair::tmem_load32(lanes + c0 + c, o);
                     if (live && patch) {
                         for (int p = b.j_clean * kTile; p <= token; ++p) {
                             const uint16_t *const v = a.v.p + (b.t0 + p) * a.v.ts + (int64_t)b.h * a.v.hs + c0 + c;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
+                            for (int e = 0; e < 32; ++e) {
                                 const float x = unpack1<F16>(v[e]);
                                 if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
                             }
@@ -713,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2)
+                    for (int e = 0; e < 32; e += 2)
                         w[(c + e) / 2] = pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
                 }
                 if (c0 + COLS == D) {  // this warp has read its part of O
