@@ -37,7 +37,8 @@ gdr_status check_cache(const gdr_kv_cache *c) {
     if (!stride_ok(c->page_stride) || !stride_ok(c->token_stride) || !stride_ok(c->head_stride))
         return GDR_ERR_INVALID_ARG;
     if (c->n_pages < 1 || c->page_size < 1 || c->max_pages < 1 || c->table_stride < 0) return GDR_ERR_INVALID_ARG;
-    if ((int64_t)c->page_size * c->max_pages > INT_MAX) return GDR_ERR_INVALID_ARG;
+    // positions and the ends of tiles past them are 32-bit
+    if ((int64_t)c->page_size * c->max_pages > INT_MAX - 1023) return GDR_ERR_INVALID_ARG;
     return GDR_OK;
 }
 

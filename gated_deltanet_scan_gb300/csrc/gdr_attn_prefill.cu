@@ -148,7 +148,8 @@ struct Cursor {
                     record_invalid(a.err);
                     t0 = t1 = 0;
                 }
-                if (t1 - t0 <= short_tokens(a.group)) t1 = t0;  // the short kernel's
+                // the short kernel's, which is launched beside this one for several sequences
+                if (a.n_seqs > 1 && t1 - t0 <= short_tokens(a.group)) t1 = t0;
             }
             const int n = (int)((uint32_t)(t1 - t0 + per_pair - 1) / (uint32_t)per_pair);
             auto from = [&](int level) {  // blocks of this index or above in the group
@@ -448,8 +449,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const uint32_t st = i % N, s_tile = g % S;
                 if (vj == 0 && v_it > 0 && !wait(Bar::OFree, v_it - 1)) break;
-                // a looked-through tile that was written was released at cluster scope before this barrier
-                // was told; an acquire at that scope (2000 clocks a block) would be for this warp's own reads
+                // A looked-through tile that was written was released at cluster scope before this barrier
+                // was told, and is read by the MMA alone.  Waits acquire at CTA scope here and for the flags
+                // (this CTA's own shared memory): at cluster scope each took 2500 clocks a block.
                 if (!wait(Bar::KvFull + st, i / N) || !wait(Bar::PFull + s_tile, g / S)) break;
                 tc_fence_after_sync();
                 const uint64_t vd = v0 + (uint64_t)(st * (Sh::STAGE >> 4));
@@ -686,8 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                  : nullptr;
             if (!wait(Bar::Inv + (it & 1), it >> 1)) break;
             const float inv = s_inv[(it & 1) * 128 + row];
-            ok = __all_sync(0xffffffffu, pair::wait_cluster(bar(Bar::Patch + (it & 3)), (it >> 2) & 1, kWaitLimit));
-            if (!ok) break;
+            if (!wait(Bar::Patch + (it & 3), it >> 2)) break;
             volatile uint32_t *const flags = s_flags + (it & 3) * 2;
             const bool patch = flags[0] | flags[1];
             __syncwarp();

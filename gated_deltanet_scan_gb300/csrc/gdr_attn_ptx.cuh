@@ -54,22 +54,6 @@ __device__ __forceinline__ void arrive_expect_remote(uint32_t cluster_bar, uint3
 __device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-// A bounded wait that acquires at cluster scope, the other side of arrive_remote_release.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, long long limit) {
-    const long long t0 = clock64();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(8192u)
-            : "memory");
-        if (ok) return true;
-        if (clock64() - t0 > limit) return false;
-    }
-}
 // Two fp32 values in one 64-bit register, and arithmetic on both.
 __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
     uint64_t r;

@@ -253,11 +253,35 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                             w.w = seen > 0 ? pack2<F16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv) : 0u;
                             *reinterpret_cast<uint4 *>(dst + e) = w;
                         }
-                    } else if (live) {
+                    } else if (!whole) {
+                        // four lanes store 64 bytes of a row together: pieces of 16 bytes are
+                        // transposed among them, in two halves of 16 columns
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4 *>(o_parts + part * D + c + e) =
-                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                            for (int p = 0; p < 8; p += 2) {
+                                uint32_t &y = o[p * 4 + e], &z = o[p * 4 + 4 + e];
+                                const uint32_t v = __shfl_xor_sync(0xffffffffu, (lane & 1) ? y : z, 1);
+                                ((lane & 1) ? y : z) = v;
+                            }
+#pragma unroll
+                            for (int p = 0; p < 8; p += 4) {
+#pragma unroll
+                                for (int q = p; q < p + 2; ++q) {
+                                    uint32_t &y = o[q * 4 + e], &z = o[q * 4 + 8 + e];
+                                    const uint32_t v = __shfl_xor_sync(0xffffffffu, (lane & 2) ? y : z, 2);
+                                    ((lane & 2) ? y : z) = v;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) {
+                            const int back = (lane & 3) - (p & 3);  // this lane's row is `back` below the piece's
+                            if (r - back < rows)
+                                *reinterpret_cast<uint4 *>(o_parts + (part - back) * D + c + (p >> 2) * 16 +
+                                                           (lane & 3) * 4) =
+                                    make_uint4(o[p * 4], o[p * 4 + 1], o[p * 4 + 2], o[p * 4 + 3]);
+                        }
                     }
                     __syncwarp();
                 }

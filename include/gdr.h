@@ -465,7 +465,7 @@ typedef struct gdr_rows {
  * aligned; strides in elements, multiples of 8, not negative, below 2^38; offsets are
  * computed in 64 bits.  page_table: DEVICE int32, entries of pages a sequence
  * does not reach yet are not read.  page_size and max_pages (pages a table row
- * holds) are at least 1, and page_size * max_pages below 2^31.  A page id outside
+ * holds) are at least 1, and page_size * max_pages at most 2^31 - 1024.  A page id outside
  * [0, n_pages) is never followed: the kernels record GDR_ERR_INVALID_ARG in the
  * device error word and leave out its writes (append) or read zeros (decode: that
  * sequence's results are then meaningless).

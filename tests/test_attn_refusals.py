@@ -77,7 +77,7 @@ def test_rows(L, bad):
 @pytest.mark.parametrize("bad", [
     dict(k=None), dict(v=A + 2), dict(page_table=None), dict(page_table=A + 2), dict(page_stride=12),
     dict(token_stride=-8), dict(head_stride=4), dict(n_pages=0), dict(page_size=0), dict(max_pages=0),
-    dict(table_stride=-1), dict(page_size=1 << 16, max_pages=1 << 15),
+    dict(table_stride=-1), dict(page_size=1 << 16, max_pages=1 << 15), dict(page_size=1, max_pages=(1 << 31) - 1023),
 ])
 def test_cache(L, bad):
     assert append(L, c=cache(**bad)) == BAD
