@@ -531,3 +531,54 @@ def test_prefill_inputs_may_be_expanded():
     v = randn(rng, (1, 2, 64), "bf16").expand(150, 2, 64)
     check_prefill(q, k, v, [150], "bf16")
     check_prefill(q[:1].expand(150, 4, 64), k, v, [100, 50], "bf16")
+
+
+# --- offsets past 32 bits -----------------------------------------------------------------------------------
+
+def spread(torch, shape, strides, dtype):
+    """An uninitialised tensor of this shape and strides (its own allocation)."""
+    size = 1 + sum((n - 1) * s for n, s in zip(shape, strides))
+    return torch.empty(size, dtype=dtype, device="cuda").as_strided(shape, strides)
+
+
+@pytest.mark.parametrize("n_tok,h_q", [(1, 4), (4, 8)])
+def test_pages_far_apart(n_tok, h_q):
+    """Pages 2^32 elements apart: offsets in the cache pass 32 bits."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(60)
+    lens, page, d = [45, 20], 16, 64
+    c = Paged(rng, lens, page, 1, d, "bf16", spare=0)
+    shape, strides = (c.k.shape[0], page, 1, d), (1 << 32, d, d, 1)
+    far_k, far_v = spread(torch, shape, strides, c.k.dtype), spread(torch, shape, strides, c.k.dtype)
+    far_k.copy_(c.k)
+    far_v.copy_(c.v)
+    k, v = randn(rng, (2 * n_tok, 1, d), "bf16"), randn(rng, (2 * n_tok, 1, d), "bf16")
+    q = randn(rng, (2 * n_tok, h_q, d), "bf16")
+    for cache in ((c.k, c.v), (far_k, far_v)):
+        gdr.gdr_attn_append(None, k, v, None, None, *cache, c.table, c.kv_lens, None)
+    assert torch.equal(far_k, c.k) and torch.equal(far_v, c.v)
+    near, _ = check_decode(c, q, n_tok, "bf16")
+    o = nan_like(q.shape, q.dtype)
+    gdr.gdr_attn_decode(q, far_k, far_v, c.table, c.kv_lens, o, n_tok)
+    torch.cuda.synchronize()
+    no_error()
+    assert torch.equal(o, near)
+
+
+@pytest.mark.parametrize("lens", [[40], [20, 20], [300]])
+def test_rows_far_apart(lens):
+    """Tokens 2^24 and more elements apart: offsets in the rows pass 32 bits."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(61)
+    T, d = sum(lens), 64
+    q, k, v = randn(rng, (T, 2, d), "bf16"), randn(rng, (T, 1, d), "bf16"), randn(rng, (T, 1, d), "bf16")
+    near, _ = check_prefill(q, k, v, lens, "bf16")
+    ts = 1 << (27 if T < 100 else 24)
+    far = [spread(torch, t.shape, (ts, d, 1), t.dtype) for t in (q, k, v, near)]
+    for t, src in zip(far, (q, k, v)):
+        t.copy_(src)
+    cu = ints(np.concatenate([[0], np.cumsum(lens)]))
+    gdr.gdr_attn_prefill(*far, cu)
+    torch.cuda.synchronize()
+    no_error()
+    assert torch.equal(far[3], near)
