@@ -20,11 +20,14 @@ struct Spec {
     int workers;     // per block of threads
     int lead;        // places
 };
-// The warp kernel: workers of one warp and 16 rows.  A start costs about 3 us, a tile 32 d
-// bytes of keys and as many of values at a 1216th of the bandwidth.  The wide kernel: one worker
-// of 128 rows per SM, 4 us against tiles of 64 tokens at a 152nd.
+// The warp kernel: workers of one warp and 16 rows, a tile 32 d bytes of keys and as many of
+// values at a 1216th of the bandwidth (d = 256: 3 us).  The wide kernel: one worker of 128
+// rows per SM, tiles of 64 tokens.  Leads measured: 512 / d, 1024 / d and 1536 / d places for
+// the first (25 sequences of d = 256 42.3, 39.4, 37.3 us; 64 sequences 120.8, 120.8, 121.6; 96 of
+// d = 128 119.5, 119.7, 121.5); 3, 4 and 6 for the second (16 draft tokens 44.6, 42.2, 41.2; 51
+// sequences of d = 128 43.7, 40.4, 42.0; 52 of d = 64 22.4, 23.0, 23.5).
 __host__ __device__ constexpr Spec spec(bool wide, int d) {
-    return wide ? Spec{128, 64, 1, 768 / d} : Spec{kWarpRows, 16, 8, 512 / d};
+    return wide ? Spec{128, 64, 1, 4} : Spec{kWarpRows, 16, 8, 1024 / d};
 }
 inline bool is_wide(int rows) { return rows > kWarpRows; }
 
