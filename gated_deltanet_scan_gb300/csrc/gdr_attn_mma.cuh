@@ -52,6 +52,17 @@ __device__ __forceinline__ bool nonfinite(uint32_t half_word) {
     constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
     return (half_word & e) == e;
 }
+// True if any of eight is: only an exponent of ones carries into its value's top bit.
+template <bool F16>
+__device__ __forceinline__ bool any_nonfinite(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    constexpr uint32_t e = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
+    return ((((a & e) + one) | ((b & e) + one) | ((c & e) + one) | ((d & e) + one)) & 0x80008000u) != 0;
+}
+// The word with infinities and NaNs replaced by zeros.
+template <bool F16>
+__device__ __forceinline__ uint32_t cleaned(uint32_t w) {
+    return w & (nonfinite<F16>(w) ? 0xFFFF0000u : ~0u) & (nonfinite<F16>(w >> 16) ? 0xFFFFu : ~0u);
+}
 
 }  // namespace attn
 }  // namespace gdr

@@ -36,6 +36,7 @@
 // NaNs by zeros before the MMA reads it; where they found any, the rows that do see
 // them get them added at the end.
 #include "gdr_attn_common.cuh"
+#include "gdr_attn_mma.cuh"
 #include "gdr_attn_ptx.cuh"
 #include "gdr_internal.h"
 #include "tc_ptx.cuh"
@@ -495,22 +496,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     turns ^= 1u << st;
                     bool here = false;
                     uint4 *const tile = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE);
-                    constexpr uint32_t e = F16 ? 0x7C007C00u : 0x7F807F80u;
-#pragma unroll 4
-                    for (int x = tid - 320; ok && x < (int)Sh::STAGE / 16; x += 64) {
-                        uint4 w = tile[x];
-                        uint32_t *const p = &w.x;
-                        bool bad = false;
+                    if (ok) {
+                        constexpr int PER = Sh::STAGE / 16 / 64;  // 16-byte pieces per thread
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const bool lo = (p[y] & e & 0xFFFFu) == (e & 0xFFFFu);
-                            const bool hi = (p[y] & e & 0xFFFF0000u) == (e & 0xFFFF0000u);
-                            bad = bad || lo || hi;
-                            p[y] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
-                        }
-                        if (bad) {
-                            tile[x] = w;
-                            here = true;
+                        for (int x0 = 0; x0 < PER; x0 += 8) {
+                            uint4 w[8];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) w[x] = tile[tid - 320 + (x0 + x) * 64];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                if (!any_nonfinite<F16>(w[x].x, w[x].y, w[x].z, w[x].w)) continue;
+                                tile[tid - 320 + (x0 + x) * 64] =
+                                    make_uint4(cleaned<F16>(w[x].x), cleaned<F16>(w[x].y), cleaned<F16>(w[x].z),
+                                               cleaned<F16>(w[x].w));
+                                here = true;
+                            }
                         }
                     }
                     if (here) fence_proxy_async_smem();

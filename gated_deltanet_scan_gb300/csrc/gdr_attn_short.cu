@@ -137,8 +137,7 @@ __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__
                                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                                  : "r"(vb + 16 * i)
                                  : "memory");
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) found = found || nonfinite<F16>(w[e]) || nonfinite<F16>(w[e] >> 16);
+                    found = found || any_nonfinite<F16>(w[0], w[1], w[2], w[3]);
                 }
                 found = __syncthreads_or(found);
                 if (found) {
@@ -165,8 +164,7 @@ __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__
                     for (int i = tid; i < kTile * D / 2; i += kThreads) {
                         uint32_t w;
                         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vb + 4 * i) : "memory");
-                        uint32_t z = nonfinite<F16>(w) ? w & 0xFFFF0000u : w;
-                        z = nonfinite<F16>(w >> 16) ? z & 0xFFFFu : z;
+                        const uint32_t z = cleaned<F16>(w);
                         if (z != w) asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + 4 * i), "r"(z) : "memory");
                     }
                     __syncthreads();

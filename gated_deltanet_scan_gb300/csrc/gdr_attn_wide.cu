@@ -306,17 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                 uint4 *const p = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE +
                                                            (chunk >> 3) * Sh::BOX + row * 128 +
                                                            (((chunk & 7) ^ (row & 7)) << 4));
-                uint4 v = *p;
-                uint32_t *const q = &v.x;
-                bool bad = false;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const bool lo = nonfinite<F16>(q[y]), hi = nonfinite<F16>(q[y] >> 16);
-                    bad = bad || lo || hi;
-                    q[y] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
-                }
-                if (bad) *p = v;
-                found = found || bad;
+                const uint4 v = *p;
+                if (!any_nonfinite<F16>(v.x, v.y, v.z, v.w)) continue;
+                *p = make_uint4(cleaned<F16>(v.x), cleaned<F16>(v.y), cleaned<F16>(v.z), cleaned<F16>(v.w));
+                found = true;
             }
             if (found) *s_found = 1;
         };
