@@ -41,6 +41,23 @@ __device__ __forceinline__ float unpack1(uint16_t w) {
         return __uint_as_float((uint32_t)w << 16);
 }
 
+// The reference m of a row's weights p = 2^(x - m), which enter P V in 16 bits.  Sums are
+// rescaled when m moves, so it follows the row's maximum only when that is TOP above it,
+// and is then LEAD under it.  bf16 rounds weights of any size relative to themselves.  fp16
+// does so from 2^-14 up, and its largest value is just under 2^16: with weights of up to
+// 2^TOP = 2^15, those of a row's other tokens keep their accuracy down to 2^-22 of the
+// largest one and are lost below 2^-33, at no cost (a reference at the maximum itself:
+// 2^-14 and 2^-25, which many tokens of little weight add up to).
+template <bool F16>
+struct Reference {
+    static constexpr float LEAD = F16 ? 8.f : 0.f, TOP = F16 ? 15.f : 8.f;
+};
+template <bool F16>
+__device__ __forceinline__ float next_reference(float m, float top) {
+    using R = Reference<F16>;
+    return top > m + R::TOP || m == -CUDART_INF_F ? fmaxf(m, top - R::LEAD) : m;
+}
+
 // Sequence of token t among packed starts cu[0 .. n]: the last s < n with cu[s] <= t (or
 // 0).  The whole warp looks, 32 places at a time: two rounds of loads for a thousand.
 __device__ __forceinline__ int find_seq_warp(const int32_t *cu, int n, int64_t t, int lane) {

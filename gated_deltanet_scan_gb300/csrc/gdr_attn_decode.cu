@@ -36,9 +36,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // tokens: the MMA's inner size in P V
-// P may exceed 1 by up to 2^kSlack before sums are rescaled: rounding is relative, so
-// P keeps its accuracy in either type, and most tiles rescale nothing.
-constexpr float kSlack = 6.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D>
@@ -208,8 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 for (int e = 1; e < 2 * TT; ++e) top = fmaxf(top, v[e]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // the reference m follows the maximum only when that is kSlack above it
-                const float mn = top > m[i] + kSlack || m[i] == -CUDART_INF_F ? fmaxf(m[i], top) : m[i];
+                const float mn = next_reference<F16>(m[i], top);
                 const float ref = mn == -CUDART_INF_F ? 0.f : mn;  // nothing visible yet: p = 2^-inf
                 c[i] = m[i] == mn ? 1.f : tc::fast_exp2(m[i] - ref);
                 m[i] = mn;

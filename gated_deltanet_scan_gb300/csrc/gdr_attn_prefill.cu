@@ -5,8 +5,8 @@
 // r % group of its token r / group.  Over tiles of 128 tokens, with the running
 // reference m of each row,
 //     x = sc Q K^T  (sc = scale log2 e),   p = 2^(x - m),   l += sum p,   O += P V,
-// and o = O / l at the end.  m follows the row's maximum only when that is 2^8 above
-// it; O and l are then multiplied by 2^(m_old - m).
+// and o = O / l at the end.  m lies under the row's maximum as Reference says and follows
+// it only when p could grow too large; O and l are then multiplied by 2^(m_old - m).
 //
 // Bound by the tensor cores: 4 d flops a visible (query, token) pair.  A pair of CTAs
 // (a cluster of two SMs) works on 256 rows with cta_group::2 MMAs: each CTA holds its
@@ -53,7 +53,6 @@ constexpr int kRows = 128;  // rows per CTA
 constexpr int kTile = 128;  // tokens per tile
 constexpr long long kWaitLimit = 4000000000LL;  // SM clocks (about 2 s)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;
 
 template <int D>
 struct Shape {
@@ -594,8 +593,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // written again only after this wait, also between two blocks' tiles
                 if (g > 0 && !wait(Bar::MReady + wq, g - 1)) break;
                 const float m_prev = j > 0 ? s_m[row] : -CUDART_INF_F;
-                const bool raise = j == 0 || x_top > m_prev + kSlack;
-                const float m = raise ? x_top : m_prev;
+                const bool raise = j == 0 || x_top > m_prev + Reference<F16>::TOP;
+                const float m = raise ? x_top - Reference<F16>::LEAD : m_prev;
                 s_m[row] = m;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(Bar::MReady + wq));

@@ -21,7 +21,6 @@ constexpr int kThreads = 128;
 constexpr int kRows = 64;  // rows per block
 constexpr int kTile = 32;  // tokens per tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 6.f;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__ Args a) {
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__
                     for (int e = 1; e < 8; ++e) top = fmaxf(top, v[e]);
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float mn = top > m[i] + kSlack || m[i] == -CUDART_INF_F ? fmaxf(m[i], top) : m[i];
+                    const float mn = next_reference<F16>(m[i], top);
                     const float ref = mn == -CUDART_INF_F ? 0.f : mn;
                     c[i] = m[i] == mn ? 1.f : tc::fast_exp2(m[i] - ref);
                     m[i] = mn;

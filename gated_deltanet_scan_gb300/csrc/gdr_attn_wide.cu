@@ -37,7 +37,6 @@ constexpr int kThreads = 384;
 constexpr int kRows = 128, kTile = 64;
 constexpr long long kWaitLimit = 4000000000LL;  // SM clocks (about 2 s)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;
 constexpr uint32_t kColsS = 256;  // TMEM: O at 0, S tiles at 256 and 320
 
 template <int D>
@@ -168,8 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     }
                     const float x_top = sc * fmaxf(pair::max3(top[0], top[1], top[2]), top[3]);
                     const float m_old = m;
-                    const bool raise = x_top > m + kSlack || m == -CUDART_INF_F;
-                    if (raise) m = fmaxf(m, x_top);
+                    m = next_reference<F16>(m, x_top);
                     const float ref = m == -CUDART_INF_F ? 0.f : m;  // nothing visible yet: p = 2^-inf
                     const float f = m_old == m ? 1.f : fast_exp2(m_old - ref);
                     if (tile > t.tile0 && __any_sync(0xffffffffu, f != 1.f)) {

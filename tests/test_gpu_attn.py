@@ -582,3 +582,37 @@ def test_rows_far_apart(lens):
     torch.cuda.synchronize()
     no_error()
     assert torch.equal(far[3], near)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [40, 400])
+@pytest.mark.parametrize("weight", [-14.25, -17.0])
+def test_small_weights_keep_their_accuracy(n, d, dtype, weight):
+    """The first token outweighs the others by 2^20 or 2^24 but has no value in half of the columns, so these
+    are sums of small weights alone."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(n + d)
+    q, k, v = torch.zeros(n, 8, d), torch.zeros(n, 2, d), torch.from_numpy(rng.uniform(0.5, 1.5, (n, 2, d)))
+    q[:, :, 3], k[1:, :, 3], v[0, :, d // 2:] = 1.0, weight, 0.0
+    q, k, v = (x.to(tdt(dtype)).cuda() for x in (q, k, v))
+
+    def check(o, lse, rows):
+        wo, wl, bo, bl = ar.prefill(f64(q), f64(k), f64(v), 1.0, [n], dtype)
+        # h of every weight holds down to 2^-22 of the largest; below, half a step of 2^-32 each
+        loose = 1.5 * n * 2.0 ** -33 if dtype == "f16" and weight < -15.25 else 0.0
+        close(o, wo[rows], bo[rows] + loose, "o")
+        close(lse, wl[rows], bl[rows], "lse")
+
+    o, lse = nan_like((n, 8, d), q.dtype), nan_like((n, 8), torch.float32)
+    gdr.gdr_attn_prefill(q, k, v, o, ints([0, n]), scale=1.0, lse=lse)
+    check(o, lse, slice(0, n))
+    page = 16
+    kc, vc = (torch.zeros(n // page + 1, page, 2, d, dtype=q.dtype, device="cuda") for _ in range(2))
+    kc.view(-1, 2, d)[:n], vc.view(-1, 2, d)[:n] = k, v
+    for n_tok in (1, 16):  # 4 rows and 64: either kernel
+        o, lse = nan_like((n_tok, 8, d), q.dtype), nan_like((n_tok, 8), torch.float32)
+        gdr.gdr_attn_decode(q[n - n_tok:], kc, vc, ints(range(n // page + 1)).view(1, -1), ints([n]), o, n_tok,
+                            scale=1.0, lse=lse)
+        check(o, lse, slice(n - n_tok, n))
+    no_error()
