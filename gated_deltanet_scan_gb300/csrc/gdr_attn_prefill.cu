@@ -51,8 +51,16 @@ constexpr int kThreads = 512;
 constexpr int kPairs = 76;   // CTA pairs on 152 SMs
 constexpr int kRows = 128;  // rows per CTA
 constexpr int kTile = 128;  // tokens per tile
-constexpr long long kWaitLimit = 4000000000LL;  // SM clocks (about 2 s)
+constexpr uint32_t kWaitLimit = 3000000000u;  // SM clocks (about 1.5 s)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// mbar_wait_bounded with a 32-bit clock, which a poll reads often enough, in few instructions.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
+    const uint32_t t0 = (uint32_t)clock();
+    while (!mbar_try_wait(bar, parity))
+        if ((uint32_t)clock() - t0 > kWaitLimit) return false;
+    return true;
+}
 
 template <int D>
 struct Shape {
@@ -266,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     // every lane of the warp waits, and all of them go on or give up
     auto wait = [&](int i, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(bar(i), parity & 1, kWaitLimit)) != 0;
+        ok = __all_sync(0xffffffffu, ok && wait_bounded(bar(i), parity & 1)) != 0;
         return ok;
     };
     // Block number `it` of this pair, from the entry the loading warp left; n = 0: there is none.
@@ -491,24 +499,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         k_count += kb.n;
                     }
                     const uint32_t st = (g + min(g + A + 1, k_count)) % N;
-                    ok = ok && mbar_wait_bounded(bar(Bar::VLocal + st), (turns >> st) & 1, kWaitLimit);
+                    ok = ok && wait_bounded(bar(Bar::VLocal + st), (turns >> st) & 1);
                     turns ^= 1u << st;
                     bool here = false;
                     uint4 *const tile = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE);
                     if (ok) {
                         constexpr int PER = Sh::STAGE / 16 / 64;  // 16-byte pieces per thread
-#pragma unroll
+#pragma unroll 1
                         for (int x0 = 0; x0 < PER; x0 += 8) {
-                            uint4 w[8];
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) w[x] = tile[tid - 320 + (x0 + x) * 64];
+                            bool bad = false;
 #pragma unroll
                             for (int x = 0; x < 8; ++x) {
-                                if (!any_nonfinite<F16>(w[x].x, w[x].y, w[x].z, w[x].w)) continue;
-                                tile[tid - 320 + (x0 + x) * 64] =
-                                    make_uint4(cleaned<F16>(w[x].x), cleaned<F16>(w[x].y), cleaned<F16>(w[x].z),
-                                               cleaned<F16>(w[x].w));
-                                here = true;
+                                const uint4 w = tile[tid - 320 + (x0 + x) * 64];
+                                bad = bad || any_nonfinite<F16>(w.x, w.y, w.z, w.w);
+                            }
+                            here = here || bad;
+                            if (!bad) continue;
+#pragma unroll 1
+                            for (int x = 0; x < 8; ++x) {
+                                uint4 &w = tile[tid - 320 + (x0 + x) * 64];
+                                w = make_uint4(cleaned<F16>(w.x), cleaned<F16>(w.y), cleaned<F16>(w.z),
+                                               cleaned<F16>(w.w));
                             }
                         }
                     }
@@ -574,8 +585,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (j * kTile + kTile - 1 > mine) {  // some row of this CTA sees only part of the tile
                     const int seen = token - j * kTile;  // columns 0 .. seen
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > seen) r[c] = 0xFF800000u;
+                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                        const int last = seen - c0;
+                        const uint32_t sees = last < 0 ? 0u : last >= 31 ? ~0u : (2u << last) - 1u;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(sees & (1u << c))) r[c0 + c] = 0xFF800000u;
+                    }
                 }
                 float top[4];
 #pragma unroll
@@ -710,17 +726,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < COLS; c += 32) {
                     uint32_t o[32];
                     pair::tmem_load32(lanes + c0 + c, o);
-                    if (live && patch) {
-                        for (int p = b.j_clean * kTile; p <= token; ++p) {
-                            const uint16_t *const v = a.v.p + (b.t0 + p) * a.v.ts + (int64_t)b.h * a.v.hs + c0 + c;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float x = unpack1<F16>(v[e]);
-                                if (!isfinite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
-                            }
-                        }
-                    }
-                    __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
                         w[(c + e) / 2] = pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
@@ -759,6 +764,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
+            // what the looked-through tiles' infinities and NaNs add to the rows that see them, in the
+            // stored row: a rare path, kept small (the roles' code has to fit the instruction cache)
+            if (live && patch) {
+#pragma unroll 1
+                for (int p = b.j_clean * kTile; p <= token; ++p) {
+                    const uint16_t *const v = a.v.p + (b.t0 + p) * a.v.ts + (int64_t)b.h * a.v.hs;
+#pragma unroll 1
+                    for (int c = 0; c < D; ++c) {
+                        const float x = unpack1<F16>(v[c]);
+                        if (!isfinite(x)) dst[c] = (uint16_t)pack2<F16>(unpack1<F16>(dst[c]) + x, 0.f);
+                    }
+                }
+            }
+            __syncwarp();
         }
         if (!ok) gave_up();
         __syncwarp();
