@@ -51,16 +51,7 @@ constexpr int kThreads = 512;
 constexpr int kPairs = 76;   // CTA pairs on 152 SMs
 constexpr int kRows = 128;  // rows per CTA
 constexpr int kTile = 128;  // tokens per tile
-constexpr uint32_t kWaitLimit = 3000000000u;  // SM clocks (about 1.5 s)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// mbar_wait_bounded with a 32-bit clock, which a poll reads often enough, in few instructions.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
-    const uint32_t t0 = (uint32_t)clock();
-    while (!mbar_try_wait(bar, parity))
-        if ((uint32_t)clock() - t0 > kWaitLimit) return false;
-    return true;
-}
 
 template <int D>
 struct Shape {
@@ -274,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     // every lane of the warp waits, and all of them go on or give up
     auto wait = [&](int i, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && wait_bounded(bar(i), parity & 1)) != 0;
+        ok = __all_sync(0xffffffffu, ok && pair::wait_bounded(bar(i), parity & 1)) != 0;
         return ok;
     };
     // Block number `it` of this pair, from the entry the loading warp left; n = 0: there is none.
@@ -328,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             auto free_stage = [&] {  // of the ring; Q's place may become free first
                 const int st = i % N, use = i / N;
                 if (use > 0 && q_waits) {
-                    const long long t_end = clock64() + kWaitLimit;
+                    const long long t_end = clock64() + pair::kWaitLimit;
                     while (ok && q_waits &&
                            !__all_sync(0xffffffffu, mbar_test_wait(bar(Bar::KvEmpty + st), (use - 1) & 1))) {
                         load_q(false);
@@ -499,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         k_count += kb.n;
                     }
                     const uint32_t st = (g + min(g + A + 1, k_count)) % N;
-                    ok = ok && wait_bounded(bar(Bar::VLocal + st), (turns >> st) & 1);
+                    ok = ok && pair::wait_bounded(bar(Bar::VLocal + st), (turns >> st) & 1);
                     turns ^= 1u << st;
                     bool here = false;
                     uint4 *const tile = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE);

@@ -54,6 +54,15 @@ __device__ __forceinline__ void arrive_expect_remote(uint32_t cluster_bar, uint3
 __device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// tc::mbar_wait_bounded in few instructions: many inlined waits crowd the instruction
+// cache.  A 32-bit clock, which the polls read often enough.
+constexpr uint32_t kWaitLimit = 3000000000u;  // SM clocks (about 1.5 s)
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
+    const uint32_t t0 = (uint32_t)clock();
+    while (!tc::mbar_try_wait(bar, parity))
+        if ((uint32_t)clock() - t0 > kWaitLimit) return false;
+    return true;
+}
 // Two fp32 values in one 64-bit register, and arithmetic on both.
 __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
     uint64_t r;

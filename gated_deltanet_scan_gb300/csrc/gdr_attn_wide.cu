@@ -35,7 +35,6 @@ using namespace tc;
 
 constexpr int kThreads = 384;
 constexpr int kRows = 128, kTile = 64;
-constexpr long long kWaitLimit = 4000000000LL;  // SM clocks (about 2 s)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kColsS = 256;  // TMEM: O at 0, S tiles at 256 and 320
 
@@ -118,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
 
     bool ok = true;
     auto wait = [&](int i, uint32_t parity) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(bar(i), parity & 1, kWaitLimit)) != 0;
+        ok = __all_sync(0xffffffffu, ok && pair::wait_bounded(bar(i), parity & 1)) != 0;
         return ok;
     };
     // Roles count stages, tiles and triples through all of the worker's triples.  Stage
@@ -155,8 +154,13 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     const int p0 = tile * kTile;
                     if (p0 + kTile > all_see) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (p0 + c >= seen) x[c] = 0xFF800000u;
+                        for (int c0 = 0; c0 < 64; c0 += 32) {
+                            const int n = seen - p0 - c0;  // columns seen
+                            const uint32_t sees = n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(sees & (1u << c))) x[c0 + c] = 0xFF800000u;
+                        }
                     }
                     float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
@@ -221,24 +225,6 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kOFree));
                     }
-                    if (live && patch) {
-                        // tiles that were cleaned: from the one in which the rows begin to differ
-                        const int from = max(t.tile0, max(0, all_see) / kTile) * kTile;
-                        const int to = min(seen, t.tile1 * kTile);
-                        for (int p = from; p < to; ++p) {
-                            const uint32_t pg = (uint32_t)p / (uint32_t)a.cache.page_size;
-                            const int page = a.cache.table[(int64_t)t.s * a.cache.table_stride + pg];
-                            if (page < 0 || page >= a.cache.n_pages) continue;
-                            const uint16_t *const v = a.cache.v + page * a.cache.page_stride +
-                                                      (int64_t)(p - (int)pg * a.cache.page_size) * a.cache.token_stride +
-                                                      t.h * a.cache.head_stride + c;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float y = unpack1<F16>(v[e]);
-                                if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-                            }
-                        }
-                    }
                     if (live && whole) {
                         uint16_t *const dst = a.o.p + tok * a.o.ts + (int64_t)hq * a.o.hs + c;
 #pragma unroll
@@ -283,6 +269,31 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     }
                     __syncwarp();
                 }
+                if (live && patch) {
+                    // tiles that were cleaned, from the one in which the rows begin to differ: what they
+                    // add to the stored row or part (a rare path, kept small)
+                    const int from = max(t.tile0, max(0, all_see) / kTile) * kTile;
+                    const int to = min(seen, t.tile1 * kTile);
+                    uint16_t *const dst = a.o.p + tok * a.o.ts + (int64_t)hq * a.o.hs;
+#pragma unroll 1
+                    for (int p = from; p < to; ++p) {
+                        const uint32_t pg = (uint32_t)p / (uint32_t)a.cache.page_size;
+                        const int page = a.cache.table[(int64_t)t.s * a.cache.table_stride + pg];
+                        if (page < 0 || page >= a.cache.n_pages) continue;
+                        const uint16_t *const v = a.cache.v + page * a.cache.page_stride +
+                                                  (int64_t)(p - (int)pg * a.cache.page_size) * a.cache.token_stride +
+                                                  t.h * a.cache.head_stride;
+#pragma unroll 1
+                        for (int c = 0; c < D; ++c) {
+                            const float y = unpack1<F16>(v[c]);
+                            if (isfinite(y)) continue;
+                            if (whole)
+                                dst[c] = (uint16_t)pack2<F16>(unpack1<F16>(dst[c]) + y, 0.f);
+                            else
+                                o_parts[part * D + c] += y;
+                        }
+                    }
+                }
                 if (live && whole && a.lse)
                     a.lse[tok * a.h_q + hq] = seen > 0 ? kLn2 * (m + log2f(l)) : -CUDART_INF_F;
                 if (live && !whole) ml_parts[part] = make_float2(m, l);
@@ -297,19 +308,24 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         constexpr int RPI = 32 / CPR;  // rows an instruction covers
         uint32_t i = 0;                // stages
         auto clean = [&](uint32_t st) {  // the values this thread copied, landed
-            bool found = false;
-#pragma unroll
-            for (int x = 0; x < 16 / RPI; ++x) {
+            auto piece = [&](int x) {
                 const int row = w * 16 + x * RPI + lane / CPR, chunk = lane % CPR;
-                uint4 *const p = reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE +
-                                                           (chunk >> 3) * Sh::BOX + row * 128 +
-                                                           (((chunk & 7) ^ (row & 7)) << 4));
-                const uint4 v = *p;
-                if (!any_nonfinite<F16>(v.x, v.y, v.z, v.w)) continue;
-                *p = make_uint4(cleaned<F16>(v.x), cleaned<F16>(v.y), cleaned<F16>(v.z), cleaned<F16>(v.w));
-                found = true;
+                return reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE + (chunk >> 3) * Sh::BOX +
+                                                 row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+            };
+            bool found = false;
+#pragma unroll 4
+            for (int x = 0; x < 16 / RPI; ++x) {
+                const uint4 v = *piece(x);
+                found = found || any_nonfinite<F16>(v.x, v.y, v.z, v.w);
             }
-            if (found) *s_found = 1;
+            if (!found) return;
+#pragma unroll 1
+            for (int x = 0; x < 16 / RPI; ++x) {
+                const uint4 v = *piece(x);
+                *piece(x) = make_uint4(cleaned<F16>(v.x), cleaned<F16>(v.y), cleaned<F16>(v.z), cleaned<F16>(v.w));
+            }
+            *s_found = 1;
         };
         auto next_stage = [&] {  // waits for the stage's place
             const uint32_t st = i % N, use = i / N;
@@ -386,18 +402,14 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             ++k_tile;
             ++kg;
         };
-        load_k();
-        if (k_more) load_k();
+#pragma unroll 1
+        for (int x = 0; x < 2 && k_more; ++x) load_k();
         while (ok && walk.next(a, sp, L.blocks_of_rows, t)) {
             for (int tile = t.tile0; ok && tile < t.tile1; ++tile) {
-                if (g > 0) {
-                    // the rows of V's tile, before K's next tile takes their place
-                    const int64_t x = (g & 1) ? v_rows[1] : v_rows[0];
-                    if (k_more) load_k();
-                    copy(a.cache.v, x, a.n_tok > 1 && (tile + 1) * kTile > t.len - a.n_tok + 1);
-                } else {
-                    copy(a.cache.v, v_rows[0], a.n_tok > 1 && (tile + 1) * kTile > t.len - a.n_tok + 1);
-                }
+                // the rows of V's tile, before K's next tile takes their place
+                const int64_t x = (g & 1) ? v_rows[1] : v_rows[0];
+                if (g > 0 && k_more) load_k();
+                copy(a.cache.v, x, a.n_tok > 1 && (tile + 1) * kTile > t.len - a.n_tok + 1);
                 ++g;
             }
         }
@@ -444,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             ++gs;
             ++i;
         };
-        score();
-        if (k_more && ok) score();
+#pragma unroll 1
+        for (int x = 0; x < 2 && k_more && ok; ++x) score();
         for (int it = 0; ok && walk.next(a, sp, L.blocks_of_rows, t); ++it) {
             for (int tile = t.tile0; ok && tile < t.tile1; ++tile) {
                 if (g > 0 && k_more) score();  // over P of the tile before, whose P V is issued
