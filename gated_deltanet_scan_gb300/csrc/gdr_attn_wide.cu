@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                                                  row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
             };
             bool found = false;
-#pragma unroll 4
+#pragma unroll
             for (int x = 0; x < 16 / RPI; ++x) {
                 const uint4 v = *piece(x);
                 found = found || any_nonfinite<F16>(v.x, v.y, v.z, v.w);
