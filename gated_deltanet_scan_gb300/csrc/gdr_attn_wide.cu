@@ -305,23 +305,22 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     } else if (warp < 8) {
         // ---- K and V: a warp's lanes hold the offsets of its 16 rows of a tile
         const int w = warp - 4;
-        constexpr int RPI = 32 / CPR;  // rows an instruction covers
         uint32_t i = 0;                // stages
         auto clean = [&](uint32_t st) {  // the values this thread copied, landed
             auto piece = [&](int x) {
-                const int row = w * 16 + x * RPI + lane / CPR, chunk = lane % CPR;
-                return reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE + (chunk >> 3) * Sh::BOX +
-                                                 row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+                const int row = w * 16 + (x & 3) * 4 + (lane >> 3);
+                return reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE + (x >> 2) * Sh::BOX + row * 128 +
+                                                 (((lane & 7) ^ (row & 7)) << 4));
             };
             bool found = false;
 #pragma unroll
-            for (int x = 0; x < 16 / RPI; ++x) {
+            for (int x = 0; x < D / 16; ++x) {
                 const uint4 v = *piece(x);
                 found = found || any_nonfinite<F16>(v.x, v.y, v.z, v.w);
             }
             if (!found) return;
 #pragma unroll 1
-            for (int x = 0; x < 16 / RPI; ++x) {
+            for (int x = 0; x < D / 16; ++x) {
                 const uint4 v = *piece(x);
                 *piece(x) = make_uint4(cleaned<F16>(v.x), cleaned<F16>(v.y), cleaned<F16>(v.z), cleaned<F16>(v.w));
             }
@@ -358,13 +357,18 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             next_stage();
             if (ok) {
                 const uint32_t to = base + Sh::OFF_RING + (i % N) * Sh::STAGE;
+                // eight lanes copy 128 bytes of a row, then the row's next 128: an offset is passed
+                // on once for all of them
 #pragma unroll
-                for (int y = 0; y < 16 / RPI; ++y) {
-                    const int lr = y * RPI + lane / CPR, row = w * 16 + lr, chunk = lane % CPR;
+                for (int y = 0; y < 4; ++y) {
+                    const int lr = y * 4 + (lane >> 3), row = w * 16 + lr;
                     const int64_t off = __shfl_sync(0xffffffffu, off16, lr);
+                    const uint32_t at = to + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+                    const uint16_t *const src = from + (off < 0 ? 0 : off) + (lane & 7) * 8;
                     // no token (past the end, or its page is out of range): zeros
-                    cp_async16(to + (chunk >> 3) * Sh::BOX + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
-                               from + (off < 0 ? 0 : off) + chunk * 8, off < 0 ? 0u : 16u);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        cp_async16(at + c * Sh::BOX, src + c * 64, off < 0 ? 0u : 16u);
                 }
                 if (look) {
                     cp_async_commit();
