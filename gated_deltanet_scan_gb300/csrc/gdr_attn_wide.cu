@@ -45,6 +45,11 @@ struct Shape {
     static constexpr uint32_t BOX = kTile * 128;      // 64 tokens, 64 columns
     static constexpr uint32_t STAGE = BOX * (D / 64);
     static constexpr int STAGES = D == 256 ? 5 : 8;
+    // Rows of a tile that one of the four loading warps copies: 32, two warps for K and two for
+    // V, or 16 of either, so that a stage's copies are all on their way sooner.  32 pays waits,
+    // arrivals and page ids of a stage half as often, 16 suits few stages: 32 against 16, d = 64
+    // 32.3 / 38.1 us, d = 128 63.8 / 70.7, d = 256 42.2 / 38.7.
+    static constexpr int LOAD_ROWS = D == 256 ? 16 : 32;
     static constexpr uint32_t OFF_RING = Q_BYTES;
     static constexpr uint32_t OFF_BAR = OFF_RING + STAGES * STAGE;
     static constexpr uint32_t OFF_WORDS = OFF_BAR + 8 * 32;  // TMEM address, flag
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         mbar_init(bar(kQFull), 96);
         mbar_init(bar(kQEmpty), 1);
         for (int i = 0; i < N; ++i) {
-            mbar_init(bar(kKvFull + i), 128);
+            mbar_init(bar(kKvFull + i), Sh::LOAD_ROWS == 32 ? 64 : 128);
             mbar_init(bar(kKvEmpty + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -120,8 +125,10 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         ok = __all_sync(0xffffffffu, ok && pair::wait_bounded(bar(i), parity & 1)) != 0;
         return ok;
     };
-    // Roles count stages, tiles and triples through all of the worker's triples.  Stage
-    // order: K0, K1, V0, K2, V1, ..., the last value tile at the end.
+    // Roles count tiles and triples through all of the worker's triples.  Stages of the ring are
+    // taken in the order K0, K1, V0, K2, V1, ...; the last value tile leaves one out.
+    auto key_stage = [](uint32_t g) { return g == 0 ? 0 : 2 * g - 1; };
+    auto value_stage = [](uint32_t g) { return 2 * g + 2; };
     Triple t;
 
     if (warp < 4) {
@@ -303,41 +310,37 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             __syncwarp();
         }
     } else if (warp < 8) {
-        // ---- K and V: a warp's lanes hold the offsets of its 16 rows of a tile
-        const int w = warp - 4;
-        uint32_t i = 0;                // stages
+        // ---- K and V: a warp's lanes hold the offsets of its rows of a tile
+        constexpr int R = Sh::LOAD_ROWS;
+        const int w = (warp - 4) & (64 / R - 1);
         auto clean = [&](uint32_t st) {  // the values this thread copied, landed
             auto piece = [&](int x) {
-                const int row = w * 16 + (x & 3) * 4 + (lane >> 3);
-                return reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE + (x >> 2) * Sh::BOX + row * 128 +
+                const int row = w * R + x % (R / 4) * 4 + (lane >> 3);
+                return reinterpret_cast<uint4 *>(smem + Sh::OFF_RING + st * Sh::STAGE + x / (R / 4) * Sh::BOX + row * 128 +
                                                  (((lane & 7) ^ (row & 7)) << 4));
             };
             bool found = false;
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
+#pragma unroll 8
+            for (int x = 0; x < R / 4 * (D / 64); ++x) {
                 const uint4 v = *piece(x);
                 found = found || any_nonfinite<F16>(v.x, v.y, v.z, v.w);
             }
             if (!found) return;
 #pragma unroll 1
-            for (int x = 0; x < D / 16; ++x) {
+            for (int x = 0; x < R / 4 * (D / 64); ++x) {
                 const uint4 v = *piece(x);
                 *piece(x) = make_uint4(cleaned<F16>(v.x), cleaned<F16>(v.y), cleaned<F16>(v.z), cleaned<F16>(v.w));
             }
             *s_found = 1;
         };
-        auto next_stage = [&] {  // waits for the stage's place
-            const uint32_t st = i % N, use = i / N;
-            if (use > 0) wait(kKvEmpty + st, use - 1);
-        };
         // A lane's row of a tile: its page id is loaded a tile early and looked at when the tile's
         // turn comes; then its offset in the cache, or -1.
         struct Ahead {
-            int page, slot, h;  // slot -1: no token
+            int page, slot;  // slot -1: no token
         };
         auto look_up = [&](const Triple &u, int tile) {
-            Ahead x{0, -1, u.h};
-            const int p = tile * kTile + w * 16 + (lane & 15);
+            Ahead x{0, -1};
+            const int p = tile * kTile + w * R + (lane & (R - 1));
             if (p < u.len) {
                 const uint32_t pg = (uint32_t)p / (uint32_t)a.cache.page_size;
                 x.slot = p - (int)pg * a.cache.page_size;
@@ -345,77 +348,73 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             }
             return x;
         };
-        auto offset = [&](const Ahead &x) -> int64_t {
-            if (x.slot < 0) return -1;
-            if (x.page < 0 || x.page >= a.cache.n_pages) {
-                record_invalid(a.err);
-                return -1;
-            }
-            return x.page * a.cache.page_stride + x.slot * a.cache.token_stride + x.h * a.cache.head_stride;
+        struct Tiles {  // of K or of V, through all triples
+            Walk walk;
+            Triple t;
+            int tile;
+            Ahead next;
+            uint32_t g;
         };
-        auto copy = [&](const uint16_t *from, int64_t off16, bool look) {
-            next_stage();
-            if (ok) {
-                const uint32_t to = base + Sh::OFF_RING + (i % N) * Sh::STAGE;
-                // eight lanes copy 128 bytes of a row, then the row's next 128: an offset is passed
-                // on once for all of them
+        auto begin = [&] {
+            Tiles x;
+            x.walk = walk;
+            x.t.tile1 = x.tile = 0;
+            x.next = Ahead{0, -1};
+            x.g = 0;
+            return x;
+        };
+        auto load = [&](Tiles &x, bool values) {  // the next tile, if there is one
+            if (x.tile == x.t.tile1) {
+                if (!x.walk.next(a, sp, L.blocks_of_rows, x.t)) return false;
+                x.tile = x.t.tile0;
+                x.next = look_up(x.t, x.tile);
+            }
+            int64_t lane_off = -1;
+            if (x.next.slot >= 0) {
+                if (x.next.page < 0 || x.next.page >= a.cache.n_pages)
+                    record_invalid(a.err);
+                else
+                    lane_off = x.next.page * a.cache.page_stride + x.next.slot * a.cache.token_stride +
+                               x.t.h * a.cache.head_stride;
+            }
+            if (++x.tile < x.t.tile1) x.next = look_up(x.t, x.tile);
+            const uint32_t i = values ? value_stage(x.g) : key_stage(x.g), st = i % N, use = i / N;
+            ++x.g;
+            if (use > 0 && !wait(kKvEmpty + st, use - 1)) return false;
+            const uint16_t *const from = values ? a.cache.v : a.cache.k;
+            const uint32_t to = base + Sh::OFF_RING + st * Sh::STAGE;
+            // eight lanes copy 128 bytes of a row, then the row's next 128: an offset is passed
+            // on once for all of them
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int lr = y * 4 + (lane >> 3), row = w * 16 + lr;
-                    const int64_t off = __shfl_sync(0xffffffffu, off16, lr);
-                    const uint32_t at = to + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
-                    const uint16_t *const src = from + (off < 0 ? 0 : off) + (lane & 7) * 8;
-                    // no token (past the end, or its page is out of range): zeros
+            for (int y = 0; y < R / 4; ++y) {
+                const int lr = y * 4 + (lane >> 3), row = w * R + lr;
+                const int64_t off = __shfl_sync(0xffffffffu, lane_off, lr);
+                const uint32_t at = to + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+                const uint16_t *const src = from + (off < 0 ? 0 : off) + (lane & 7) * 8;
+                // no token (past the end, or its page is out of range): zeros
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        cp_async16(at + c * Sh::BOX, src + c * 64, off < 0 ? 0u : 16u);
-                }
-                if (look) {
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    clean(i % N);
-                    mbar_arrive(bar(kKvFull + i % N));
-                } else {
-                    cp_async_arrive(bar(kKvFull + i % N));
-                }
-                ++i;
+                for (int c = 0; c < D / 64; ++c)
+                    cp_async16(at + c * Sh::BOX, src + c * 64, off < 0 ? 0u : 16u);
             }
+            if (values && a.n_tok > 1 && x.tile * kTile > x.t.len - a.n_tok + 1) {
+                cp_async_commit();
+                cp_async_wait<0>();
+                clean(st);
+                mbar_arrive(bar(kKvFull + st));
+            } else {
+                cp_async_arrive(bar(kKvFull + st));
+            }
+            return true;
         };
-        Walk k_walk = walk;
-        Triple kt;
-        kt.tile0 = kt.tile1 = 0;
-        int k_tile = 0;
-        bool k_more = true;
-        Ahead k_next{0, -1, 0};
-        int64_t v_rows[2] = {-1, -1};        // offsets of the K tiles whose values are still to come
-        uint32_t kg = 0, g = 0;              // tiles of K and V
-        auto load_k = [&] {
-            if (k_tile == kt.tile1) {
-                k_more = k_walk.next(a, sp, L.blocks_of_rows, kt);
-                if (!k_more) return;
-                k_tile = kt.tile0;
-                k_next = look_up(kt, k_tile);
-            }
-            const int64_t x = offset(k_next);
-            if (kg & 1)
-                v_rows[1] = x;
-            else
-                v_rows[0] = x;
-            if (k_tile + 1 < kt.tile1) k_next = look_up(kt, k_tile + 1);
-            copy(a.cache.k, x, false);
-            ++k_tile;
-            ++kg;
-        };
-#pragma unroll 1
-        for (int x = 0; x < 2 && k_more; ++x) load_k();
-        while (ok && walk.next(a, sp, L.blocks_of_rows, t)) {
-            for (int tile = t.tile0; ok && tile < t.tile1; ++tile) {
-                // the rows of V's tile, before K's next tile takes their place
-                const int64_t x = (g & 1) ? v_rows[1] : v_rows[0];
-                if (g > 0 && k_more) load_k();
-                copy(a.cache.v, x, a.n_tok > 1 && (tile + 1) * kTile > t.len - a.n_tok + 1);
-                ++g;
-            }
+        if constexpr (R == 32) {
+            Tiles x = begin();
+            while (load(x, warp >= 6)) {}
+        } else {
+            Tiles k = begin(), v = begin();
+            load(k, false);
+            do
+                load(k, false);
+            while (load(v, true));
         }
         cp_async_commit();
         cp_async_wait<0>();
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         const uint64_t q0 = smem_desc_sw128(base, 0, 1024);
         const uint64_t k0 = smem_desc_sw128(base + Sh::OFF_RING, 0, 1024);
         const uint64_t v0 = smem_desc_sw128(base + Sh::OFF_RING, Sh::BOX, 1024);
-        uint32_t i = 0, gs = 0, g = 0;
+        uint32_t gs = 0, g = 0;
         Walk k_walk = walk;
         Triple kt;
         kt.tile0 = kt.tile1 = 0;
@@ -440,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                 if (!k_more || !wait(kQFull, ++k_it)) return;
                 k_tile = kt.tile0;
             }
-            const uint32_t st = i % N;
+            const uint32_t i = key_stage(gs), st = i % N;
             if (!wait(kKvFull + st, i / N)) return;
             fence_proxy_async_smem();  // copies by other threads, before the MMAs read them
             tc_fence_after_sync();
@@ -458,7 +457,6 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             __syncwarp();
             ++k_tile;
             ++gs;
-            ++i;
         };
 #pragma unroll 1
         for (int x = 0; x < 2 && k_more && ok; ++x) score();
@@ -466,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             for (int tile = t.tile0; ok && tile < t.tile1; ++tile) {
                 if (g > 0 && k_more) score();  // over P of the tile before, whose P V is issued
                 if (!ok) break;
-                const uint32_t st = i % N;
+                const uint32_t i = value_stage(g), st = i % N;
                 if (tile == t.tile0 && it > 0 && !wait(kOFree, it - 1)) break;
                 if (!wait(kKvFull + st, i / N) || !wait(kPFull + (g & 1), g >> 1)) break;
                 fence_proxy_async_smem();
@@ -482,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     if (tile == t.tile1 - 1) mma_commit(bar(kODone));
                 }
                 __syncwarp();
-                ++i;
                 ++g;
             }
         }
