@@ -64,9 +64,10 @@ cudaError_t launch_append(const Args &a, cudaStream_t s);
 // Prompts: a short sequence goes to the short kernel, a longer one to the two-SM kernel;
 // each skips the other's.  Short is what fills at most one of the two-SM kernel's blocks
 // (256 rows), up to 128 tokens.  Measured with all sequences in one kernel, short against
-// two-SM: 16 heads of 256 in groups of 4, 64 tokens 8.2 / 12.3 us (32 sequences 19.7 / 20.5),
-// 128 tokens x 8 14.2 / 15.3, x 32 44.6 / 32.3; 16 heads of 128 in groups of 1, 128 tokens
-// x 8 9.8 / 14.8, x 32 25.1 / 38.0, 256 tokens x 8 20.6 / 18.4, x 32 68.2 / 47.6.
+// two-SM: 16 heads of 256 in groups of 4, 64 tokens x 8 8.0 / 11.0 us, x 32 20.9 / 18.7,
+// 128 tokens x 8 13.7 / 12.1, x 32 44.0 / 27.0; 16 heads of 128 in groups of 1, 128 tokens
+// x 8 9.9 / 12.7, x 32 25.3 / 27.1, 256 tokens x 8 21.4 / 16.4, x 32 67.7 / 36.0; of 64,
+// 128 tokens x 32 16.5 / 24.3.
 __host__ __device__ constexpr int short_tokens(int group) { return 256 / group < 128 ? 256 / group : 128; }
 cudaError_t launch_prefill(const Args &a, cudaStream_t s);
 // `after`: launched as a programmatic dependent of the two-SM kernel just before it.
