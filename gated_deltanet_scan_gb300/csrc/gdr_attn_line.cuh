@@ -24,8 +24,8 @@ struct Spec {
 // values at a 1216th of the bandwidth (d = 256: 3 us).  The wide kernel: one worker of 128
 // rows per SM, tiles of 64 tokens.  Leads measured: 512 / d, 1024 / d and 1536 / d places for
 // the first (25 sequences of d = 256 42.3, 39.4, 37.3 us; 64 sequences 120.8, 120.8, 121.6; 96 of
-// d = 128 119.5, 119.7, 121.5); 3, 4 and 6 for the second (16 draft tokens 44.6, 42.2, 41.2; 51
-// sequences of d = 128 43.7, 40.4, 42.0; 52 of d = 64 22.4, 23.0, 23.5).
+// d = 128 119.5, 119.7, 121.5); 3, 4 and 6 for the second (16 draft tokens 39.8, 38.5, 38.6; 50
+// sequences of d = 128 47.2, 47.6, 47.8; 52 of d = 64 30.3, 29.9, 30.5).
 __host__ __device__ constexpr Spec spec(bool wide, int d) {
     return wide ? Spec{128, 64, 1, 4} : Spec{kWarpRows, 16, 8, 1024 / d};
 }
