@@ -1,0 +1,88 @@
+"""Attention operators on the GPU at values, scales and arguments where they can go wrong: infinite keys and
+values that a token does see, scales near zero, and what the device checks itself."""
+
+import numpy as np
+import pytest
+
+import gated_deltanet_scan_gb300 as gdr
+from tests import attn_ref as ar
+from tests import gpu_util as gu
+from tests.test_gpu_attn import Paged, check_decode, check_prefill, close, f64, ints, nan_like, no_error, randn, run_decode
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+NAN = float("nan")
+
+
+# --- infinite values ------------------------------------------------------------------------------------------
+
+def takes(got, bad):
+    """All of got is the infinity `bad`, or NaN where bad is."""
+    torch = gu.torch_mod()
+    return bool(torch.all(torch.isnan(got) if bad != bad else got == bad))
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f16"))
+@pytest.mark.parametrize("d,hq", [(64, 1), (64, 3), (128, 2), (256, 1), (256, 4)])
+@pytest.mark.parametrize("bad", [INF, -INF, NAN])
+def test_prefill_rows_take_the_infinity_of_a_value_they_see(d, hq, bad, dtype):
+    """Scores of normal variates divided by their deviation: every weight is over 2^-24 of the largest, so what a
+    column of an infinite value gives is that infinity, in both kernels (64 and 90 tokens, and 300)."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(70 + d)
+    lens = [64, 300, 90 if hq < 3 else 57]
+    T, ends = sum(lens), [int(x) for x in np.cumsum(lens)]
+    q, k, v = randn(rng, (T, hq, d), dtype), randn(rng, (T, 1, d), dtype), randn(rng, (T, 1, d), dtype)
+    cu = ints([0] + ends)
+    hit = torch.zeros(d, dtype=torch.bool, device="cuda")
+    hit[3::5] = True
+    for at in (0, 31, 32, 63, 64, 64 + 127, 64 + 128, 64 + 250, 363, 364, T - 1):
+        v2 = v.clone()
+        v2[at, :, 3::5] = bad
+        o = nan_like((T, hq, d), q.dtype)
+        gdr.gdr_attn_prefill(q, k, v2, o, cu)
+        end = next(e for e in ends if e > at)
+        assert takes(o[at:end][..., hit], bad), at
+        assert torch.all(torch.isfinite(o[at:end][..., ~hit])), at
+        rest = torch.ones(T, dtype=torch.bool, device="cuda")
+        rest[at:end] = False
+        assert torch.all(torch.isfinite(o[rest])), at
+    no_error()
+
+
+@pytest.mark.parametrize("n", [90, 300])
+def test_prefill_opposite_infinities_cancel_to_nan(n):
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(71)
+    q, k, v = (randn(rng, (n, 1, 64), "bf16") for _ in range(3))
+    v[5, 0, 7], v[n - 20, 0, 7] = INF, -INF
+    o = nan_like(q.shape, q.dtype)
+    gdr.gdr_attn_prefill(q, k, v, o, ints([0, n]))
+    col = o[:, 0, 7]
+    assert torch.all(torch.isfinite(col[:5])) and takes(col[5:n - 20], INF) and takes(col[n - 20:], NAN)
+    no_error()
+
+
+@pytest.mark.parametrize("n", [19, 203, 3000])  # in one worker's tile, and split over workers and joined
+@pytest.mark.parametrize("heads", [4, 1])  # 64 rows and 16: either kernel
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bad", [INF, -INF, NAN])
+def test_decode_rows_take_the_infinity_of_a_value_they_see(d, bad, heads, n):
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(72)
+    n_tok = 16
+    c = Paged(rng, [n], 32, 1, d, "bf16")
+    q = randn(rng, (n_tok, heads, d), "bf16")
+    hit = torch.zeros(d, dtype=torch.bool, device="cuda")
+    hit[1::3] = True
+    for p in (0, n - 16, n - 11, n - 1):
+        at = (int(c.table_np[0, p // 32]), p % 32)
+        kept = c.v[at].clone()
+        c.v[at[0], at[1], :, 1::3] = bad
+        o, _ = run_decode(c, q, n_tok)
+        j = max(0, p - (n - n_tok))
+        assert takes(o[j:][..., hit], bad), p
+        assert torch.all(torch.isfinite(o[j:][..., ~hit])) and torch.all(torch.isfinite(o[:j])), p
+        c.v[at] = kept
+    no_error()
