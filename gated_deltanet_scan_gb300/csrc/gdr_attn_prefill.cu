@@ -624,7 +624,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 l *= m_own == m ? 1.f : fast_exp2(m_own - m);
                 m_own = m;
                 uint64_t sum[2] = {0, 0};
-                const uint64_t sc2 = pair::pack_f32x2(sc, sc), m2 = pair::pack_f32x2(-m, -m);
+                const float ref = m == -CUDART_INF_F ? 0.f : m;  // no finite score yet: p = 2^-inf
+                const uint64_t sc2 = pair::pack_f32x2(sc, sc), m2 = pair::pack_f32x2(-ref, -ref);
 #pragma unroll
                 for (int quarter = 0; quarter < 4; ++quarter) {
                     uint32_t p[16];

@@ -86,3 +86,76 @@ def test_decode_rows_take_the_infinity_of_a_value_they_see(d, bad, heads, n):
         assert torch.all(torch.isfinite(o[j:][..., ~hit])) and torch.all(torch.isfinite(o[:j])), p
         c.v[at] = kept
     no_error()
+
+
+# --- scores of minus infinity -------------------------------------------------------------------------------
+
+def hidden_by_keys(rng, n, m, hq, d, dtype, scale):
+    """q, k, v of one sequence whose first m tokens have a score of minus infinity for every query."""
+    q, k, v = randn(rng, (n, hq, d), dtype), randn(rng, (n, 1, d), dtype), randn(rng, (n, 1, d), dtype)
+    q[..., 0] = 1.0
+    k[:m, :, 0] = -INF if scale > 0 else INF
+    return q, k, v
+
+
+HIDDEN = [
+    # d, h_q, lens, of which so many first tokens
+    (64, 2, [90, 60], [40, 33]), (256, 4, [64], [32]),  # the short kernel
+    (64, 1, [300], [128]), (128, 2, [400], [130]), (128, 4, [700, 300], [257, 128]), (256, 4, [600], [300]),
+    (256, 1, [390], [389]), (64, 5, [520], [500]), (128, 1, [1000], [640]),
+]
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f16"))
+@pytest.mark.parametrize("scale", [0.1, -0.1])
+@pytest.mark.parametrize("d,hq,lens,first", HIDDEN)
+def test_prefill_scores_of_minus_infinity_weigh_nothing(d, hq, lens, first, scale, dtype):
+    """What a row gives is the softmax of its other tokens: the definition's weights of exp(-infinity) = 0."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(73 + d)
+    parts = [hidden_by_keys(rng, n, m, hq, d, dtype, scale) for n, m in zip(lens, first)]
+    q, k, v = (torch.cat([p[i] for p in parts]) for i in range(3))
+    o, lse = nan_like(q.shape, q.dtype), nan_like(q.shape[:2], torch.float32)
+    gdr.gdr_attn_prefill(q, k, v, o, ints(np.concatenate([[0], np.cumsum(lens)])), scale=scale, lse=lse)
+    torch.cuda.synchronize()
+    no_error()
+    t = 0
+    for n, m in zip(lens, first):
+        r = slice(t + m, t + n)
+        wo, wl, bo, bl = ar.prefill(f64(q[r]), f64(k[r]), f64(v[r]), scale, [n - m], dtype)
+        close(o[r], wo, bo, "o")
+        close(lse[r], wl, bl, "lse")
+        t += n
+
+
+HIDDEN_CACHE = [
+    # d, h_q, n_tok, lens, of which so many first tokens
+    (64, 4, 1, [300], [120]), (256, 4, 1, [4000], [3990]), (128, 8, 2, [40, 200, 16], [20, 190, 7]),
+    (256, 4, 16, [300], [120]), (128, 40, 1, [2000, 64], [1990, 10]), (64, 8, 12, [40, 200, 16], [20, 180, 3]),
+    (64, 2, 1, [9] * 700, [4] * 700), (64, 20, 1, [70] * 300, [64] * 300),  # sequences that one worker sees whole
+]
+
+
+@pytest.mark.parametrize("dtype", ("bf16", "f16"))
+@pytest.mark.parametrize("d,hq,n_tok,lens,first", HIDDEN_CACHE)
+def test_decode_scores_of_minus_infinity_weigh_nothing(d, hq, n_tok, lens, first, dtype):
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(75 + d)
+    c = Paged(rng, lens, 16, 1, d, dtype)
+    q = randn(rng, (len(lens) * n_tok, hq, d), dtype)
+    q[..., 0] = 1.0
+    for s, m in enumerate(first):
+        p = np.arange(m)
+        c.k[c.table_np[s, p // 16], p % 16, :, 0] = -INF
+    o, lse = run_decode(c, q, n_tok)
+    torch.cuda.synchronize()
+    no_error()
+    k64, v64, q64 = f64(c.k), f64(c.v), f64(q)
+    for s in list(range(len(lens)))[:6]:
+        n, m, r = lens[s], first[s], slice(s * n_tok, (s + 1) * n_tok)
+        k, v = ar.gather(k64, c.table_np[s], n)[m:], ar.gather(v64, c.table_np[s], n)[m:]
+        for h in range(hq):
+            wo, wl, bo, bl = ar.attend(q64[r, h], k[:, 0], v[:, 0], d ** -0.5,
+                                       n - n_tok - m + np.arange(1, n_tok + 1), dtype)
+            close(o[r, h], wo, bo, "o")
+            close(lse[r, h], wl, bl, "lse")
