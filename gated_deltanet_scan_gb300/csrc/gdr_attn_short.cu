@@ -139,11 +139,38 @@ __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__
                     found = found || any_nonfinite<F16>(w[0], w[1], w[2], w[3]);
                 }
                 found = __syncthreads_or(found);
+                if (found) {
+#pragma unroll 1
+                    for (int t = 0; t < kTile && p0 + t < len; ++t) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t w;
+                            asm volatile("ld.shared.b32 %0, [%1];"
+                                         : "=r"(w)
+                                         : "r"(vb + t * (D * 2) + ((n ^ (t & 7)) << 4) + cq * 4)
+                                         : "memory");
+                            if (!nonfinite<F16>(w) && !nonfinite<F16>(w >> 16)) continue;
+                            const float2 v = unpack2<F16>(w);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                if (p0 + t > token[i]) continue;
+                                if (nonfinite<F16>(w)) acc[n][2 * i] += v.x;
+                                if (nonfinite<F16>(w >> 16)) acc[n][2 * i + 1] += v.y;
+                            }
+                        }
+                    }
+                    __syncthreads();
+                    for (int i = tid; i < kTile * D / 2; i += kThreads) {
+                        uint32_t w;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vb + 4 * i) : "memory");
+                        const uint32_t z = cleaned<F16>(w);
+                        if (z != w) asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + 4 * i), "r"(z) : "memory");
+                    }
+                    __syncthreads();
+                }
             }
 
-            const bool some = p0 <= warp_last;  // some row of the warp sees some token of the tile
-            uint32_t pf[2][4] = {};             // P as MMA operands
-            if (some) {
+            if (p0 <= warp_last) {  // some row of the warp sees some token of the tile
                 float x[4][4];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[i >> 2][i & 3] = 0.f;
@@ -165,6 +192,7 @@ __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__
                     }
                 }
                 const bool masked = p0 + kTile - 1 > warp_first;
+                uint32_t pf[2][4];
                 float c[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -181,7 +209,8 @@ __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const float mn = next_reference<F16>(m[i], top);
                     const float ref = mn == -CUDART_INF_F ? 0.f : mn;
-                    c[i] = m[i] == mn ? 1.f : tc::fast_exp2(m[i] - ref);
+                    // the first tile's factor is 1, not 2^-inf = 0: the sums may hold added infinities
+                    c[i] = m[i] == mn || m[i] == -CUDART_INF_F ? 1.f : tc::fast_exp2(m[i] - ref);
                     m[i] = mn;
                     l[i] *= c[i];
 #pragma unroll
@@ -200,52 +229,21 @@ __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__
                         acc[n][3] *= c[1];
                     }
                 }
-                if (found) {  // after the rescaling: a row's first tile rescales by 0
-#pragma unroll 1
-                    for (int t = 0; t < kTile && p0 + t < len; ++t) {
+                {
+                    const int row = lane & 15;
+                    uint32_t at[4];  // chunk (n + (lane >> 4)) ^ (row & 7)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            uint32_t w;
-                            asm volatile("ld.shared.b32 %0, [%1];"
-                                         : "=r"(w)
-                                         : "r"(vb + t * (D * 2) + ((n ^ (t & 7)) << 4) + cq * 4)
-                                         : "memory");
-                            if (!nonfinite<F16>(w) && !nonfinite<F16>(w >> 16)) continue;
-                            const float2 v = unpack2<F16>(w);
+                    for (int i = 0; i < 4; ++i)
+                        at[i] = vb + row * (D * 2) + (((2 * i) ^ (lane >> 4) ^ (row & 7)) << 4);
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                if (p0 + t > token[i]) continue;
-                                if (nonfinite<F16>(w)) acc[n][2 * i] += v.x;
-                                if (nonfinite<F16>(w >> 16)) acc[n][2 * i + 1] += v.y;
-                            }
+                    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                        for (int n = 0; n < NT; n += 2) {
+                            uint32_t b[4];
+                            ldsm4t(at[(n >> 1) & 3] + t * 16 * D * 2 + (n >> 3) * 128, b);
+                            mma16816<F16>(acc[n], pf[t], b[0], b[1]);
+                            mma16816<F16>(acc[n + 1], pf[t], b[2], b[3]);
                         }
-                    }
-                }
-            }
-            if (found) {
-                __syncthreads();
-                for (int i = tid; i < kTile * D / 2; i += kThreads) {
-                    uint32_t w;
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(vb + 4 * i) : "memory");
-                    const uint32_t z = cleaned<F16>(w);
-                    if (z != w) asm volatile("st.shared.b32 [%0], %1;" ::"r"(vb + 4 * i), "r"(z) : "memory");
-                }
-                __syncthreads();
-            }
-            if (some) {
-                const int row = lane & 15;
-                uint32_t at[4];  // chunk (n + (lane >> 4)) ^ (row & 7)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    at[i] = vb + row * (D * 2) + (((2 * i) ^ (lane >> 4) ^ (row & 7)) << 4);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
-                        uint32_t b[4];
-                        ldsm4t(at[(n >> 1) & 3] + t * 16 * D * 2 + (n >> 3) * 128, b);
-                        mma16816<F16>(acc[n], pf[t], b[0], b[1]);
-                        mma16816<F16>(acc[n + 1], pf[t], b[2], b[3]);
                     }
                 }
             }
