@@ -58,6 +58,10 @@ __device__ __forceinline__ float next_reference(float m, float top) {
     return top > m + R::TOP || m == -CUDART_INF_F ? fmaxf(m, top - R::LEAD) : m;
 }
 
+// 1 / l for the output o = O / l; a row without a finite score (it sees no token, or its
+// scores are all minus infinity) has l = 0 and O = 0, and gives o = 0 and lse = ln 0.
+__device__ __forceinline__ float inverse_sum(float l) { return 1.f / (l == 0.f ? 1.f : l); }
+
 // Sequence of token t among packed starts cu[0 .. n]: the last s < n with cu[s] <= t (or
 // 0).  The whole warp looks, 32 places at a time: two rounds of loads for a thousand.
 __device__ __forceinline__ int find_seq_warp(const int32_t *cu, int n, int64_t t, int lane) {

@@ -307,15 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (out_row[i] < 0) continue;
-                const float inv = seen[i] > 0 ? 1.f / l[i] : 0.f;
+                const float inv = seen[i] > 0 ? inverse_sum(l[i]) : 0.f;
                 const int64_t t = quotient(out_row[i], a.h_q);
                 uint16_t *dst = a.o.p + t * a.o.ts + (out_row[i] - t * a.h_q) * a.o.hs;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     *reinterpret_cast<uint32_t *>(dst + n * 8 + cq * 2) =
                         pack2<F16>(acc[n][2 * i] * inv, acc[n][2 * i + 1] * inv);
-                if (a.lse && cq == 0)
-                    a.lse[out_row[i]] = seen[i] > 0 ? kLn2 * (m[i] + log2f(l[i])) : -CUDART_INF_F;
+                if (a.lse && cq == 0) a.lse[out_row[i]] = seen[i] > 0 ? kLn2 * (m[i] + log2f(l[i])) : -CUDART_INF_F;
             }
         } else {
             // the part goes to the workspace, or, where the triple goes on in the next worker, to
@@ -480,7 +479,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
         }
     }
     const bool sees = len - a.n_tok + j + 1 > 0;
-    const float inv = sees ? 1.f / l : 0.f;
+    const float inv = sees ? inverse_sum(l) : 0.f;
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) dst[word0 + 32 * e] = pack2<F16>(acc[e].x * inv, acc[e].y * inv);
     if (write_lse) a.lse[row] = sees ? kLn2 * (m + log2f(l)) : -CUDART_INF_F;

@@ -666,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     // the place of 1 / l: read for the block before last
                     if (it >= 2 && !wait(Bar::Read + ((it - 2) & 3), (it - 2) >> 2)) break;
-                    s_inv[slot * 128 + row] = 1.f / l;
+                    s_inv[slot * 128 + row] = inverse_sum(l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(Bar::Inv + slot));
                     if (a.lse && tok < per_cta && token < b.len)

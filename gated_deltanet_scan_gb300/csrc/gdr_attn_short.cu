@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             if (token[i] < 0) continue;
-            const float inv = 1.f / l[i];
+            const float inv = inverse_sum(l[i]);
             const int64_t t = t0 + token[i];
             uint16_t *const dst = a.o.p + t * a.o.ts + (out_row[i] - t * a.h_q) * a.o.hs;
 #pragma unroll

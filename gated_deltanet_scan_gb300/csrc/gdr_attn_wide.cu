@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             const bool patch = *s_found != 0;
             const int64_t tok = (int64_t)t.s * a.n_tok + j;
             const int64_t part = ((int64_t)me * 2 + (cut.start(me) >= t.seg0 ? 0 : 1)) * L.part_rows + row;
-            const float inv = seen > 0 ? 1.f / l : 0.f;
+            const float inv = inverse_sum(l);
             if (work) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     }
                 }
                 if (live && whole && a.lse)
-                    a.lse[tok * a.h_q + hq] = seen > 0 ? kLn2 * (m + log2f(l)) : -CUDART_INF_F;
+                    a.lse[tok * a.h_q + hq] = kLn2 * (m + log2f(l));
                 if (live && !whole) ml_parts[part] = make_float2(m, l);
             } else if (lane == 0) {
                 mbar_arrive(bar(kOFree));

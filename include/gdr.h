@@ -516,7 +516,7 @@ gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int3
  * outside [0, t_total] make the kernel skip the sequences that use them and record
  * GDR_ERR_INVALID_ARG in the device error word).  A token never sees a later one's
  * or another sequence's key or value, whatever these hold (NaN and infinities
- * included).
+ * included).  A row whose scores are all minus infinity has o = 0 and lse = -infinity.
  *
  *   q, o [t_total][h_q][d]; k, v [t_total][h_kv][d] (strided rows, dims->dtype)
  *   lse  NULL, or DEVICE fp32 [t_total][h_q]: log sum_j exp(scale q_i . k_j)
@@ -533,10 +533,11 @@ gdr_status gdr_attn_prefill(const gdr_attn_dims *dims, int32_t n_seqs, const int
  * of sequence s, row s * n_tok + j, has position kv_lens[s] - n_tok + j and sees
  * the positions up to its own:
  *     o = sum_{p <= kv_lens[s] - n_tok + j} softmax_p(scale q . k_p) v_p.
- * A query that sees nothing (kv_lens[s] < n_tok - j, or 0) has o = 0 and lse =
- * -infinity.  kv_lens[s] outside [0, max_pages * page_size] counts as 0 and records
- * GDR_ERR_INVALID_ARG in the device error word.  What the cache holds past a
- * sequence's tokens is never used, nor a later draft token's key or value.
+ * A query that sees nothing (kv_lens[s] < n_tok - j, or 0), or whose scores are all
+ * minus infinity, has o = 0 and lse = -infinity.  kv_lens[s] outside
+ * [0, max_pages * page_size] counts as 0 and records GDR_ERR_INVALID_ARG in the device
+ * error word.  What the cache holds past a sequence's tokens is never used, nor a later
+ * draft token's key or value.
  *
  * The work of all sequences is cut into equal parts, one per resident block,
  * whatever the lengths; sequences that are cut have their parts joined by a second

@@ -128,6 +128,22 @@ def test_prefill_scores_of_minus_infinity_weigh_nothing(d, hq, lens, first, scal
         t += n
 
 
+@pytest.mark.parametrize("dtype", ("bf16", "f16"))
+@pytest.mark.parametrize("d,hq,lens,first", HIDDEN)
+def test_prefill_rows_without_a_finite_score_are_zero(d, hq, lens, first, dtype):
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(74 + d)
+    parts = [hidden_by_keys(rng, n, m, hq, d, dtype, 0.1) for n, m in zip(lens, first)]
+    q, k, v = (torch.cat([p[i] for p in parts]) for i in range(3))
+    o, lse = nan_like(q.shape, q.dtype), nan_like(q.shape[:2], torch.float32)
+    gdr.gdr_attn_prefill(q, k, v, o, ints(np.concatenate([[0], np.cumsum(lens)])), scale=0.1, lse=lse)
+    t = 0
+    for n, m in zip(lens, first):
+        assert torch.all(o[t:t + m] == 0) and takes(lse[t:t + m], -INF)
+        t += n
+    no_error()
+
+
 HIDDEN_CACHE = [
     # d, h_q, n_tok, lens, of which so many first tokens
     (64, 4, 1, [300], [120]), (256, 4, 1, [4000], [3990]), (128, 8, 2, [40, 200, 16], [20, 190, 7]),
@@ -159,3 +175,18 @@ def test_decode_scores_of_minus_infinity_weigh_nothing(d, hq, n_tok, lens, first
                                        n - n_tok - m + np.arange(1, n_tok + 1), dtype)
             close(o[r, h], wo, bo, "o")
             close(lse[r, h], wl, bl, "lse")
+
+
+@pytest.mark.parametrize("d,hq,n_tok,lens", [
+    (64, 4, 1, [300]), (256, 4, 1, [4000, 1]), (128, 8, 2, [40, 200, 16]), (256, 4, 16, [300, 7]),
+    (128, 40, 1, [2000, 64]), (64, 2, 1, [9] * 700), (64, 20, 1, [70] * 300)])
+def test_decode_rows_without_a_finite_score_are_zero(d, hq, n_tok, lens):
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(76 + d)
+    c = Paged(rng, lens, 16, 1, d, "bf16")
+    q = randn(rng, (len(lens) * n_tok, hq, d), "bf16")
+    q[..., 0] = 1.0
+    c.k[..., 0] = -INF
+    o, lse = run_decode(c, q, n_tok)
+    assert torch.all(o == 0) and takes(lse, -INF)
+    no_error()
