@@ -12,6 +12,8 @@
 namespace gdr {
 namespace attn {
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 __device__ __forceinline__ void record_invalid(int32_t *err) { atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG); }
 
 // Two 16-bit values of a word as floats, and back (round to nearest even).
@@ -56,6 +58,13 @@ template <bool F16>
 __device__ __forceinline__ float next_reference(float m, float top) {
     using R = Reference<F16>;
     return top > m + R::TOP || m == -CUDART_INF_F ? fmaxf(m, top - R::LEAD) : m;
+}
+
+// Factor of scores that are masked before it is applied: scale log2(e) without its sign.  A
+// scale of 0 still has to leave a masked score at minus infinity, so the smallest float
+// stands in for it: times any finite score that stays under 2^-21, a weight of 1.
+__device__ __forceinline__ float softmax_scale(float scale) {
+    return fmaxf(fabsf(scale) * kLog2e, __uint_as_float(1u));
 }
 
 // 1 / l for the output o = O / l; a row without a finite score (it sees no token, or its

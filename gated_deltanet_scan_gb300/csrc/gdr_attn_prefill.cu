@@ -51,7 +51,6 @@ constexpr int kThreads = 512;
 constexpr int kPairs = 76;   // CTA pairs on 152 SMs
 constexpr int kRows = 128;  // rows per CTA
 constexpr int kTile = 128;  // tokens per tile
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Shape {
@@ -551,8 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- P: warpgroup wg takes the tiles with g % 2 == wg; a thread is a row
         const int wg = warp >> 2, row = tid & 127, wq = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-        // a scale of 0 still has to leave a masked score at minus infinity
-        const float sc = fmaxf(fabsf(a.scale), 1e-30f) * kLog2e;
+        const float sc = softmax_scale(a.scale);
         const int tok = row / a.group, head_in_group = row - tok * a.group;
         const uint32_t p_bars = pair::map_to(bar(Bar::PFull), 0);
         uint32_t g0 = 0;              // tiles before this block's

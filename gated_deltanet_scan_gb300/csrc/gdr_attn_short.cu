@@ -20,7 +20,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kRows = 64;  // rows per block
 constexpr int kTile = 32;  // tokens per tile
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) short_kernel(const __grid_constant__ Args a) {

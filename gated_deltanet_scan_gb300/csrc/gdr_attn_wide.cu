@@ -35,7 +35,6 @@ using namespace tc;
 
 constexpr int kThreads = 384;
 constexpr int kRows = 128, kTile = 64;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kColsS = 256;  // TMEM: O at 0, S tiles at 256 and 320
 
 template <int D>
@@ -135,8 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         // ---- P and O; a thread is a row
         const int row = tid;
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        // a scale of 0 still has to leave a masked score at minus infinity
-        const float sc = fmaxf(fabsf(a.scale), 1e-30f) * kLog2e;
+        const float sc = softmax_scale(a.scale);
         float2 *const ml_parts = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + L.ml);
         float *const o_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + L.o);
         uint32_t g = 0;  // tiles

@@ -190,3 +190,21 @@ def test_decode_rows_without_a_finite_score_are_zero(d, hq, n_tok, lens):
     o, lse = run_decode(c, q, n_tok)
     assert torch.all(o == 0) and takes(lse, -INF)
     no_error()
+
+
+# --- scales ---------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("power,scale", [(60, 0.0), (55, 2.0 ** -110), (55, -2.0 ** -110), (60, 2.0 ** -135)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scales_near_zero_and_large_products(d, power, scale):
+    """Products near 2^115 with scales that bring them to a few units, or to nothing; fp32 holds both."""
+    gu.require_gpu()
+    rng = np.random.default_rng(78)
+    size = 2.0 ** power
+    q, k = randn(rng, (400, 2, d), "bf16", size), randn(rng, (400, 1, d), "bf16", size)
+    v = randn(rng, (400, 1, d), "bf16")
+    check_prefill(q, k, v, [60, 340], "bf16", scale=scale)
+    c = Paged(rng, [300, 17], 16, 1, d, "bf16")
+    c.k *= size
+    check_decode(c, randn(rng, (4, 4, d), "bf16", size), 2, "bf16", scale=scale)
+    check_decode(c, randn(rng, (2, 40, d), "bf16", size), 1, "bf16", scale=scale)
