@@ -76,10 +76,10 @@ gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int3
     if (st != GDR_OK) return st;
     if (n_seqs < 0 || t_total < 0 || (n_seqs == 0 && t_total > 0)) return GDR_ERR_INVALID_ARG;
     if (rot_dim < 0 || rot_dim > dims->d || (rot_dim & 1)) return GDR_ERR_INVALID_ARG;
+    if (t_total == 0) return GDR_OK;  // an empty batch's tensors may have no address
     if (rot_dim > 0 && !aligned(inv_freq, 4)) return GDR_ERR_INVALID_ARG;
     st = check_cache(cache);
     if (st != GDR_OK) return st;
-    if (t_total == 0) return GDR_OK;
     if (t_total > INT_MAX) return GDR_ERR_UNSUPPORTED;
     if (cu_seqlens ? !aligned(cu_seqlens, 4) : t_total % n_seqs != 0) return GDR_ERR_INVALID_ARG;
     if (!aligned(kv_lens, 4) || !rows_ok(k) || !rows_ok(v)) return GDR_ERR_INVALID_ARG;
@@ -147,9 +147,9 @@ gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_
     gdr_status st = check_dims(dims);
     if (st != GDR_OK) return st;
     if (n_seqs < 0 || n_tok < 1 || n_tok > 16) return GDR_ERR_INVALID_ARG;
+    if (n_seqs == 0) return GDR_OK;
     st = check_cache(cache);
     if (st != GDR_OK) return st;
-    if (n_seqs == 0) return GDR_OK;
     if (!rows_ok(q) || !rows_ok(o) || !aligned(kv_lens, 4) || (lse && !aligned(lse, 4))) return GDR_ERR_INVALID_ARG;
     if ((int64_t)n_seqs * n_tok > INT_MAX / dims->h_q) return GDR_ERR_UNSUPPORTED;
     const size_t need = decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);

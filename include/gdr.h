@@ -501,7 +501,7 @@ typedef struct gdr_kv_cache {
  * A sequence whose positions leave [0, max_pages * page_size) has the tokens outside
  * left out of the cache, and GDR_ERR_INVALID_ARG recorded in the device error word;
  * entries of cu_seqlens outside [0, t_total] likewise skip the sequence.  dims->scale
- * is not used.  n_seqs = 0 or t_total = 0 is a no-op.
+ * is not used.  n_seqs = 0 or t_total = 0 is a no-op, whatever the pointers are.
  */
 gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, int64_t t_total,
                            const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *q_out,
@@ -520,7 +520,7 @@ gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int3
  *
  *   q, o [t_total][h_q][d]; k, v [t_total][h_kv][d] (strided rows, dims->dtype)
  *   lse  NULL, or DEVICE fp32 [t_total][h_q]: log sum_j exp(scale q_i . k_j)
- * t_total below 2^31.  No workspace.
+ * t_total below 2^31.  No workspace.  n_seqs = 0 or t_total = 0 is a no-op.
  */
 gdr_status gdr_attn_prefill(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, int64_t t_total,
                             const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *o, float *lse,
@@ -543,7 +543,7 @@ gdr_status gdr_attn_prefill(const gdr_attn_dims *dims, int32_t n_seqs, const int
  * whatever the lengths; sequences that are cut have their parts joined by a second
  * launch in a fixed order, so results do not change from run to run.
  *
- *   q, o       [n_seqs * n_tok][h_q][d]; n_seqs * n_tok * h_q below 2^31
+ *   q, o       [n_seqs * n_tok][h_q][d]; n_seqs * n_tok * h_q below 2^31; n_seqs = 0 is a no-op
  *   kv_lens    DEVICE int32 [n_seqs]
  *   lse        NULL, or DEVICE fp32 [n_seqs * n_tok][h_q]
  *   workspace  DEVICE, 16-byte aligned, at least gdr_attn_decode_workspace_bytes();

@@ -208,3 +208,24 @@ def test_scales_near_zero_and_large_products(d, power, scale):
     c.k *= size
     check_decode(c, randn(rng, (4, 4, d), "bf16", size), 2, "bf16", scale=scale)
     check_decode(c, randn(rng, (2, 40, d), "bf16", size), 1, "bf16", scale=scale)
+
+
+# --- empty batches --------------------------------------------------------------------------------------------
+
+def test_empty_batches_are_no_ops():
+    torch = gu.require_gpu()
+    bf, cuda = torch.bfloat16, torch.device("cuda")
+    q, k = torch.empty(0, 4, 64, dtype=bf, device=cuda), torch.empty(0, 2, 64, dtype=bf, device=cuda)
+    kc, vc = (torch.ones(5, 16, 2, 64, dtype=bf, device=cuda) for _ in range(2))
+    none, table = ints([]), torch.empty(0, 3, dtype=torch.int32, device=cuda)
+    inv = torch.ones(8, device=cuda)
+    gdr.gdr_attn_append(q, k, k, q, k, kc, vc, table, none, inv)
+    gdr.gdr_attn_append(q, k, k, q, k, kc, vc, table, none, inv, ints([0]))
+    gdr.gdr_attn_append(None, k, k, None, None, kc, vc, torch.zeros(2, 3, dtype=torch.int32, device=cuda),
+                        ints([3, 4]), inv, ints([0, 0, 0]))  # two sequences, nothing new
+    gdr.gdr_attn_prefill(q, k, k, q, ints([0]))
+    gdr.gdr_attn_prefill(q, k, k, q, ints([0, 0, 0]))
+    gdr.gdr_attn_decode(q, kc, vc, table, none, q)
+    gdr.gdr_attn_decode(q, kc, vc, table, none, q, 4, lse=torch.empty(0, 4, device=cuda))
+    assert torch.all(kc == 1) and torch.all(vc == 1)
+    no_error()
