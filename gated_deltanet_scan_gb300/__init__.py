@@ -434,14 +434,15 @@ def gdr_selftest_wait_timeout(limit_cycles: int, *, stream=None, device=None) ->
 # A decode step's kernels take a few microseconds, so its call must not cost the
 # host more: every attribute of a tensor is read once.
 
-_attn_types = None  # dtype -> code, int32, fp32, and the raw current stream of a device index
+_attn_types = None  # dtype -> code, int32, fp32, the raw current stream of a device index, the current device
 
 
 def _attn_init():
     global _attn_types
     torch = _torch()
     _attn_types = ({torch.bfloat16: GDR_BF16, torch.float16: GDR_F16, torch.float32: GDR_F32}, torch.int32,
-                   torch.float32, getattr(torch._C, "_cuda_getCurrentRawStream", None))
+                   torch.float32, getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                   getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
     return _attn_types
 
 
@@ -455,6 +456,9 @@ def _attn_dims(h_q: int, h_kv: int, d: int, dtype, scale) -> gdr_attn_dims:
 def _attn_stream(stream, dev: int):
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
+    current = _attn_types[4]()
+    if current != dev:  # kernels, streams' default handle and the error word are the current device's
+        raise ValueError(f"tensors are on device {dev}, but device {current} is current")
     if stream is None:
         raw = _attn_types[3]
         return raw(dev) if raw is not None else _torch().cuda.current_stream(dev).cuda_stream
