@@ -5,6 +5,7 @@
 
 #include "gdr_attn.h"
 #include "gdr_internal.h"
+#include "gdr_overlap.h"
 
 namespace gdr {
 namespace attn {
@@ -16,6 +17,15 @@ bool aligned(const void *p, uintptr_t bytes) { return p && (reinterpret_cast<uin
 bool stride_ok(int64_t s) { return s >= 0 && s < kMaxStride && (s & 7) == 0; }
 bool rows_ok(const gdr_rows *r) {
     return r && aligned(r->ptr, 16) && stride_ok(r->token_stride) && stride_ok(r->head_stride);
+}
+// Rows that a kernel writes.
+bool out_rows_ok(const gdr_rows *r, int64_t tokens, int heads, int d) {
+    return rows_ok(r) && !overlap(tokens, r->token_stride, heads, r->head_stride, d);
+}
+bool out_cache_ok(const gdr_kv_cache *c, int heads, int d) {  // any two of its three dimensions
+    return !overlap(c->n_pages, c->page_stride, c->page_size, c->token_stride, d) &&
+           !overlap(c->page_size, c->token_stride, heads, c->head_stride, d) &&
+           !overlap(c->n_pages, c->page_stride, heads, c->head_stride, d);
 }
 Rows to_rows(const gdr_rows *r) {
     if (!r) return Rows{nullptr, 0, 0};
@@ -83,8 +93,10 @@ gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int3
     if (t_total > INT_MAX) return GDR_ERR_UNSUPPORTED;
     if (cu_seqlens ? !aligned(cu_seqlens, 4) : t_total % n_seqs != 0) return GDR_ERR_INVALID_ARG;
     if (!aligned(kv_lens, 4) || !rows_ok(k) || !rows_ok(v)) return GDR_ERR_INVALID_ARG;
-    if (!q != !q_out || (q && (!rows_ok(q) || !rows_ok(q_out)))) return GDR_ERR_INVALID_ARG;
-    if (k_out && !rows_ok(k_out)) return GDR_ERR_INVALID_ARG;
+    if (!q != !q_out || (q && (!rows_ok(q) || !out_rows_ok(q_out, t_total, dims->h_q, dims->d))))
+        return GDR_ERR_INVALID_ARG;
+    if (k_out && !out_rows_ok(k_out, t_total, dims->h_kv, dims->d)) return GDR_ERR_INVALID_ARG;
+    if (!out_cache_ok(cache, dims->h_kv, dims->d)) return GDR_ERR_INVALID_ARG;
     // in place: the same rows (a row is read whole before it is written)
     if (q && q->ptr == q_out->ptr &&
         (q->token_stride != q_out->token_stride || q->head_stride != q_out->head_stride))
@@ -119,7 +131,8 @@ gdr_status gdr_attn_prefill(const gdr_attn_dims *dims, int32_t n_seqs, const int
     if (n_seqs < 0 || t_total < 0 || (n_seqs == 0 && t_total > 0)) return GDR_ERR_INVALID_ARG;
     if (t_total == 0) return GDR_OK;
     if (t_total > INT_MAX) return GDR_ERR_UNSUPPORTED;
-    if (!aligned(cu_seqlens, 4) || !rows_ok(q) || !rows_ok(k) || !rows_ok(v) || !rows_ok(o))
+    if (!aligned(cu_seqlens, 4) || !rows_ok(q) || !rows_ok(k) || !rows_ok(v) ||
+        !out_rows_ok(o, t_total, dims->h_q, dims->d))
         return GDR_ERR_INVALID_ARG;
     if (lse && !aligned(lse, 4)) return GDR_ERR_INVALID_ARG;
     Args a = make_args(dims);
@@ -150,7 +163,9 @@ gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_
     if (n_seqs == 0) return GDR_OK;
     st = check_cache(cache);
     if (st != GDR_OK) return st;
-    if (!rows_ok(q) || !rows_ok(o) || !aligned(kv_lens, 4) || (lse && !aligned(lse, 4))) return GDR_ERR_INVALID_ARG;
+    if (!rows_ok(q) || !out_rows_ok(o, (int64_t)n_seqs * n_tok, dims->h_q, dims->d) || !aligned(kv_lens, 4) ||
+        (lse && !aligned(lse, 4)))
+        return GDR_ERR_INVALID_ARG;
     if ((int64_t)n_seqs * n_tok > INT_MAX / dims->h_q) return GDR_ERR_UNSUPPORTED;
     const size_t need = decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);
     if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return GDR_ERR_INVALID_ARG;

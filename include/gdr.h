@@ -440,7 +440,10 @@ gdr_status gdr_state_restore(const gdr_dims *dims, int32_t n_seqs, const float *
  *     ptr[t * token_stride + h * head_stride + x],
  * strides in elements.  ptr is 16-byte aligned and both strides are multiples of
  * 8, not negative, and below 2^38 (GDR_ERR_INVALID_ARG otherwise).  Rows that are
- * written must not overlap one another.
+ * written must not overlap one another, nor the cache's where it is written: strides
+ * that make them do so are GDR_ERR_INVALID_ARG (inputs may have such strides, e.g. 0).
+ * Outputs must not overlap inputs or other outputs either (o is not q), but for
+ * gdr_attn_append's rows in place; this is not checked.
  */
 typedef struct gdr_attn_dims {
     int32_t h_q;   /* query heads; a multiple of h_kv */
