@@ -43,6 +43,15 @@ __device__ __forceinline__ float unpack1(uint16_t w) {
         return __uint_as_float((uint32_t)w << 16);
 }
 
+// Two weights p >= 0 as bf16 pairs whose sum holds 16 bits of them: cut to bf16, and the rest
+// rounded to it.  The rest is taken of p (1 + 2^-23), so that neither part is 0 (from 2^-103
+// up) and an infinite value times either is that infinity.
+__device__ __forceinline__ void split2(float a, float b, uint32_t &cut, uint32_t &rest) {
+    constexpr float kOver = 1.00000011920928955f;  // 1 + 2^-23
+    cut = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    rest = pack2<false>(fmaf(a, kOver, -__uint_as_float(cut << 16)), fmaf(b, kOver, -__uint_as_float(cut & 0xFFFF0000u)));
+}
+
 // The reference m of a row's weights p = 2^(x - m), which enter P V in 16 bits.  Sums are
 // rescaled when m moves, so it follows the row's maximum only when that is TOP above it,
 // and is then LEAD under it.  bf16 rounds weights of any size relative to themselves.  fp16

@@ -22,8 +22,13 @@
 // programmatic dependent launch, joins the blocks' parts from the workspace; always in
 // the order of the tokens.
 //
-// P is rounded to the tensors' type for P V (its sum l is not): that is the only
-// rounding between the inputs and the output's own.
+// P enters P V in 16 bits (its sum l does not): that is the only rounding between the
+// inputs and the output's own.  fp16 holds 11 bits of a weight.  bf16 holds 8, which added
+// as much error as the output's own rounding (64 sequences of d = 256: 0.00226 of o's rms
+// against 0.00166 for that rounding alone), so bf16 weights are two operands, cut and
+// rest, of a second product each: error 0.00166, 121.3 us instead of 120.4 (one sequence
+// of 131,072 tokens 93.4 / 92.7; 64 of 2,000, d = 128, 98.4 / 97.7; of 4,000, d = 64, 58.1 /
+// 55.6).
 #include "gdr_attn_line.cuh"
 #include "gdr_attn_mma.cuh"
 #include "gdr_internal.h"
@@ -189,7 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     }
                 }
             }
-            uint32_t pf[TT / 2][4];  // P as MMA operands
+            constexpr int PARTS = F16 ? 1 : 2;
+            uint32_t pf[PARTS][TT / 2][4];  // P as MMA operands, bf16 ones in two parts
             float c[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -213,7 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 for (int e = 0; e < TT; ++e) {
                     const float p = tc::fast_exp2(v[2 * e] - ref), q = tc::fast_exp2(v[2 * e + 1] - ref);
                     l[i] += p + q;
-                    pf[e >> 1][(e & 1) * 2 + i] = pack2<F16>(p, q);
+                    const int f = (e & 1) * 2 + i;
+                    if constexpr (F16)
+                        pf[0][e >> 1][f] = pack2<true>(p, q);
+                    else
+                        split2(p, q, pf[0][e >> 1][f], pf[PARTS - 1][e >> 1][f]);
                 }
             }
             if (__any_sync(0xffffffffu, c[0] != 1.f || c[1] != 1.f)) {
@@ -288,8 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                     for (int n = 0; n < NT; n += 2) {
                         uint32_t b[4];
                         ldsm4t(at[(n >> 1) & 3] + t * 16 * D * 2 + (n >> 3) * 128, b);
-                        mma16816<F16>(acc[n], pf[t], b[0], b[1]);
-                        mma16816<F16>(acc[n + 1], pf[t], b[2], b[3]);
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i) {
+                            mma16816<F16>(acc[n], pf[i][t], b[0], b[1]);
+                            mma16816<F16>(acc[n + 1], pf[i][t], b[2], b[3]);
+                        }
                     }
                 }
             }

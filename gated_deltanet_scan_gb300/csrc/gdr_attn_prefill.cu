@@ -30,6 +30,9 @@
 //   O / l   a warpgroup reads O when a block's last P V is done, and stores the result while
 //           the next block's first tiles are already in work.
 //
+// P is rounded to 16 bits, the second MMA's type: the products bound this kernel, and more
+// bits would take a third one.
+//
 // A token must not see what later tokens or other sequences hold, even a NaN, and 0
 // times NaN is NaN.  In S that is a select.  In the few tiles in which some row of the
 // pair does not see every token, two warps replace the value tile's infinities and

@@ -19,6 +19,10 @@
 //   P, O     one warpgroup, a row per thread: P of every tile, and O at a triple's end.
 // All roles run over the triples' ends, so the loads never stop.
 //
+// P is rounded to 16 bits.  A second product with what bf16's rounding left, as in
+// gdr_attn_decode.cu, would halve o's squared error and take 10% longer (16 draft tokens of 32
+// sequences of 2,000, d = 128: 77.6 against 69.5 us; 8 of 512 to 8,192, d = 256: 39.4 / 38.6).
+//
 // Draft tokens' values that some row does not see are cleaned of infinities and NaNs by
 // the threads that copied them, and added at the end to the rows that see them.
 #include "gdr_attn_line.cuh"

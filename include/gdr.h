@@ -431,7 +431,11 @@ gdr_status gdr_state_restore(const gdr_dims *dims, int32_t n_seqs, const float *
  * of the last 1 to 16 tokens of every sequence over its pages.
  *
  * Types: q, k, v, o and the cache all have dims->dtype, GDR_BF16 or GDR_F16;
- * scores, softmax statistics and sums are fp32, and each output is rounded once.
+ * scores, softmax statistics and sums are fp32, and each output is rounded once.  The
+ * softmax's weights are rounded for their product with v (not for their sum): fp16's to
+ * 11 bits, bf16's to 8, or to 16 in gdr_attn_decode with n_tok * h_q / h_kv <= 16.  An
+ * infinite value that a row sees makes its column of o that infinity if the token's weight
+ * is over 2^-32 (fp16) or 2^-100 (bf16) of the row's largest, and else perhaps NaN.
  * Head sizes: d in {64, 128, 256}.  Query head h reads key/value head
  * h / (h_q / h_kv); h_q / h_kv <= 128.
  *

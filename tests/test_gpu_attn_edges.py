@@ -229,3 +229,38 @@ def test_empty_batches_are_no_ops():
     gdr.gdr_attn_decode(q, kc, vc, table, none, q, 4, lse=torch.empty(0, 4, device=cuda))
     assert torch.all(kc == 1) and torch.all(vc == 1)
     no_error()
+
+
+# --- the weights' bits ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens", [[40], [3000], [33] * 400])  # cut and joined in a block or by the second launch; whole
+@pytest.mark.parametrize("d,n_tok,h_q", [(64, 1, 4), (128, 3, 2), (256, 1, 16), (256, 4, 4)])
+def test_decode_weights_hold_16_bits(d, n_tok, h_q, lens):
+    """bf16, up to 16 rows.  Half of the tokens weigh 1 and have the value 1, the other half weigh e^-x, between
+    two bf16 values, and have -1: what is left shows the weights' rounding, which is the same in all of them.  A
+    weight is its first 8 bits and the rest (up to 2^-7 of it) rounded to 8 bits: off by 2^-15.  The other terms are
+    those of tests/attn_ref.py, with sum_j p_j |v_j| = 1."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(90)
+    c = Paged(rng, lens, 16, 1, d, "bf16")
+    q = torch.zeros(len(lens) * n_tok, h_q, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = 1.0
+    x = torch.tensor([0.0035, 0.0011, 0.0059, 0.0095] * h_q, device="cuda").to(torch.bfloat16)[:h_q]
+    c.k.zero_()
+    c.v.fill_(1.0)
+    for s, n in enumerate(lens):
+        p = np.arange(1, n, 2)
+        c.k[c.table_np[s, p // 16], p % 16, :, 5] = -1.0
+        c.v[c.table_np[s, p // 16], p % 16] = -1.0
+    q[..., 5] = x
+    o, lse = run_decode(c, q, n_tok, scale=1.0)
+    no_error()
+    o, w = f64(o), np.exp(-f64(x))
+    for s, n in enumerate(lens):
+        for j in range(n_tok):
+            seen = n - n_tok + j + 1
+            one, other = (seen + 1) // 2, seen // 2
+            want = (one - other * w) / (one + other * w)  # per head
+            bound = 2.0 ** -8 * np.abs(want) + (1 + 2.0 ** -8) * (2.0 ** -15 + 2 * d * 2.0 ** -24 * f64(x) + 2.0 ** -16)
+            err = np.abs(o[s * n_tok + j] - want[:, None]) - bound[:, None]
+            assert np.all(err <= 0), (s, j, err.max())
