@@ -194,6 +194,16 @@ def test_decode_rows_without_a_finite_score_are_zero(d, hq, n_tok, lens):
 
 # --- scales ---------------------------------------------------------------------------------------------------
 
+@pytest.mark.parametrize("hq", [2, 40])  # 2 rows and 40: either kernel
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1.0])
+def test_decode_scales(scale, hq):
+    gu.require_gpu()
+    rng = np.random.default_rng(77)
+    c = Paged(rng, [300, 17, 1], 16, 1, 128, "bf16", stale=NAN)
+    check_decode(c, randn(rng, (3, hq, 128), "bf16"), 1, "bf16", scale=scale)
+    check_decode(c, randn(rng, (12, hq, 128), "bf16"), 4, "bf16", scale=scale)
+
+
 @pytest.mark.parametrize("power,scale", [(60, 0.0), (55, 2.0 ** -110), (55, -2.0 ** -110), (60, 2.0 ** -135)])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_scales_near_zero_and_large_products(d, power, scale):
@@ -208,6 +218,100 @@ def test_scales_near_zero_and_large_products(d, power, scale):
     c.k *= size
     check_decode(c, randn(rng, (4, 4, d), "bf16", size), 2, "bf16", scale=scale)
     check_decode(c, randn(rng, (2, 40, d), "bf16", size), 1, "bf16", scale=scale)
+
+
+# --- what the device checks itself --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n_tok,h_q", [(1, 2), (16, 4), (1, 40)])  # 2 rows; 64 and 40, which are the wide kernel's
+def test_decode_bad_lengths_and_pages(n_tok, h_q):
+    """A bad length counts as none, a bad page is read as zeros; the other sequence is not touched by either."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(80)
+    c = Paged(rng, [200, 90], 16, 1, 64, "bf16")
+    q = randn(rng, (2 * n_tok, h_q, 64), "bf16")
+    good, _ = run_decode(c, q, n_tok)
+    no_error()
+    most = c.table.shape[1] * 16
+    for bad in (-1, most + 1, 2 ** 31 - 1):
+        o, lse = nan_like(q.shape, q.dtype), nan_like(q.shape[:2], torch.float32)
+        gdr.gdr_attn_decode(q, c.k, c.v, c.table, ints([bad, 90]), o, n_tok, lse=lse)
+        assert gdr.gdr_device_error(device="cuda") == gdr.GDR_ERR_INVALID_ARG
+        assert torch.all(o[:n_tok] == 0) and takes(lse[:n_tok], -INF)
+        # (cut elsewhere on the line, the second sequence's sums are in another order)
+        wo, wl, bo, bl = ar.decode(f64(q[n_tok:]), f64(c.k), f64(c.v), c.table_np[1:], [90], n_tok, 0.125, "bf16")
+        close(o[n_tok:], wo, bo, "o")
+        close(lse[n_tok:], wl, bl, "lse")
+    for page in (-7, c.k.shape[0], 2 ** 31 - 1):
+        for slot in (0, 12):  # the first page, and the one that holds the last tokens
+            table = c.table.clone()
+            table[0, slot] = page
+            o = nan_like(q.shape, q.dtype)
+            gdr.gdr_attn_decode(q, c.k, c.v, table, c.kv_lens, o, n_tok)
+            assert gdr.gdr_device_error(device="cuda") == gdr.GDR_ERR_INVALID_ARG
+            assert torch.equal(o[n_tok:], good[n_tok:])
+            # zeros in the place of the page's keys and values
+            k64, v64 = ar.gather(f64(c.k), c.table_np[0], 200), ar.gather(f64(c.v), c.table_np[0], 200)
+            k64[16 * slot:16 * slot + 16] = 0.0
+            v64[16 * slot:16 * slot + 16] = 0.0
+            for h in range(h_q):
+                wo, _, bo, _ = ar.attend(f64(q[:n_tok, h]), k64[:, 0], v64[:, 0], 0.125,
+                                         200 - n_tok + np.arange(1, n_tok + 1), "bf16")
+                close(o[:n_tok, h], wo, bo, "o")
+
+
+STARTS = [
+    # total, starts; a sequence is valid when 0 <= start <= end <= total
+    (9, [0, -2, 9]), (9, [0, 20, 9]), (9, [3, 5, 9]), (9, [0, 4, 12]),
+    (900, [400, 300, 900]), (900, [0, 400, 1200]), (900, [-1, 400, 900]), (900, [0, 300, -5, 600, 900]),
+    (900, [300, 900, 2 ** 31 - 1]), (900, [0, 20, 1000, 20, 900]), (900, [-2 ** 31, 2 ** 31 - 1]),
+]
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("total,starts", STARTS)
+def test_prefill_bad_starts_skip_their_sequences(total, starts, d):
+    """Both prefill kernels: sequences with a start or end out of range or before its start write nothing and are
+    recorded, the others give what they give alone."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(81)
+    q, k, v = randn(rng, (total, 2, d), "bf16"), randn(rng, (total, 1, d), "bf16"), randn(rng, (total, 1, d), "bf16")
+    o = nan_like(q.shape, q.dtype)
+    gdr.gdr_attn_prefill(q, k, v, o, ints(starts))
+    valid = [0 <= a <= b <= total for a, b in zip(starts, starts[1:])]
+    want_code = gdr.GDR_OK if all(valid) else gdr.GDR_ERR_INVALID_ARG
+    assert gdr.gdr_device_error(device="cuda") == want_code
+    rest = torch.ones(total, dtype=torch.bool, device="cuda")
+    for a, b, ok in zip(starts, starts[1:], valid):
+        if ok and b > a:
+            rest[a:b] = False
+            wo, _, bo, _ = ar.prefill(f64(q[a:b]), f64(k[a:b]), f64(v[a:b]), d ** -0.5, [b - a], "bf16")
+            close(o[a:b], wo, bo, "o")
+    assert takes(o[rest], NAN)
+
+
+@pytest.mark.parametrize("total,starts,taken", [
+    (9, [0, -2, 9], []), (9, [0, 20, 9], []), (9, [3, 5, 9], [0, 1]), (9, [0, 4, 12], [0]), (60, [0, 30, 99], [0]),
+])
+def test_append_bad_starts_leave_out_their_tokens(total, starts, taken):
+    """Tokens of no valid sequence are recorded and written nowhere; valid sequences are appended whole."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(82)
+    n = len(starts) - 1
+    lens = [40] * n
+    c = Paged(rng, lens, 16, 1, 64, "bf16")
+    k, v = randn(rng, (total, 1, 64), "bf16"), randn(rng, (total, 1, 64), "bf16")
+    want_k, want_v = c.k.clone(), c.v.clone()
+    ko = nan_like(k.shape, k.dtype)
+    want = ko.clone()
+    gdr.gdr_attn_append(None, k, v, None, ko, c.k, c.v, c.table, c.kv_lens, None, ints(starts))
+    assert gdr.gdr_device_error(device="cuda") == gdr.GDR_ERR_INVALID_ARG  # each case leaves some token out
+    for s in taken:
+        a, b = starts[s], starts[s + 1]
+        pos = np.arange(40 - (b - a), 40)
+        want_k[c.table_np[s, pos // 16], pos % 16], want_v[c.table_np[s, pos // 16], pos % 16] = k[a:b], v[a:b]
+        want[a:b] = k[a:b]
+    assert torch.equal(c.k, want_k) and torch.equal(c.v, want_v)
+    assert torch.equal(ko.view(torch.int16), want.view(torch.int16))
 
 
 # --- empty batches --------------------------------------------------------------------------------------------
