@@ -6,8 +6,10 @@
 // reduced in 64-bit fixed point: f_i / 2 pi modulo one turn is held as a fraction
 // of 2^64 (from the float's bits and the 64 leading bits of 1 / 2 pi: off by 2^-62 of
 // itself), p times it wraps around exactly, and the top 32 bits of the product are
-// the signed fraction of a turn that cos and sin take.  At p = 2^24 the angle is still
-// good to 2^-32 turns; a 32-bit float product would be off by whole radians.
+// the signed fraction of a turn.  At p = 2^24 they are off by at most one step of 2^-32 turns
+// for frequencies of a few hundred (by 2^-21 turns at 2^20, the largest); cos and sin take
+// them as a float, off by up to 2^-26 turns.  A 32-bit float product p f would be off by whole
+// radians.
 //
 // Bound by HBM for prompts (every row read once, every output written once) and by
 // latency for a few tokens.  One 16-byte vector (8 values) per lane, d / 8 lanes a
@@ -46,7 +48,7 @@ __device__ __forceinline__ uint64_t turn_of(float f) {
     const uint32_t u = __float_as_uint(f);
     const int e = (u >> 23) & 0xFF;
     const uint64_t m = (u & 0x7FFFFFu) | (e ? 0x800000u : 0u);
-    const int down = 150 - (e ? e : 1);  // -E: at least 7 below 2^20
+    const int down = 150 - (e ? e : 1);  // -E: at least 4 below 2^20
     const uint64_t lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
     const uint64_t t = down <= 0 ? lo : down < 64 ? (lo >> down) | (hi << (64 - down)) : down < 128 ? hi >> (down - 64) : 0;
     return u >> 31 ? 0 - t : t;

@@ -16,7 +16,7 @@
 // copies several tiles ahead: no warp waits for another, and while one starts or ends a
 // sequence the others of its SM keep the memory busy.  Both products are warp-level
 // m16n8k16 MMAs on the 16-bit rows with fp32 sums: at 4 flops a byte the tensor pipes are
-// far from busy (17%), so the rows they pad cost nothing.  A sequence that one worker sees
+// far from busy (26%), so the rows they pad cost nothing.  A sequence that one worker sees
 // whole is written by it; the others leave (m, l, O): the workers of a block, next to
 // each other on the line, join what they can among themselves, and a second kernel, a
 // programmatic dependent launch, joins the blocks' parts from the workspace; always in

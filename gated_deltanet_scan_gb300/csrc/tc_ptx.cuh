@@ -27,9 +27,11 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t byt
 }
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    // acquire at CTA scope (every producer is in this CTA: its threads, its
-    // MMAs, or bulk copies into its own shared memory); the hint lets the
-    // hardware park the thread up to ~8 us instead of re-polling
+    // acquire at CTA scope: the producers are this CTA's threads, its MMAs, or bulk
+    // copies into its own shared memory.  (The two-SM attention kernel also waits so for
+    // arrivals of the other CTA; what those order is in TMEM or read by an MMA, behind
+    // fences of its own, or was released at cluster scope: see the comments there.)  The
+    // hint lets the hardware park the thread up to ~8 us instead of re-polling
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"

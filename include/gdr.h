@@ -495,8 +495,9 @@ typedef struct gdr_kv_cache {
  * every query and key head are rot_dim / 2 pairs (x, y): values i and
  * i + rot_dim / 2, or, interleaved, 2 i and 2 i + 1.  With a = p * inv_freq[i],
  *     (x, y) -> (x cos a - y sin a, x sin a + y cos a),
- * the angle reduced exactly enough (64-bit fixed point) that far positions lose
- * nothing; the other values are copied.  q_out, k_out and the cached key are the
+ * the angle reduced in 64-bit fixed point, so that far positions lose nothing: at
+ * position 2^24 it is off by under 2^-25 turns for frequencies of a few hundred and less,
+ * as at position 1 (by 2^-20 at 2^20); the other values are copied.  q_out, k_out and the cached key are the
  * rotated rows rounded once; values are copied.
  *
  *   q, q_out   [t_total][h_q][d]; q_out may be q (same strides).  Both NULL: no queries.
@@ -506,8 +507,9 @@ typedef struct gdr_kv_cache {
  *   inv_freq   DEVICE fp32 [rot_dim / 2], each value's magnitude below 2^20; NULL when rot_dim is 0
  *   rot_dim    even, 0 .. d
  * A sequence whose positions leave [0, max_pages * page_size) has the tokens outside
- * left out of the cache, and GDR_ERR_INVALID_ARG recorded in the device error word;
- * entries of cu_seqlens outside [0, t_total] likewise skip the sequence.  dims->scale
+ * left out of the cache, and GDR_ERR_INVALID_ARG recorded in the device error word.
+ * Tokens that cu_seqlens gives to no sequence within [0, t_total] are likewise recorded,
+ * and written nowhere (in a list that is not non-decreasing, other tokens too may be).  dims->scale
  * is not used.  n_seqs = 0 or t_total = 0 is a no-op, whatever the pointers are.
  */
 gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, int64_t t_total,
