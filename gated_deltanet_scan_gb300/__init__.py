@@ -434,7 +434,9 @@ def gdr_selftest_wait_timeout(limit_cycles: int, *, stream=None, device=None) ->
 # A decode step's kernels take a few microseconds, so its call must not cost the
 # host more: every attribute of a tensor is read once.
 
-_attn_types = None  # dtype -> code, int32, fp32, the raw current stream of a device index, the current device
+# dtype -> code, int32, fp32, the raw current stream of a device index, the current device (None: there is only one,
+# and nothing to ask, which would take half a microsecond)
+_attn_types = None
 
 
 def _attn_init():
@@ -442,7 +444,7 @@ def _attn_init():
     torch = _torch()
     _attn_types = ({torch.bfloat16: GDR_BF16, torch.float16: GDR_F16, torch.float32: GDR_F32}, torch.int32,
                    torch.float32, getattr(torch._C, "_cuda_getCurrentRawStream", None),
-                   getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
+                   torch.cuda.current_device if torch.cuda.device_count() > 1 else None)
     return _attn_types
 
 
@@ -456,9 +458,9 @@ def _attn_dims(h_q: int, h_kv: int, d: int, dtype, scale) -> gdr_attn_dims:
 def _attn_stream(stream, dev: int):
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    current = _attn_types[4]()
-    if current != dev:  # kernels, streams' default handle and the error word are the current device's
-        raise ValueError(f"tensors are on device {dev}, but device {current} is current")
+    if _attn_types[4] is not None and _attn_types[4]() != dev:
+        # kernels, streams' default handle and the error word are the current device's
+        raise ValueError(f"tensors are on device {dev}, but device {_attn_types[4]()} is current")
     if stream is None:
         raw = _attn_types[3]
         return raw(dev) if raw is not None else _torch().cuda.current_stream(dev).cuda_stream

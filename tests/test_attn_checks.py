@@ -38,7 +38,8 @@ def test_binding_wants_the_tensors_device_current(L, monkeypatch):
     for name in ("gdr_attn_append", "gdr_attn_prefill", "gdr_attn_decode"):
         monkeypatch.setattr(L, name, lambda *a: called.append(a) or OK)
     monkeypatch.setattr(gdr, "_attn_types", None)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     q, k, kc = new(6, 4, 64), new(6, 2, 64), new(5, 16, 2, 64)
     lens, table = new(2, dtype=torch.int32), new(2, 3, dtype=torch.int32)
     calls = (lambda: gdr.gdr_attn_prefill(q, k, k, q, new(3, dtype=torch.int32), stream=0),
@@ -49,7 +50,7 @@ def test_binding_wants_the_tensors_device_current(L, monkeypatch):
             call()
     assert not called
     monkeypatch.setattr(gdr, "_attn_types", None)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     for call in calls:
         call()
     assert len(called) == 3
