@@ -6,7 +6,7 @@
 // reduced in 64-bit fixed point: f_i / 2 pi modulo one turn is held as a fraction
 // of 2^64 (from the float's bits and the 64 leading bits of 1 / 2 pi: off by 2^-62 of
 // itself), p times it wraps around exactly, and the top 32 bits of the product are
-// the signed fraction of a turn.  At p = 2^24 they are off by at most one step of 2^-32 turns
+// the signed fraction of a turn.  At p = 2^24 they are off by a step or two of 2^-32 turns
 // for frequencies of a few hundred (by 2^-21 turns at 2^20, the largest); cos and sin take
 // them as a float, off by up to 2^-26 turns.  A 32-bit float product p f would be off by whole
 // radians.
