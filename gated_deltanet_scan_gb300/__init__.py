@@ -22,6 +22,8 @@ __all__ = [
     "gdr_verify_block", "gdr_verify_commit",
     "gdr_state_snapshot", "gdr_state_restore", "gdr_device_error", "gdr_selftest_wait_timeout", "gdr_status_string",
     "gdr_attn_append", "gdr_attn_prefill", "gdr_attn_decode", "gdr_attn_decode_workspace_bytes",
+    "gdr_verify_tree", "gdr_verify_tree_commit",
+    "gdr_attn_append_tree", "gdr_attn_decode_tree", "gdr_attn_decode_tree_workspace_bytes", "gdr_attn_commit_tree",
     "gdr_attn_dims", "gdr_rows", "gdr_kv_cache",
     "GDR_F32", "GDR_BF16", "GDR_F16", "GDR_FLAG_QK_L2NORM", "GDR_FLAG_BETA_LOGITS",
 ]
@@ -118,6 +120,19 @@ _SIGS = {
                          ctypes.POINTER(gdr_kv_cache), _P, _ROWS, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "gdr_attn_decode_workspace_bytes": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, ctypes.c_int32],
                                         ctypes.c_size_t),
+    "gdr_verify_tree": ([ctypes.POINTER(gdr_dims), ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                         _P], ctypes.c_int),
+    "gdr_verify_tree_commit": ([ctypes.POINTER(gdr_dims), ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P],
+                               ctypes.c_int),
+    "gdr_attn_append_tree": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, ctypes.c_int32, _P, _ROWS, _ROWS, _ROWS,
+                              _ROWS, _ROWS, ctypes.POINTER(gdr_kv_cache), _P, _P, ctypes.c_int32, ctypes.c_int32, _P],
+                             ctypes.c_int),
+    "gdr_attn_decode_tree": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, ctypes.c_int32, _P, _ROWS,
+                              ctypes.POINTER(gdr_kv_cache), _P, _ROWS, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "gdr_attn_decode_tree_workspace_bytes": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, ctypes.c_int32],
+                                             ctypes.c_size_t),
+    "gdr_attn_commit_tree": ([ctypes.POINTER(gdr_attn_dims), ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_int32,
+                              ctypes.c_int64, ctypes.POINTER(gdr_kv_cache), _P, _P, _P], ctypes.c_int),
     "gdr_device_error": ([_P, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "gdr_selftest_wait_timeout": ([ctypes.c_int64, _P], ctypes.c_int),
 }
@@ -532,6 +547,12 @@ def gdr_attn_append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens
     kv_lens int32 [n], each sequence's tokens including the new ones; inv_freq fp32
     [rot_dim / 2] (None: no rotation); cu_seqlens int32 [n + 1], or None when every
     sequence has T / n new tokens."""
+    _append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens, inv_freq, cu_seqlens, None, interleaved,
+            stream)
+
+
+def _append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens, inv_freq, cu_seqlens, parents, interleaved,
+            stream) -> None:
     kv = k.shape
     if len(kv) != 3:
         raise ValueError("k must be [T, H_kv, d]")
@@ -553,13 +574,19 @@ def gdr_attn_append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens
         ko = _rows(k_out, kv, dtype, dev, "k_out")
     i32, f32 = _attn_types[1], _attn_types[2]
     half = 0 if inv_freq is None else inv_freq.shape[0]
-    st = (_lib or lib()).gdr_attn_append(
-        dims, n, None if cu_seqlens is None else _plain(cu_seqlens, (n + 1,), i32, dev, "cu_seqlens"), T, qr, kr, vr,
-        qo, ko, _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
-        _plain(kv_lens, (n,), i32, dev, "kv_lens"), _plain(inv_freq, (half,), f32, dev, "inv_freq") if half else None,
-        2 * half, 1 if interleaved else 0, _attn_stream(stream, dev))
+    rest = (qr, kr, vr, qo, ko, _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
+            _plain(kv_lens, (n,), i32, dev, "kv_lens"),
+            _plain(inv_freq, (half,), f32, dev, "inv_freq") if half else None, 2 * half, 1 if interleaved else 0,
+            _attn_stream(stream, dev))
+    if parents is not None:
+        n_tok = _tree_rows(parents, n, T)
+        st = (_lib or lib()).gdr_attn_append_tree(dims, n, n_tok, _plain(parents, (n, n_tok), i32, dev, "parents"),
+                                                  *rest)
+    else:
+        st = (_lib or lib()).gdr_attn_append(
+            dims, n, None if cu_seqlens is None else _plain(cu_seqlens, (n + 1,), i32, dev, "cu_seqlens"), T, *rest)
     if st != GDR_OK:
-        raise GdrError(st, "gdr_attn_append")
+        raise GdrError(st, "gdr_attn_append" if parents is None else "gdr_attn_append_tree")
 
 
 def gdr_attn_prefill(q, k, v, o, cu_seqlens, *, scale: Optional[float] = None, lse=None, stream=None) -> None:
@@ -594,6 +621,10 @@ def gdr_attn_decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok: int = 1,
     and kv_lens as for gdr_attn_append; lse fp32 [n * n_tok, H_q] or None.  Without
     ``workspace`` (a device tensor of gdr_attn_decode_workspace_bytes bytes) one is taken
     from torch's allocator on the call's stream."""
+    _decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok, None, scale, lse, workspace, stream)
+
+
+def _decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok, parents, scale, lse, workspace, stream) -> None:
     qs = q.shape
     if len(qs) != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [n * n_tok, H_q, d] and the caches [n_pages, page_size, H_kv, d]")
@@ -606,7 +637,8 @@ def gdr_attn_decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok: int = 1,
     L = _lib or lib()
     if workspace is None:
         torch = _torch()
-        need = int(L.gdr_attn_decode_workspace_bytes(dims, n, n_tok))
+        size = L.gdr_attn_decode_workspace_bytes if parents is None else L.gdr_attn_decode_tree_workspace_bytes
+        need = int(size(dims, n, n_tok))
         if need > 0:
             s = stream if stream is not None else torch.cuda.current_stream(q.device)
             if isinstance(s, int):
@@ -615,11 +647,128 @@ def gdr_attn_decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok: int = 1,
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != dev:
         raise ValueError(f"workspace is not on device {dev}")
-    st = L.gdr_attn_decode(
-        dims, n, n_tok, _rows(q, qs, dtype, dev, "q"),
-        _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
-        _plain(kv_lens, (n,), _attn_types[1], dev, "kv_lens"), _rows(o, qs, dtype, dev, "o"),
-        None if lse is None else _plain(lse, (qs[0], h_q), _attn_types[2], dev, "lse"), _ptr(workspace),
-        0 if workspace is None else workspace.nbytes, _attn_stream(stream, dev))
+    rest = (_rows(q, qs, dtype, dev, "q"), _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
+            _plain(kv_lens, (n,), _attn_types[1], dev, "kv_lens"), _rows(o, qs, dtype, dev, "o"),
+            None if lse is None else _plain(lse, (qs[0], h_q), _attn_types[2], dev, "lse"), _ptr(workspace),
+            0 if workspace is None else workspace.nbytes, _attn_stream(stream, dev))
+    if parents is None:
+        st = L.gdr_attn_decode(dims, n, n_tok, *rest)
+    else:
+        st = L.gdr_attn_decode_tree(dims, n, n_tok, _plain(parents, (n, n_tok), _attn_types[1], dev, "parents"), *rest)
     if st != GDR_OK:
-        raise GdrError(st, "gdr_attn_decode")
+        raise GdrError(st, "gdr_attn_decode" if parents is None else "gdr_attn_decode_tree")
+
+
+# --- trees of drafted tokens ------------------------------------------------------
+
+def _tree_rows(parents, n: int, rows: int) -> int:
+    """Rows of each of n trees; ``rows`` is what the tensors have."""
+    if parents.dim() != 2 or parents.shape[0] != n:
+        raise ValueError(f"parents must have shape ({n}, n_tok)")
+    n_tok = parents.shape[1]
+    if rows != n * n_tok:
+        raise ValueError(f"the tensors must have n * n_tok = {n * n_tok} rows, not {rows}")
+    return n_tok
+
+
+def gdr_attn_append_tree(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens, inv_freq, parents, *,
+                         interleaved: bool = False, stream=None) -> None:
+    """gdr_attn_append for trees of drafted tokens (see gdr_attn_append_tree in
+    include/gdr.h): parents int32 [n, n_tok], tensors of n * n_tok rows; a node's
+    position is its path's, its slot its row's; rows that are no nodes are written nowhere."""
+    if parents is None:
+        raise ValueError("parents must be an int32 tensor [n, n_tok]")
+    _append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens, inv_freq, None, parents, interleaved, stream)
+
+
+def gdr_attn_decode_tree_workspace_bytes(q, k_cache, parents) -> int:
+    """Device scratch bytes gdr_attn_decode_tree needs."""
+    dims = _attn_dims(q.shape[1], k_cache.shape[2], k_cache.shape[3], q.dtype, None)
+    return int(lib().gdr_attn_decode_tree_workspace_bytes(dims, *parents.shape))
+
+
+def gdr_attn_decode_tree(q, k_cache, v_cache, page_table, kv_lens, o, parents, *, scale: Optional[float] = None,
+                         lse=None, workspace=None, stream=None) -> None:
+    """Attention of every sequence's tree of up to 64 drafted tokens over its paged cache
+    (see gdr_attn_decode_tree in include/gdr.h): parents int32 [n, n_tok]; everything else as
+    for gdr_attn_decode, the workspace of gdr_attn_decode_tree_workspace_bytes bytes."""
+    n_tok = _tree_rows(parents, kv_lens.shape[0], q.shape[0])
+    _decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok, parents, scale, lse, workspace, stream)
+
+
+def gdr_attn_commit_tree(k_cache, v_cache, page_table, kv_lens, parents, last, lens_out=None, *, stream=None) -> None:
+    """Move every tree's accepted path, which ends in node ``last`` (int32 [n], -1: none), to
+    the front of the tree's slots (see gdr_attn_commit_tree in include/gdr.h).  k_cache,
+    v_cache [n_pages, page_size, H_kv, d], or [layers, n_pages, page_size, H_kv, d] for all
+    layers at once; lens_out int32 [n] (not kv_lens itself) receives the new lengths."""
+    if k_cache.dim() == 5:
+        if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+            raise ValueError("k_cache and v_cache must have the same shape and strides")
+        layers, stride = k_cache.shape[0], k_cache.stride(0)
+        if layers == 0:
+            return
+        k_cache, v_cache = k_cache[0], v_cache[0]
+    elif k_cache.dim() == 4:
+        layers, stride = 1, 0
+    else:
+        raise ValueError("the caches must be [n_pages, page_size, H_kv, d] or [layers, n_pages, page_size, H_kv, d]")
+    h_kv, d = k_cache.shape[2:]
+    dtype, dev = k_cache.dtype, k_cache.get_device()
+    dims = _attn_dims(h_kv, h_kv, d, dtype, 1.0)
+    i32, n = _attn_types[1], kv_lens.shape[0]
+    n_tok = _tree_rows(parents, n, n * parents.shape[-1])
+    st = (_lib or lib()).gdr_attn_commit_tree(
+        dims, n, n_tok, _plain(parents, (n, n_tok), i32, dev, "parents"), _plain(last, (n,), i32, dev, "last"), layers,
+        stride if layers > 1 else 0, _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
+        _plain(kv_lens, (n,), i32, dev, "kv_lens"),
+        None if lens_out is None else _plain(lens_out, (n,), i32, dev, "lens_out"), _attn_stream(stream, dev))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_attn_commit_tree")
+
+
+def gdr_verify_tree(q, k, v, g, beta, state, o, parents, *, deltas=None, scale: float = 1.0, qk_l2norm: bool = False,
+                    beta_logits: bool = False, stream=None) -> None:
+    """The rule along every path of each sequence's tree of up to 64 drafted tokens, from its
+    state, which stays as it is (see gdr_verify_tree in include/gdr.h).  parents int32
+    [n, n_tok]; q, k [n * n_tok, H_qk, d]; v, o [n * n_tok, H_v, d]; g, beta [n * n_tok, H_v]
+    fp32; state [n, H_v, d, d] fp32; ``deltas`` (fp32, shaped like v) receives the corrections
+    that gdr_verify_tree_commit takes."""
+    qs, vs = tuple(q.shape), tuple(v.shape)
+    if len(qs) != 3 or len(vs) != 3 or state.dim() != 4:
+        raise ValueError("q must be [T, H_qk, d], v [T, H_v, d] and state [n, H_v, d, d]")
+    n, T, hv, d = state.shape[0], qs[0], vs[1], qs[2]
+    dims = make_dims(q, v, o, 64, scale, flags_of(qk_l2norm, beta_logits))
+    dev = q.get_device()
+    types = _attn_types or _attn_init()
+    n_tok = _tree_rows(parents, n, T)
+    f32 = types[2]
+    st = (_lib or lib()).gdr_verify_tree(
+        dims, n, n_tok, _plain(parents, (n, n_tok), types[1], dev, "parents"), _plain(q, qs, q.dtype, dev, "q"),
+        _plain(k, qs, q.dtype, dev, "k"), _plain(v, (T, hv, d), q.dtype, dev, "v"), _plain(g, (T, hv), f32, dev, "g"),
+        _plain(beta, (T, hv), f32, dev, "beta"), _plain(state, (n, hv, d, d), f32, dev, "state"),
+        _plain(o, (T, hv, d), o.dtype, dev, "o"),
+        None if deltas is None else _plain(deltas, (T, hv, d), f32, dev, "deltas"), _attn_stream(stream, dev))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_verify_tree")
+
+
+def gdr_verify_tree_commit(k, g, deltas, state, parents, last, *, qk_l2norm: bool = False, stream=None) -> None:
+    """Move every state to its tree's last accepted node, in place (see
+    gdr_verify_tree_commit in include/gdr.h): ``last`` int32 [n], -1 for none; k, g and deltas
+    as gdr_verify_tree took and wrote them."""
+    if k.dim() != 3 or state.dim() != 4:
+        raise ValueError("k must be [T, H_qk, d] and state [n, H_v, d, d]")
+    (n, hv, d, _), T = state.shape, k.shape[0]
+    dims = gdr_dims(h_qk=k.shape[1], h_v=hv, d_k=d, d_v=d, chunk=64, in_dtype=_dtype_code(k), out_dtype=GDR_F32,
+                    scale=1.0, flags=flags_of(qk_l2norm))
+    dev = state.get_device()
+    types = _attn_types or _attn_init()
+    n_tok = _tree_rows(parents, n, T)
+    i32, f32 = types[1], types[2]
+    st = (_lib or lib()).gdr_verify_tree_commit(
+        dims, n, n_tok, _plain(parents, (n, n_tok), i32, dev, "parents"), _plain(last, (n,), i32, dev, "last"),
+        _plain(k, (T, k.shape[1], d), k.dtype, dev, "k"), _plain(g, (T, hv), f32, dev, "g"),
+        _plain(deltas, (T, hv, d), f32, dev, "deltas"), _plain(state, (n, hv, d, d), f32, dev, "state"),
+        _attn_stream(stream, dev))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_verify_tree_commit")

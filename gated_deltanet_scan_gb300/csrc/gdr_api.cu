@@ -86,6 +86,16 @@ bool tensors_ok(const void *q, const void *k, const void *v, const float *g, con
 
 gdr_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA; }
 
+bool aligned4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Trees of drafted tokens: at most 64 rows each, and a grid of 8 blocks per (sequence, V head).
+gdr_status check_tree(const gdr_dims *d, int32_t n_seqs, int32_t n_tok) {
+    const gdr_status st = check_dims(d);
+    if (st != GDR_OK) return st;
+    if (n_seqs < 0 || n_tok < 1 || n_tok > 64) return GDR_ERR_INVALID_ARG;
+    return (int64_t)n_seqs * d->h_v > INT_MAX / 8 ? GDR_ERR_UNSUPPORTED : GDR_OK;
+}
+
 bool use_tensor_core_prefill(const gdr_dims *d) {
     return d->chunk == 64 && d->d_k == 128 && d->in_dtype == GDR_BF16;
 }
@@ -499,6 +509,54 @@ gdr_status gdr_verify_commit(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok
     a.snapshot_in = snapshot;
     a.state = state;
     return from_cuda(launch_commit(a, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdr_status gdr_verify_tree(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents, const void *q,
+                           const void *k, const void *v, const float *g, const float *beta, const float *state,
+                           void *o, float *deltas, gdr_stream_t stream) {
+    const gdr_status st = check_tree(dims, n_seqs, n_tok);
+    if (st != GDR_OK || n_seqs == 0) return st;
+    if (!aligned4(parents) || !tensors_ok(q, k, v, g, beta, state, o)) return GDR_ERR_INVALID_ARG;
+    if (deltas && !aligned16(deltas)) return GDR_ERR_INVALID_ARG;
+    int32_t *err = device_error_word();
+    if (!err) return GDR_ERR_CUDA;
+    Args a = make_args(dims);
+    a.n_seqs = n_seqs;
+    a.fixed_len = n_tok;
+    a.t_total = (int64_t)n_seqs * n_tok;
+    a.parents = parents;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.beta = beta;
+    a.state = const_cast<float *>(state);  // only read
+    a.o = o;
+    a.deltas = deltas;
+    return from_cuda(launch_tree(a, err, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdr_status gdr_verify_tree_commit(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
+                                  const int32_t *last, const void *k, const float *g, const float *deltas, float *state,
+                                  gdr_stream_t stream) {
+    const gdr_status st = check_tree(dims, n_seqs, n_tok);
+    if (st != GDR_OK || n_seqs == 0) return st;
+    if (!aligned4(parents) || !aligned4(last)) return GDR_ERR_INVALID_ARG;
+    const void *ps[] = {k, g, deltas, state};
+    for (const void *p : ps)
+        if (!p || !aligned16(p)) return GDR_ERR_INVALID_ARG;
+    int32_t *err = device_error_word();
+    if (!err) return GDR_ERR_CUDA;
+    Args a = make_args(dims);
+    a.n_seqs = n_seqs;
+    a.fixed_len = n_tok;
+    a.parents = parents;
+    a.last = last;
+    a.k = k;
+    a.g = g;
+    a.deltas = const_cast<float *>(deltas);  // only read
+    a.state = state;
+    return from_cuda(launch_tree_commit(a, err, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 static gdr_status copy_states(const gdr_dims *dims, int32_t n_seqs, const float *src, float *dst,

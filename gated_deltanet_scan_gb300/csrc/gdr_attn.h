@@ -53,9 +53,16 @@ struct Args {
     Rows q_out, k_out;  // append: p is nullptr where not wanted
     Cache cache;
     const int32_t *kv_lens;
+    int least;               // smallest length but 0 that a sequence may have
+    const int32_t *parents;  // a tree's, [n_seqs][n_tok]; nullptr: the last tokens are a chain
     float *lse;
     const float *inv_freq;
     int rot, interleaved;
+    // compaction: the caches of n_layers layers, layer_stride elements apart
+    const int32_t *last;  // each tree's last accepted node, or -1
+    int32_t *lens_out;    // nullptr where not wanted
+    int n_layers;
+    int64_t layer_stride;
     void *ws;
     int32_t *err;
 };
@@ -73,6 +80,7 @@ cudaError_t launch_prefill(const Args &a, cudaStream_t s);
 // `after`: launched as a programmatic dependent of the two-SM kernel just before it.
 cudaError_t launch_prefill_short(const Args &a, bool after, cudaStream_t s);
 cudaError_t launch_decode(const Args &a, cudaStream_t s);
+cudaError_t launch_compact(const Args &a, cudaStream_t s);
 size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok);
 
 }  // namespace attn

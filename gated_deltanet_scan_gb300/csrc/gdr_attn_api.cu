@@ -70,18 +70,13 @@ Cache to_cache(const gdr_kv_cache *c) {
 
 gdr_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA; }
 
-}  // namespace
-}  // namespace attn
-}  // namespace gdr
+bool nodes_ok(int32_t n_tok) { return n_tok >= 1 && n_tok <= 64; }
 
-using namespace gdr::attn;
-
-extern "C" {
-
-gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, int64_t t_total,
-                           const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *q_out,
-                           const gdr_rows *k_out, const gdr_kv_cache *cache, const int32_t *kv_lens,
-                           const float *inv_freq, int32_t rot_dim, int32_t interleaved, gdr_stream_t stream) {
+// `parents`: of trees of t_total / n_seqs rows each, or nullptr.
+gdr_status append(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, const int32_t *parents,
+                  int64_t t_total, const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *q_out,
+                  const gdr_rows *k_out, const gdr_kv_cache *cache, const int32_t *kv_lens, const float *inv_freq,
+                  int32_t rot_dim, int32_t interleaved, gdr_stream_t stream) {
     gdr_status st = check_dims(dims);
     if (st != GDR_OK) return st;
     if (n_seqs < 0 || t_total < 0 || (n_seqs == 0 && t_total > 0)) return GDR_ERR_INVALID_ARG;
@@ -107,6 +102,7 @@ gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int3
     Args a = make_args(dims);
     a.n_seqs = n_seqs;
     a.cu = cu_seqlens;
+    a.parents = parents;
     a.t_total = t_total;
     a.q = to_rows(q);
     a.k = to_rows(k);
@@ -121,6 +117,64 @@ gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int3
     a.err = gdr::device_error_word();
     if (!a.err) return GDR_ERR_CUDA;
     return from_cuda(launch_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// `parents`: of trees of n_tok rows each, or nullptr.
+gdr_status decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents, const gdr_rows *q,
+                  const gdr_kv_cache *cache, const int32_t *kv_lens, const gdr_rows *o, float *lse, void *workspace,
+                  size_t workspace_bytes, gdr_stream_t stream) {
+    gdr_status st = check_dims(dims);
+    if (st != GDR_OK) return st;
+    if (n_seqs < 0) return GDR_ERR_INVALID_ARG;
+    if (n_seqs == 0) return GDR_OK;
+    st = check_cache(cache);
+    if (st != GDR_OK) return st;
+    if (!rows_ok(q) || !out_rows_ok(o, (int64_t)n_seqs * n_tok, dims->h_q, dims->d) || !aligned(kv_lens, 4) ||
+        (lse && !aligned(lse, 4)))
+        return GDR_ERR_INVALID_ARG;
+    if ((int64_t)n_seqs * n_tok > INT_MAX / dims->h_q) return GDR_ERR_UNSUPPORTED;
+    const size_t need = decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);
+    if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return GDR_ERR_INVALID_ARG;
+    Args a = make_args(dims);
+    a.n_seqs = n_seqs;
+    a.n_tok = n_tok;
+    a.t_total = (int64_t)n_seqs * n_tok;
+    a.q = to_rows(q);
+    a.o = to_rows(o);
+    a.cache = to_cache(cache);
+    a.kv_lens = kv_lens;
+    a.parents = parents;
+    a.least = parents ? n_tok : 0;
+    a.lse = lse;
+    a.ws = workspace;
+    a.err = gdr::device_error_word();
+    if (!a.err) return GDR_ERR_CUDA;
+    return from_cuda(launch_decode(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace gdr
+
+using namespace gdr::attn;
+
+extern "C" {
+
+gdr_status gdr_attn_append(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, int64_t t_total,
+                           const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *q_out,
+                           const gdr_rows *k_out, const gdr_kv_cache *cache, const int32_t *kv_lens,
+                           const float *inv_freq, int32_t rot_dim, int32_t interleaved, gdr_stream_t stream) {
+    return append(dims, n_seqs, cu_seqlens, nullptr, t_total, q, k, v, q_out, k_out, cache, kv_lens, inv_freq, rot_dim,
+                  interleaved, stream);
+}
+
+gdr_status gdr_attn_append_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
+                                const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *q_out,
+                                const gdr_rows *k_out, const gdr_kv_cache *cache, const int32_t *kv_lens,
+                                const float *inv_freq, int32_t rot_dim, int32_t interleaved, gdr_stream_t stream) {
+    if (n_seqs < 0 || !nodes_ok(n_tok) || (n_seqs > 0 && !aligned(parents, 4))) return GDR_ERR_INVALID_ARG;
+    return append(dims, n_seqs, nullptr, parents, (int64_t)n_seqs * n_tok, q, k, v, q_out, k_out, cache, kv_lens,
+                  inv_freq, rot_dim, interleaved, stream);
 }
 
 gdr_status gdr_attn_prefill(const gdr_attn_dims *dims, int32_t n_seqs, const int32_t *cu_seqlens, int64_t t_total,
@@ -157,31 +211,59 @@ size_t gdr_attn_decode_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs
 gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const gdr_rows *q,
                            const gdr_kv_cache *cache, const int32_t *kv_lens, const gdr_rows *o, float *lse,
                            void *workspace, size_t workspace_bytes, gdr_stream_t stream) {
+    const gdr_status st = check_dims(dims);
+    if (st != GDR_OK) return st;
+    if (n_tok < 1 || n_tok > 16) return GDR_ERR_INVALID_ARG;
+    return decode(dims, n_seqs, n_tok, nullptr, q, cache, kv_lens, o, lse, workspace, workspace_bytes, stream);
+}
+
+size_t gdr_attn_decode_tree_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok) {
+    if (check_dims(dims) != GDR_OK || n_seqs <= 0 || !nodes_ok(n_tok)) return 0;
+    return decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);
+}
+
+gdr_status gdr_attn_decode_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
+                                const gdr_rows *q, const gdr_kv_cache *cache, const int32_t *kv_lens, const gdr_rows *o,
+                                float *lse, void *workspace, size_t workspace_bytes, gdr_stream_t stream) {
+    const gdr_status st = check_dims(dims);
+    if (st != GDR_OK) return st;
+    if (!nodes_ok(n_tok) || (n_seqs > 0 && !aligned(parents, 4))) return GDR_ERR_INVALID_ARG;
+    return decode(dims, n_seqs, n_tok, parents, q, cache, kv_lens, o, lse, workspace, workspace_bytes, stream);
+}
+
+gdr_status gdr_attn_commit_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
+                                const int32_t *last, int32_t n_layers, int64_t layer_stride, const gdr_kv_cache *cache,
+                                const int32_t *kv_lens, int32_t *lens_out, gdr_stream_t stream) {
     gdr_status st = check_dims(dims);
     if (st != GDR_OK) return st;
-    if (n_seqs < 0 || n_tok < 1 || n_tok > 16) return GDR_ERR_INVALID_ARG;
+    if (n_seqs < 0 || !nodes_ok(n_tok) || n_layers < 1) return GDR_ERR_INVALID_ARG;
     if (n_seqs == 0) return GDR_OK;
+    if (!aligned(parents, 4) || !aligned(last, 4) || !aligned(kv_lens, 4) || (lens_out && !aligned(lens_out, 4)))
+        return GDR_ERR_INVALID_ARG;
+    // other blocks read a sequence's length while one writes its new one
+    if (lens_out && lens_out < kv_lens + n_seqs && kv_lens < lens_out + n_seqs) return GDR_ERR_INVALID_ARG;
     st = check_cache(cache);
     if (st != GDR_OK) return st;
-    if (!rows_ok(q) || !out_rows_ok(o, (int64_t)n_seqs * n_tok, dims->h_q, dims->d) || !aligned(kv_lens, 4) ||
-        (lse && !aligned(lse, 4)))
+    if (!stride_ok(layer_stride) || !out_cache_ok(cache, dims->h_kv, dims->d)) return GDR_ERR_INVALID_ARG;
+    if (overlap(n_layers, layer_stride, cache->n_pages, cache->page_stride, dims->d) ||
+        overlap(n_layers, layer_stride, cache->page_size, cache->token_stride, dims->d) ||
+        overlap(n_layers, layer_stride, dims->h_kv, cache->head_stride, dims->d))
         return GDR_ERR_INVALID_ARG;
-    if ((int64_t)n_seqs * n_tok > INT_MAX / dims->h_q) return GDR_ERR_UNSUPPORTED;
-    const size_t need = decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);
-    if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return GDR_ERR_INVALID_ARG;
+    // a block per 128 16-byte vectors of a row in all layers, in a grid dimension of 65535
+    if ((int64_t)n_layers * dims->h_kv * (dims->d / 4) > 65535 * (int64_t)128) return GDR_ERR_UNSUPPORTED;
     Args a = make_args(dims);
     a.n_seqs = n_seqs;
     a.n_tok = n_tok;
-    a.t_total = (int64_t)n_seqs * n_tok;
-    a.q = to_rows(q);
-    a.o = to_rows(o);
+    a.parents = parents;
+    a.last = last;
+    a.n_layers = n_layers;
+    a.layer_stride = layer_stride;
     a.cache = to_cache(cache);
     a.kv_lens = kv_lens;
-    a.lse = lse;
-    a.ws = workspace;
+    a.lens_out = lens_out;
     a.err = gdr::device_error_word();
     if (!a.err) return GDR_ERR_CUDA;
-    return from_cuda(launch_decode(a, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_compact(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

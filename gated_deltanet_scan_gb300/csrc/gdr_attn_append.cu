@@ -20,8 +20,13 @@
 // the row (halves a multiple of 8 apart: shuffles) or read again by value (other
 // halves).  A row is read whole by its warp before any of it is written, so outputs
 // may be the inputs.
+//
+// Of a tree of drafted tokens a node's position is that of its path's end, and its slot the
+// row's: the warp finds the tree's masks (gdr_tree.cuh) once per sequence, while its first
+// vectors are on their way, and |A_j| - 1 is the node's depth.
 #include "gdr_attn_common.cuh"
 #include "gdr_internal.h"
+#include "gdr_tree.cuh"
 
 namespace gdr {
 namespace attn {
@@ -54,7 +59,7 @@ __device__ __forceinline__ uint64_t turn_of(float f) {
     return u >> 31 ? 0 - t : t;
 }
 
-template <int D, bool F16, int PAIR>
+template <int D, bool F16, int PAIR, bool TREE>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
     append_kernel(const __grid_constant__ Args a, const Split sp) {
     constexpr bool kPaired = PAIR == kInterleaved || PAIR == kRagged;
@@ -104,10 +109,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
     const int even = (int)(a.t_total / a.n_seqs);  // tokens per sequence without cu
     int s = a.cu ? find_seq_warp(a.cu, a.n_seqs, first, lane) : (int)(first / even);
 
+    tree::Masks nodes;
+    int nodes_of = -1;  // the sequence whose tree they are
+
     for (int64_t t = first; t < last; ++t) {
         int64_t t0, t1;
         bool known = true;
-        if (a.cu) {
+        if (!TREE && a.cu) {
             while (s + 1 < a.n_seqs && a.cu[s + 1] <= t) ++s;
             t0 = a.cu[s];
             t1 = a.cu[s + 1];
@@ -117,7 +125,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
             t0 = (int64_t)s * even;
             t1 = t0 + even;
         }
-        const int64_t pos = known ? (int64_t)a.kv_lens[s] - (t1 - t) : -1;
+        int64_t pos = known ? (int64_t)a.kv_lens[s] - (t1 - t) : -1;
+        int64_t turned_by = pos;  // the position the angles go by
+        if constexpr (TREE) {
+            if (s != nodes_of) {
+                nodes_of = s;
+                nodes = tree::masks(a.parents + t0, even, lane);
+                if (nodes.bad) record_invalid(a.err);
+            }
+            const int j = (int)(t - t0), depth = __popcll(tree::mask_of(nodes, j)) - 1;
+            known = depth >= 0;  // the row is a node
+            turned_by = pos - j + depth;
+            if (pos < j) pos = -1;  // fewer tokens than the tree has rows
+        }
         int64_t slot = -1;  // offset of the token's slot in the cache, in elements
         if (pos >= 0 && pos < (int64_t)a.cache.max_pages * a.cache.page_size) {
             const int pg = (int)pos / a.cache.page_size;
@@ -126,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
                 slot = page * a.cache.page_stride +
                        (int64_t)((int)pos - pg * a.cache.page_size) * a.cache.token_stride;
         }
-        if (slot < 0) record_invalid(a.err);
+        if (slot < 0 && (!TREE || known)) record_invalid(a.err);
 
         float cs[8], sn[8];
         if constexpr (PAIR != kNone) {
@@ -137,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
                     sn[e] = -sn[e - 1];
                 } else {
                     const int32_t w =
-                        (int32_t)(((uint64_t)pos * turn[kPaired ? e / 2 : e]) >> 32);
+                        (int32_t)(((uint64_t)turned_by * turn[kPaired ? e / 2 : e]) >> 32);
                     sincospif((float)w * 4.656612873077393e-10f, &sn[e], &cs[e]);  // 2^-31 half turns
                     if (kPaired || e0 + e < half) sn[e] = -sn[e];
                 }
@@ -220,15 +240,22 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
     }
 }
 
+template <int D, bool F16, bool TREE>
+void launch_as(const Args &a, int pairing, const Split &sp, unsigned blocks, cudaStream_t s) {
+    switch (pairing) {
+        case kNone: append_kernel<D, F16, kNone, TREE><<<blocks, kThreads, 0, s>>>(a, sp); break;
+        case kInterleaved: append_kernel<D, F16, kInterleaved, TREE><<<blocks, kThreads, 0, s>>>(a, sp); break;
+        case kRagged: append_kernel<D, F16, kRagged, TREE><<<blocks, kThreads, 0, s>>>(a, sp); break;
+        case kShuffle: append_kernel<D, F16, kShuffle, TREE><<<blocks, kThreads, 0, s>>>(a, sp); break;
+        default: append_kernel<D, F16, kByValue, TREE><<<blocks, kThreads, 0, s>>>(a, sp); break;
+    }
+}
 template <int D, bool F16>
 void launch(const Args &a, int pairing, const Split &sp, unsigned blocks, cudaStream_t s) {
-    switch (pairing) {
-        case kNone: append_kernel<D, F16, kNone><<<blocks, kThreads, 0, s>>>(a, sp); break;
-        case kInterleaved: append_kernel<D, F16, kInterleaved><<<blocks, kThreads, 0, s>>>(a, sp); break;
-        case kRagged: append_kernel<D, F16, kRagged><<<blocks, kThreads, 0, s>>>(a, sp); break;
-        case kShuffle: append_kernel<D, F16, kShuffle><<<blocks, kThreads, 0, s>>>(a, sp); break;
-        default: append_kernel<D, F16, kByValue><<<blocks, kThreads, 0, s>>>(a, sp); break;
-    }
+    if (a.parents)
+        launch_as<D, F16, true>(a, pairing, sp, blocks, s);
+    else
+        launch_as<D, F16, false>(a, pairing, sp, blocks, s);
 }
 
 }  // namespace

@@ -32,6 +32,7 @@
 #include "gdr_attn_line.cuh"
 #include "gdr_attn_mma.cuh"
 #include "gdr_internal.h"
+#include "gdr_tree.cuh"
 #include "tc_ptx.cuh"
 
 namespace gdr {
@@ -51,7 +52,7 @@ struct Shape {
     static_assert(SLOTS * SLOT >= 16 * D * 4, "a ring holds its worker's part");
 };
 
-template <int D, bool F16>
+template <int D, bool F16, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Args a) {
     using Sh = Shape<D>;
     constexpr Spec sp = spec(false, D);
@@ -104,6 +105,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             }
         };
         look_up(tile0);
+        // A tree's masks: at most 16 rows, so at most 16 nodes
+        tree::Masks nodes;
+        if constexpr (TREE) nodes = tree::masks(a.parents + (int64_t)s * a.n_tok, a.n_tok, lane);
         auto issue = [&](int step) {
             if (step < steps) {
                 if (!(step & 1)) {
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         // Q: rows lane / 4 and + 8 of this warp's 16, as MMA fragments
         uint32_t qf[KS][4];
         int64_t out_row[2];  // output row, or -1
-        int seen[2];         // tokens the row sees
+        int seen[2];         // tokens the row sees; of a tree's node, its mask
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = tr.rb * 16 + r0 + 8 * i;
@@ -147,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 const int64_t t = (int64_t)s * a.n_tok + j;
                 out_row[i] = t * a.h_q + h * a.group + g;
                 seen[i] = max(0, len - a.n_tok + j + 1);
+                if constexpr (TREE) seen[i] = j;
                 src = a.q.p + t * a.q.ts + (int64_t)(h * a.group + g) * a.q.hs;
             }
 #pragma unroll
@@ -155,7 +160,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 qf[k][2 + i] = src ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 8 + cq * 2) : 0u;
             }
         }
-        const int all_see = len - a.n_tok + 1;  // tokens every row sees
+        if constexpr (TREE) {
+            if (nodes.bad) record_invalid(a.err);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int mask = (int)tree::mask_of(nodes, seen[i]);
+                seen[i] = out_row[i] >= 0 ? mask : 0;
+            }
+        }
+        const int base = len - a.n_tok;              // a tree's first slot
+        const int all_see = TREE ? base : base + 1;  // tokens every row sees
+        // whether row i sees token p of a tile that not all rows see whole (p < len + 16)
+        auto sees = [&](int i, int64_t p) {
+            if constexpr (TREE)
+                return p < base || (seen[i] >> (int)(p - base) & 1);
+            else
+                return p < seen[i];
+        };
 
         float acc[NT][4];
 #pragma unroll
@@ -203,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 2 * TT; ++e) {
                     v[e] = sc * (x[0][e >> 1][2 * i + (e & 1)] + x[1][e >> 1][2 * i + (e & 1)]);
-                    if (masked && p0 + (e >> 1) * 8 + cq * 2 + (e & 1) >= seen[i]) v[e] = -CUDART_INF_F;
+                    if (masked && !sees(i, p0 + (e >> 1) * 8 + cq * 2 + (e & 1))) v[e] = -CUDART_INF_F;
                 }
                 float top = v[0];
 #pragma unroll
@@ -241,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             __syncwarp();
             issue(step + Sh::SLOTS);
             const uint32_t vb = slots + ((step + 1) % Sh::SLOTS) * Sh::SLOT;
-            if (masked && a.n_tok > 1) {
+            if (masked && (TREE || a.n_tok > 1)) {
                 // Rows that do not see a draft token have p = 0 for it, and 0 times an
                 // infinity or NaN would reach them: such values are added to the rows
                 // that see them (p > 0 leaves them as they are) and replaced by zeros.
@@ -270,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                             const float2 v = unpack2<F16>(w);
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                if (p >= seen[i]) continue;
+                                if (!sees(i, p)) continue;
                                 if (nonfinite<F16>(w)) acc[n][2 * i] += v.x;
                                 if (nonfinite<F16>(w >> 16)) acc[n][2 * i + 1] += v.y;
                             }
@@ -315,18 +336,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
         }
+        if constexpr (TREE) {
+            // rows that are no nodes took the tokens before the tree with the others: undone here
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (seen[i] != 0) continue;
+                m[i] = -CUDART_INF_F;
+                l[i] = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[n][2 * i] = acc[n][2 * i + 1] = 0.f;
+            }
+        }
         if (tile0 == 0 && tile1 == tiles) {  // the worker saw the whole triple
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (out_row[i] < 0) continue;
-                const float inv = seen[i] > 0 ? inverse_sum(l[i]) : 0.f;
+                const float inv = seen[i] != 0 ? inverse_sum(l[i]) : 0.f;
                 const int64_t t = quotient(out_row[i], a.h_q);
                 uint16_t *dst = a.o.p + t * a.o.ts + (out_row[i] - t * a.h_q) * a.o.hs;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     *reinterpret_cast<uint32_t *>(dst + n * 8 + cq * 2) =
                         pack2<F16>(acc[n][2 * i] * inv, acc[n][2 * i + 1] * inv);
-                if (a.lse && cq == 0) a.lse[out_row[i]] = seen[i] > 0 ? kLn2 * (m[i] + log2f(l[i])) : -CUDART_INF_F;
+                if (a.lse && cq == 0) a.lse[out_row[i]] = seen[i] != 0 ? kLn2 * (m[i] + log2f(l[i])) : -CUDART_INF_F;
             }
         } else {
             // the part goes to the workspace, or, where the triple goes on in the next worker, to
@@ -384,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
 // Joins the parts of every row that more than one worker saw, in the order of the
 // tokens, and writes the rows that see nothing.  With WPR > 1 a block is WPR warps on 64
 // columns of one row, which share the row's parts; else a warp is one row.
-template <int D, bool F16, int WPR>
+template <int D, bool F16, int WPR, bool TREE>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, const bool wide) {
     constexpr int V = WPR > 1 ? 2 : D / 32;  // columns per lane
     constexpr int RPB = 8 / WPR;             // rows per block
@@ -490,26 +522,26 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
             acc[0].y += c * s_acc[i][lane].y;
         }
     }
-    const bool sees = len - a.n_tok + j + 1 > 0;
+    const bool sees = TREE || len - a.n_tok + j + 1 > 0;  // a tree's rows that are no nodes have l = 0
     const float inv = sees ? inverse_sum(l) : 0.f;
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) dst[word0 + 32 * e] = pack2<F16>(acc[e].x * inv, acc[e].y * inv);
     if (write_lse) a.lse[row] = sees ? kLn2 * (m + log2f(l)) : -CUDART_INF_F;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool TREE>
 cudaError_t launch_warps(const Args &a, cudaStream_t s) {
     static SmemOptIn opt_in;
-    const cudaError_t e = opt_in.set(reinterpret_cast<const void *>(decode_kernel<D, F16>), (int)Shape<D>::SMEM);
+    const cudaError_t e = opt_in.set(reinterpret_cast<const void *>(decode_kernel<D, F16, TREE>), (int)Shape<D>::SMEM);
     if (e != cudaSuccess) return e;
-    decode_kernel<D, F16><<<kBlocks, kThreads, Shape<D>::SMEM, s>>>(a);
+    decode_kernel<D, F16, TREE><<<kBlocks, kThreads, Shape<D>::SMEM, s>>>(a);
     return cudaGetLastError();
 }
 
-template <int D, bool F16>
-cudaError_t launch(const Args &a, cudaStream_t s) {
+template <int D, bool F16, bool TREE>
+cudaError_t launch_as(const Args &a, cudaStream_t s) {
     const bool wide = is_wide(a.n_tok * a.group);
-    const cudaError_t e = wide ? launch_decode_wide(a, s) : launch_warps<D, F16>(a, s);
+    const cudaError_t e = wide ? launch_decode_wide(a, s) : launch_warps<D, F16, TREE>(a, s);
     if (e != cudaSuccess) return e;
     // The join: 8 warps on every 64 columns of a row where a row has many parts (few
     // triples for the blocks), else a warp per row.
@@ -525,8 +557,13 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 8>, a, wide)
-                : cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 1>, a, wide);
+    return many ? cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 8, TREE>, a, wide)
+                : cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 1, TREE>, a, wide);
+}
+
+template <int D, bool F16>
+cudaError_t launch(const Args &a, cudaStream_t s) {
+    return a.parents ? launch_as<D, F16, true>(a, s) : launch_as<D, F16, false>(a, s);
 }
 
 }  // namespace

@@ -50,10 +50,10 @@ __host__ __device__ inline Layout layout(int rows, const Spec &sp, int d, int n_
     return L;
 }
 
-// Tokens of sequence s; outside [0, limit] counts as none.
+// Tokens of sequence s; outside [0, limit], or fewer than a tree's nodes, counts as none.
 __device__ __forceinline__ int64_t length_of(const Args &a, int s) {
     const int64_t n = a.kv_lens[s];
-    return n < 0 || n > (int64_t)a.cache.max_pages * a.cache.page_size ? 0 : n;
+    return n < a.least || n > (int64_t)a.cache.max_pages * a.cache.page_size ? 0 : n;
 }
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {  // a, b >= 0; mostly 32-bit values
     return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);

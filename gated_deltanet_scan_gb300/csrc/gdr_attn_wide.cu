@@ -29,6 +29,7 @@
 #include "gdr_attn_mma.cuh"
 #include "gdr_attn_ptx.cuh"
 #include "gdr_internal.h"
+#include "gdr_tree.cuh"
 #include "tc_ptx.cuh"
 
 namespace gdr {
@@ -74,7 +75,7 @@ enum Bar {
 };
 static_assert(kBars <= 32, "barrier words");
 
-template <int D, bool F16>
+template <int D, bool F16, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant__ Args a) {
     using Sh = Shape<D>;
     constexpr Spec sp = spec(true, D);
@@ -142,12 +143,26 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         float2 *const ml_parts = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + L.ml);
         float *const o_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + L.o);
         uint32_t g = 0;  // tiles
+        tree::Masks nodes;
+        int nodes_of = -1;  // the sequence whose tree they are
         for (int it = 0; ok && walk.next(a, sp, L.blocks_of_rows, t); ++it) {
             const int r = t.rb * kRows + row;
             const bool live = r < rows;
             const int j = r / a.group, hq = t.h * a.group + r - j * a.group;
-            const int seen = live ? max(0, t.len - a.n_tok + j + 1) : 0;
-            const int all_see = t.len - a.n_tok + 1;
+            const int tree0 = t.len - a.n_tok;  // a tree's first slot
+            const int seen = live ? max(0, tree0 + j + 1) : 0;
+            const int all_see = TREE ? tree0 : tree0 + 1;
+            uint64_t mask = 0;
+            if constexpr (TREE) {
+                if (t.s != nodes_of) {
+                    nodes_of = t.s;
+                    nodes = tree::masks(a.parents + (int64_t)t.s * a.n_tok, a.n_tok, lane);
+                    if (nodes.bad) record_invalid(a.err);
+                }
+                mask = tree::mask_of(nodes, j & 63);
+                if (!live) mask = 0;
+            }
+            const bool any = TREE ? mask != 0 : seen > 0;  // the row sees something
             const bool work = t.rb * kRows + warp * 32 < rows;  // some row of the warp is live
             float m = -CUDART_INF_F, l = 0.f;
             for (int tile = t.tile0; tile < t.tile1; ++tile, ++g) {
@@ -164,8 +179,13 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     if (p0 + kTile > all_see) {
 #pragma unroll
                         for (int c0 = 0; c0 < 64; c0 += 32) {
-                            const int n = seen - p0 - c0;  // columns seen
-                            const uint32_t sees = n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+                            uint32_t sees;
+                            if constexpr (TREE) {
+                                sees = tree::sees32(mask, p0 + c0 - tree0);
+                            } else {
+                                const int n = seen - p0 - c0;  // columns seen
+                                sees = n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+                            }
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
                                 if (!(sees & (1u << c))) x[c0 + c] = 0xFF800000u;
@@ -218,6 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             }
             if (!ok || !wait(kODone, it)) break;
             tc_fence_after_sync();
+            if constexpr (TREE) {
+                // a row that is no node took the tokens before the tree with the others: undone here
+                if (!any) {
+                    m = -CUDART_INF_F;
+                    l = 0.f;
+                }
+            }
             // O, whole or as a part
             const bool whole = t.tile0 == 0 && t.tile1 == t.tiles;
             const bool patch = *s_found != 0;
@@ -240,13 +267,17 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                         for (int e = 0; e < 32; e += 8) {
                             uint4 w;
                             // a row that sees nothing is zero, whatever its O holds
-                            w.x = seen > 0 ? pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv) : 0u;
-                            w.y = seen > 0 ? pack2<F16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv) : 0u;
-                            w.z = seen > 0 ? pack2<F16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv) : 0u;
-                            w.w = seen > 0 ? pack2<F16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv) : 0u;
+                            w.x = any ? pack2<F16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv) : 0u;
+                            w.y = any ? pack2<F16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv) : 0u;
+                            w.z = any ? pack2<F16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv) : 0u;
+                            w.w = any ? pack2<F16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv) : 0u;
                             *reinterpret_cast<uint4 *>(dst + e) = w;
                         }
                     } else if (!whole) {
+                        if constexpr (TREE) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = any ? o[e] : 0u;
+                        }
                         // four lanes store 64 bytes of a row together: pieces of 16 bytes are
                         // transposed among them, in two halves of 16 columns
 #pragma unroll
@@ -282,10 +313,11 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     // tiles that were cleaned, from the one in which the rows begin to differ: what they
                     // add to the stored row or part (a rare path, kept small)
                     const int from = max(t.tile0, max(0, all_see) / kTile) * kTile;
-                    const int to = min(seen, t.tile1 * kTile);
+                    const int to = TREE ? (any ? min(t.len, t.tile1 * kTile) : 0) : min(seen, t.tile1 * kTile);
                     uint16_t *const dst = a.o.p + tok * a.o.ts + (int64_t)hq * a.o.hs;
 #pragma unroll 1
                     for (int p = from; p < to; ++p) {
+                        if (TREE && !(tree::sees32(mask, p - tree0) & 1u)) continue;
                         const uint32_t pg = (uint32_t)p / (uint32_t)a.cache.page_size;
                         const int page = a.cache.table[(int64_t)t.s * a.cache.table_stride + pg];
                         if (page < 0 || page >= a.cache.n_pages) continue;
@@ -398,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                 for (int c = 0; c < D / 64; ++c)
                     cp_async16(at + c * Sh::BOX, src + c * 64, off < 0 ? 0u : 16u);
             }
-            if (values && a.n_tok > 1 && x.tile * kTile > x.t.len - a.n_tok + 1) {
+            if (values && (TREE || a.n_tok > 1) && x.tile * kTile > x.t.len - a.n_tok + (TREE ? 0 : 1)) {
                 cp_async_commit();
                 cp_async_wait<0>();
                 clean(st);
@@ -518,13 +550,18 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
+template <int D, bool F16, bool TREE>
+cudaError_t launch_as(const Args &a, cudaStream_t s) {
+    static SmemOptIn opt_in;
+    const cudaError_t e = opt_in.set(reinterpret_cast<const void *>(wide_kernel<D, F16, TREE>), (int)Shape<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    wide_kernel<D, F16, TREE><<<kBlocks, kThreads, Shape<D>::SMEM, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <int D, bool F16>
 cudaError_t launch(const Args &a, cudaStream_t s) {
-    static SmemOptIn opt_in;
-    const cudaError_t e = opt_in.set(reinterpret_cast<const void *>(wide_kernel<D, F16>), (int)Shape<D>::SMEM);
-    if (e != cudaSuccess) return e;
-    wide_kernel<D, F16><<<kBlocks, kThreads, Shape<D>::SMEM, s>>>(a);
-    return cudaGetLastError();
+    return a.parents ? launch_as<D, F16, true>(a, s) : launch_as<D, F16, false>(a, s);
 }
 
 }  // namespace

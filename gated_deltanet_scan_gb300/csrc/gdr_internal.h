@@ -33,6 +33,8 @@ struct Args {
     float *deltas;              // optional per-token corrections u_t (verify block), fp32 like v
     const int32_t *accepted;    // verify commit: accepted tokens per sequence (device)
     const float *snapshot_in;   // verify commit: the state before the block
+    const int32_t *parents;     // trees of drafted tokens: [n_seqs][fixed_len]
+    const int32_t *last;        // their commit: each tree's last accepted node, or -1 (device)
     // tensor-core prefill: only chunks [c_lo, c_hi) of each sequence (0, INT32_MAX: all of them)
     int c_lo, c_hi;
 };
@@ -89,6 +91,11 @@ int segment_cut(int64_t n_chunks, int P, int p);
 cudaError_t launch_segmented(const Args &a, int P, uint8_t *ws, const SegLayout &L, int32_t *err, cudaStream_t s);
 // Verify commit: state = e^{G_a} snapshot + sum_{j<a} e^{G_a - G_j} k_j u_j^T per (sequence, V head).
 cudaError_t launch_commit(const Args &a, int32_t *err, cudaStream_t s);
+
+// The rule over trees of 1 <= fixed_len <= 64 drafted tokens (gdr_tree_rule.cu), and the
+// accepted path's state in place of the one before.
+cudaError_t launch_tree(const Args &a, int32_t *err, cudaStream_t s);
+cudaError_t launch_tree_commit(const Args &a, int32_t *err, cudaStream_t s);
 
 // bf16 tensor [d2][d1][d0] (d0 contiguous) as a TMA map with box {box0, 1, 64}.
 bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,

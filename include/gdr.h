@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define GDR_ABI_VERSION 10
+#define GDR_ABI_VERSION 11
 
 /* Same object as cudaStream_t; declared here so callers need no CUDA header. */
 typedef struct CUstream_st *gdr_stream_t;
@@ -414,6 +414,61 @@ gdr_status gdr_verify_commit(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok
                              const void *k, const float *g, const float *deltas, const float *snapshot,
                              float *state, gdr_stream_t stream);
 
+/*
+ * Trees of drafted tokens.  A drafter that keeps several continuations gives every sequence
+ * a tree of up to 64 tokens instead of a chain of up to 16; five entry points verify it:
+ * gdr_verify_tree and gdr_verify_tree_commit in the rule's layers, gdr_attn_append_tree,
+ * gdr_attn_decode_tree and gdr_attn_commit_tree in the attention layers.  All take
+ *
+ *   n_tok    rows of every tree, 1 .. 64 (GDR_ERR_INVALID_ARG otherwise); row s * n_tok + j
+ *            of the tensors is row j of sequence s
+ *   parents  DEVICE int32 [n_seqs][n_tok]: parents[j] is -1 (a child of the sequence's last
+ *            committed token; there may be several), 0 <= parents[j] < j (an earlier row, which
+ *            is a node), or -2: the row is no node (trees of one batch are padded to the same
+ *            n_tok).  A row with any other parent is treated as no node, and
+ *            GDR_ERR_INVALID_ARG is recorded in the device error word.
+ *
+ * Below, A_j is node j with its ancestors: its path.  What the rows outside a node's path
+ * hold (NaN and infinities included) does not reach it; the gates, keys and values of rows
+ * that are no nodes are not used at all.  A chain, parents[j] = j - 1, is what
+ * gdr_verify_block and gdr_attn_decode do for up to 16 tokens.
+ */
+
+/*
+ * The rule along every path of a tree, from the sequence's state S_0:
+ *     S_j = e^{g_j} (I - beta_j k_j k_j^T) S_parent(j) + beta_j k_j v_j^T,   o_j = scale S_j^T q_j.
+ * With G_j the sum of g over A_j this is, node by node,
+ *     u_j = beta_j (v_j - e^{G_j} S_0^T k_j) - sum_{i in A_j, i < j} beta_j e^{G_j - G_i} (k_j . k_i) u_i
+ *     o_j = scale (e^{G_j} S_0^T q_j + sum_{i in A_j} e^{G_j - G_i} (q_j . k_i) u_i)
+ * (the closed form of S_T after a chunk on the Qwen3.5-9B NPU model card, "How it works",
+ * taken along the paths of a tree).  The state is read and left as it is, so no snapshot is
+ * needed: gdr_verify_tree_commit moves it to the accepted node.
+ *
+ *   q, k [n_seqs * n_tok][H_qk][d_k]; v, o [n_seqs * n_tok][H_v][d_v]; g, beta [n_seqs * n_tok][H_v]
+ *   state  [n_seqs][H_v][d_k][d_v]
+ *   deltas NULL, or fp32 [n_seqs * n_tok][H_v][d_v] that receives the corrections u_j
+ * Rows of o and deltas that are no nodes are set to zero.  dims->chunk has no effect;
+ * dims->flags as everywhere.  Products are exact in the inputs' values and summed in fp32,
+ * whatever the kernel (the state's values enter tensor-core products in three bf16 parts,
+ * which hold all their 24 bits); the sums of g are fp64.  n_seqs * H_v is below 2^28
+ * (GDR_ERR_UNSUPPORTED otherwise); n_seqs = 0 is a no-op, whatever the pointers are.
+ */
+gdr_status gdr_verify_tree(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents, const void *q,
+                           const void *k, const void *v, const float *g, const float *beta, const float *state,
+                           void *o, float *deltas, gdr_stream_t stream);
+
+/*
+ * Moves every state to its tree's accepted node a = last[s], in place:
+ *     state[s] = e^{G_a} state[s] + sum_{i in A_a} e^{G_a - G_i} k_i u_i^T.
+ *   last   DEVICE int32 [n_seqs]: the last accepted node of each tree, or -1 for none (the state
+ *          stays as it is).  A value that is neither a node's row nor -1 counts as -1 and records
+ *          GDR_ERR_INVALID_ARG in the device error word.
+ *   k, g, deltas: the tensors of gdr_verify_tree (with the flag GDR_FLAG_QK_L2NORM as there); state in/out.
+ */
+gdr_status gdr_verify_tree_commit(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
+                                  const int32_t *last, const void *k, const float *g, const float *deltas, float *state,
+                                  gdr_stream_t stream);
+
 /* Copy n_seqs states (H_v * d_k * d_v floats each) from `state` to `snapshot`. */
 gdr_status gdr_state_snapshot(const gdr_dims *dims, int32_t n_seqs, const float *state,
                               float *snapshot, gdr_stream_t stream);
@@ -564,6 +619,56 @@ gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_
 
 /* Bytes of workspace gdr_attn_decode needs (0 for invalid dims).  Depends on the shapes only. */
 size_t gdr_attn_decode_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok);
+
+/*
+ * gdr_attn_append for trees of drafted tokens (n_tok, parents and A_j: see "Trees of drafted
+ * tokens" above).  kv_lens[s] includes the tree's n_tok rows, so row j's slot is
+ * kv_lens[s] - n_tok + j; its position, which the angles go by, is the path's:
+ * kv_lens[s] - n_tok + |A_j| - 1.  Rows that are no nodes are written nowhere: not to the
+ * cache, q_out or k_out.  kv_lens[s] < n_tok (with a node in the tree) or beyond
+ * max_pages * page_size leaves what has no slot out of the cache and records
+ * GDR_ERR_INVALID_ARG in the device error word.  Everything else as in gdr_attn_append.
+ */
+gdr_status gdr_attn_append_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
+                                const gdr_rows *q, const gdr_rows *k, const gdr_rows *v, const gdr_rows *q_out,
+                                const gdr_rows *k_out, const gdr_kv_cache *cache, const int32_t *kv_lens,
+                                const float *inv_freq, int32_t rot_dim, int32_t interleaved, gdr_stream_t stream);
+
+/*
+ * gdr_attn_decode for trees of drafted tokens: with base = kv_lens[s] - n_tok, row j sees the
+ * positions before base and the slots base + i of the nodes i in A_j, its own among them.
+ * A row that is no node, or whose scores are all minus infinity, has o = 0 and lse = -infinity, and so have the rows of
+ * a sequence with kv_lens[s] = 0 (which is not in the batch: its parents are not read).  kv_lens[s] in 1 .. n_tok - 1, or
+ * outside [0, max_pages * page_size], counts as 0 and records GDR_ERR_INVALID_ARG in the
+ * device error word.  n_tok is up to 64; everything else as in gdr_attn_decode.
+ */
+gdr_status gdr_attn_decode_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
+                                const gdr_rows *q, const gdr_kv_cache *cache, const int32_t *kv_lens, const gdr_rows *o,
+                                float *lse, void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/* Bytes of workspace gdr_attn_decode_tree needs (0 for invalid dims).  Depends on the shapes only. */
+size_t gdr_attn_decode_tree_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok);
+
+/*
+ * Moves every tree's accepted path to the front of the tree's slots, in the caches of
+ * n_layers layers at once: the keys and values of the path's nodes, in rising order, go to
+ * the slots base, base + 1, ... (base = kv_lens[s] - n_tok), where their positions have been
+ * all along.  What the other slots of the tree hold afterwards is of no use.
+ *   last          DEVICE int32 [n_seqs]: the last accepted node, or -1 for none; any other value
+ *                 counts as -1 and records GDR_ERR_INVALID_ARG in the device error word
+ *   n_layers      at least 1; value x of layer l lies layer_stride * l elements on, in k and v alike
+ *                 (layer_stride: a multiple of 8, not negative, below 2^38)
+ *   cache         layer 0's; one page table for all layers
+ *   lens_out      NULL, or DEVICE int32 [n_seqs]: the new lengths, base + |A_last| (kv_lens[s]
+ *                 itself where that is 0 or out of range); must not overlap kv_lens
+ * dims->h_q, dtype and scale have no effect on the result.  A sequence with kv_lens[s] = 0 is
+ * not in the batch; one in 1 .. n_tok - 1 or beyond max_pages * page_size is left as it is and
+ * recorded.  Rows whose page id is out of range are left out and recorded.  Slots of a tree
+ * must not be shared between sequences.
+ */
+gdr_status gdr_attn_commit_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
+                                const int32_t *last, int32_t n_layers, int64_t layer_stride, const gdr_kv_cache *cache,
+                                const int32_t *kv_lens, int32_t *lens_out, gdr_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
