@@ -95,6 +95,8 @@ cudaError_t launch_commit(const Args &a, int32_t *err, cudaStream_t s);
 // The rule over trees of 1 <= fixed_len <= 64 drafted tokens (gdr_tree_rule.cu), and the
 // accepted path's state in place of the one before.
 cudaError_t launch_tree(const Args &a, int32_t *err, cudaStream_t s);
+// launch_tree for bf16 inputs (gdr_tree_tc.cu).
+cudaError_t launch_tree_tc(const Args &a, int32_t *err, cudaStream_t s);
 cudaError_t launch_tree_commit(const Args &a, int32_t *err, cudaStream_t s);
 
 // bf16 tensor [d2][d1][d0] (d0 contiguous) as a TMA map with box {box0, 1, 64}.

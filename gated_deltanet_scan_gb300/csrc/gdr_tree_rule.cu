@@ -224,6 +224,7 @@ cudaError_t launch_commit_as(const Args &a, int32_t *err, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree(const Args &a, int32_t *err, cudaStream_t s) {
+    if (a.in_bf16) return launch_tree_tc(a, err, s);
     if (a.d == 32) return launch_plain<32>(a, err, s);
     if (a.d == 64) return launch_plain<64>(a, err, s);
     return launch_plain<128>(a, err, s);
