@@ -30,17 +30,17 @@ struct Masks {
     bool bad;       // one of them has a parent that cannot be one
 };
 
-// Of the tree at `parents` (n rows), by a whole warp.  With SUMS, `sum` holds a number for
+// Parents of rows lane and lane + 32.
+__device__ __forceinline__ int2 load_parents(const int32_t *parents, int n, int lane) {
+    return make_int2(lane < n ? parents[lane] : -2, lane + 32 < n ? parents[lane + 32] : -2);
+}
+
+// Of a tree of n rows with these parents, by a whole warp.  With SUMS, `sum` holds a number for
 // each of the lane's rows, and gets the sum of those of the row's path (0 for no node).
 template <bool SUMS = false>
-__device__ __forceinline__ Masks masks(const int32_t *parents, int n, int lane, double *sum = nullptr) {
+__device__ __forceinline__ Masks masks(int2 parents, int n, int lane, double *sum = nullptr) {
     Masks m;
-    int to[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int j = lane + 32 * i;
-        to[i] = j < n ? parents[j] : -2;
-    }
+    int to[2] = {parents.x, parents.y};
     m.bad = false;
     bool node[2];
 #pragma unroll
@@ -106,6 +106,10 @@ __device__ __forceinline__ Masks masks(const int32_t *parents, int n, int lane, 
         }
     }
     return m;
+}
+
+__device__ __forceinline__ Masks masks(const int32_t *parents, int n, int lane) {
+    return masks(load_parents(parents, n, lane), n, lane);
 }
 
 // The mask of row j (the same or another for every lane).

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(NT) tree_commit_kernel(const __grid_constant__
             const int j = lane + 32 * i;
             sum[i] = j < n ? (double)a.g[(row0 + j) * a.h_v + h] : 0.0;
         }
-        const tree::Masks m = tree::masks<true>(a.parents + row0, n, lane, sum);
+        const tree::Masks m = tree::masks<true>(tree::load_parents(a.parents + row0, n, lane), n, lane, sum);
         uint64_t path = tree::mask_of(m, last & 63);
         if (last < 0 || last >= n) path = 0;
         const int count = __popcll(path);

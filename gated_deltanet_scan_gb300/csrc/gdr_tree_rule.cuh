@@ -43,7 +43,7 @@ __device__ __forceinline__ void load_nodes(Nodes &s, const Args &a, int seq, int
         sum[i] = j < n ? (double)a.g[(row0 + j) * a.h_v + h] : 0.0;
         b[i] = j < n ? a.beta[(row0 + j) * a.h_v + h] : 0.f;
     }
-    const Masks m = masks<true>(a.parents + row0, n, lane, sum);
+    const Masks m = masks<true>(load_parents(a.parents + row0, n, lane), n, lane, sum);
     if (lead && m.bad) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
     int depth[2], deepest = 0;
 #pragma unroll
