@@ -514,6 +514,11 @@ def _cache(k_cache, v_cache, page_table, n_seqs: int, heads: int, d: int, dtype,
         raise ValueError(f"the caches must have shape (n_pages, page_size, {heads}, {d}), not {tuple(shape)}")
     if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
+    return _cache_of(shape, strides, k_cache, v_cache, page_table, n_seqs, dtype, dev)
+
+
+def _cache_of(shape, strides, k_cache, v_cache, page_table, n_seqs: int, dtype, dev: int) -> gdr_kv_cache:
+    """A layer's cache of this shape and strides, at the start of k_cache and v_cache."""
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError(f"the caches must have dtype {dtype}")
     if strides[3] != 1:
@@ -532,7 +537,7 @@ def _cache(k_cache, v_cache, page_table, n_seqs: int, heads: int, d: int, dtype,
         raise ValueError(f"the caches and page_table must be on device {dev}")
     n_pages, page = shape[0], shape[1]
     return gdr_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), strides[0] if n_pages > 1 else 0,
-                        strides[1] if page > 1 else 0, strides[2] if heads > 1 else 0, page_table.data_ptr(),
+                        strides[1] if page > 1 else 0, strides[2] if shape[2] > 1 else 0, page_table.data_ptr(),
                         rs if n > 1 else 0, n_pages, page, width)
 
 
@@ -701,25 +706,26 @@ def gdr_attn_commit_tree(k_cache, v_cache, page_table, kv_lens, parents, last, l
     the front of the tree's slots (see gdr_attn_commit_tree in include/gdr.h).  k_cache,
     v_cache [n_pages, page_size, H_kv, d], or [layers, n_pages, page_size, H_kv, d] for all
     layers at once; lens_out int32 [n] (not kv_lens itself) receives the new lengths."""
-    if k_cache.dim() == 5:
-        if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
-            raise ValueError("k_cache and v_cache must have the same shape and strides")
-        layers, stride = k_cache.shape[0], k_cache.stride(0)
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) == 4:
+        layers, stride = 1, 0
+    elif len(shape) == 5:
+        layers, stride = shape[0], strides[0] if shape[0] > 1 else 0
         if layers == 0:
             return
-        k_cache, v_cache = k_cache[0], v_cache[0]
-    elif k_cache.dim() == 4:
-        layers, stride = 1, 0
+        shape, strides = shape[1:], strides[1:]
     else:
         raise ValueError("the caches must be [n_pages, page_size, H_kv, d] or [layers, n_pages, page_size, H_kv, d]")
-    h_kv, d = k_cache.shape[2:]
+    if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    h_kv, d = shape[2], shape[3]
     dtype, dev = k_cache.dtype, k_cache.get_device()
     dims = _attn_dims(h_kv, h_kv, d, dtype, 1.0)
     i32, n = _attn_types[1], kv_lens.shape[0]
     n_tok = _tree_rows(parents, n, n * parents.shape[-1])
     st = (_lib or lib()).gdr_attn_commit_tree(
         dims, n, n_tok, _plain(parents, (n, n_tok), i32, dev, "parents"), _plain(last, (n,), i32, dev, "last"), layers,
-        stride if layers > 1 else 0, _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
+        stride, _cache_of(shape, strides, k_cache, v_cache, page_table, n, dtype, dev),
         _plain(kv_lens, (n,), i32, dev, "kv_lens"),
         None if lens_out is None else _plain(lens_out, (n,), i32, dev, "lens_out"), _attn_stream(stream, dev))
     if st != GDR_OK:
