@@ -3,33 +3,34 @@
 // Formulas: gdr_tree_rule.cuh, with the corrections solved for: the unit triangular I + N, whose
 // row j has entries at j's ancestors only, has an inverse T with entries at the same places, so
 //     u_j = sum_{i in A_j} T_ji R_i,   o_j = e^{G_j} S_0^T q_j + sum_{i in A_j} W_ji R_i,   W = P T,
-// R_j = beta_j (v_j - e^{G_j} S_0^T k_j).  T and W need no state: they are ready when it arrives,
-// and the rest is two products a state column enters, both on the tensor cores.
+// R_j = beta_j (v_j - e^{G_j} S_0^T k_j).  T and W need no state; the rest is two products that
+// a state's columns enter, both on the tensor cores.
 //
-// A block of 512 threads has one (sequence, V head), four threads one of the state's columns.
-// The first product, X^T = S_0^T [K; Q]^T, has M = d columns, N = 2 n nodes and inner size d, so
-// the state is the operand that lives in TMEM: a thread reads its quarter of a column from memory
-// (32 lanes, 128 bytes a row), splits each value exactly into three bf16 parts and stores them at
-// its lane, and gets its column's products back there.  The second, [U; O]^T = R^T [T; W]^T, has
-// inner size n: R, split likewise, is made from the first's results in the same lanes.  Neither
-// passes through shared memory.  Of the nine products of parts, the six that reach 2^-24 are made.
+// One block of 512 threads an SM walks consecutive (sequence, V head) pairs:
 //
-//   K, Q   cp.async into the swizzled operand layout, rows [0, r) and [r, 2 r), r = n rounded
-//          up to 16
-//   Gram   [K; Q] K^T, to shared memory, and from there N and P: a list of its ancestors for
-//          every node
-//   T, W   level by level (a node's row needs its ancestors' rows); an ancestor's own ancestors are
-//          the list's first entries, so entry r of node j is -sum_s N_js (entry r of ancestor s)
-//   parts  of the state: middle and low, then, over them, high: TMEM holds two parts (128 columns at
-//          d = 128) and the products (128) of two blocks an SM; small parts first, so that their
-//          sums round small
+//   gates    (warp 15) the tree, and the sums of the gates along its paths, a pair ahead of
+//   factors  (warps 8 .. 13) K and Q of a QK head by cp.async into the operand layout; the Gram
+//            products [K; Q] K^T, read into shared memory; N and P of every ancestor; T and W level by
+//            level (a node's row needs its ancestors' rows; an ancestor's own ancestors are the list's
+//            first entries, so entry r of node j is -sum_s N_js (entry r of ancestor s)); the bf16
+//            parts of T - I and W into an operand tile.  What is the tree's or the QK head's is kept for
+//            the pairs that share it.  All this for the pair after the one that
+//   states   (warps 0 .. 7) have: a thread reads half a column of the state (32 lanes, 128 bytes a
+//            row), splits each value exactly into three bf16 parts and stores them at its lane of TMEM:
+//            X^T = S_0^T [K; Q]^T has M = d columns, N = 2 n nodes and inner size d, and the state is
+//            the operand that lives in TMEM.  R and e^G S_0^T q are made from X in place, and
+//            [U; O]^T is what they are plus R^T [T - I; W]^T, inner size n, R's parts in TMEM too.  The
+//            state and R pass through no shared memory.  Of the nine products of parts, the six that
+//            reach 2^-24 are made, smallest first.  The next pair's state is loaded during the second
+//            product and the outputs.
+//   MMAs     (warp 14) both products: an issuing thread stands still while the tensor pipe is full.
 //
 // A node's rows of T and W are zero but at its ancestors, and zero times an infinity or NaN would
 // reach it: such values of R (rare) enter the product as zeros and are added afterwards to the
 // nodes whose path they are on.
 //
-// Bound by instructions, which is what every choice here saves: the same sums over the lists of
-// ancestors, a thread a column, took 48,000 warp instructions a block at 64 nodes.
+// Every role's code runs once a pair, so it is kept small for the instruction cache: rare and
+// long parts are loops of their own.
 //
 // d < 128 leaves lanes (and warps) idle.
 #include "gdr_attn.h"
@@ -44,41 +45,75 @@ namespace {
 using namespace tc;
 
 constexpr int NT = 512;
-constexpr int kShares = NT / 128;  // threads of a column
+constexpr int kStates = 256, kFactors = 192;  // threads of these roles
 constexpr int kNodes = tree::kMaxNodes;
 constexpr int GL = kNodes + 1;  // floats of a Gram row in shared memory
 constexpr int kEntries = kNodes * (kNodes - 1) / 2;  // of the ancestors' lists
-constexpr uint32_t kCols = 256;
+constexpr int kGrid = 152;
 
-// Shared memory: K and Q, then the Gram products.  T and W lie over the end of these, and their
-// bf16 parts, [T; W] of 128 rows each, over K, Q and the rest.
 struct Shape {
-    static constexpr uint32_t BLOCK = 128 * 128;  // 128 rows, 64 columns
-    static constexpr uint32_t OFF_GRAM = 2 * BLOCK;
-    static constexpr uint32_t OFF_TW = 3 * BLOCK;
-    static constexpr uint32_t OFF_LIST = OFF_TW + 16896;  // float4 each
-    static_assert(OFF_LIST >= OFF_GRAM + 128 * GL * 4 && OFF_LIST >= OFF_TW + kEntries * 8, "the two fit");
-    static constexpr uint32_t OFF_PAIR = OFF_LIST + kNodes * 128 * 4;  // the lists' place holds R, where it is needed
-    static_assert(kNodes * 128 * 4 >= kEntries * 16, "the lists");
-    static constexpr uint32_t BYTES = OFF_PAIR + kEntries * 4;
-    static_assert(3 * BYTES > 228 * 1024, "two blocks, whose TMEM fits, are all that an SM takes");
+    static constexpr uint32_t BLOCK = 128 * 128;          // 128 rows of 64 values
+    static constexpr uint32_t KQ = 2 * BLOCK;             // rows [0, r) K, [r, 2 r) Q, r = n rounded up to 16; two of them
+    static constexpr uint32_t OFF_B = 2 * KQ;             // three parts of [T; W], rows likewise
+    static constexpr uint32_t OFF_GRAM = OFF_B + 3 * BLOCK;
+    static constexpr uint32_t OFF_TW = OFF_GRAM + 128 * GL * 4;    // float2 an entry
+    static constexpr uint32_t OFF_NP = OFF_TW + kEntries * 8;      // float2 an entry
+    static constexpr uint32_t OFF_PAIR = OFF_NP + kEntries * 8;    // node | ancestor << 6 | place << 12 | ancestor's list << 18
+    static constexpr uint32_t OFF_R = OFF_PAIR + kEntries * 4;     // R with infinities and NaNs, [n][d]
+    static constexpr uint32_t BYTES = OFF_R + kNodes * 128 * 4;
+    // TMEM columns: the state's parts, X (then U and O), the Gram products, R's parts
+    static constexpr uint32_t A = 0, X = 192, GRAM = 320, RP = 384;
+};
+// What a role reports without waiting for who waits for it has a barrier for either of two buffers, so that no
+// phase is passed over.
+enum Bar {
+    kTables = 0,    // [2] gates -> factors
+    kKqFull = 2,    // [2] factors -> MMAs
+    kGateFull = 4,  // [2] factors -> states, gates
+    kBFull = 6,     // factors -> MMAs
+    kBFree,         // MMAs (or states) -> factors
+    kGram,          // a commit -> factors
+    kParts,         // states -> MMAs
+    kFirst,         // a commit -> states
+    kRParts,        // states -> MMAs
+    kSecond,        // a commit -> states
+    kBars
 };
 
-// One, or eight, columns of this thread's lane (complete after pair::tmem_store_wait).
-__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+// The gates run two pairs ahead of the factors, these one of the states: trees have four buffers.
+struct Tables {
+    uint64_t mask[4][kNodes];
+    uint64_t real[4];          // the rows that are nodes
+    int start[4][kNodes];      // where a node's list starts: the lists lie level by level
+    int level[4][kNodes + 1];  // where those of a level do
+    int levels[4];
+    float2 sum[2][kNodes];  // G as two floats
+    float grown[2][kNodes], beta[2][kNodes], rq[kNodes];
+    float4 gate[2][kNodes];  // beta, e^G / |k|, e^G / |q|, P_jj
+    uint32_t tmem, odd;
+    uint64_t bar[kBars];
+};
+
+// Columns of this thread's lane loaded (complete after pair::tmem_load_wait) and stored (after
+// pair::tmem_store_wait).
+__device__ __forceinline__ void tmem_load16_start(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_load1_start(uint32_t taddr, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
 }
 __device__ __forceinline__ void tmem_store1(uint32_t taddr, uint32_t r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
 }
-
-// Eight columns of this thread's lane, complete after pair::tmem_load_wait.
-__device__ __forceinline__ void tmem_load8_start(uint32_t taddr, uint32_t *r) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
@@ -90,233 +125,312 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t 
     mid = __byte_perm(__float_as_uint(ra), __float_as_uint(rb), 0x7632);
     lo = __byte_perm(__float_as_uint(ra - cut(ra)), __float_as_uint(rb - cut(rb)), 0x7632);
 }
+__device__ __forceinline__ bool is_odd(uint32_t x) { return (x & 0x7F800000u) == 0x7F800000u; }  // infinite or NaN
 
-template <int D, typename Out>
-__global__ void __launch_bounds__(NT, 2) tree_tc_kernel(const __grid_constant__ Args a, int32_t *err) {
-    using Sh = Shape;
-    constexpr uint32_t A0 = 0, A1 = D / 2, X = 128, PART = 32;  // TMEM columns; PART: of R's parts, from 0
-    extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t s_bar[4];
-    __shared__ uint32_t s_tmem;
-    __shared__ uint64_t s_mask[kNodes], s_real;  // s_real: the rows that are nodes
-    __shared__ float2 s_sum[kNodes];
-    __shared__ float s_grown[kNodes], s_beta[kNodes], s_rq[kNodes];
-    __shared__ int s_start[kNodes];      // where a node's list starts: the lists lie level by level
-    __shared__ int s_level[kNodes + 1];  // where those of a level do
-    __shared__ int s_levels;
-    __shared__ float4 s_gate[kNodes];   // beta, e^G / |k|, e^G / |q|, P_jj
-    float *const s_gram = reinterpret_cast<float *>(smem + Sh::OFF_GRAM);
-    float2 *const s_tw = reinterpret_cast<float2 *>(smem + Sh::OFF_TW);
-    float4 *const s_list = reinterpret_cast<float4 *>(smem + Sh::OFF_LIST);
-    // an entry's node, its ancestor and where the node's list starts: t | i << 8 | start << 16
-    uint32_t *const s_pair = reinterpret_cast<uint32_t *>(smem + Sh::OFF_PAIR);
-    const uint32_t base = smem_u32(smem);
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int h = blockIdx.x % a.h_v, seq = blockIdx.x / a.h_v, hq = h / (a.h_v / a.h_qk);
-    const int n = a.fixed_len, nr = (n + 15) & ~15;
-    const int64_t row0 = (int64_t)seq * n;
-    // the warps of a column block (TMEM lanes) share its inner values, its nodes and its Gram columns
-    const int col = tid & 127, share = warp >> 2;
-    const bool work = col - lane < D;
-    uint32_t bar[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bar[i] = smem_u32(s_bar + i);
+// A pair, and what the factors share with the pair before.
+struct Item {
+    int seq, h, hq;
+    bool new_tree, new_kq;
+};
+struct Items {
+    int at, end, seq, hq;
+    __device__ __forceinline__ explicit Items(const Args &a) : seq(-1), hq(-1) {
+        const int total = a.n_seqs * a.h_v, each = total / gridDim.x, rest = total % gridDim.x;
+        at = blockIdx.x * each + min((int)blockIdx.x, rest);
+        end = at + each + ((int)blockIdx.x < rest ? 1 : 0);
+    }
+    __device__ __forceinline__ Item next(const Args &a) {
+        Item it;
+        it.seq = at / a.h_v;
+        it.h = at - it.seq * a.h_v;
+        it.hq = it.h / (a.h_v / a.h_qk);
+        it.new_tree = it.seq != seq;
+        it.new_kq = it.new_tree || it.hq != hq;
+        seq = it.seq;
+        hq = it.hq;
+        ++at;
+        return it;
+    }
+};
 
-    // ---- every load of the block is on its way before anything is waited for, the tree's first
-    int2 parents;
-    float gate_in[2], beta_in[2];
-    if (warp == 0) {
-        parents = tree::load_parents(a.parents + row0, n, lane);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int j = lane + 32 * i;
-            gate_in[i] = j < n ? a.g[(row0 + j) * a.h_v + h] : 0.f;
-            beta_in[i] = j < n ? a.beta[(row0 + j) * a.h_v + h] : 0.f;
-        }
-    }
-    {
-        constexpr int CPR = D / 8, RPI = NT / CPR;  // 16-byte chunks of a row, rows at a time
-        const int c = tid % CPR;
-        const int64_t step = (int64_t)a.h_qk * D, first = (row0 * a.h_qk + hq) * D + c * 8;
-        const uint32_t to = base + (c >> 3) * Sh::BLOCK;
-#pragma unroll 1
-        for (int t = tid / CPR; t < n; t += RPI) {
-            const int64_t at = first + t * step;
-            attn::cp_async16(to + sw128_offset(t, c & 7), static_cast<const uint16_t *>(a.k) + at, 16u);
-            attn::cp_async16(to + sw128_offset(nr + t, c & 7), static_cast<const uint16_t *>(a.q) + at, 16u);
-        }
-        attn::cp_async_commit();
-    }
-    constexpr int KX = D / kShares, k0w = KX / 2;  // inner values of a thread, and TMEM columns they take
-    float x[KX];
-    if (work) {
-        const float *const state = a.state + (((int64_t)seq * a.h_v + h) * D + share * KX) * D + col;
-#pragma unroll
-        for (int i = 0; i < KX; ++i) x[i] = __ldcs(state + i * D);
-    }
-    if (warp == 0) {
-        double sum[2] = {(double)gate_in[0], (double)gate_in[1]};
-        const tree::Masks m = tree::masks<true>(parents, n, lane, sum);
-        if (m.bad && h == 0) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
-        int depth[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int j = lane + 32 * i;
-            const float hi = (float)sum[i], lo = (float)(sum[i] - (double)hi);
-            s_mask[j] = m.a[i];
-            s_sum[j] = make_float2(hi, lo);
-            s_grown[j] = expf(hi) * (1.f + lo);
-            s_beta[j] = a.beta_logits ? 1.f / (1.f + expf(-beta_in[i])) : beta_in[i];
-            depth[i] = __popcll(m.a[i]);
-        }
-        const uint32_t real[2] = {__ballot_sync(0xffffffffu, m.a[0] != 0), __ballot_sync(0xffffffffu, m.a[1] != 0)};
-        if (lane == 0) s_real = (uint64_t)real[1] << 32 | real[0];
-        const int levels = __reduce_max_sync(0xffffffffu, max(depth[0], depth[1]));
-        const uint32_t below = (1u << lane) - 1u;
-        int at = 0;
-#pragma unroll 1
-        for (int d = 0; d < levels; ++d) {  // d ancestors
-            const uint32_t b0 = __ballot_sync(0xffffffffu, depth[0] == d + 1), b1 = __ballot_sync(0xffffffffu, depth[1] == d + 1);
-            if (lane == 0) s_level[d] = at;
-            if (depth[0] == d + 1) s_start[lane] = at + __popc(b0 & below) * d;
-            if (depth[1] == d + 1) s_start[lane + 32] = at + (__popc(b0) + __popc(b1 & below)) * d;
-            at += (__popc(b0) + __popc(b1)) * d;
-        }
-        if (lane == 0) {
-            s_level[levels] = at;
-            s_levels = levels;
-        }
-    } else if (warp == 1) {
-        tmem_alloc(smem_u32(&s_tmem), kCols);
-        tmem_relinquish();
-        if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mbar_init(bar[i], 1);
-            fence_mbar_init();
-        }
-        __syncwarp();
-    }
-    attn::cp_async_wait<0>();
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = s_tmem, lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint64_t kq = smem_desc_sw128(base, 0, 1024);
-    bool ok = true;
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, pair::wait_bounded(bar, parity & 1));
+}
 
-    // ---- Gram products [K; Q] K^T, a row per lane; the ancestors' lists beside them
-    if (warp == 0 && elect_one()) {
-        const uint32_t id = idesc_bf16_f32(128, nr, 0, 0);
+// ---- the gates' warp -----------------------------------------------------------------------------
+__device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
+    const int lane = threadIdx.x & 31, n = a.fixed_len;
+    auto bar = [&](int i) { return smem_u32(s.bar + i); };
+    int trees = -1;
+    int to[6][2];  // rows' pointers, each step twice as far up
+    Items items(a);
 #pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {
-            const uint64_t at = kq + (((k >> 2) * Sh::BLOCK + (k & 3) * 32) >> 4);
-            mma_bf16(tmem + X, at, at, id, k > 0);
+    for (int i = 0; items.at < items.end; ++i) {
+        const Item it = items.next(a);
+        const int64_t row0 = (int64_t)it.seq * n;
+        int2 parents;
+        if (it.new_tree) parents = tree::load_parents(a.parents + row0, n, lane);
+        float g[2], b[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int j = lane + 32 * x;
+            g[x] = j < n ? a.g[(row0 + j) * a.h_v + it.h] : 0.f;
+            b[x] = j < n ? a.beta[(row0 + j) * a.h_v + it.h] : 0.f;
         }
-        mma_commit(bar[0]);
-    }
-    __syncwarp();
-    if (tid < n && s_mask[tid] != 0) {
-        uint64_t up = s_mask[tid] & ~(1ull << tid);
-        int e = s_start[tid];
-        const uint32_t rest = (uint32_t)e << 16 | tid;
+        // the buffers are free once the factors have used them two pairs ago
+        if (i >= 2 && !wait_warp(bar(kGateFull + (i & 1)), (i - 2) >> 1)) return false;
+        if (it.new_tree) {
+            const int z = ++trees & 3;
+            const tree::Masks m = tree::masks(parents, n, lane);
+            if (m.bad) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
+            const uint32_t below = (1u << lane) - 1u;
+            const uint32_t real[2] = {__ballot_sync(0xffffffffu, m.a[0] != 0), __ballot_sync(0xffffffffu, m.a[1] != 0)};
+            int depth[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                s.mask[z][lane + 32 * x] = m.a[x];
+                depth[x] = __popcll(m.a[x]);
+                to[0][x] = m.a[x] ? (x ? parents.y : parents.x) : -2;
+            }
+#pragma unroll
+            for (int k = 1; k < 6; ++k) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int p = to[k - 1][x];
+                    const int t0 = __shfl_sync(0xffffffffu, to[k - 1][0], p & 31);
+                    const int t1 = __shfl_sync(0xffffffffu, to[k - 1][1], p & 31);
+                    to[k][x] = p < 0 ? p : p & 32 ? t1 : t0;
+                }
+            }
+            const int deepest = __reduce_max_sync(0xffffffffu, max(depth[0], depth[1]));
+            int at = 0;
 #pragma unroll 1
-        for (; up; up &= up - 1) s_pair[e++] = rest | (uint32_t)(__ffsll((long long)up) - 1) << 8;
-    }
-    if (a.qk_norm) {  // |q_t|: eight lanes a row
-        const int r = tid >> 3;
-        float sq = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 8; c += 8) {
-            if (c + (tid & 7) >= D / 8 || r >= n) continue;
-            const uint4 w = *reinterpret_cast<const uint4 *>(smem + (c >> 3) * Sh::BLOCK + sw128_offset(nr + r, tid & 7));
-            const uint32_t y[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float lo = __uint_as_float(y[i] << 16), hi = __uint_as_float(y[i] & 0xFFFF0000u);
-                sq = fmaf(lo, lo, fmaf(hi, hi, sq));
+            for (int d = 0; d < deepest; ++d) {  // d ancestors
+                const uint32_t b0 = __ballot_sync(0xffffffffu, depth[0] == d + 1);
+                const uint32_t b1 = __ballot_sync(0xffffffffu, depth[1] == d + 1);
+                if (lane == 0) s.level[z][d] = at;
+                if (depth[0] == d + 1) s.start[z][lane] = at + __popc(b0 & below) * d;
+                if (depth[1] == d + 1) s.start[z][lane + 32] = at + (__popc(b0) + __popc(b1 & below)) * d;
+                at += (__popc(b0) + __popc(b1)) * d;
+            }
+            if (lane == 0) {
+                s.level[z][deepest] = at;
+                s.levels[z] = deepest;
+                s.real[z] = (uint64_t)real[1] << 32 | real[0];
             }
         }
+        // sums of the gates along the paths: in doubles, since their differences enter exponentials
+        double sum[2] = {to[0][0] == -2 ? 0.0 : (double)g[0], to[0][1] == -2 ? 0.0 : (double)g[1]};
 #pragma unroll
-        for (int d = 1; d < 8; d <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
-        if ((tid & 7) == 0 && r < n) s_rq[r] = l2norm_scale(sq);
-    }
-    __syncwarp();
-    ok = pair::wait_bounded(bar[0], 0) && ok;
-    __syncwarp();
-    tc_fence_after_sync();
-    if (16 * share < nr) {
-        uint32_t y[16];
-        pair::tmem_load16(lanes + X + 16 * share, y);
-        if (col < 2 * nr) {
+        for (int k = 0; k < 6; ++k) {
+            double more[2];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s_gram[col * GL + 16 * share + i] = __uint_as_float(y[i]);
+            for (int x = 0; x < 2; ++x) {
+                const double s0 = __shfl_sync(0xffffffffu, sum[0], to[k][x] & 31);
+                const double s1 = __shfl_sync(0xffffffffu, sum[1], to[k][x] & 31);
+                more[x] = to[k][x] & 32 ? s1 : s0;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (to[k][x] >= 0) sum[x] += more[x];
         }
-    }
-    if (tid < n && !a.qk_norm) s_rq[tid] = 1.f;
-    tc_fence_before_sync();
-    __syncthreads();
-    const int levels = s_levels, entries = s_level[levels];
-    auto unit = [&](int t) { return a.qk_norm ? l2norm_scale(s_gram[t * GL + t]) : 1.f; };  // 1 / |k_t|
-#pragma unroll 1
-    for (int e = tid; e < entries; e += NT) {
-        const int t = s_pair[e] & 255, i = s_pair[e] >> 8 & 255;
-        const float f = tree::decay(s_sum[t], s_sum[i]) * unit(i);
-        s_list[e] = make_float4(s_beta[t] * f * unit(t) * s_gram[t * GL + i], f * s_rq[t] * s_gram[(nr + t) * GL + i],
-                                __int_as_float(s_start[i]), 0.f);
-    }
-    if (tid < kNodes) {
-        float4 gate = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (tid < n) {
-            const float rk = unit(tid);
-            gate = make_float4(s_beta[tid], s_grown[tid] * rk, s_grown[tid] * s_rq[tid],
-                               s_rq[tid] * rk * s_gram[(nr + tid) * GL + tid]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int j = lane + 32 * x;
+            const float hi = (float)sum[x], lo = (float)(sum[x] - (double)hi);
+            s.sum[i & 1][j] = make_float2(hi, lo);
+            s.grown[i & 1][j] = expf(hi) * (1.f + lo);
+            s.beta[i & 1][j] = a.beta_logits ? 1.f / (1.f + expf(-b[x])) : b[x];
         }
-        s_gate[tid] = gate;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kTables + (i & 1)));
     }
-    __syncthreads();
+    return true;
+}
 
-    // ---- T and W: entry r of a node with d ancestors, by the first share's threads
-    if (share == 0) {
+// ---- the factors' warps --------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s) {
+    using Sh = Shape;
+    constexpr uint32_t ID = 2;
+    constexpr int N = kFactors;
+    float *const s_gram = reinterpret_cast<float *>(smem + Sh::OFF_GRAM);
+    float2 *const s_tw = reinterpret_cast<float2 *>(smem + Sh::OFF_TW);
+    float2 *const s_np = reinterpret_cast<float2 *>(smem + Sh::OFF_NP);
+    uint32_t *const s_pair = reinterpret_cast<uint32_t *>(smem + Sh::OFF_PAIR);
+    uint8_t *const parts = smem + Sh::OFF_B;
+    const uint32_t base = smem_u32(smem);
+    const int tid = threadIdx.x - kStates, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int n = a.fixed_len, nr = (n + 15) & ~15;
+    auto bar = [&](int i) { return smem_u32(s.bar + i); };
+    auto wait_all = [&](int i, uint32_t parity) { return !pair::named_or(ID, N, !pair::wait_bounded(bar(i), parity & 1)); };
+    auto load_kq = [&](const Item &it, int kq) {
+        constexpr int CPR = D / 8, RPI = N / CPR;  // 16-byte chunks of a row, rows at a time
+        const int c = tid % CPR;
+        const int64_t row0 = (int64_t)it.seq * n, step = (int64_t)a.h_qk * D, first = (row0 * a.h_qk + it.hq) * D + c * 8;
+        const uint32_t dst = base + kq * Sh::KQ + (c >> 3) * Sh::BLOCK;
+#pragma unroll 1
+        for (int t = tid / CPR; t < n; t += RPI) {
+            attn::cp_async16(dst + sw128_offset(t, c & 7), static_cast<const uint16_t *>(a.k) + first + t * step, 16u);
+            attn::cp_async16(dst + sw128_offset(nr + t, c & 7), static_cast<const uint16_t *>(a.q) + first + t * step, 16u);
+        }
+        attn::cp_async_commit();
+    };
+    int kq = 0, trees = -1, grams = -1, entries = 0, levels = 0;
+    Items items(a);
+    Item next = items.next(a);
+    load_kq(next, 0);
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+        const Item it = next;
+        const bool more = items.at < items.end;
+        if (more) next = items.next(a);
+        if (it.new_tree) ++trees;
+        const int z = trees & 3;
+        uint8_t *const tile = smem + kq * Sh::KQ;
+        if (it.new_kq) {
+            attn::cp_async_wait<0>();
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+        }
+        if (!wait_all(kTables + (i & 1), i >> 1)) return false;
+        if (it.new_kq && tid == 0) mbar_arrive(bar(kKqFull + kq));
+        // -- the ancestors' lists, the Gram products, |q|
+        if (it.new_tree) {
+            levels = s.levels[z];
+            entries = s.level[z][levels];
+            if (tid < n) {
+                const uint64_t mask = s.mask[z][tid];
+                const int at = s.start[z][tid];
+                int r = 0;
+#pragma unroll 1
+                for (uint64_t up = mask & ~(1ull << tid); up; ++r, up &= up - 1) {
+                    const int j = __ffsll((long long)up) - 1;
+                    s_pair[at + r] = (uint32_t)(tid | j << 6 | r << 12 | s.start[z][j] << 18);
+                }
+            }
+        }
+        if (it.new_kq) {
+            ++grams;
+            if (warp == 4) {
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint64_t at = smem_desc_sw128(base + kq * Sh::KQ, 0, 1024);
+                    const uint32_t id = idesc_bf16_f32(128, nr, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t x = at + (((k >> 2) * Sh::BLOCK + (k & 3) * 32) >> 4);
+                        mma_bf16(s.tmem + Sh::GRAM, x, x, id, k > 0);
+                    }
+                    mma_commit(bar(kGram));
+                }
+                __syncwarp();
+            }
+            if (a.qk_norm) {  // four lanes a row
+#pragma unroll 1
+                for (int r = tid >> 2; r < ((n + 7) & ~7); r += N / 4) {  // whole warps
+                    float sq = 0.f;
+#pragma unroll
+                    for (int c0 = 0; c0 < D / 8; c0 += 4) {
+                        const int c = c0 + (tid & 3);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * Sh::BLOCK +
+                                                                         sw128_offset(nr + r, c & 7));
+                        const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float lo = __uint_as_float(y[x] << 16), hi = __uint_as_float(y[x] & 0xFFFF0000u);
+                            sq = fmaf(lo, lo, fmaf(hi, hi, sq));
+                        }
+                    }
+                    sq += __shfl_xor_sync(0xffffffffu, sq, 1);
+                    sq += __shfl_xor_sync(0xffffffffu, sq, 2);
+                    if ((tid & 3) == 0 && r < n) s.rq[r] = l2norm_scale(sq);
+                }
+            } else if (tid < n) {
+                s.rq[tid] = 1.f;
+            }
+            if (!wait_all(kGram, grams)) return false;
+            tc_fence_after_sync();
+            if (warp < 4) {  // a row per lane
+#pragma unroll 1
+                for (int c = 0; c < nr; c += 16) {
+                    uint32_t y[16];
+                    pair::tmem_load16(s.tmem + ((uint32_t)(warp * 32) << 16) + Sh::GRAM + c, y);
+                    if (tid < 2 * nr) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) s_gram[tid * GL + c + k] = __uint_as_float(y[k]);
+                    }
+                }
+            }
+            named_sync(ID, N);
+        }
+        // -- N and P, and the nodes' own factors
+        auto unit = [&](int t) { return a.qk_norm ? l2norm_scale(s_gram[t * GL + t]) : 1.f; };  // 1 / |k_t|
+        const float2 *const s_sum = s.sum[i & 1];
+        const float *const s_beta = s.beta[i & 1];
+        float4 *const s_gate = s.gate[i & 1];
+        if (tid < kNodes) {
+            float4 gate = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s.real[z] >> tid & 1) {
+                const float rk = unit(tid), grown = s.grown[i & 1][tid];
+                gate = make_float4(s_beta[tid], grown * rk, grown * s.rq[tid],
+                                   s.rq[tid] * rk * s_gram[(nr + tid) * GL + tid]);
+            }
+            s_gate[tid] = gate;
+        }
+#pragma unroll 1
+        for (int e = tid; e < entries; e += N) {
+            const int t = s_pair[e] & 63, j = s_pair[e] >> 6 & 63;
+            const float f = tree::decay(s_sum[t], s_sum[j]) * unit(j);
+            s_np[e] = make_float2(s_beta[t] * f * unit(t) * s_gram[t * GL + j], f * s.rq[t] * s_gram[(nr + t) * GL + j]);
+        }
+        named_sync(ID, N);
+        if (tid == 0) mbar_arrive(bar(kGateFull + (i & 1)));
+        // -- T and W: place r of a node with d ancestors
         auto finish = [&](int e, int t, float m, float w) {
-            const float4 f = s_list[e];
+            const float2 f = s_np[e];
             const float y = -(f.x + m);
             s_tw[e] = make_float2(y, fmaf(s_gate[t].w, y, f.y + w));
         };
 #pragma unroll 1
         for (int d = 1; d < levels; ++d) {
-            const int e0 = s_level[d], e1 = s_level[d + 1];
+            const int e0 = s.level[z][d], e1 = s.level[z][d + 1];
             if (d <= 8) {  // a thread an entry, its up to seven terms at once
 #pragma unroll 1
-                for (int e = e0 + tid; e < e1; e += 128) {
+                for (int e = e0 + tid; e < e1; e += N) {
                     const uint32_t p = s_pair[e];
-                    const int at = p >> 16, r = e - at;
-                    float4 f[7];
-                    float y[7], m = 0.f, w = 0.f;
+                    const int r = p >> 12 & 63, at = e - r;
+                    float2 f[7];
+                    uint32_t up[7];
+                    float m = 0.f, w = 0.f;
 #pragma unroll
-                    for (int s = 0; s < 7; ++s) {
-                        if (s + 1 >= d) break;
-                        f[s] = s_list[at + min(r + 1 + s, d - 1)];
+                    for (int x = 0; x < 7; ++x) {
+                        if (x + 1 >= d) break;
+                        const int y = at + min(r + 1 + x, d - 1);
+                        f[x] = s_np[y];
+                        up[x] = s_pair[y] >> 18;
                     }
 #pragma unroll
-                    for (int s = 0; s < 7; ++s) {
-                        if (s + 1 >= d) break;
-                        y[s] = r + 1 + s < d ? s_tw[__float_as_int(f[s].z) + r].x : 0.f;
-                        m = fmaf(f[s].x, y[s], m);
-                        w = fmaf(f[s].y, y[s], w);
+                    for (int x = 0; x < 7; ++x) {
+                        if (x + 1 >= d) break;
+                        const float y = r + 1 + x < d ? s_tw[up[x] + r].x : 0.f;
+                        m = fmaf(f[x].x, y, m);
+                        w = fmaf(f[x].y, y, w);
                     }
-                    finish(e, p & 255, m, w);
+                    finish(e, p & 63, m, w);
                 }
             } else {  // eight lanes an entry
 #pragma unroll 1
-                for (int e4 = e0 + (tid >> 5) * 4; e4 < e1; e4 += 16) {  // whole warps
-                    const int e = min(e4 + (lane >> 3), e1 - 1), at = s_pair[e] >> 16, r = e - at;
+                for (int e4 = e0 + (tid >> 5) * 4; e4 < e1; e4 += N / 8) {  // whole warps
+                    const int e = min(e4 + (lane >> 3), e1 - 1);
+                    const uint32_t p = s_pair[e];
+                    const int r = p >> 12 & 63, at = e - r;
                     float m = 0.f, w = 0.f;
 #pragma unroll 1
-                    for (int s = r + 1 + (tid & 7); s < d; s += 8) {
-                        const float4 f = s_list[at + s];
-                        const float y = s_tw[__float_as_int(f.z) + r].x;
+                    for (int x = r + 1 + (tid & 7); x < d; x += 8) {
+                        const float2 f = s_np[at + x];
+                        const float y = s_tw[(s_pair[at + x] >> 18) + r].x;
                         m = fmaf(f.x, y, m);
                         w = fmaf(f.y, y, w);
                     }
@@ -325,214 +439,303 @@ __global__ void __launch_bounds__(NT, 2) tree_tc_kernel(const __grid_constant__ 
                         m += __shfl_xor_sync(0xffffffffu, m, y);
                         w += __shfl_xor_sync(0xffffffffu, w, y);
                     }
-                    if ((tid & 7) == 0 && e4 + (lane >> 3) < e1) finish(e, s_pair[e] & 255, m, w);
+                    if ((tid & 7) == 0 && e4 + (lane >> 3) < e1) finish(e, p & 63, m, w);
                 }
             }
-            named_sync(1, 128);
+            named_sync(ID, N);
         }
-    }
-
-    // ---- the state's parts, and its products with K and Q
-    uint32_t hi[k0w];
-    auto store_part = [&](uint32_t at, const uint32_t *w) {
-        if constexpr (k0w == 16) {
-            pair::tmem_store16(lanes + at + share * 16, w);
-        } else {
-#pragma unroll
-            for (int i = 0; i < k0w; ++i) tmem_store1(lanes + at + share * k0w + i, w[i]);
-        }
-    };
-    if (work) {
-        uint32_t mid[k0w], lo[k0w];
-#pragma unroll
-        for (int i = 0; i < k0w; ++i) split3(x[2 * i], x[2 * i + 1], hi[i], mid[i], lo[i]);
-        store_part(A0, lo);
-        store_part(A1, mid);
-        pair::tmem_store_wait();
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    const uint32_t id_x = idesc_bf16_f32(128, 2 * nr, 0, 0);
-    auto products = [&](bool first) {  // the two parts in place, or the last
+        // -- their parts, once the pair before is done with its own (and so with K and Q before this one's)
+        if (i > 0 && !wait_all(kBFree, i - 1)) return false;
+        if (more && next.new_kq) load_kq(next, kq ^ 1);
+        if (it.new_tree) {  // the places of another tree's entries
 #pragma unroll 1
-        for (int i = 0; i < (first ? 2 : 1) * (D / 16); ++i) {
-            const int k = i % (D / 16);
-            pair::mma_ts_one(tmem + X, tmem + A0 + i * 8, kq + (((k >> 2) * Sh::BLOCK + (k & 3) * 32) >> 4), id_x,
-                             !first || i > 0);
+            for (int x = tid; x < 3 * (int)Sh::BLOCK / 16; x += N)
+                reinterpret_cast<uint4 *>(parts)[x] = make_uint4(0u, 0u, 0u, 0u);
+            named_sync(ID, N);
         }
-    };
-    if (warp == 0) {
-        tc_fence_after_sync();
-        if (elect_one()) {
-            products(true);
-            mma_commit(bar[1]);
-        }
-        __syncwarp();
-    }
-    // this thread's values on their way
-    const int64_t step = (int64_t)a.h_v * D, out0 = (row0 * a.h_v + h) * D + col;
-    constexpr int KN = kNodes / kShares;
-    const int t0 = share * KN;
-    uint32_t v[KN];
-    if (work && t0 < n) {
-        const uint16_t *const from = static_cast<const uint16_t *>(a.v) + out0;
+#pragma unroll 1
+        for (int e = tid; e < entries + n; e += N) {  // T and W at the ancestors, W at the node itself
+            const int t = e < entries ? s_pair[e] & 63 : e - entries, j = e < entries ? s_pair[e] >> 6 & 63 : t;
+            const float2 f = e < entries ? s_tw[e] : make_float2(0.f, s_gate[t].w);
+            uint32_t part[3];
+            split3(f.x, f.y, part[0], part[1], part[2]);
+            uint8_t *const at = parts + sw128_offset(t, j >> 3) + (j & 7) * 2;
+            uint8_t *const aw = parts + sw128_offset(nr + t, j >> 3) + (j & 7) * 2;
 #pragma unroll
-        for (int i = 0; i < KN; ++i) v[i] = from[min(t0 + i, n - 1) * step];
-    }
-    ok = pair::wait_bounded(bar[1], 0) && ok;
-    __syncwarp();
-    if (work) {
-        tc_fence_after_sync();
-        store_part(A0, hi);
-        pair::tmem_store_wait();
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    if (warp == 0) {
-        tc_fence_after_sync();
-        if (elect_one()) {
-            products(false);
-            mma_commit(bar[2]);
-        }
-        __syncwarp();
-    }
-
-    // ---- R, its parts, and T's and W's
-    ok = pair::wait_bounded(bar[2], 0) && ok;
-    __syncwarp();
-    tc_fence_after_sync();
-    // no MMA reads K and Q any more
-    for (int x = tid; x < 2 * nr * 8; x += NT) {
-#pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4 *>(smem + p * Sh::BLOCK + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    float qs[KN];
-    bool odd = false;  // some R is an infinity or NaN
-    static_assert(KN == 16, "a share's nodes are one TMEM load");
-    uint32_t r[KN];
-    const uint32_t real = (uint32_t)(s_real >> t0);  // bit i: row t0 + i is a node
-    if (work && t0 < nr) {
-        float most = 0.f;
-#pragma unroll
-        for (int i0 = 0; i0 < KN; i0 += 8) {
-            uint32_t x[16];
-            tmem_load8_start(lanes + X + t0 + i0, x);
-            tmem_load8_start(lanes + X + nr + t0 + i0, x + 8);
-            pair::tmem_load_wait(x);
-#pragma unroll
-            for (int i = i0; i < i0 + 8; ++i) {
-                const float4 gate = s_gate[t0 + i];
-                const float y = gate.x * (__uint_as_float(v[i] << 16) - gate.y * __uint_as_float(x[i - i0]));
-                r[i] = real >> i & 1 ? __float_as_uint(y) : 0u;
-                most = fmaf(__uint_as_float(r[i]), 0.f, most);  // NaN from the first infinity or NaN on
-                qs[i] = gate.z * __uint_as_float(x[8 + i - i0]);
+            for (int p = 0; p < 3; ++p) {
+                *reinterpret_cast<uint16_t *>(at + p * Sh::BLOCK) = (uint16_t)part[p];
+                *reinterpret_cast<uint16_t *>(aw + p * Sh::BLOCK) = (uint16_t)(part[p] >> 16);
             }
         }
-        odd = most != 0.f;
+        fence_proxy_async_smem();
+        named_sync(ID, N);
+        if (tid == 0) mbar_arrive(bar(kBFull));
+        if (!more) break;
+        if (next.new_kq) kq ^= 1;
     }
-    odd = __syncthreads_or(odd);
-    float *const s_r = reinterpret_cast<float *>(smem + Sh::OFF_LIST);  // the lists' N and P are no longer needed
-    if (work && t0 < nr) {
-        uint32_t part[3][KN / 2];
-#pragma unroll
-        for (int i = 0; i < KN; ++i) {
-            if (!odd) break;
-            if (t0 + i < n) s_r[(t0 + i) * D + col] = __uint_as_float(r[i]);
-            if ((r[i] & 0x7F800000u) == 0x7F800000u) r[i] = 0u;
+    return true;
+}
+
+// ---- the MMAs' warp --------------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ bool products(const Args &a, uint8_t *smem, Tables &s) {
+    using Sh = Shape;
+    const bool issue = elect_one();
+    const int nr = (a.fixed_len + 15) & ~15;
+    const uint32_t base = smem_u32(smem), tmem = s.tmem;
+    auto bar = [&](int i) { return smem_u32(s.bar + i); };
+    const uint32_t id = idesc_bf16_f32(128, 2 * nr, 0, 0);
+    const uint64_t d_b = smem_desc_sw128(base + Sh::OFF_B, 0, 1024);
+    int loads = -1;
+    Items items(a);
+#pragma unroll 1
+    for (int i = 0; items.at < items.end; ++i) {
+        const Item it = items.next(a);
+        if (it.new_kq) {
+            ++loads;
+            if (!wait_warp(bar(kKqFull + (loads & 1)), loads >> 1)) return false;
         }
-#pragma unroll
-        for (int i = 0; i < KN / 2; ++i)
-            split3(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), part[0][i], part[1][i], part[2][i]);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) tmem_store8(lanes + p * PART + t0 / 2, part[p]);
-        pair::tmem_store_wait();
-    }
-    for (int e = tid; e < entries + n; e += NT) {  // the ancestors, and the node itself
-        const int t = e < entries ? s_pair[e] & 255 : e - entries, i = e < entries ? s_pair[e] >> 8 & 255 : t;
-        const float2 f = e < entries ? s_tw[e] : make_float2(1.f, s_gate[t].w);
-        uint32_t hi, mid, lo;
-        split3(f.x, f.y, hi, mid, lo);
-        uint8_t *const at = smem + sw128_offset(t, i >> 3) + (i & 7) * 2, *const aw = smem + sw128_offset(nr + t, i >> 3) + (i & 7) * 2;
-        const uint32_t part[3] = {hi, mid, lo};
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            *reinterpret_cast<uint16_t *>(at + p * Sh::BLOCK) = (uint16_t)part[p];
-            *reinterpret_cast<uint16_t *>(aw + p * Sh::BLOCK) = (uint16_t)(part[p] >> 16);
-        }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before_sync();
-    __syncthreads();
-    if (warp == 0) {
+        if (!wait_warp(bar(kParts), i)) return false;
         tc_fence_after_sync();
-        if (elect_one()) {
-            auto pass = [&](int r_part, int t_part, bool first) {
+        if (issue) {
+            const uint64_t d_kq = smem_desc_sw128(base + (loads & 1) * Sh::KQ, 0, 1024);
+#pragma unroll 1
+            for (int p = 0; p < 3; ++p) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    pair::mma_ts_one(tmem + Sh::X, tmem + Sh::A + p * (D / 2) + k * 8,
+                                     d_kq + (((k >> 2) * Sh::BLOCK + (k & 3) * 32) >> 4), id, p > 0 || k > 0);
+            }
+            mma_commit(bar(kFirst));
+        }
+        __syncwarp();
+        if (!wait_warp(bar(kBFull), i) || !wait_warp(bar(kRParts), i)) return false;
+        tc_fence_after_sync();
+        if (issue) {
+#pragma unroll 1
+            for (int p = 0; p < 6; ++p) {
+                // parts of R and of T, W: 2 0, 1 1, 0 2, 1 0, 0 1, 0 0
+                const int r_part = 0x001012 >> (4 * p) & 15, t_part = 0x010210 >> (4 * p) & 15;
 #pragma unroll
                 for (int k = 0; k < kNodes / 16; ++k) {
                     if (k * 16 >= nr) break;
-                    pair::mma_ts_one(tmem + X, tmem + r_part * PART + k * 8, kq + ((t_part * Sh::BLOCK + k * 32) >> 4), id_x,
-                                     !first || k > 0);
+                    pair::mma_ts_one(tmem + Sh::X, tmem + Sh::RP + r_part * 32 + k * 8,
+                                     d_b + ((t_part * Sh::BLOCK + k * 32) >> 4), id, 1);
                 }
-            };
-            pass(2, 0, true);
-            pass(1, 1, false);
-            pass(0, 2, false);
-            pass(1, 0, false);
-            pass(0, 1, false);
-            pass(0, 0, false);
-            mma_commit(bar[3]);
+            }
+            if (!*reinterpret_cast<volatile uint32_t *>(&s.odd)) mma_commit(bar(kBFree));
+            mma_commit(bar(kSecond));
         }
         __syncwarp();
     }
-    ok = pair::wait_bounded(bar[3], 0) && ok;
-    __syncwarp();
-    if (work && t0 < n) {
-        tc_fence_after_sync();
-        uint32_t u[KN], o[KN];
-        pair::tmem_load16(lanes + X + t0, u);
-        pair::tmem_load16(lanes + X + nr + t0, o);
+    return true;
+}
+
+// ---- the states' warps -----------------------------------------------------------------------------
+template <int D, typename Out>
+__device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) {
+    using Sh = Shape;
+    constexpr uint32_t ID = 1;
+    constexpr int KX = D / 2;       // a thread's values of its column
+    constexpr int KN = kNodes / 2;  // and nodes, in two groups of 16
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int n = a.fixed_len, nr = (n + 15) & ~15;
+    const int col = tid & 127, share = warp >> 2, t0 = share * KN;
+    const bool work = col - lane < D;
+    const uint32_t lanes = s.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    auto bar = [&](int i) { return smem_u32(s.bar + i); };
+    const int64_t step = (int64_t)a.h_v * D;
+    float *const s_r = reinterpret_cast<float *>(smem + Sh::OFF_R) + col;
+    float x[KX];
+    auto load_state = [&](int64_t pair) {
+        if (!work) return;
+        const float *const from = a.state + (pair * D + share * KX) * D + col;
 #pragma unroll
-        for (int i = 0; i < KN; ++i) o[i] = __float_as_uint(qs[i] + __uint_as_float(o[i]));
-        if (odd) {
-#pragma unroll
-            for (int i = 0; i < KN; ++i) {
-                if (t0 + i >= n) break;
-                const uint64_t mask = s_mask[t0 + i];
-                const int at = s_start[t0 + i];
-                float x = __uint_as_float(u[i]), y = __uint_as_float(o[i]);
-                int e = 0;
+        for (int i = 0; i < KX; ++i) x[i] = __ldcs(from + i * D);
+    };
+    int trees = -1;
+    bool ok = true;
+    Items items(a);
+    load_state(items.at);
 #pragma unroll 1
-                for (uint64_t up = mask; up; up &= up - 1, ++e) {
-                    const float w = s_r[(__ffsll((long long)up) - 1) * D + col];
-                    if (isfinite(w)) continue;
-                    const float2 f = up & (up - 1) ? s_tw[at + e] : make_float2(1.f, s_gate[t0 + i].w);
-                    x = fmaf(f.x, w, x);
-                    y = fmaf(f.y, w, y);
+    for (int i = 0; items.at < items.end; ++i) {
+        const int64_t pair_at = items.at;
+        const Item it = items.next(a);
+        if (it.new_tree) ++trees;
+        // -- the state's parts, low first
+        if (work) {
+#pragma unroll
+            for (int c = 0; c < KX / 2; c += 8) {
+                uint32_t part[3][8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) split3(x[2 * (c + k)], x[2 * (c + k) + 1], part[2][k], part[1][k], part[0][k]);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) tmem_store8(lanes + Sh::A + p * (D / 2) + share * (KX / 2) + c, part[p]);
+            }
+            pair::tmem_store_wait();
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kParts));
+        const int64_t out0 = ((int64_t)it.seq * n * a.h_v + it.h) * D + col;
+        const uint16_t *const values = static_cast<const uint16_t *>(a.v) + out0;
+        uint32_t v[KN];
+        if (work && t0 < n) {
+#pragma unroll
+            for (int k = 0; k < KN; ++k) v[k] = values[min(t0 + k, n - 1) * step];
+        }
+        // -- R and its parts, and what they are added to
+        ok = wait_warp(bar(kGateFull + (i & 1)), i >> 1) && ok;
+        ok = wait_warp(bar(kFirst), i) && ok;
+        if (pair::named_or(ID, kStates, !ok)) return false;
+        tc_fence_after_sync();
+        const float4 *const s_gate = s.gate[i & 1] + t0;
+        float most = 0.f;
+        if (work) {
+#pragma unroll
+            for (int k0 = 0; k0 < KN; k0 += 16) {
+                if (t0 + k0 >= nr) break;
+                uint32_t y[32], part[3][8];
+                tmem_load16_start(lanes + Sh::X + t0 + k0, y);
+                tmem_load16_start(lanes + Sh::X + nr + t0 + k0, y + 16);
+                pair::tmem_load_wait(y);
+                const uint32_t real = (uint32_t)(s.real[trees & 3] >> (t0 + k0));
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float4 gate = s_gate[k0 + k];
+                    const float r = gate.x * (__uint_as_float(v[k0 + k] << 16) - gate.y * __uint_as_float(y[k]));
+                    const bool node = real >> k & 1;
+                    y[k] = node ? __float_as_uint(r) : 0u;
+                    y[16 + k] = node ? __float_as_uint(gate.z * __uint_as_float(y[16 + k])) : 0u;
+                    most = fmaf(__uint_as_float(y[k]), 0.f, most);  // NaN from the first infinity or NaN on
                 }
-                u[i] = __float_as_uint(x);
-                o[i] = __float_as_uint(y);
-            }
-        }
-        Out *to = static_cast<Out *>(a.o) + out0 + t0 * step;
+                pair::tmem_store16(lanes + Sh::X + t0 + k0, y);
+                pair::tmem_store16(lanes + Sh::X + nr + t0 + k0, y + 16);
 #pragma unroll
-        for (int i = 0; i < KN; ++i) {
-            if (t0 + i >= n) break;
-            const float y = real >> i & 1 ? a.scale * __uint_as_float(o[i]) : 0.f;
-            if constexpr (sizeof(Out) == 2)
-                *to = __float2bfloat16_rn(y);
-            else
-                *to = y;
-            to += step;
+                for (int k = 0; k < 16; ++k) y[k] = is_odd(y[k]) ? 0u : y[k];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    split3(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]), part[0][k], part[1][k], part[2][k]);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) tmem_store8(lanes + Sh::RP + p * 32 + (t0 + k0) / 2, part[p]);
+            }
+            pair::tmem_store_wait();
         }
-        if (a.deltas) {
+        tc_fence_before_sync();
+        const bool odd = pair::named_or(ID, kStates, most != 0.f);
+        if (tid == 0) {
+            s.odd = odd;
+            mbar_arrive(bar(kRParts));
+        }
+        if (items.at < items.end) load_state(pair_at + 1);
+        // -- U and O
+        ok = wait_warp(bar(kSecond), i) && ok;
+        tc_fence_after_sync();
+        if (odd) {  // infinities and NaNs of R to the nodes whose path they are on: rare, and small
+            const uint64_t *const mask = s.mask[trees & 3];
+            if (work) {
+#pragma unroll 1
+                for (int t = t0; t < min(n, t0 + KN); ++t) {
+                    uint32_t y[1];
+                    tmem_load1_start(lanes + Sh::X + t, y[0]);
+                    pair::tmem_load_wait(y);
+                    s_r[t * D] = __uint_as_float(y[0]);
+                }
+            }
+            named_sync(ID, kStates);
+            if (work) {
+#pragma unroll 1
+                for (int t = t0; t < min(n, t0 + KN); ++t) {
+                    uint32_t y[2];
+                    tmem_load1_start(lanes + Sh::X + t, y[0]);
+                    tmem_load1_start(lanes + Sh::X + nr + t, y[1]);
+                    pair::tmem_load_wait(y);
+#pragma unroll 1
+                    for (uint64_t up = mask[t]; up; up &= up - 1) {
+                        // R_j is infinite or NaN where U without its part is, before any is added
+                        const int j = __ffsll((long long)up) - 1;
+                        const float w = s_r[j * D];
+                        if (!is_odd(__float_as_uint(w))) continue;
+                        float f[2] = {0.f, 0.f};  // T and W, the sums of their parts
+#pragma unroll 1
+                        for (int p = 2; p >= 0; --p) {
+                            const uint8_t *const at = smem + Sh::OFF_B + p * Sh::BLOCK + (j & 7) * 2;
+                            f[0] += __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + sw128_offset(t, j >> 3)) << 16);
+                            f[1] += __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + sw128_offset(nr + t, j >> 3)) << 16);
+                        }
+                        if (j != t) y[0] = __float_as_uint(fmaf(f[0], w, __uint_as_float(y[0])));
+                        y[1] = __float_as_uint(fmaf(f[1], w, __uint_as_float(y[1])));
+                    }
+                    tmem_store1(lanes + Sh::X + t, y[0]);
+                    tmem_store1(lanes + Sh::X + nr + t, y[1]);
+                }
+                pair::tmem_store_wait();
+            }
+            named_sync(ID, kStates);
+            if (tid == 0) mbar_arrive(bar(kBFree));
+        }
+        if (work && ok) {
+            Out *to_o = static_cast<Out *>(a.o) + out0 + t0 * step;
             float *to_u = a.deltas + out0 + t0 * step;
+#pragma unroll 1
+            for (int k0 = t0; k0 < min(n, t0 + KN); k0 += 16) {
+                uint32_t y[32];
+                tmem_load16_start(lanes + Sh::X + k0, y);
+                tmem_load16_start(lanes + Sh::X + nr + k0, y + 16);
+                pair::tmem_load_wait(y);
 #pragma unroll
-            for (int i = 0; i < KN; ++i) {
-                if (t0 + i >= n) break;
-                *to_u = real >> i & 1 ? __uint_as_float(u[i]) : 0.f;
-                to_u += step;
+                for (int k = 0; k < 16; ++k) {
+                    if (k0 + k >= n) break;
+                    const float o = a.scale * __uint_as_float(y[16 + k]);
+                    if constexpr (sizeof(Out) == 2)
+                        *to_o = __float2bfloat16_rn(o);
+                    else
+                        *to_o = o;
+                    to_o += step;
+                }
+                if (!a.deltas) continue;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    if (k0 + k >= n) break;
+                    *to_u = __uint_as_float(y[k]);
+                    to_u += step;
+                }
             }
         }
+        tc_fence_before_sync();
+    }
+    return ok;
+}
+
+template <int D, typename Out>
+__global__ void __launch_bounds__(NT, 1) tree_tc_kernel(const __grid_constant__ Args a, int32_t *err) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Tables s;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    if (warp == 8) {
+        tmem_alloc(smem_u32(&s.tmem), 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(s.bar + i), i == kParts ? kStates / 32 : 1);
+        fence_mbar_init();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    bool ok;
+    if (warp < kStates / 32) {  // 256 (184 + 64) registers of the 512 x 128 that the block has
+        pair::more_registers<184>();
+        ok = states<D, Out>(a, smem, s);
+    } else {
+        pair::fewer_registers<64>();
+        if (warp < (kStates + kFactors) / 32)
+            ok = factors<D>(a, smem, s);
+        else if (warp == 14)
+            ok = products<D>(a, smem, s);
+        else
+            ok = gates(a, err, s);
     }
     if (!ok) {
         // a wait gave up: leave the MMAs in flight time to end before their operands go
@@ -543,7 +746,7 @@ __global__ void __launch_bounds__(NT, 2) tree_tc_kernel(const __grid_constant__ 
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, kCols);
+    if (warp == 8) tmem_dealloc(s.tmem, 512);
 }
 
 template <int D, typename Out>
@@ -551,7 +754,8 @@ cudaError_t launch_as(const Args &a, int32_t *err, cudaStream_t s) {
     static attn::SmemOptIn opt_in;
     const cudaError_t e = opt_in.set(reinterpret_cast<const void *>(tree_tc_kernel<D, Out>), (int)Shape::BYTES);
     if (e != cudaSuccess) return e;
-    tree_tc_kernel<D, Out><<<(unsigned)((int64_t)a.n_seqs * a.h_v), NT, Shape::BYTES, s>>>(a, err);
+    const int64_t pairs = (int64_t)a.n_seqs * a.h_v;
+    tree_tc_kernel<D, Out><<<(unsigned)(pairs < kGrid ? pairs : kGrid), NT, Shape::BYTES, s>>>(a, err);
     return cudaGetLastError();
 }
 
