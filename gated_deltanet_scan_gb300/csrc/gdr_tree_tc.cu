@@ -6,31 +6,35 @@
 // R_j = beta_j (v_j - e^{G_j} S_0^T k_j).  T and W need no state; the rest is two products that
 // a state's columns enter, both on the tensor cores.
 //
-// One block of 512 threads an SM walks consecutive (sequence, V head) pairs:
+// One block of 1024 threads an SM walks consecutive (sequence, V head) pairs:
 //
-//   gates    (warp 15) the tree, and the sums of the gates along its paths, a pair ahead of
-//   factors  (warps 8 .. 13) K and Q of a QK head by cp.async into the operand layout; the Gram
-//            products [K; Q] K^T, read into shared memory; N and P of every ancestor; T and W level by
+//   gates    (warp 31) the tree, and the sums of the gates along its paths, a pair or two ahead of
+//   factors  (warps 24 .. 29) K and Q of a QK head by cp.async into the operand layout; the Gram
+//            products [K; Q] K^T, of which the paths' are kept; N and P of every ancestor; T and W level by
 //            level (a node's row needs its ancestors' rows; an ancestor's own ancestors are the list's
-//            first entries, so entry r of node j is -sum_s N_js (entry r of ancestor s)); the bf16
-//            parts of T - I and W into an operand tile.  What is the tree's or the QK head's is kept for
-//            the pairs that share it.  All this for the pair after the one that
-//   states   (warps 0 .. 7) have: a thread reads half a column of the state (32 lanes, 128 bytes a
-//            row), splits each value exactly into three bf16 parts and stores them at its lane of TMEM:
-//            X^T = S_0^T [K; Q]^T has M = d columns, N = 2 n nodes and inner size d, and the state is
-//            the operand that lives in TMEM.  R and e^G S_0^T q are made from X in place, and
-//            [U; O]^T is what they are plus R^T [T - I; W]^T, inner size n, R's parts in TMEM too.  The
-//            state and R pass through no shared memory.  Of the nine products of parts, the six that
-//            reach 2^-24 are made, smallest first.  The next pair's state is loaded during the second
-//            product and the outputs.
-//   MMAs     (warp 14) both products: an issuing thread stands still while the tensor pipe is full.
+//            first entries, so entry r of node j is -sum_s N_js (entry r of ancestor s)), for two V heads
+//            of a QK head at once (where they fit), since the steps are a chain of loads; then, pair by pair, the bf16
+//            parts of T - I and W into an operand tile
+//   states   (warps 16 .. 23) a thread has half a column of the state, from a ring of 16 rows a stage that
+//            bulk copies fill (loads into registers held 4,000 clocks up at 64 nodes: an SM has some
+//            32 KB of them on their way); it splits each value exactly into three bf16 parts and stores
+//            them at its lane of TMEM: X^T = S_0^T [K; Q]^T has M = d columns, N = 2 n nodes and inner
+//            size d, and the state is the operand that lives in TMEM
+//   rows     (warps 0 .. 15) R and e^G S_0^T q are made from X in place, and [U; O]^T is what they are
+//            plus R^T [T - I; W]^T, inner size n, R's parts in TMEM too.  Neither the state nor R passes
+//            through shared memory.  Of the nine products of parts, the six that reach 2^-24 are made,
+//            smallest first.
+//   MMAs     (warp 30) both products: an issuing thread stands still while the tensor pipe is full.
+//
+// The chain X, R, U and O of a pair is what takes the time; everything else is done while the pairs
+// before go through it.
 //
 // A node's rows of T and W are zero but at its ancestors, and zero times an infinity or NaN would
 // reach it: such values of R (rare) enter the product as zeros and are added afterwards to the
 // nodes whose path they are on.
 //
-// Every role's code runs once a pair, so it is kept small for the instruction cache: rare and
-// long parts are loops of their own.
+// Every role's code runs once a pair or two, and the first pair waits for all of it to come from
+// memory: it is kept small, in loops where registers allow.
 //
 // d < 128 leaves lanes (and warps) idle.
 #include "gdr_attn.h"
@@ -44,52 +48,60 @@ namespace {
 
 using namespace tc;
 
-constexpr int NT = 512;
-constexpr int kStates = 256, kFactors = 192;  // threads of these roles
+constexpr int NT = 1024;
+constexpr int kRows = 512, kStates = 256, kFactors = 192;  // threads of these roles, in this order
+constexpr int kShares = kRows / 128;                       // threads of a column
 constexpr int kNodes = tree::kMaxNodes;
-constexpr int GL = kNodes + 1;  // floats of a Gram row in shared memory
 constexpr int kEntries = kNodes * (kNodes - 1) / 2;  // of the ancestors' lists
+constexpr int kSecondHead = kEntries / 2;            // where a second V head's are, if it fits
+constexpr int kSlots = 3, kStageRows = 16;           // of the state's ring, for either half of its warps
 constexpr int kGrid = 152;
 
 struct Shape {
     static constexpr uint32_t BLOCK = 128 * 128;          // 128 rows of 64 values
     static constexpr uint32_t KQ = 2 * BLOCK;             // rows [0, r) K, [r, 2 r) Q, r = n rounded up to 16; two of them
     static constexpr uint32_t OFF_B = 2 * KQ;             // three parts of [T; W], rows likewise
-    static constexpr uint32_t OFF_GRAM = OFF_B + 3 * BLOCK;
-    static constexpr uint32_t OFF_TW = OFF_GRAM + 128 * GL * 4;    // float2 an entry
-    static constexpr uint32_t OFF_NP = OFF_TW + kEntries * 8;      // float2 an entry
-    static constexpr uint32_t OFF_PAIR = OFF_NP + kEntries * 8;    // node | ancestor << 6 | place << 12 | ancestor's list << 18
-    static constexpr uint32_t OFF_R = OFF_PAIR + kEntries * 4;     // R with infinities and NaNs, [n][d]
-    static constexpr uint32_t BYTES = OFF_R + kNodes * 128 * 4;
+    static constexpr uint32_t OFF_NP = OFF_B + 3 * BLOCK;       // N and P, float2 an entry
+    static constexpr uint32_t OFF_T = OFF_NP + kEntries * 8;     // T
+    static constexpr uint32_t OFF_W = OFF_T + kEntries * 4;      // W
+    static constexpr uint32_t OFF_PAIR = OFF_W + kEntries * 4;   // node | ancestor << 6 | place << 12 | ancestor's list << 18
+    static constexpr uint32_t OFF_V = OFF_PAIR + kEntries * 4;   // [n][d]
+    static constexpr uint32_t STAGE = kStageRows * 128 * 4;
+    static constexpr uint32_t OFF_S = OFF_V + kNodes * 128 * 2;
+    static constexpr uint32_t BYTES = OFF_S + 2 * kSlots * STAGE;
+    static_assert(OFF_V % 16 == 0 && OFF_S % 16 == 0, "bulk copies");
     // TMEM columns: the state's parts, X (then U and O), the Gram products, R's parts
     static constexpr uint32_t A = 0, X = 192, GRAM = 320, RP = 384;
 };
-// What a role reports without waiting for who waits for it has a barrier for either of two buffers, so that no
-// phase is passed over.
+// What a role reports without waiting for who waits for it has a barrier for each of some buffers, so that
+// no phase is passed over.
 enum Bar {
     kTables = 0,    // [2] gates -> factors
     kKqFull = 2,    // [2] factors -> MMAs
-    kGateFull = 4,  // [2] factors -> states, gates
-    kBFull = 6,     // factors -> MMAs
-    kBFree,         // MMAs (or states) -> factors
+    kGateFull = 4,  // [4] factors -> rows, gates
+    kBFull = 8,     // factors -> MMAs
+    kBFree,         // MMAs (or rows) -> factors
     kGram,          // a commit -> factors
     kParts,         // states -> MMAs
-    kFirst,         // a commit -> states
-    kRParts,        // states -> MMAs
-    kSecond,        // a commit -> states
-    kBars
+    kFirst,         // a commit -> rows, states
+    kRParts,        // rows -> MMAs
+    kSecond,        // a commit -> rows
+    kXFree,         // rows -> MMAs
+    kVFull,         // copies -> rows
+    kSFull,         // [2][kSlots] copies -> states
+    kBars = kSFull + 2 * kSlots
 };
 
-// The gates run two pairs ahead of the factors, these one of the states: trees have four buffers.
+// The gates run ahead of the factors, these of the rows: trees and gates have four buffers.
 struct Tables {
     uint64_t mask[4][kNodes];
     uint64_t real[4];          // the rows that are nodes
-    int start[4][kNodes];      // where a node's list starts: the lists lie level by level
-    int level[4][kNodes + 1];  // where those of a level do
+    uint16_t start[4][kNodes];      // where a node's list starts: the lists lie level by level
+    uint16_t level[4][kNodes + 1];  // where those of a level do
     int levels[4];
     float2 sum[2][kNodes];  // G as two floats
-    float grown[2][kNodes], beta[2][kNodes], rq[kNodes];
-    float4 gate[2][kNodes];  // beta, e^G / |k|, e^G / |q|, P_jj
+    float grown[2][kNodes], beta[2][kNodes], rq[kNodes], kk[kNodes], qk[kNodes];  // k . k and q . k of a node
+    float4 gate[4][kNodes];  // beta, e^G / |k|, e^G / |q|, P_jj
     uint32_t tmem, odd;
     uint64_t bar[kBars];
 };
@@ -162,14 +174,12 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
     const int lane = threadIdx.x & 31, n = a.fixed_len;
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
     int trees = -1;
-    int to[6][2];  // rows' pointers, each step twice as far up
     Items items(a);
 #pragma unroll 1
     for (int i = 0; items.at < items.end; ++i) {
         const Item it = items.next(a);
         const int64_t row0 = (int64_t)it.seq * n;
-        int2 parents;
-        if (it.new_tree) parents = tree::load_parents(a.parents + row0, n, lane);
+        const int2 parents = tree::load_parents(a.parents + row0, n, lane);
         float g[2], b[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -178,29 +188,66 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
             b[x] = j < n ? a.beta[(row0 + j) * a.h_v + it.h] : 0.f;
         }
         // the buffers are free once the factors have used them two pairs ago
-        if (i >= 2 && !wait_warp(bar(kGateFull + (i & 1)), (i - 2) >> 1)) return false;
+        if (i >= 2 && !wait_warp(bar(kGateFull + (i - 2 & 3)), i - 2 >> 2)) return false;
+        // masks and sums of the gates along the paths by pointer jumping (gdr_tree.cuh); sums in doubles,
+        // since their differences enter exponentials
+        int to[2] = {parents.x, parents.y};
+        uint64_t mask[2];
+        double sum[2];
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int j = lane + 32 * x;
+            if (to[x] < -2 || to[x] >= j) {
+                bad = bad || j < n;
+                to[x] = -2;
+            }
+            mask[x] = to[x] != -2 ? 1ull << j : 0;
+            sum[x] = to[x] != -2 ? (double)g[x] : 0.0;
+        }
+#pragma unroll 1
+        for (int step = 1; step < n; step <<= 1) {
+            uint64_t up[2];
+            int next[2];
+            double more[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int from = to[x] & 31;
+                const bool high = to[x] & 32;
+                const uint64_t u0 = tree::shfl64(mask[0], from), u1 = tree::shfl64(mask[1], from);
+                const int t0 = __shfl_sync(0xffffffffu, to[0], from), t1 = __shfl_sync(0xffffffffu, to[1], from);
+                const double s0 = __shfl_sync(0xffffffffu, sum[0], from), s1 = __shfl_sync(0xffffffffu, sum[1], from);
+                up[x] = high ? u1 : u0;
+                next[x] = high ? t1 : t0;
+                more[x] = high ? s1 : s0;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (to[x] >= 0) {
+                    mask[x] |= up[x];
+                    sum[x] += more[x];
+                    to[x] = next[x];
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (mask[x] != 0 && to[x] == -2) {  // a path that ends in a row that is no node
+                bad = true;
+                mask[x] = 0;
+                sum[x] = 0.0;
+            }
+        }
         if (it.new_tree) {
             const int z = ++trees & 3;
-            const tree::Masks m = tree::masks(parents, n, lane);
-            if (m.bad) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
+            if (bad) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
             const uint32_t below = (1u << lane) - 1u;
-            const uint32_t real[2] = {__ballot_sync(0xffffffffu, m.a[0] != 0), __ballot_sync(0xffffffffu, m.a[1] != 0)};
+            const uint32_t real[2] = {__ballot_sync(0xffffffffu, mask[0] != 0), __ballot_sync(0xffffffffu, mask[1] != 0)};
             int depth[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                s.mask[z][lane + 32 * x] = m.a[x];
-                depth[x] = __popcll(m.a[x]);
-                to[0][x] = m.a[x] ? (x ? parents.y : parents.x) : -2;
-            }
-#pragma unroll
-            for (int k = 1; k < 6; ++k) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int p = to[k - 1][x];
-                    const int t0 = __shfl_sync(0xffffffffu, to[k - 1][0], p & 31);
-                    const int t1 = __shfl_sync(0xffffffffu, to[k - 1][1], p & 31);
-                    to[k][x] = p < 0 ? p : p & 32 ? t1 : t0;
-                }
+                s.mask[z][lane + 32 * x] = mask[x];
+                depth[x] = __popcll(mask[x]);
             }
             const int deepest = __reduce_max_sync(0xffffffffu, max(depth[0], depth[1]));
             int at = 0;
@@ -208,39 +255,25 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
             for (int d = 0; d < deepest; ++d) {  // d ancestors
                 const uint32_t b0 = __ballot_sync(0xffffffffu, depth[0] == d + 1);
                 const uint32_t b1 = __ballot_sync(0xffffffffu, depth[1] == d + 1);
-                if (lane == 0) s.level[z][d] = at;
-                if (depth[0] == d + 1) s.start[z][lane] = at + __popc(b0 & below) * d;
-                if (depth[1] == d + 1) s.start[z][lane + 32] = at + (__popc(b0) + __popc(b1 & below)) * d;
+                if (lane == 0) s.level[z][d] = (uint16_t)at;
+                if (depth[0] == d + 1) s.start[z][lane] = (uint16_t)(at + __popc(b0 & below) * d);
+                if (depth[1] == d + 1) s.start[z][lane + 32] = (uint16_t)(at + (__popc(b0) + __popc(b1 & below)) * d);
                 at += (__popc(b0) + __popc(b1)) * d;
             }
             if (lane == 0) {
-                s.level[z][deepest] = at;
+                s.level[z][deepest] = (uint16_t)at;
                 s.levels[z] = deepest;
                 s.real[z] = (uint64_t)real[1] << 32 | real[0];
             }
         }
-        // sums of the gates along the paths: in doubles, since their differences enter exponentials
-        double sum[2] = {to[0][0] == -2 ? 0.0 : (double)g[0], to[0][1] == -2 ? 0.0 : (double)g[1]};
-#pragma unroll
-        for (int k = 0; k < 6; ++k) {
-            double more[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const double s0 = __shfl_sync(0xffffffffu, sum[0], to[k][x] & 31);
-                const double s1 = __shfl_sync(0xffffffffu, sum[1], to[k][x] & 31);
-                more[x] = to[k][x] & 32 ? s1 : s0;
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (to[k][x] >= 0) sum[x] += more[x];
-        }
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
             const int j = lane + 32 * x;
-            const float hi = (float)sum[x], lo = (float)(sum[x] - (double)hi);
+            const double y = x ? sum[1] : sum[0];
+            const float hi = (float)y, lo = (float)(y - (double)hi), logit = x ? b[1] : b[0];
             s.sum[i & 1][j] = make_float2(hi, lo);
             s.grown[i & 1][j] = expf(hi) * (1.f + lo);
-            s.beta[i & 1][j] = a.beta_logits ? 1.f / (1.f + expf(-b[x])) : b[x];
+            s.beta[i & 1][j] = a.beta_logits ? 1.f / (1.f + expf(-logit)) : logit;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kTables + (i & 1)));
@@ -254,13 +287,12 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
     using Sh = Shape;
     constexpr uint32_t ID = 2;
     constexpr int N = kFactors;
-    float *const s_gram = reinterpret_cast<float *>(smem + Sh::OFF_GRAM);
-    float2 *const s_tw = reinterpret_cast<float2 *>(smem + Sh::OFF_TW);
     float2 *const s_np = reinterpret_cast<float2 *>(smem + Sh::OFF_NP);
+    float *const s_t = reinterpret_cast<float *>(smem + Sh::OFF_T), *const s_w = reinterpret_cast<float *>(smem + Sh::OFF_W);
     uint32_t *const s_pair = reinterpret_cast<uint32_t *>(smem + Sh::OFF_PAIR);
     uint8_t *const parts = smem + Sh::OFF_B;
     const uint32_t base = smem_u32(smem);
-    const int tid = threadIdx.x - kStates, lane = tid & 31;
+    const int tid = threadIdx.x - kRows - kStates, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int n = a.fixed_len, nr = (n + 15) & ~15;
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
@@ -282,9 +314,9 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
     Item next = items.next(a);
     load_kq(next, 0);
 #pragma unroll 1
-    for (int i = 0;; ++i) {
+    for (int i = 0;;) {
         const Item it = next;
-        const bool more = items.at < items.end;
+        bool more = items.at < items.end;
         if (more) next = items.next(a);
         if (it.new_tree) ++trees;
         const int z = trees & 3;
@@ -311,7 +343,13 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                 }
             }
         }
-        if (it.new_kq) {
+        const bool two = more && !next.new_kq && entries <= kSecondHead;  // another V head of the QK head
+        if (two) {
+            if (!wait_all(kTables + (i + 1 & 1), i + 1 >> 1)) return false;
+            more = items.at < items.end;
+            if (more) next = items.next(a);
+        }
+        {
             ++grams;
             if (warp == 4) {
                 tc_fence_after_sync();
@@ -327,7 +365,7 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                 }
                 __syncwarp();
             }
-            if (a.qk_norm) {  // four lanes a row
+            if (a.qk_norm && it.new_kq) {  // four lanes a row
 #pragma unroll 1
                 for (int r = tid >> 2; r < ((n + 7) & ~7); r += N / 4) {  // whole warps
                     float sq = 0.f;
@@ -347,129 +385,145 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                     sq += __shfl_xor_sync(0xffffffffu, sq, 2);
                     if ((tid & 3) == 0 && r < n) s.rq[r] = l2norm_scale(sq);
                 }
-            } else if (tid < n) {
+            } else if (!a.qk_norm && tid < n) {
                 s.rq[tid] = 1.f;
             }
             if (!wait_all(kGram, grams)) return false;
             tc_fence_after_sync();
-            if (warp < 4) {  // a row per lane
+            if (warp < 4) {  // a row of K or Q per lane: what is on its node's path
+                const int row = tid < nr ? tid : tid - nr;
+                const bool is_k = tid < nr;
+                uint64_t mask = row < n && tid < 2 * nr ? s.mask[z][row] : 0;
+                float *to = reinterpret_cast<float *>(s_np + (mask ? s.start[z][row] : 0)) + (is_k ? 0 : 1);
 #pragma unroll 1
                 for (int c = 0; c < nr; c += 16) {
                     uint32_t y[16];
                     pair::tmem_load16(s.tmem + ((uint32_t)(warp * 32) << 16) + Sh::GRAM + c, y);
-                    if (tid < 2 * nr) {
+                    const uint32_t bits = (uint32_t)(mask >> c);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) s_gram[tid * GL + c + k] = __uint_as_float(y[k]);
+                    for (int k = 0; k < 16; ++k) {
+                        if (!(bits >> k & 1)) continue;
+                        if (c + k == row)
+                            (is_k ? s.kk : s.qk)[row] = __uint_as_float(y[k]);
+                        else {
+                            *to = __uint_as_float(y[k]);
+                            to += 2;
+                        }
                     }
                 }
+                tc_fence_before_sync();
             }
             named_sync(ID, N);
         }
         // -- N and P, and the nodes' own factors
-        auto unit = [&](int t) { return a.qk_norm ? l2norm_scale(s_gram[t * GL + t]) : 1.f; };  // 1 / |k_t|
-        const float2 *const s_sum = s.sum[i & 1];
-        const float *const s_beta = s.beta[i & 1];
-        float4 *const s_gate = s.gate[i & 1];
-        if (tid < kNodes) {
+        auto unit = [&](int t) { return a.qk_norm ? l2norm_scale(s.kk[t]) : 1.f; };  // 1 / |k_t|
+        const int i1 = i + 1;
+        if (tid < 2 * kNodes) {
+            const int j = tid & 63, x = tid >> 6, b = i + x & 1;
             float4 gate = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (s.real[z] >> tid & 1) {
-                const float rk = unit(tid), grown = s.grown[i & 1][tid];
-                gate = make_float4(s_beta[tid], grown * rk, grown * s.rq[tid],
-                                   s.rq[tid] * rk * s_gram[(nr + tid) * GL + tid]);
+            if (s.real[z] >> j & 1) {
+                const float rk = unit(j), grown = s.grown[b][j];
+                gate = make_float4(s.beta[b][j], grown * rk, grown * s.rq[j], s.rq[j] * rk * s.qk[j]);
             }
-            s_gate[tid] = gate;
+            if (x == 0 || two) s.gate[i + x & 3][j] = gate;
         }
 #pragma unroll 1
         for (int e = tid; e < entries; e += N) {
             const int t = s_pair[e] & 63, j = s_pair[e] >> 6 & 63;
-            const float f = tree::decay(s_sum[t], s_sum[j]) * unit(j);
-            s_np[e] = make_float2(s_beta[t] * f * unit(t) * s_gram[t * GL + j], f * s.rq[t] * s_gram[(nr + t) * GL + j]);
+            const float2 raw = s_np[e];
+            const float kk = unit(t) * unit(j) * raw.x, qk = s.rq[t] * unit(j) * raw.y;
+#pragma unroll 1
+            for (int x = 0; x < (two ? 2 : 1); ++x) {
+                const int b = i + x & 1;
+                const float y = tree::decay(s.sum[b][t], s.sum[b][j]);
+                s_np[e + x * kSecondHead] = make_float2(s.beta[b][t] * y * kk, y * qk);
+            }
         }
         named_sync(ID, N);
-        if (tid == 0) mbar_arrive(bar(kGateFull + (i & 1)));
-        // -- T and W: place r of a node with d ancestors
-        auto finish = [&](int e, int t, float m, float w) {
-            const float2 f = s_np[e];
-            const float y = -(f.x + m);
-            s_tw[e] = make_float2(y, fmaf(s_gate[t].w, y, f.y + w));
-        };
+        if (tid == 0) {
+            mbar_arrive(bar(kGateFull + (i & 3)));
+            if (two) mbar_arrive(bar(kGateFull + (i1 & 3)));
+        }
+        // -- T and W: place r of a node with d ancestors, 2 lanes an entry, or 8 where paths are long
 #pragma unroll 1
         for (int d = 1; d < levels; ++d) {
             const int e0 = s.level[z][d], e1 = s.level[z][d + 1];
-            if (d <= 8) {  // a thread an entry, its up to seven terms at once
+            const int log = d <= 8 ? 1 : 3, per = 32 >> log, part = lane & ((1 << log) - 1);
 #pragma unroll 1
-                for (int e = e0 + tid; e < e1; e += N) {
-                    const uint32_t p = s_pair[e];
-                    const int r = p >> 12 & 63, at = e - r;
-                    float2 f[7];
-                    uint32_t up[7];
-                    float m = 0.f, w = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 7; ++x) {
-                        if (x + 1 >= d) break;
-                        const int y = at + min(r + 1 + x, d - 1);
-                        f[x] = s_np[y];
-                        up[x] = s_pair[y] >> 18;
+            for (int e_warp = e0 + warp * per; e_warp < e1; e_warp += N / 32 * per) {  // whole warps
+                const int mine = e_warp + (lane >> log), e = min(mine, e1 - 1);
+                const uint32_t p = s_pair[e];
+                const int r = p >> 12 & 63, at = e - r;
+                float m0 = 0.f, w0 = 0.f, m1 = 0.f, w1 = 0.f;
+#pragma unroll 2
+                for (int x = r + 1 + part; x < d; x += 1 << log) {
+                    const float2 f = s_np[at + x];
+                    const int up = (s_pair[at + x] >> 18) + r;
+                    const float y = s_t[up];
+                    m0 = fmaf(f.x, y, m0);
+                    w0 = fmaf(f.y, y, w0);
+                    if (two) {
+                        const float2 g = s_np[at + x + kSecondHead];
+                        const float z = s_t[up + kSecondHead];
+                        m1 = fmaf(g.x, z, m1);
+                        w1 = fmaf(g.y, z, w1);
                     }
-#pragma unroll
-                    for (int x = 0; x < 7; ++x) {
-                        if (x + 1 >= d) break;
-                        const float y = r + 1 + x < d ? s_tw[up[x] + r].x : 0.f;
-                        m = fmaf(f[x].x, y, m);
-                        w = fmaf(f[x].y, y, w);
-                    }
-                    finish(e, p & 63, m, w);
                 }
-            } else {  // eight lanes an entry
 #pragma unroll 1
-                for (int e4 = e0 + (tid >> 5) * 4; e4 < e1; e4 += N / 8) {  // whole warps
-                    const int e = min(e4 + (lane >> 3), e1 - 1);
-                    const uint32_t p = s_pair[e];
-                    const int r = p >> 12 & 63, at = e - r;
-                    float m = 0.f, w = 0.f;
-#pragma unroll 1
-                    for (int x = r + 1 + (tid & 7); x < d; x += 8) {
-                        const float2 f = s_np[at + x];
-                        const float y = s_tw[(s_pair[at + x] >> 18) + r].x;
-                        m = fmaf(f.x, y, m);
-                        w = fmaf(f.y, y, w);
+                for (int y = 1; y < 1 << log; y <<= 1) {
+                    m0 += __shfl_xor_sync(0xffffffffu, m0, y);
+                    w0 += __shfl_xor_sync(0xffffffffu, w0, y);
+                    m1 += __shfl_xor_sync(0xffffffffu, m1, y);
+                    w1 += __shfl_xor_sync(0xffffffffu, w1, y);
+                }
+                if (part == 0 && mine < e1) {
+                    const float2 f = s_np[e];
+                    const float y = -(f.x + m0);
+                    s_t[e] = y;
+                    s_w[e] = fmaf(s.gate[i & 3][p & 63].w, y, f.y + w0);
+                    if (two) {
+                        const float2 g = s_np[e + kSecondHead];
+                        const float z = -(g.x + m1);
+                        s_t[e + kSecondHead] = z;
+                        s_w[e + kSecondHead] = fmaf(s.gate[i1 & 3][p & 63].w, z, g.y + w1);
                     }
-#pragma unroll
-                    for (int y = 1; y < 8; y <<= 1) {
-                        m += __shfl_xor_sync(0xffffffffu, m, y);
-                        w += __shfl_xor_sync(0xffffffffu, w, y);
-                    }
-                    if ((tid & 7) == 0 && e4 + (lane >> 3) < e1) finish(e, p & 63, m, w);
                 }
             }
             named_sync(ID, N);
         }
-        // -- their parts, once the pair before is done with its own (and so with K and Q before this one's)
-        if (i > 0 && !wait_all(kBFree, i - 1)) return false;
-        if (more && next.new_kq) load_kq(next, kq ^ 1);
-        if (it.new_tree) {  // the places of another tree's entries
+        // -- pair by pair, their parts, once the pair before is done with its own (and so with K and Q before
+        // this one's)
 #pragma unroll 1
-            for (int x = tid; x < 3 * (int)Sh::BLOCK / 16; x += N)
-                reinterpret_cast<uint4 *>(parts)[x] = make_uint4(0u, 0u, 0u, 0u);
-            named_sync(ID, N);
-        }
+        for (const int last = i + (two ? 1 : 0); i <= last; ++i) {
+            const bool first = i < last || !two;
+            const int from = first ? 0 : kSecondHead;
+            if (i > 0 && !wait_all(kBFree, i - 1)) return false;
+            if (first && more && next.new_kq) load_kq(next, kq ^ 1);
+            if (first && it.new_tree) {  // the places of another tree's entries
 #pragma unroll 1
-        for (int e = tid; e < entries + n; e += N) {  // T and W at the ancestors, W at the node itself
-            const int t = e < entries ? s_pair[e] & 63 : e - entries, j = e < entries ? s_pair[e] >> 6 & 63 : t;
-            const float2 f = e < entries ? s_tw[e] : make_float2(0.f, s_gate[t].w);
-            uint32_t part[3];
-            split3(f.x, f.y, part[0], part[1], part[2]);
-            uint8_t *const at = parts + sw128_offset(t, j >> 3) + (j & 7) * 2;
-            uint8_t *const aw = parts + sw128_offset(nr + t, j >> 3) + (j & 7) * 2;
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                *reinterpret_cast<uint16_t *>(at + p * Sh::BLOCK) = (uint16_t)part[p];
-                *reinterpret_cast<uint16_t *>(aw + p * Sh::BLOCK) = (uint16_t)(part[p] >> 16);
+                for (int x = tid; x < 3 * (int)Sh::BLOCK / 16; x += N)
+                    reinterpret_cast<uint4 *>(parts)[x] = make_uint4(0u, 0u, 0u, 0u);
+                named_sync(ID, N);
             }
+#pragma unroll 1
+            for (int e = tid; e < entries + n; e += N) {  // T and W at the ancestors, W at the node itself
+                const int t = e < entries ? s_pair[e] & 63 : e - entries, j = e < entries ? s_pair[e] >> 6 & 63 : t;
+                float2 f = make_float2(0.f, s.gate[i & 3][t].w);
+                if (e < entries) f = make_float2(s_t[e + from], s_w[e + from]);
+                uint32_t part[3];
+                split3(f.x, f.y, part[0], part[1], part[2]);
+                uint8_t *const at = parts + sw128_offset(t, j >> 3) + (j & 7) * 2;
+                uint8_t *const aw = parts + sw128_offset(nr + t, j >> 3) + (j & 7) * 2;
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    *reinterpret_cast<uint16_t *>(at + p * Sh::BLOCK) = (uint16_t)part[p];
+                    *reinterpret_cast<uint16_t *>(aw + p * Sh::BLOCK) = (uint16_t)(part[p] >> 16);
+                }
+            }
+            fence_proxy_async_smem();
+            named_sync(ID, N);
+            if (tid == 0) mbar_arrive(bar(kBFull));
         }
-        fence_proxy_async_smem();
-        named_sync(ID, N);
-        if (tid == 0) mbar_arrive(bar(kBFull));
         if (!more) break;
         if (next.new_kq) kq ^= 1;
     }
@@ -495,7 +549,7 @@ __device__ __forceinline__ bool products(const Args &a, uint8_t *smem, Tables &s
             ++loads;
             if (!wait_warp(bar(kKqFull + (loads & 1)), loads >> 1)) return false;
         }
-        if (!wait_warp(bar(kParts), i)) return false;
+        if (!wait_warp(bar(kParts), i) || (i > 0 && !wait_warp(bar(kXFree), i - 1))) return false;
         tc_fence_after_sync();
         if (issue) {
             const uint64_t d_kq = smem_desc_sw128(base + (loads & 1) * Sh::KQ, 0, 1024);
@@ -532,12 +586,72 @@ __device__ __forceinline__ bool products(const Args &a, uint8_t *smem, Tables &s
 }
 
 // ---- the states' warps -----------------------------------------------------------------------------
-template <int D, typename Out>
+template <int D>
 __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) {
     using Sh = Shape;
+    constexpr int PER = D / kStageRows / 2;  // stages of a pair for each half of the warps: every other one
+    constexpr uint32_t BYTES = kStageRows * D * 4;
+    const int tid = threadIdx.x - kRows, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int col = tid & 127, half = warp >> 2;
+    const bool work = col - lane < D;
+    const uint32_t lanes = s.tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    auto bar = [&](int i) { return smem_u32(s.bar + i); };
+    uint8_t *const ring = smem + Sh::OFF_S + half * kSlots * Sh::STAGE;
+    Items items(a);
+    const int pairs = items.end - items.at, stages = pairs * PER;
+    const float *const state = a.state + (int64_t)items.at * D * D;
+    auto load = [&](int q) {  // this half's stage q of all
+        if (q >= stages) return;
+        const int slot = q % kSlots;
+        mbar_arrive_expect_tx(bar(kSFull + half * kSlots + slot), BYTES);
+        bulk_load(smem_u32(ring + slot * Sh::STAGE), state + ((int64_t)q * 2 + half) * kStageRows * D, BYTES,
+                  bar(kSFull + half * kSlots + slot));
+    };
+    if (col == 0) {
+        for (int q = 0; q < kSlots; ++q) load(q);
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0, q = 0; i < pairs; ++i) {
+        bool ok = i == 0 || wait_warp(bar(kFirst), i - 1);
+        tc_fence_after_sync();
+#pragma unroll 1
+        for (int k = 0; k < PER; ++k, ++q) {
+            ok = ok && wait_warp(bar(kSFull + half * kSlots + q % kSlots), q / kSlots);
+            const float *const x = reinterpret_cast<const float *>(ring + q % kSlots * Sh::STAGE) + col;
+            float y[kStageRows];
+            if (work) {
+#pragma unroll
+                for (int r = 0; r < kStageRows; ++r) y[r] = x[r * D];
+            }
+            if (pair::named_or(3 + half, kStates / 2, !ok)) return false;  // the stage is read
+            if (col == 0) load(q + kSlots);
+            __syncwarp();
+            if (work) {
+                uint32_t part[3][kStageRows / 2];
+#pragma unroll
+                for (int r = 0; r < kStageRows / 2; ++r) split3(y[2 * r], y[2 * r + 1], part[2][r], part[1][r], part[0][r]);
+#pragma unroll
+                for (int p = 0; p < 3; ++p)  // low first
+                    tmem_store8(lanes + Sh::A + p * (D / 2) + (2 * k + half) * (kStageRows / 2), part[p]);
+            }
+        }
+        pair::tmem_store_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kParts));
+    }
+    return true;
+}
+
+// ---- the rows' warps -------------------------------------------------------------------------------
+template <int D, typename Out>
+__device__ __forceinline__ bool rows(const Args &a, uint8_t *smem, Tables &s) {
+    using Sh = Shape;
     constexpr uint32_t ID = 1;
-    constexpr int KX = D / 2;       // a thread's values of its column
-    constexpr int KN = kNodes / 2;  // and nodes, in two groups of 16
+    constexpr int KN = kNodes / kShares;  // a thread's nodes
+    static_assert(KN == 16, "a thread's nodes are one TMEM load");
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int n = a.fixed_len, nr = (n + 15) & ~15;
@@ -546,117 +660,88 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
     const uint32_t lanes = s.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
     const int64_t step = (int64_t)a.h_v * D;
-    float *const s_r = reinterpret_cast<float *>(smem + Sh::OFF_R) + col;
-    float x[KX];
-    auto load_state = [&](int64_t pair) {
-        if (!work) return;
-        const float *const from = a.state + (pair * D + share * KX) * D + col;
-#pragma unroll
-        for (int i = 0; i < KX; ++i) x[i] = __ldcs(from + i * D);
+    const uint16_t *const s_v = reinterpret_cast<const uint16_t *>(smem + Sh::OFF_V) + t0 * D + col;
+    auto load_values = [&](const Item &it) {  // by the first warp
+        if (warp != 0) return;
+        const uint16_t *const from = static_cast<const uint16_t *>(a.v) + ((int64_t)it.seq * n * a.h_v + it.h) * D;
+        if (lane == 0) mbar_arrive_expect_tx(bar(kVFull), n * D * 2);
+        __syncwarp();
+        for (int t = lane; t < n; t += 32) bulk_load(smem_u32(smem + Sh::OFF_V) + t * D * 2, from + t * step, D * 2, bar(kVFull));
+        __syncwarp();
     };
     int trees = -1;
     bool ok = true;
     Items items(a);
-    load_state(items.at);
+    Item next = items.next(a);
+    load_values(next);
 #pragma unroll 1
-    for (int i = 0; items.at < items.end; ++i) {
-        const int64_t pair_at = items.at;
-        const Item it = items.next(a);
+    for (int i = 0;; ++i) {
+        const Item it = next;
+        const bool more = items.at < items.end;
+        if (more) next = items.next(a);
         if (it.new_tree) ++trees;
-        // -- the state's parts, low first
-        if (work) {
-#pragma unroll
-            for (int c = 0; c < KX / 2; c += 8) {
-                uint32_t part[3][8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) split3(x[2 * (c + k)], x[2 * (c + k) + 1], part[2][k], part[1][k], part[0][k]);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) tmem_store8(lanes + Sh::A + p * (D / 2) + share * (KX / 2) + c, part[p]);
-            }
-            pair::tmem_store_wait();
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kParts));
         const int64_t out0 = ((int64_t)it.seq * n * a.h_v + it.h) * D + col;
-        const uint16_t *const values = static_cast<const uint16_t *>(a.v) + out0;
-        uint32_t v[KN];
-        if (work && t0 < n) {
-#pragma unroll
-            for (int k = 0; k < KN; ++k) v[k] = values[min(t0 + k, n - 1) * step];
-        }
         // -- R and its parts, and what they are added to
-        ok = wait_warp(bar(kGateFull + (i & 1)), i >> 1) && ok;
+        ok = wait_warp(bar(kGateFull + (i & 3)), i >> 2) && ok;
+        ok = wait_warp(bar(kVFull), i) && ok;
         ok = wait_warp(bar(kFirst), i) && ok;
-        if (pair::named_or(ID, kStates, !ok)) return false;
+        if (pair::named_or(ID, kRows, !ok)) return false;
         tc_fence_after_sync();
-        const float4 *const s_gate = s.gate[i & 1] + t0;
         float most = 0.f;
-        if (work) {
+        if (work && t0 < nr) {
+            const float4 *const s_gate = s.gate[i & 3] + t0;
+            const uint32_t real = (uint32_t)(s.real[trees & 3] >> t0);
+            uint32_t y[32], part[3][8];
+            tmem_load16_start(lanes + Sh::X + t0, y);
+            tmem_load16_start(lanes + Sh::X + nr + t0, y + 16);
+            pair::tmem_load_wait(y);
 #pragma unroll
-            for (int k0 = 0; k0 < KN; k0 += 16) {
-                if (t0 + k0 >= nr) break;
-                uint32_t y[32], part[3][8];
-                tmem_load16_start(lanes + Sh::X + t0 + k0, y);
-                tmem_load16_start(lanes + Sh::X + nr + t0 + k0, y + 16);
-                pair::tmem_load_wait(y);
-                const uint32_t real = (uint32_t)(s.real[trees & 3] >> (t0 + k0));
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float4 gate = s_gate[k0 + k];
-                    const float r = gate.x * (__uint_as_float(v[k0 + k] << 16) - gate.y * __uint_as_float(y[k]));
-                    const bool node = real >> k & 1;
-                    y[k] = node ? __float_as_uint(r) : 0u;
-                    y[16 + k] = node ? __float_as_uint(gate.z * __uint_as_float(y[16 + k])) : 0u;
-                    most = fmaf(__uint_as_float(y[k]), 0.f, most);  // NaN from the first infinity or NaN on
-                }
-                pair::tmem_store16(lanes + Sh::X + t0 + k0, y);
-                pair::tmem_store16(lanes + Sh::X + nr + t0 + k0, y + 16);
+            for (int k = 0; k < 16; ++k) {
+                const float4 gate = s_gate[k];
+                const float r = gate.x * (__uint_as_float((uint32_t)s_v[k * D] << 16) - gate.y * __uint_as_float(y[k]));
+                const bool node = real >> k & 1;
+                y[k] = node ? __float_as_uint(r) : 0u;
+                y[16 + k] = node ? __float_as_uint(gate.z * __uint_as_float(y[16 + k])) : 0u;
+                most = fmaf(__uint_as_float(y[k]), 0.f, most);  // NaN from the first infinity or NaN on
+            }
+            pair::tmem_store16(lanes + Sh::X + t0, y);
+            pair::tmem_store16(lanes + Sh::X + nr + t0, y + 16);
+            if (most != 0.f) {
 #pragma unroll
                 for (int k = 0; k < 16; ++k) y[k] = is_odd(y[k]) ? 0u : y[k];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    split3(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]), part[0][k], part[1][k], part[2][k]);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) tmem_store8(lanes + Sh::RP + p * 32 + (t0 + k0) / 2, part[p]);
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                split3(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]), part[0][k], part[1][k], part[2][k]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) tmem_store8(lanes + Sh::RP + p * 32 + t0 / 2, part[p]);
             pair::tmem_store_wait();
         }
         tc_fence_before_sync();
-        const bool odd = pair::named_or(ID, kStates, most != 0.f);
+        const bool odd = pair::named_or(ID, kRows, most != 0.f);
         if (tid == 0) {
             s.odd = odd;
             mbar_arrive(bar(kRParts));
         }
-        if (items.at < items.end) load_state(pair_at + 1);
+        if (more) load_values(next);
         // -- U and O
         ok = wait_warp(bar(kSecond), i) && ok;
         tc_fence_after_sync();
         if (odd) {  // infinities and NaNs of R to the nodes whose path they are on: rare, and small
-            const uint64_t *const mask = s.mask[trees & 3];
-            if (work) {
+            if (work && share == 0) {
+                // R_j is one where U_j is, as long as nothing is added to it: from the last node down
 #pragma unroll 1
-                for (int t = t0; t < min(n, t0 + KN); ++t) {
-                    uint32_t y[1];
-                    tmem_load1_start(lanes + Sh::X + t, y[0]);
-                    pair::tmem_load_wait(y);
-                    s_r[t * D] = __uint_as_float(y[0]);
-                }
-            }
-            named_sync(ID, kStates);
-            if (work) {
-#pragma unroll 1
-                for (int t = t0; t < min(n, t0 + KN); ++t) {
+                for (int t = n - 1; t >= 0; --t) {
                     uint32_t y[2];
                     tmem_load1_start(lanes + Sh::X + t, y[0]);
                     tmem_load1_start(lanes + Sh::X + nr + t, y[1]);
                     pair::tmem_load_wait(y);
 #pragma unroll 1
-                    for (uint64_t up = mask[t]; up; up &= up - 1) {
-                        // R_j is infinite or NaN where U without its part is, before any is added
+                    for (uint64_t up = s.mask[trees & 3][t]; up; up &= up - 1) {
                         const int j = __ffsll((long long)up) - 1;
-                        const float w = s_r[j * D];
-                        if (!is_odd(__float_as_uint(w))) continue;
+                        uint32_t w[1];
+                        tmem_load1_start(lanes + Sh::X + j, w[0]);
+                        pair::tmem_load_wait(w);
                         float f[2] = {0.f, 0.f};  // T and W, the sums of their parts
 #pragma unroll 1
                         for (int p = 2; p >= 0; --p) {
@@ -664,48 +749,55 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
                             f[0] += __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + sw128_offset(t, j >> 3)) << 16);
                             f[1] += __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(at + sw128_offset(nr + t, j >> 3)) << 16);
                         }
-                        if (j != t) y[0] = __float_as_uint(fmaf(f[0], w, __uint_as_float(y[0])));
-                        y[1] = __float_as_uint(fmaf(f[1], w, __uint_as_float(y[1])));
+                        const float u = fmaf(f[0], __uint_as_float(w[0]), __uint_as_float(y[0]));
+                        const float o = fmaf(f[1], __uint_as_float(w[0]), __uint_as_float(y[1]));
+                        if (is_odd(w[0]) && j != t) y[0] = __float_as_uint(u);
+                        if (is_odd(w[0])) y[1] = __float_as_uint(o);
+                        __syncwarp();  // the next load is the whole warp's
                     }
                     tmem_store1(lanes + Sh::X + t, y[0]);
                     tmem_store1(lanes + Sh::X + nr + t, y[1]);
+                    pair::tmem_store_wait();
                 }
-                pair::tmem_store_wait();
             }
-            named_sync(ID, kStates);
+            tc_fence_before_sync();
+            named_sync(ID, kRows);
+            tc_fence_after_sync();
             if (tid == 0) mbar_arrive(bar(kBFree));
         }
-        if (work && ok) {
+        if (work && ok && t0 < n) {
             Out *to_o = static_cast<Out *>(a.o) + out0 + t0 * step;
             float *to_u = a.deltas + out0 + t0 * step;
-#pragma unroll 1
-            for (int k0 = t0; k0 < min(n, t0 + KN); k0 += 16) {
-                uint32_t y[32];
-                tmem_load16_start(lanes + Sh::X + k0, y);
-                tmem_load16_start(lanes + Sh::X + nr + k0, y + 16);
-                pair::tmem_load_wait(y);
+            uint32_t y[32];
+            tmem_load16_start(lanes + Sh::X + t0, y);
+            tmem_load16_start(lanes + Sh::X + nr + t0, y + 16);
+            pair::tmem_load_wait(y);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kXFree));
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                if (t0 + k >= n) break;
+                const float o = a.scale * __uint_as_float(y[16 + k]);
+                if constexpr (sizeof(Out) == 2)
+                    *to_o = __float2bfloat16_rn(o);
+                else
+                    *to_o = o;
+                to_o += step;
+            }
+            if (a.deltas) {
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    if (k0 + k >= n) break;
-                    const float o = a.scale * __uint_as_float(y[16 + k]);
-                    if constexpr (sizeof(Out) == 2)
-                        *to_o = __float2bfloat16_rn(o);
-                    else
-                        *to_o = o;
-                    to_o += step;
-                }
-                if (!a.deltas) continue;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    if (k0 + k >= n) break;
+                    if (t0 + k >= n) break;
                     *to_u = __uint_as_float(y[k]);
                     to_u += step;
                 }
             }
+        } else if (lane == 0) {
+            mbar_arrive(bar(kXFree));
         }
-        tc_fence_before_sync();
+        if (!more) return ok;
     }
-    return ok;
 }
 
 template <int D, typename Out>
@@ -713,30 +805,28 @@ __global__ void __launch_bounds__(NT, 1) tree_tc_kernel(const __grid_constant__ 
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ Tables s;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-    if (warp == 8) {
+    if (warp == 0) {
         tmem_alloc(smem_u32(&s.tmem), 512);
         tmem_relinquish();
     }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(s.bar + i), i == kParts ? kStates / 32 : 1);
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(s.bar + i), i == kParts ? kStates / 32 : i == kXFree ? kRows / 32 : 1);
         fence_mbar_init();
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     bool ok;
-    if (warp < kStates / 32) {  // 256 (184 + 64) registers of the 512 x 128 that the block has
-        pair::more_registers<184>();
-        ok = states<D, Out>(a, smem, s);
-    } else {
-        pair::fewer_registers<64>();
-        if (warp < (kStates + kFactors) / 32)
-            ok = factors<D>(a, smem, s);
-        else if (warp == 14)
-            ok = products<D>(a, smem, s);
-        else
-            ok = gates(a, err, s);
-    }
+    if (warp < kRows / 32)
+        ok = rows<D, Out>(a, smem, s);
+    else if (warp < (kRows + kStates) / 32)
+        ok = states<D>(a, smem, s);
+    else if (warp < (kRows + kStates + kFactors) / 32)
+        ok = factors<D>(a, smem, s);
+    else if (warp == NT / 32 - 2)
+        ok = products<D>(a, smem, s);
+    else
+        ok = gates(a, err, s);
     if (!ok) {
         // a wait gave up: leave the MMAs in flight time to end before their operands go
         atomicCAS(err, 0, (int32_t)GDR_ERR_DEVICE_TIMEOUT);
@@ -746,7 +836,7 @@ __global__ void __launch_bounds__(NT, 1) tree_tc_kernel(const __grid_constant__ 
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(s.tmem, 512);
+    if (warp == 0) tmem_dealloc(s.tmem, 512);
 }
 
 template <int D, typename Out>
