@@ -52,7 +52,7 @@ constexpr int NT = 1024;
 constexpr int kRows = 512, kStates = 256, kFactors = 192;  // threads of these roles, in this order
 constexpr int kShares = kRows / 128;                       // threads of a column
 constexpr int kNodes = tree::kMaxNodes;
-constexpr int kEntries = kNodes * (kNodes - 1) / 2;  // of the ancestors' lists
+constexpr int kEntries = kNodes * (kNodes + 1) / 2;  // of the paths' lists: ancestors, and the node itself last
 constexpr int kSecondHead = kEntries / 2;            // where a second V head's are, if it fits
 constexpr int kSlots = 3, kStageRows = 16;           // of the state's ring, for either half of its warps
 constexpr int kGrid = 152;
@@ -78,16 +78,17 @@ struct Shape {
 enum Bar {
     kTables = 0,    // [2] gates -> factors
     kKqFull = 2,    // [2] factors -> MMAs
-    kGateFull = 4,  // [4] factors -> rows, gates
-    kBFull = 8,     // factors -> MMAs
+    kGateFull = 4,  // [4] factors -> rows
+    kTabFree = 8,   // [2] factors -> gates
+    kBFull = 10,    // factors -> MMAs
     kBFree,         // MMAs (or rows) -> factors
     kGram,          // a commit -> factors
     kParts,         // states -> MMAs
     kFirst,         // a commit -> rows, states
-    kRParts,        // rows -> MMAs
+    kRParts,        // rows -> MMAs, states
     kSecond,        // a commit -> rows
     kXFree,         // rows -> MMAs
-    kVFull,         // copies -> rows
+    kVFull,         // states (their copies) -> rows
     kSFull,         // [2][kSlots] copies -> states
     kBars = kSFull + 2 * kSlots
 };
@@ -100,7 +101,7 @@ struct Tables {
     uint16_t level[4][kNodes + 1];  // where those of a level do
     int levels[4];
     float2 sum[2][kNodes];  // G as two floats
-    float grown[2][kNodes], beta[2][kNodes], rq[kNodes], kk[kNodes], qk[kNodes];  // k . k and q . k of a node
+    float grown[2][kNodes], beta[2][kNodes], rk[kNodes], rq[kNodes];  // 1 / |k|, 1 / |q|
     float4 gate[4][kNodes];  // beta, e^G / |k|, e^G / |q|, P_jj
     uint32_t tmem, odd;
     uint64_t bar[kBars];
@@ -188,7 +189,7 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
             b[x] = j < n ? a.beta[(row0 + j) * a.h_v + it.h] : 0.f;
         }
         // the buffers are free once the factors have used them two pairs ago
-        if (i >= 2 && !wait_warp(bar(kGateFull + (i - 2 & 3)), i - 2 >> 2)) return false;
+        if (i >= 2 && !wait_warp(bar(kTabFree + (i & 1)), i - 2 >> 1)) return false;
         // masks and sums of the gates along the paths by pointer jumping (gdr_tree.cuh); sums in doubles,
         // since their differences enter exponentials
         int to[2] = {parents.x, parents.y};
@@ -256,9 +257,9 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
                 const uint32_t b0 = __ballot_sync(0xffffffffu, depth[0] == d + 1);
                 const uint32_t b1 = __ballot_sync(0xffffffffu, depth[1] == d + 1);
                 if (lane == 0) s.level[z][d] = (uint16_t)at;
-                if (depth[0] == d + 1) s.start[z][lane] = (uint16_t)(at + __popc(b0 & below) * d);
-                if (depth[1] == d + 1) s.start[z][lane + 32] = (uint16_t)(at + (__popc(b0) + __popc(b1 & below)) * d);
-                at += (__popc(b0) + __popc(b1)) * d;
+                if (depth[0] == d + 1) s.start[z][lane] = (uint16_t)(at + __popc(b0 & below) * (d + 1));
+                if (depth[1] == d + 1) s.start[z][lane + 32] = (uint16_t)(at + (__popc(b0) + __popc(b1 & below)) * (d + 1));
+                at += (__popc(b0) + __popc(b1)) * (d + 1);
             }
             if (lane == 0) {
                 s.level[z][deepest] = (uint16_t)at;
@@ -337,7 +338,7 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                 const int at = s.start[z][tid];
                 int r = 0;
 #pragma unroll 1
-                for (uint64_t up = mask & ~(1ull << tid); up; ++r, up &= up - 1) {
+                for (uint64_t up = mask; up; ++r, up &= up - 1) {
                     const int j = __ffsll((long long)up) - 1;
                     s_pair[at + r] = (uint32_t)(tid | j << 6 | r << 12 | s.start[z][j] << 18);
                 }
@@ -393,7 +394,7 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
             if (warp < 4) {  // a row of K or Q per lane: what is on its node's path
                 const int row = tid < nr ? tid : tid - nr;
                 const bool is_k = tid < nr;
-                uint64_t mask = row < n && tid < 2 * nr ? s.mask[z][row] : 0;
+                const uint64_t mask = row < n && tid < 2 * nr ? s.mask[z][row] : 0;
                 float *to = reinterpret_cast<float *>(s_np + (mask ? s.start[z][row] : 0)) + (is_k ? 0 : 1);
 #pragma unroll 1
                 for (int c = 0; c < nr; c += 16) {
@@ -402,10 +403,7 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                     const uint32_t bits = (uint32_t)(mask >> c);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        if (!(bits >> k & 1)) continue;
-                        if (c + k == row)
-                            (is_k ? s.kk : s.qk)[row] = __uint_as_float(y[k]);
-                        else {
+                        if (bits >> k & 1) {
                             *to = __uint_as_float(y[k]);
                             to += 2;
                         }
@@ -416,33 +414,41 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
             named_sync(ID, N);
         }
         // -- N and P, and the nodes' own factors
-        auto unit = [&](int t) { return a.qk_norm ? l2norm_scale(s.kk[t]) : 1.f; };  // 1 / |k_t|
         const int i1 = i + 1;
         if (tid < 2 * kNodes) {
             const int j = tid & 63, x = tid >> 6, b = i + x & 1;
             float4 gate = make_float4(0.f, 0.f, 0.f, 0.f);
             if (s.real[z] >> j & 1) {
-                const float rk = unit(j), grown = s.grown[b][j];
-                gate = make_float4(s.beta[b][j], grown * rk, grown * s.rq[j], s.rq[j] * rk * s.qk[j]);
+                const float2 own = s_np[s.start[z][j] + __popcll(s.mask[z][j]) - 1];
+                const float rk = a.qk_norm ? l2norm_scale(own.x) : 1.f, grown = s.grown[b][j];
+                gate = make_float4(s.beta[b][j], grown * rk, grown * s.rq[j], s.rq[j] * rk * own.y);
+                if (x == 0) s.rk[j] = rk;
             }
             if (x == 0 || two) s.gate[i + x & 3][j] = gate;
-        }
-#pragma unroll 1
-        for (int e = tid; e < entries; e += N) {
-            const int t = s_pair[e] & 63, j = s_pair[e] >> 6 & 63;
-            const float2 raw = s_np[e];
-            const float kk = unit(t) * unit(j) * raw.x, qk = s.rq[t] * unit(j) * raw.y;
-#pragma unroll 1
-            for (int x = 0; x < (two ? 2 : 1); ++x) {
-                const int b = i + x & 1;
-                const float y = tree::decay(s.sum[b][t], s.sum[b][j]);
-                s_np[e + x * kSecondHead] = make_float2(s.beta[b][t] * y * kk, y * qk);
-            }
         }
         named_sync(ID, N);
         if (tid == 0) {
             mbar_arrive(bar(kGateFull + (i & 3)));
             if (two) mbar_arrive(bar(kGateFull + (i1 & 3)));
+        }
+#pragma unroll 1
+        for (int e = tid; e < entries; e += N) {
+            const int t = s_pair[e] & 63, j = s_pair[e] >> 6 & 63;
+            const float2 raw = s_np[e];
+            const float kk = s.rk[t] * s.rk[j] * raw.x, qk = s.rq[t] * s.rk[j] * raw.y;
+            {
+                const float y = tree::decay(s.sum[i & 1][t], s.sum[i & 1][j]);
+                s_np[e] = make_float2(s.beta[i & 1][t] * y * kk, y * qk);
+            }
+            if (two) {
+                const float y = tree::decay(s.sum[i1 & 1][t], s.sum[i1 & 1][j]);
+                s_np[e + kSecondHead] = make_float2(s.beta[i1 & 1][t] * y * kk, y * qk);
+            }
+        }
+        named_sync(ID, N);
+        if (tid == 0) {
+            mbar_arrive(bar(kTabFree + (i & 1)));
+            if (two) mbar_arrive(bar(kTabFree + (i1 & 1)));
         }
         // -- T and W: place r of a node with d ancestors, 2 lanes an entry, or 8 where paths are long
 #pragma unroll 1
@@ -476,7 +482,7 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                     m1 += __shfl_xor_sync(0xffffffffu, m1, y);
                     w1 += __shfl_xor_sync(0xffffffffu, w1, y);
                 }
-                if (part == 0 && mine < e1) {
+                if (part == 0 && mine < e1 && r < d) {
                     const float2 f = s_np[e];
                     const float y = -(f.x + m0);
                     s_t[e] = y;
@@ -506,10 +512,9 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                 named_sync(ID, N);
             }
 #pragma unroll 1
-            for (int e = tid; e < entries + n; e += N) {  // T and W at the ancestors, W at the node itself
-                const int t = e < entries ? s_pair[e] & 63 : e - entries, j = e < entries ? s_pair[e] >> 6 & 63 : t;
-                float2 f = make_float2(0.f, s.gate[i & 3][t].w);
-                if (e < entries) f = make_float2(s_t[e + from], s_w[e + from]);
+            for (int e = tid; e < entries; e += N) {  // T and W at the ancestors, W at the node itself
+                const int t = s_pair[e] & 63, j = s_pair[e] >> 6 & 63;
+                const float2 f = j == t ? make_float2(0.f, s.gate[i & 3][t].w) : make_float2(s_t[e + from], s_w[e + from]);
                 uint32_t part[3];
                 split3(f.x, f.y, part[0], part[1], part[2]);
                 uint8_t *const at = parts + sw128_offset(t, j >> 3) + (j & 7) * 2;
@@ -608,10 +613,20 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
         bulk_load(smem_u32(ring + slot * Sh::STAGE), state + ((int64_t)q * 2 + half) * kStageRows * D, BYTES,
                   bar(kSFull + half * kSlots + slot));
     };
+    auto load_values = [&](int64_t pair) {
+        constexpr int CPR = D / 8, RPI = kStates / CPR;  // 16-byte chunks of a row, rows at a time
+        const int n = a.fixed_len, c = tid % CPR;
+        const int64_t seq = pair / a.h_v, row = seq * n * a.h_v + (pair - seq * a.h_v);
+        for (int t = tid / CPR; t < n; t += RPI)
+            attn::cp_async16(smem_u32(smem + Sh::OFF_V) + (t * D + c * 8) * 2,
+                             static_cast<const uint16_t *>(a.v) + (row + (int64_t)t * a.h_v) * D + c * 8, 16u);
+        attn::cp_async_arrive(bar(kVFull));
+    };
     if (col == 0) {
         for (int q = 0; q < kSlots; ++q) load(q);
     }
     __syncwarp();
+    load_values(items.at);
 #pragma unroll 1
     for (int i = 0, q = 0; i < pairs; ++i) {
         bool ok = i == 0 || wait_warp(bar(kFirst), i - 1);
@@ -641,7 +656,13 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kParts));
+        // the next pair's values, once the rows are done with this one's
+        if (i + 1 < pairs) {
+            if (!wait_warp(bar(kRParts), i)) return false;
+            load_values(items.at + i + 1);
+        }
     }
+    attn::cp_async_wait<0>();
     return true;
 }
 
@@ -661,19 +682,10 @@ __device__ __forceinline__ bool rows(const Args &a, uint8_t *smem, Tables &s) {
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
     const int64_t step = (int64_t)a.h_v * D;
     const uint16_t *const s_v = reinterpret_cast<const uint16_t *>(smem + Sh::OFF_V) + t0 * D + col;
-    auto load_values = [&](const Item &it) {  // by the first warp
-        if (warp != 0) return;
-        const uint16_t *const from = static_cast<const uint16_t *>(a.v) + ((int64_t)it.seq * n * a.h_v + it.h) * D;
-        if (lane == 0) mbar_arrive_expect_tx(bar(kVFull), n * D * 2);
-        __syncwarp();
-        for (int t = lane; t < n; t += 32) bulk_load(smem_u32(smem + Sh::OFF_V) + t * D * 2, from + t * step, D * 2, bar(kVFull));
-        __syncwarp();
-    };
     int trees = -1;
     bool ok = true;
     Items items(a);
     Item next = items.next(a);
-    load_values(next);
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const Item it = next;
@@ -723,7 +735,6 @@ __device__ __forceinline__ bool rows(const Args &a, uint8_t *smem, Tables &s) {
             s.odd = odd;
             mbar_arrive(bar(kRParts));
         }
-        if (more) load_values(next);
         // -- U and O
         ok = wait_warp(bar(kSecond), i) && ok;
         tc_fence_after_sync();
@@ -810,7 +821,7 @@ __global__ void __launch_bounds__(NT, 1) tree_tc_kernel(const __grid_constant__ 
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(s.bar + i), i == kParts ? kStates / 32 : i == kXFree ? kRows / 32 : 1);
+        for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(s.bar + i), i == kParts ? kStates / 32 : i == kXFree ? kRows / 32 : i == kVFull ? kStates : 1);
         fence_mbar_init();
     }
     tc_fence_before_sync();
