@@ -10,11 +10,12 @@
 //
 //   gates    (warp 31) the tree, and the sums of the gates along its paths, a pair or two ahead of
 //   factors  (warps 24 .. 29) K and Q of a QK head by cp.async into the operand layout; the Gram
-//            products [K; Q] K^T, of which the paths' are kept; N and P of every ancestor; T and W level by
-//            level (a node's row needs its ancestors' rows; an ancestor's own ancestors are the list's
-//            first entries, so entry r of node j is -sum_s N_js (entry r of ancestor s)), for two V heads
-//            of a QK head at once (where they fit), since the steps are a chain of loads; then, pair by pair, the bf16
-//            parts of T - I and W into an operand tile
+//            products [K; Q] K^T, of which the paths' are kept; N and P of every ancestor; T and W, for
+//            two V heads of a QK head at once (where they fit), since the steps are chains of loads; then,
+//            pair by pair, the bf16 parts of T - I and W into an operand tile.  T comes by doubling: blocks
+//            of b = 1, 2, 4, ... levels of the paths are inverted; joining an even block and the odd one
+//            under it, T_ti = -sum_s T_ts Y_si with Y_si = sum_j N_sj T_ji, s in the odd block and j in the
+//            even one, so a path of 64 takes six rounds of two steps (level by level it takes 63).
 //   states   (warps 16 .. 23) a thread has half a column of the state, from a ring of 16 rows a stage that
 //            bulk copies fill (loads into registers held 4,000 clocks up at 64 nodes: an SM has some
 //            32 KB of them on their way); it splits each value exactly into three bf16 parts and stores
@@ -54,7 +55,10 @@ constexpr int kShares = kRows / 128;                       // threads of a colum
 constexpr int kNodes = tree::kMaxNodes;
 constexpr int kEntries = kNodes * (kNodes + 1) / 2;  // of the paths' lists: ancestors, and the node itself last
 constexpr int kSecondHead = kEntries / 2;            // where a second V head's are, if it fits
-constexpr int kSlots = 3, kStageRows = 16;           // of the state's ring, for either half of its warps
+constexpr int kStageRows = 16;  // of the state's rings, one for either half of its warps
+__host__ __device__ constexpr int ring_slots(int half) { return half == 0 ? 3 : 2; }
+constexpr int kSlots = ring_slots(0) + ring_slots(1);
+constexpr int kJoins = 6;  // of blocks of 1, 2, ..., 32 levels
 constexpr int kGrid = 152;
 
 struct Shape {
@@ -64,11 +68,13 @@ struct Shape {
     static constexpr uint32_t OFF_NP = OFF_B + 3 * BLOCK;       // N and P, float2 an entry
     static constexpr uint32_t OFF_T = OFF_NP + kEntries * 8;     // T
     static constexpr uint32_t OFF_W = OFF_T + kEntries * 4;      // W
-    static constexpr uint32_t OFF_PAIR = OFF_W + kEntries * 4;   // node | ancestor << 6 | place << 12 | ancestor's list << 18
-    static constexpr uint32_t OFF_V = OFF_PAIR + kEntries * 4;   // [n][d]
+    static constexpr uint32_t OFF_ITEM = OFF_W + kEntries * 4;   // entries join by join, the nodes themselves last: struct Entry
+    static constexpr uint32_t OFF_UP = OFF_ITEM + kEntries * 4;  // where the ancestor's own list starts, 16 bits an entry
+    static constexpr uint32_t OFF_ANC = OFF_UP + kEntries * 2;   // the ancestor, 8 bits an entry
+    static constexpr uint32_t OFF_V = OFF_ANC + kEntries;        // [n][d]
     static constexpr uint32_t STAGE = kStageRows * 128 * 4;
     static constexpr uint32_t OFF_S = OFF_V + kNodes * 128 * 2;
-    static constexpr uint32_t BYTES = OFF_S + 2 * kSlots * STAGE;
+    static constexpr uint32_t BYTES = OFF_S + kSlots * STAGE;
     static_assert(OFF_V % 16 == 0 && OFF_S % 16 == 0, "bulk copies");
     // TMEM columns: the state's parts, X (then U and O), the Gram products, R's parts
     static constexpr uint32_t A = 0, X = 192, GRAM = 320, RP = 384;
@@ -89,17 +95,17 @@ enum Bar {
     kSecond,        // a commit -> rows
     kXFree,         // rows -> MMAs
     kVFull,         // states (their copies) -> rows
-    kSFull,         // [2][kSlots] copies -> states
-    kBars = kSFull + 2 * kSlots
+    kSFull,         // [kSlots] copies -> states
+    kBars = kSFull + kSlots
 };
 
 // The gates run ahead of the factors, these of the rows: trees and gates have four buffers.
 struct Tables {
     uint64_t mask[4][kNodes];
     uint64_t real[4];          // the rows that are nodes
-    uint16_t start[4][kNodes];      // where a node's list starts: the lists lie level by level
-    uint16_t level[4][kNodes + 1];  // where those of a level do
-    int levels[4];
+    uint64_t plane[4][kJoins];  // those whose level (number of ancestors) has bit k
+    uint16_t start[4][kNodes];  // where a node's list starts
+    int entries[4], deepest[4];  // of all lists; ancestors of the deepest node
     float2 sum[2][kNodes];  // G as two floats
     float grown[2][kNodes], beta[2][kNodes], rk[kNodes], rq[kNodes];  // 1 / |k|, 1 / |q|
     float4 gate[4][kNodes];  // beta, e^G / |k|, e^G / |q|, P_jj
@@ -140,6 +146,15 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t 
 }
 __device__ __forceinline__ bool is_odd(uint32_t x) { return (x & 0x7F800000u) == 0x7F800000u; }  // infinite or NaN
 
+// An entry of a path's list, packed: its place, the node, the ancestor's level and the node's.
+struct Entry {
+    int e, t, r, d;
+    __device__ __forceinline__ explicit Entry(uint32_t p) : e(p & 4095), t(p >> 12 & 63), r(p >> 18 & 63), d(p >> 24) {}
+    static __device__ __forceinline__ uint32_t pack(int e, int t, int r, int d) {
+        return (uint32_t)(e | t << 12 | r << 18 | d << 24);
+    }
+};
+
 // A pair, and what the factors share with the pair before.
 struct Item {
     int seq, h, hq;
@@ -176,18 +191,23 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
     int trees = -1;
     Items items(a);
-#pragma unroll 1
-    for (int i = 0; items.at < items.end; ++i) {
-        const Item it = items.next(a);
+    int2 parents;
+    float g[2], b[2];
+    auto load = [&](const Item &it) {
         const int64_t row0 = (int64_t)it.seq * n;
-        const int2 parents = tree::load_parents(a.parents + row0, n, lane);
-        float g[2], b[2];
+        parents = tree::load_parents(a.parents + row0, n, lane);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int j = lane + 32 * x;
             g[x] = j < n ? a.g[(row0 + j) * a.h_v + it.h] : 0.f;
             b[x] = j < n ? a.beta[(row0 + j) * a.h_v + it.h] : 0.f;
         }
+    };
+    Item it = items.next(a);
+    load(it);  // before anything else of the block
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0;; ++i) {
         // the buffers are free once the factors have used them two pairs ago
         if (i >= 2 && !wait_warp(bar(kTabFree + (i & 1)), i - 2 >> 1)) return false;
         // masks and sums of the gates along the paths by pointer jumping (gdr_tree.cuh); sums in doubles,
@@ -242,28 +262,31 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
         if (it.new_tree) {
             const int z = ++trees & 3;
             if (bad) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
-            const uint32_t below = (1u << lane) - 1u;
             const uint32_t real[2] = {__ballot_sync(0xffffffffu, mask[0] != 0), __ballot_sync(0xffffffffu, mask[1] != 0)};
-            int depth[2];
+            int length[2], at = 0;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 s.mask[z][lane + 32 * x] = mask[x];
-                depth[x] = __popcll(mask[x]);
+                length[x] = __popcll(mask[x]);
+                int upto = length[x];
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto, d);
+                    if (lane >= d) upto += y;
+                }
+                s.start[z][lane + 32 * x] = (uint16_t)(at + upto - length[x]);
+                at += __shfl_sync(0xffffffffu, upto, 31);
             }
-            const int deepest = __reduce_max_sync(0xffffffffu, max(depth[0], depth[1]));
-            int at = 0;
+            const int longest = __reduce_max_sync(0xffffffffu, max(length[0], length[1]));
 #pragma unroll 1
-            for (int d = 0; d < deepest; ++d) {  // d ancestors
-                const uint32_t b0 = __ballot_sync(0xffffffffu, depth[0] == d + 1);
-                const uint32_t b1 = __ballot_sync(0xffffffffu, depth[1] == d + 1);
-                if (lane == 0) s.level[z][d] = (uint16_t)at;
-                if (depth[0] == d + 1) s.start[z][lane] = (uint16_t)(at + __popc(b0 & below) * (d + 1));
-                if (depth[1] == d + 1) s.start[z][lane + 32] = (uint16_t)(at + (__popc(b0) + __popc(b1 & below)) * (d + 1));
-                at += (__popc(b0) + __popc(b1)) * (d + 1);
+            for (int k = 0; k < kJoins; ++k) {
+                const uint32_t p0 = __ballot_sync(0xffffffffu, length[0] > 0 && (length[0] - 1 >> k & 1));
+                const uint32_t p1 = __ballot_sync(0xffffffffu, length[1] > 0 && (length[1] - 1 >> k & 1));
+                if (lane == 0) s.plane[z][k] = (uint64_t)p1 << 32 | p0;
             }
             if (lane == 0) {
-                s.level[z][deepest] = (uint16_t)at;
-                s.levels[z] = deepest;
+                s.entries[z] = at;
+                s.deepest[z] = longest - 1;
                 s.real[z] = (uint64_t)real[1] << 32 | real[0];
             }
         }
@@ -278,8 +301,10 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kTables + (i & 1)));
+        if (items.at == items.end) return true;
+        it = items.next(a);
+        load(it);
     }
-    return true;
 }
 
 // ---- the factors' warps --------------------------------------------------------------------------
@@ -290,10 +315,12 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
     constexpr int N = kFactors;
     float2 *const s_np = reinterpret_cast<float2 *>(smem + Sh::OFF_NP);
     float *const s_t = reinterpret_cast<float *>(smem + Sh::OFF_T), *const s_w = reinterpret_cast<float *>(smem + Sh::OFF_W);
-    uint32_t *const s_pair = reinterpret_cast<uint32_t *>(smem + Sh::OFF_PAIR);
+    uint32_t *const s_item = reinterpret_cast<uint32_t *>(smem + Sh::OFF_ITEM);
+    uint16_t *const s_up = reinterpret_cast<uint16_t *>(smem + Sh::OFF_UP);
+    uint8_t *const s_anc = smem + Sh::OFF_ANC;
     uint8_t *const parts = smem + Sh::OFF_B;
     const uint32_t base = smem_u32(smem);
-    const int tid = threadIdx.x - kRows - kStates, lane = tid & 31;
+    const int tid = threadIdx.x - kRows - kStates;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int n = a.fixed_len, nr = (n + 15) & ~15;
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
@@ -310,10 +337,12 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
         }
         attn::cp_async_commit();
     };
-    int kq = 0, trees = -1, grams = -1, entries = 0, levels = 0;
+    int kq = 0, trees = -1, grams = -1, entries = 0, deepest = 0;
     Items items(a);
     Item next = items.next(a);
     load_kq(next, 0);
+    __syncthreads();
+    tc_fence_after_sync();
 #pragma unroll 1
     for (int i = 0;;) {
         const Item it = next;
@@ -329,20 +358,10 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
         }
         if (!wait_all(kTables + (i & 1), i >> 1)) return false;
         if (it.new_kq && tid == 0) mbar_arrive(bar(kKqFull + kq));
-        // -- the ancestors' lists, the Gram products, |q|
+        // -- the Gram products, |q|, the paths' lists
         if (it.new_tree) {
-            levels = s.levels[z];
-            entries = s.level[z][levels];
-            if (tid < n) {
-                const uint64_t mask = s.mask[z][tid];
-                const int at = s.start[z][tid];
-                int r = 0;
-#pragma unroll 1
-                for (uint64_t up = mask; up; ++r, up &= up - 1) {
-                    const int j = __ffsll((long long)up) - 1;
-                    s_pair[at + r] = (uint32_t)(tid | j << 6 | r << 12 | s.start[z][j] << 18);
-                }
-            }
+            entries = s.entries[z];
+            deepest = s.deepest[z];
         }
         const bool two = more && !next.new_kq && entries <= kSecondHead;  // another V head of the QK head
         if (two) {
@@ -365,6 +384,29 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                     mma_commit(bar(kGram));
                 }
                 __syncwarp();
+            }
+            if (it.new_tree && tid < n && s.mask[z][tid]) {
+                const uint64_t mask = s.mask[z][tid], below = (1ull << tid) - 1;
+                const int d = __popcll(mask) - 1, at = s.start[z][tid];
+                int r = 0, from = 0;
+#pragma unroll 1
+                for (uint64_t up = mask; up; ++r, up &= up - 1) {
+                    const int j = __ffsll((long long)up) - 1;
+                    s_up[at + r] = s.start[z][j];
+                    s_anc[at + r] = (uint8_t)j;
+                }
+                // a node of level d has b entries in the join of blocks of b levels where d has bit b
+#pragma unroll 1
+                for (int k = 0; k < kJoins; ++k) {
+                    const uint64_t plane = s.plane[z][k];
+                    const int b = 1 << k, to = from + __popcll(plane & below) * b, r0 = d & -2 * b;
+                    if (d & b) {
+#pragma unroll 1
+                        for (int x = 0; x < b; ++x) s_item[to + x] = Entry::pack(at + r0 + x, tid, r0 + x, d);
+                    }
+                    from += __popcll(plane) * b;
+                }
+                s_item[from + __popcll(s.real[z] & below)] = Entry::pack(at + d, tid, d, d);
             }
             if (a.qk_norm && it.new_kq) {  // four lanes a row
 #pragma unroll 1
@@ -432,8 +474,9 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
             if (two) mbar_arrive(bar(kGateFull + (i1 & 3)));
         }
 #pragma unroll 1
-        for (int e = tid; e < entries; e += N) {
-            const int t = s_pair[e] & 63, j = s_pair[e] >> 6 & 63;
+        for (int x = tid; x < entries; x += N) {
+            const Entry it(s_item[x]);
+            const int e = it.e, t = it.t, j = s_anc[e];
             const float2 raw = s_np[e];
             const float kk = s.rk[t] * s.rk[j] * raw.x, qk = s.rq[t] * s.rk[j] * raw.y;
             {
@@ -450,53 +493,73 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
             mbar_arrive(bar(kTabFree + (i & 1)));
             if (two) mbar_arrive(bar(kTabFree + (i1 & 1)));
         }
-        // -- T and W: place r of a node with d ancestors, 2 lanes an entry, or 8 where paths are long
+        // -- T, joining blocks of b levels: entry (t, j), t in an odd block and j in the even one above it
 #pragma unroll 1
-        for (int d = 1; d < levels; ++d) {
-            const int e0 = s.level[z][d], e1 = s.level[z][d + 1];
-            const int log = d <= 8 ? 1 : 3, per = 32 >> log, part = lane & ((1 << log) - 1);
+        for (int k = 0, x0 = 0, x1; 1 << k <= deepest; ++k, x0 = x1) {
+            const int b = 1 << k;
+            x1 = x0 + __popcll(s.plane[z][k]) * b;
+            // Y = N + N T, over the rest of the even block; it lies where W will
 #pragma unroll 1
-            for (int e_warp = e0 + warp * per; e_warp < e1; e_warp += N / 32 * per) {  // whole warps
-                const int mine = e_warp + (lane >> log), e = min(mine, e1 - 1);
-                const uint32_t p = s_pair[e];
-                const int r = p >> 12 & 63, at = e - r;
-                float m0 = 0.f, w0 = 0.f, m1 = 0.f, w1 = 0.f;
-#pragma unroll 2
-                for (int x = r + 1 + part; x < d; x += 1 << log) {
-                    const float2 f = s_np[at + x];
-                    const int up = (s_pair[at + x] >> 18) + r;
-                    const float y = s_t[up];
-                    m0 = fmaf(f.x, y, m0);
-                    w0 = fmaf(f.y, y, w0);
-                    if (two) {
-                        const float2 g = s_np[at + x + kSecondHead];
-                        const float z = s_t[up + kSecondHead];
-                        m1 = fmaf(g.x, z, m1);
-                        w1 = fmaf(g.y, z, w1);
-                    }
+            for (int x = x0 + tid; x < x1; x += N) {
+                const Entry it(s_item[x]);
+                const int at = it.e - it.r, end = (it.r | b - 1) + 1;
+                float m0 = s_np[it.e].x, m1 = two ? s_np[it.e + kSecondHead].x : 0.f;
+#pragma unroll 4
+                for (int y = it.r + 1; y < end; ++y) {
+                    const int up = s_up[at + y] + it.r;
+                    m0 = fmaf(s_np[at + y].x, s_t[up], m0);
+                    if (two) m1 = fmaf(s_np[at + y + kSecondHead].x, s_t[up + kSecondHead], m1);
                 }
+                s_w[it.e] = m0;
+                if (two) s_w[it.e + kSecondHead] = m1;
+            }
+            named_sync(ID, N);
+            // T = -(Y + T Y), over the odd block's levels before
 #pragma unroll 1
-                for (int y = 1; y < 1 << log; y <<= 1) {
-                    m0 += __shfl_xor_sync(0xffffffffu, m0, y);
-                    w0 += __shfl_xor_sync(0xffffffffu, w0, y);
-                    m1 += __shfl_xor_sync(0xffffffffu, m1, y);
-                    w1 += __shfl_xor_sync(0xffffffffu, w1, y);
+            for (int x = x0 + tid; x < x1; x += N) {
+                const Entry it(s_item[x]);
+                const int at = it.e - it.r;
+                float m0 = s_w[it.e], m1 = two ? s_w[it.e + kSecondHead] : 0.f;
+#pragma unroll 4
+                for (int y = it.d & -b; y < it.d; ++y) {
+                    const int up = s_up[at + y] + it.r;
+                    m0 = fmaf(s_t[at + y], s_w[up], m0);
+                    if (two) m1 = fmaf(s_t[at + y + kSecondHead], s_w[up + kSecondHead], m1);
                 }
-                if (part == 0 && mine < e1 && r < d) {
-                    const float2 f = s_np[e];
-                    const float y = -(f.x + m0);
-                    s_t[e] = y;
-                    s_w[e] = fmaf(s.gate[i & 3][p & 63].w, y, f.y + w0);
-                    if (two) {
-                        const float2 g = s_np[e + kSecondHead];
-                        const float z = -(g.x + m1);
-                        s_t[e + kSecondHead] = z;
-                        s_w[e + kSecondHead] = fmaf(s.gate[i1 & 3][p & 63].w, z, g.y + w1);
-                    }
-                }
+                s_t[it.e] = -m0;
+                if (two) s_t[it.e + kSecondHead] = -m1;
             }
             named_sync(ID, N);
         }
+        // -- W = P T; at the node itself, where T - I is 0, its P
+#pragma unroll 1
+        for (int x = tid; x < entries; x += N) {
+            const Entry it(s_item[x]);
+            const int at = it.e - it.r;
+            const float p0 = s.gate[i & 3][it.t].w, p1 = s.gate[i1 & 3][it.t].w;
+            float w0 = p0, w1 = p1, y0 = 0.f, y1 = 0.f;
+            if (it.r < it.d) {
+                y0 = s_t[it.e];
+                w0 = fmaf(p0, y0, s_np[it.e].y);
+                if (two) {
+                    y1 = s_t[it.e + kSecondHead];
+                    w1 = fmaf(p1, y1, s_np[it.e + kSecondHead].y);
+                }
+#pragma unroll 4
+                for (int y = it.r + 1; y < it.d; ++y) {
+                    const int up = s_up[at + y] + it.r;
+                    w0 = fmaf(s_np[at + y].y, s_t[up], w0);
+                    if (two) w1 = fmaf(s_np[at + y + kSecondHead].y, s_t[up + kSecondHead], w1);
+                }
+            }
+            s_w[it.e] = w0;
+            s_t[it.e] = y0;
+            if (two) {
+                s_w[it.e + kSecondHead] = w1;
+                s_t[it.e + kSecondHead] = y1;
+            }
+        }
+        named_sync(ID, N);
         // -- pair by pair, their parts, once the pair before is done with its own (and so with K and Q before
         // this one's)
 #pragma unroll 1
@@ -512,9 +575,10 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
                 named_sync(ID, N);
             }
 #pragma unroll 1
-            for (int e = tid; e < entries; e += N) {  // T and W at the ancestors, W at the node itself
-                const int t = s_pair[e] & 63, j = s_pair[e] >> 6 & 63;
-                const float2 f = j == t ? make_float2(0.f, s.gate[i & 3][t].w) : make_float2(s_t[e + from], s_w[e + from]);
+            for (int x = tid; x < entries; x += N) {  // T and W at the ancestors, W at the node itself
+                const Entry it(s_item[x]);
+                const int t = it.t, j = s_anc[it.e];
+                const float2 f = make_float2(s_t[it.e + from], s_w[it.e + from]);
                 uint32_t part[3];
                 split3(f.x, f.y, part[0], part[1], part[2]);
                 uint8_t *const at = parts + sw128_offset(t, j >> 3) + (j & 7) * 2;
@@ -541,12 +605,15 @@ __device__ __forceinline__ bool products(const Args &a, uint8_t *smem, Tables &s
     using Sh = Shape;
     const bool issue = elect_one();
     const int nr = (a.fixed_len + 15) & ~15;
-    const uint32_t base = smem_u32(smem), tmem = s.tmem;
+    const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
     const uint32_t id = idesc_bf16_f32(128, 2 * nr, 0, 0);
     const uint64_t d_b = smem_desc_sw128(base + Sh::OFF_B, 0, 1024);
     int loads = -1;
     Items items(a);
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = s.tmem;
 #pragma unroll 1
     for (int i = 0; items.at < items.end; ++i) {
         const Item it = items.next(a);
@@ -600,19 +667,22 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int col = tid & 127, half = warp >> 2;
     const bool work = col - lane < D;
-    const uint32_t lanes = s.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
-    uint8_t *const ring = smem + Sh::OFF_S + half * kSlots * Sh::STAGE;
+    const int first_slot = half * ring_slots(0), slots = half ? ring_slots(1) : ring_slots(0);
+    uint8_t *const ring = smem + Sh::OFF_S + first_slot * Sh::STAGE;
     Items items(a);
     const int pairs = items.end - items.at, stages = pairs * PER;
     const float *const state = a.state + (int64_t)items.at * D * D;
     auto load = [&](int q) {  // this half's stage q of all
         if (q >= stages) return;
-        const int slot = q % kSlots;
-        mbar_arrive_expect_tx(bar(kSFull + half * kSlots + slot), BYTES);
+        const int slot = q % slots;
+        mbar_arrive_expect_tx(bar(kSFull + first_slot + slot), BYTES);
         bulk_load(smem_u32(ring + slot * Sh::STAGE), state + ((int64_t)q * 2 + half) * kStageRows * D, BYTES,
-                  bar(kSFull + half * kSlots + slot));
+                  bar(kSFull + first_slot + slot));
     };
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t lanes = s.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     auto load_values = [&](int64_t pair) {
         constexpr int CPR = D / 8, RPI = kStates / CPR;  // 16-byte chunks of a row, rows at a time
         const int n = a.fixed_len, c = tid % CPR;
@@ -623,7 +693,7 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
         attn::cp_async_arrive(bar(kVFull));
     };
     if (col == 0) {
-        for (int q = 0; q < kSlots; ++q) load(q);
+        for (int q = 0; q < slots; ++q) load(q);
     }
     __syncwarp();
     load_values(items.at);
@@ -633,15 +703,15 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
         tc_fence_after_sync();
 #pragma unroll 1
         for (int k = 0; k < PER; ++k, ++q) {
-            ok = ok && wait_warp(bar(kSFull + half * kSlots + q % kSlots), q / kSlots);
-            const float *const x = reinterpret_cast<const float *>(ring + q % kSlots * Sh::STAGE) + col;
+            ok = ok && wait_warp(bar(kSFull + first_slot + q % slots), q / slots);
+            const float *const x = reinterpret_cast<const float *>(ring + q % slots * Sh::STAGE) + col;
             float y[kStageRows];
             if (work) {
 #pragma unroll
                 for (int r = 0; r < kStageRows; ++r) y[r] = x[r * D];
             }
             if (pair::named_or(3 + half, kStates / 2, !ok)) return false;  // the stage is read
-            if (col == 0) load(q + kSlots);
+            if (col == 0) load(q + slots);
             __syncwarp();
             if (work) {
                 uint32_t part[3][kStageRows / 2];
@@ -656,10 +726,10 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kParts));
-        // the next pair's values, once the rows are done with this one's
-        if (i + 1 < pairs) {
-            if (!wait_warp(bar(kRParts), i)) return false;
-            load_values(items.at + i + 1);
+        // its values, once the rows are done with those of the pair before
+        if (i > 0) {
+            if (!wait_warp(bar(kRParts), i - 1)) return false;
+            load_values(items.at + i);
         }
     }
     attn::cp_async_wait<0>();
@@ -678,6 +748,8 @@ __device__ __forceinline__ bool rows(const Args &a, uint8_t *smem, Tables &s) {
     const int n = a.fixed_len, nr = (n + 15) & ~15;
     const int col = tid & 127, share = warp >> 2, t0 = share * KN;
     const bool work = col - lane < D;
+    __syncthreads();
+    tc_fence_after_sync();
     const uint32_t lanes = s.tmem + ((uint32_t)((warp & 3) * 32) << 16);
     auto bar = [&](int i) { return smem_u32(s.bar + i); };
     const int64_t step = (int64_t)a.h_v * D;
@@ -819,14 +891,16 @@ __global__ void __launch_bounds__(NT, 1) tree_tc_kernel(const __grid_constant__ 
     if (warp == 0) {
         tmem_alloc(smem_u32(&s.tmem), 512);
         tmem_relinquish();
-    }
-    if (threadIdx.x == 32) {
-        for (int i = 0; i < kBars; ++i) mbar_init(smem_u32(s.bar + i), i == kParts ? kStates / 32 : i == kXFree ? kRows / 32 : i == kVFull ? kStates : 1);
+    } else if (threadIdx.x == 32) {
+        for (int i = 0; i < kBars; ++i)
+            mbar_init(smem_u32(s.bar + i), i == kParts    ? kStates / 32
+                                           : i == kXFree  ? kRows / 32
+                                           : i == kVFull  ? kStates
+                                                          : 1);
         fence_mbar_init();
     }
     tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
+    // every role begins with a __syncthreads(), before which it may issue loads of its own
     bool ok;
     if (warp < kRows / 32)
         ok = rows<D, Out>(a, smem, s);
@@ -839,7 +913,7 @@ __global__ void __launch_bounds__(NT, 1) tree_tc_kernel(const __grid_constant__ 
     else
         ok = gates(a, err, s);
     if (!ok) {
-        // a wait gave up: leave the MMAs in flight time to end before their operands go
+        // a wait gave up: leave the MMAs and copies in flight time to end before their memory goes
         atomicCAS(err, 0, (int32_t)GDR_ERR_DEVICE_TIMEOUT);
         const long long t_end = clock64() + 4000000;
         while (clock64() < t_end) {}
