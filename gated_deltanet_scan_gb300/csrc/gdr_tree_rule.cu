@@ -132,7 +132,7 @@ __device__ __forceinline__ void load_path(Path &s, const Args &a, int seq, int h
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int j = lane + 32 * i;
-        sum[i] = j < n ? (double)a.g[(row0 + j) * a.h_v + h] : 0.0;
+        sum[i] = j < n ? tree::gate(a.g[(row0 + j) * a.h_v + h]) : 0.0;
     }
     const tree::Masks m = tree::masks<true>(parents, n, lane, sum);
     uint64_t path = tree::mask_of(m, last & 63);

@@ -31,6 +31,10 @@ struct Nodes {
 // doubles, kept as two floats each.
 __device__ __forceinline__ float decay(float2 t, float2 i) { return expf((t.x - i.x) + (t.y - i.y)); }
 
+// A gate as it enters the sums.  e^{-10^4} is zero, and so is every factor over such a gate; what is
+// lower (minus infinity, a state that is forgotten) would leave no difference of sums behind it.
+__device__ __forceinline__ double gate(float g) { return g < -1e4f ? -1e4 : (double)g; }
+
 // By one warp; `lead`: of the block that reports what is wrong with the tree.
 __device__ __forceinline__ void load_nodes(Nodes &s, const Args &a, int seq, int h, int32_t *err, bool lead) {
     const int lane = threadIdx.x & 31, n = a.fixed_len;
@@ -40,7 +44,7 @@ __device__ __forceinline__ void load_nodes(Nodes &s, const Args &a, int seq, int
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int j = lane + 32 * i;
-        sum[i] = j < n ? (double)a.g[(row0 + j) * a.h_v + h] : 0.0;
+        sum[i] = j < n ? gate(a.g[(row0 + j) * a.h_v + h]) : 0.0;
         b[i] = j < n ? a.beta[(row0 + j) * a.h_v + h] : 0.f;
     }
     const Masks m = masks<true>(load_parents(a.parents + row0, n, lane), n, lane, sum);

@@ -224,7 +224,7 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
                 to[x] = -2;
             }
             mask[x] = to[x] != -2 ? 1ull << j : 0;
-            sum[x] = to[x] != -2 ? (double)g[x] : 0.0;
+            sum[x] = to[x] != -2 ? tree::gate(g[x]) : 0.0;
         }
 #pragma unroll 1
         for (int step = 1; step < n; step <<= 1) {
