@@ -579,17 +579,19 @@ def _append(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv_lens, inv_fr
         ko = _rows(k_out, kv, dtype, dev, "k_out")
     i32, f32 = _attn_types[1], _attn_types[2]
     half = 0 if inv_freq is None else inv_freq.shape[0]
+    if parents is not None:
+        n_tok = _tree_rows(parents, n, T)
+        tree = _plain(parents, (n, n_tok), i32, dev, "parents")
+    elif cu_seqlens is not None:
+        cu_seqlens = _plain(cu_seqlens, (n + 1,), i32, dev, "cu_seqlens")
     rest = (qr, kr, vr, qo, ko, _cache(k_cache, v_cache, page_table, n, h_kv, d, dtype, dev),
             _plain(kv_lens, (n,), i32, dev, "kv_lens"),
             _plain(inv_freq, (half,), f32, dev, "inv_freq") if half else None, 2 * half, 1 if interleaved else 0,
             _attn_stream(stream, dev))
     if parents is not None:
-        n_tok = _tree_rows(parents, n, T)
-        st = (_lib or lib()).gdr_attn_append_tree(dims, n, n_tok, _plain(parents, (n, n_tok), i32, dev, "parents"),
-                                                  *rest)
+        st = (_lib or lib()).gdr_attn_append_tree(dims, n, n_tok, tree, *rest)
     else:
-        st = (_lib or lib()).gdr_attn_append(
-            dims, n, None if cu_seqlens is None else _plain(cu_seqlens, (n + 1,), i32, dev, "cu_seqlens"), T, *rest)
+        st = (_lib or lib()).gdr_attn_append(dims, n, cu_seqlens, T, *rest)
     if st != GDR_OK:
         raise GdrError(st, "gdr_attn_append" if parents is None else "gdr_attn_append_tree")
 
@@ -640,6 +642,8 @@ def _decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok, parents, scale, 
     dtype, dev = q.dtype, q.get_device()
     dims = _attn_dims(h_q, h_kv, d, dtype, scale)
     L = _lib or lib()
+    if parents is not None:
+        tree = _plain(parents, (n, n_tok), _attn_types[1], dev, "parents")
     if workspace is None:
         torch = _torch()
         size = L.gdr_attn_decode_workspace_bytes if parents is None else L.gdr_attn_decode_tree_workspace_bytes
@@ -659,7 +663,7 @@ def _decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok, parents, scale, 
     if parents is None:
         st = L.gdr_attn_decode(dims, n, n_tok, *rest)
     else:
-        st = L.gdr_attn_decode_tree(dims, n, n_tok, _plain(parents, (n, n_tok), _attn_types[1], dev, "parents"), *rest)
+        st = L.gdr_attn_decode_tree(dims, n, n_tok, tree, *rest)
     if st != GDR_OK:
         raise GdrError(st, "gdr_attn_decode" if parents is None else "gdr_attn_decode_tree")
 
