@@ -81,7 +81,7 @@ cudaError_t launch_prefill(const Args &a, cudaStream_t s);
 cudaError_t launch_prefill_short(const Args &a, bool after, cudaStream_t s);
 cudaError_t launch_decode(const Args &a, cudaStream_t s);
 cudaError_t launch_compact(const Args &a, cudaStream_t s);
-size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok);
+size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok, bool tree);
 
 }  // namespace attn
 }  // namespace gdr

@@ -133,7 +133,7 @@ gdr_status decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, cons
         (lse && !aligned(lse, 4)))
         return GDR_ERR_INVALID_ARG;
     if ((int64_t)n_seqs * n_tok > INT_MAX / dims->h_q) return GDR_ERR_UNSUPPORTED;
-    const size_t need = decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);
+    const size_t need = decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok, parents != nullptr);
     if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return GDR_ERR_INVALID_ARG;
     Args a = make_args(dims);
     a.n_seqs = n_seqs;
@@ -205,7 +205,7 @@ gdr_status gdr_attn_prefill(const gdr_attn_dims *dims, int32_t n_seqs, const int
 
 size_t gdr_attn_decode_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok) {
     if (check_dims(dims) != GDR_OK || n_seqs <= 0 || n_tok < 1 || n_tok > 16) return 0;
-    return decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);
+    return decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok, false);
 }
 
 gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const gdr_rows *q,
@@ -219,7 +219,7 @@ gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_
 
 size_t gdr_attn_decode_tree_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok) {
     if (check_dims(dims) != GDR_OK || n_seqs <= 0 || !nodes_ok(n_tok)) return 0;
-    return decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok);
+    return decode_workspace_bytes(dims->h_q, dims->h_kv, dims->d, n_seqs, n_tok, true);
 }
 
 gdr_status gdr_attn_decode_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,

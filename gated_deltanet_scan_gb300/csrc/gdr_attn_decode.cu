@@ -55,7 +55,7 @@ struct Shape {
 template <int D, bool F16, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_constant__ Args a) {
     using Sh = Shape<D>;
-    constexpr Spec sp = spec(false, D);
+    constexpr Spec sp = spec(kFew, D);
     constexpr int TT = kTile / 8;  // 8-token column tiles of S
     constexpr int KS = D / 16;   // inner steps of Q K^T
     constexpr int NT = D / 8;    // output column tiles
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, wk = tid >> 5, lane = tid & 31;
     const int rows = a.n_tok * a.group;
-    const Layout L = layout(rows, sp, D, a.n_seqs);
+    const Layout L = layout(rows, sp, D, (int64_t)a.n_seqs * a.h_kv);
     const Cut cut(s_line.place(a, sp, L.blocks_of_rows), kWarps);
     int me;
     Walk walk = s_line.walk(cut, wk, me);
@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 for (int n = 0; n < NT; ++n) acc[n][2 * i] = acc[n][2 * i + 1] = 0.f;
             }
         }
+        if (tile0 == 0 && lane == 0) leave_parts(a, sp, L, cut, me, s, h, tr.rb, seg0, tiles);
         if (tile0 == 0 && tile1 == tiles) {  // the worker saw the whole triple
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -413,120 +414,163 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
     }
 }
 
-// Joins the parts of every row that more than one worker saw, in the order of the
-// tokens, and writes the rows that see nothing.  With WPR > 1 a block is WPR warps on 64
-// columns of one row, which share the row's parts; else a warp is one row.
-template <int D, bool F16, int WPR, bool TREE>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, const bool wide) {
-    constexpr int V = WPR > 1 ? 2 : D / 32;  // columns per lane
-    constexpr int RPB = 8 / WPR;             // rows per block
-    __shared__ float2 s_acc[WPR > 1 ? WPR : 1][32];
-    __shared__ float2 s_ml[WPR];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % WPR;
-    const uint32_t row = blockIdx.x * RPB + warp / WPR;
-    const int word0 = WPR > 1 ? blockIdx.y * 32 + lane : lane;  // this lane's first pair of columns
-    if (row >= a.t_total * a.h_q) return;
-    const uint32_t t = row / (uint32_t)a.h_q;
-    const int hq = (int)(row - t * a.h_q);
-    const int s = (int)(t / (uint32_t)a.n_tok), j = (int)(t - (uint32_t)s * a.n_tok);
-    const int h = hq / a.group, g = hq - h * a.group;
-    const Spec sp = spec(wide, D);
-    const Layout L = layout(a.n_tok * a.group, sp, D, a.n_seqs);
-    const int r = j * a.group + g, rb = r / sp.block_rows, lr = r - rb * sp.block_rows;
-    uint32_t *const dst = reinterpret_cast<uint32_t *>(a.o.p + t * a.o.ts + hq * a.o.hs);
-    const bool write_lse = a.lse && lane == 0 && blockIdx.y == 0;
-    const int64_t len = length_of(a, s);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (len == 0) {
-        if (w == 0) {
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) dst[word0 + 32 * e] = 0u;
-            if (write_lse) a.lse[row] = -CUDART_INF_F;
-        }
-        return;
-    }
-    const int64_t tiles = (len + sp.tile - 1) / sp.tile;
-    const int64_t *const line = reinterpret_cast<const int64_t *>(a.ws);
-    const int64_t seg0 = line[s] + ((int64_t)h * L.blocks_of_rows + rb) * (tiles + sp.lead);
-    const Cut cut(line[a.n_seqs], sp.workers);
-    const int w0 = cut.part_of(seg0 + sp.lead), w1 = cut.part_of(seg0 + sp.lead + tiles - 1);
-    if (w0 == w1) return;
-
-    const float2 *const ml = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.ml);
-    const float2 *const po = reinterpret_cast<const float2 *>(static_cast<const uint8_t *>(a.ws) + L.o);
-    // a worker's part is its first where its own start is not before the triple's: so
-    // all parts but perhaps the first one's
-    // all but the last worker's part are joined within their blocks: the parts are those of the
-    // first such worker of every block, and the last worker's
-    const int per_block = cut.per_block, b0 = w0 / per_block;
-    const int n_parts = (w1 - 1) / per_block - b0 + 2;
-    const int64_t row0 = cut.start(w0) >= seg0 ? 0 : L.part_rows;
-    auto part_row = [&](int i) {
-        const int wk = i == 0 ? w0 : i == n_parts - 1 ? w1 : (b0 + i) * per_block;
-        return (int64_t)wk * 2 * L.part_rows + (i == 0 ? row0 : 0) + lr;
-    };
-    float2 acc[V / 2];
-    float m = -CUDART_INF_F, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) acc[e] = make_float2(0.f, 0.f);
-    constexpr int U = 4;  // parts in flight
-#pragma unroll 1
-    for (int i = w; i < n_parts; i += WPR * U) {
-        float2 x[U][V / 2], v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t pr = part_row(min(i + u * WPR, n_parts - 1));
-            v[u] = __ldcg(ml + pr);
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) x[u][e] = __ldcg(po + pr * (D / 2) + word0 + 32 * e);
-        }
+// What parts of a row add up to, in the order they are added, some at a time.
+struct Sum {
+    float m, l;
+    float4 o;
+    __device__ __forceinline__ Sum() : l(0.f), o{0.f, 0.f, 0.f, 0.f} { m = -CUDART_INF_F; }
+    // Parts (m, l, x), of which `some` are there.
+    template <int U>
+    __device__ __forceinline__ void add(const float2 (&ml)[U], const float4 (&x)[U], int some) {
         float top = m;
 #pragma unroll
-        for (int u = 0; u < U; ++u) top = fmaxf(top, i + u * WPR < n_parts ? v[u].x : top);
+        for (int u = 0; u < U; ++u) top = fmaxf(top, u < some ? ml[u].x : top);
         const float ref = top == -CUDART_INF_F ? 0.f : top;
         const float c0 = m == top ? 1.f : tc::fast_exp2(m - ref);
         m = top;
         l *= c0;
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-            acc[e].x *= c0;
-            acc[e].y *= c0;
-        }
+        o = make_float4(o.x * c0, o.y * c0, o.z * c0, o.w * c0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i + u * WPR >= n_parts) break;
-            const float c = tc::fast_exp2(v[u].x - ref);
-            l += c * v[u].y;
+            if (u >= some) break;
+            const float c = tc::fast_exp2(ml[u].x - ref);
+            l += c * ml[u].y;
+            o.x += c * x[u].x;
+            o.y += c * x[u].y;
+            o.z += c * x[u].z;
+            o.w += c * x[u].w;
+        }
+    }
+};
+template <bool F16>
+__device__ __forceinline__ uint2 pack4(float4 o, float inv) {
+    return make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
+}
+
+constexpr int kJoinThreads = 256;
+template <int D>
+constexpr int kJoinRows = 4 * kJoinThreads / D;  // a block's
+constexpr int kAtOnce = 4;  // parts added at once
+
+// What the joins' threads would else work out, each for itself.
+struct Join {
+    const Parts *triples;
+    const float2 *ml;
+    const float4 *o;
+    int part_rows, block_rows, blocks_of_rows;
+    int groups;  // blocks of threads of a triple
+};
+struct Joined {  // where a row's result goes
+    const Args &a;
+    int s, h;
+    template <bool F16, bool TREE>
+    __device__ __forceinline__ void put(int r, int c, const Sum &sum, int64_t len, bool with_lse) const {
+        const int j = r / a.group, hq = h * a.group + r - j * a.group;
+        const int64_t t = (int64_t)s * a.n_tok + j;
+        const bool sees = len > 0 && (TREE || len - a.n_tok + j + 1 > 0);  // a tree's rows that are no nodes have l = 0
+        reinterpret_cast<uint2 *>(a.o.p + t * a.o.ts + hq * a.o.hs)[c] =
+            pack4<F16>(sum.o, sees ? inverse_sum(sum.l) : 0.f);
+        if (a.lse && with_lse) a.lse[t * a.h_q + hq] = sees ? kLn2 * (sum.m + log2f(sum.l)) : -CUDART_INF_F;
+    }
+};
+
+// Joins the parts of every row that more than one worker saw, in the order of the tokens, and
+// writes the rows that see nothing.  A block takes the 1024 / D next rows of a triple, a thread four
+// columns of a row.  Only parts that are there are loaded (most triples of a batch have two).  Bound by the
+// chain of loads, lengths, parts' places, parts, of each wave of blocks.  32 trees of 32 rows, d = 256,
+// whole: 84.7 us; two and four rows a thread 83.8 and 84.2, but a long sequence's rows then join one
+// after another (30 parts each: 61 us against 29); more blocks an SM, by fewer registers: 87.
+template <int D, bool F16, bool TREE>
+__global__ void __launch_bounds__(kJoinThreads, 4)
+    join_kernel(const __grid_constant__ Args a, const __grid_constant__ Join w) {
+    constexpr int TPR = D / 4;
+    const uint32_t triple = blockIdx.x / (uint32_t)w.groups, group = blockIdx.x - triple * w.groups;
+    const uint32_t head = triple / (uint32_t)w.blocks_of_rows;
+    Joined to{a, (int)(head / (uint32_t)a.h_kv), 0};
+    to.h = (int)(head - (uint32_t)to.s * a.h_kv);
+    const int r0 = (int)(triple - head * w.blocks_of_rows) * w.block_rows, c = threadIdx.x % TPR;
+    const int lr = (int)group * kJoinRows<D> + threadIdx.x / TPR;
+    const bool live = lr < min(w.part_rows, a.n_tok * a.group - r0);
+    const int64_t len = length_of(a, to.s);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!live) return;
+    if (len == 0) {
+        to.put<F16, TREE>(r0 + lr, c, Sum(), 0, c == 0);
+        return;
+    }
+    const Parts parts = w.triples[triple];
+    if (parts.count == 1) return;
+    const float2 *const ml = w.ml + lr;
+    const float4 *const po = w.o + (int64_t)lr * TPR + c;
+    Sum sum;
+#pragma unroll 1
+    for (int i = 0; i < parts.count; i += 2 * kAtOnce) {
+        float2 v[2][kAtOnce];
+        float4 y[2][kAtOnce];
 #pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-                acc[e].x += c * x[u][e].x;
-                acc[e].y += c * x[u][e].y;
+        for (int u = 0; u < 2 * kAtOnce; ++u) {
+            if (i + u < parts.count) {
+                const int64_t at = parts.row(i + u, w.part_rows);
+                v[u / kAtOnce][u % kAtOnce] = __ldcg(ml + at);
+                y[u / kAtOnce][u % kAtOnce] = __ldcg(po + at * TPR);
             }
         }
+        sum.add<kAtOnce>(v[0], y[0], parts.count - i);
+        if (i + kAtOnce < parts.count) sum.add<kAtOnce>(v[1], y[1], parts.count - i - kAtOnce);
     }
-    if constexpr (WPR > 1) {
-        s_acc[w][lane] = acc[0];
-        if (lane == 0) s_ml[w] = make_float2(m, l);
-        __syncthreads();  // the block is one row: its warps come here together
-        if (w != 0) return;
+    to.put<F16, TREE>(r0 + lr, c, sum, len, c == 0);
+}
+
+// The same where rows have many parts (few triples for the blocks): eight warps share the parts of
+// one row's 128 columns.
+template <int D, bool F16, bool TREE>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_many_kernel(const __grid_constant__ Args a, const __grid_constant__ Join j) {
+    constexpr int W = kJoinThreads / 32;
+    __shared__ float4 s_o[W][32];
+    __shared__ float2 s_ml[W];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.y * 32 + lane;
+    const bool mine = c < D / 4;  // d = 64: half of the lanes
+    const uint32_t rows = (uint32_t)a.n_tok * a.group, head = blockIdx.x / rows;
+    const int r = (int)(blockIdx.x - head * rows), rb = r / j.block_rows, lr = r - rb * j.block_rows;
+    Joined to{a, (int)(head / (uint32_t)a.h_kv), 0};
+    to.h = (int)(head - (uint32_t)to.s * a.h_kv);
+    const int64_t len = length_of(a, to.s);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (len == 0) {
+        if (w == 0 && mine) to.put<F16, TREE>(r, c, Sum(), 0, c == 0);
+        return;
+    }
+    const Parts parts = j.triples[(int64_t)head * j.blocks_of_rows + rb];
+    if (parts.count == 1) return;
+    Sum sum;
+#pragma unroll 1
+    for (int i = w; i < parts.count; i += W * kAtOnce) {
+        float2 v[kAtOnce];
+        float4 y[kAtOnce];
 #pragma unroll
-        for (int i = 1; i < WPR; ++i) m = fmaxf(m, s_ml[i].x);
-        const float ref = m == -CUDART_INF_F ? 0.f : m;
-        l = 0.f;
-        acc[0] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < WPR; ++i) {
-            const float c = tc::fast_exp2(s_ml[i].x - ref);
-            l += c * s_ml[i].y;
-            acc[0].x += c * s_acc[i][lane].x;
-            acc[0].y += c * s_acc[i][lane].y;
+        for (int u = 0; u < kAtOnce; ++u) {
+            if (u > 0 && i + u * W >= parts.count) break;
+            const int64_t at = parts.row(i + u * W, j.part_rows) + lr;
+            v[u] = __ldcg(j.ml + at);
+            y[u] = __ldcg(j.o + at * (D / 4) + (mine ? c : 0));
         }
+        sum.add<kAtOnce>(v, y, (parts.count - i + W - 1) / W);
     }
-    const bool sees = TREE || len - a.n_tok + j + 1 > 0;  // a tree's rows that are no nodes have l = 0
-    const float inv = sees ? inverse_sum(l) : 0.f;
+    s_o[w][lane] = sum.o;
+    if (lane == 0) s_ml[w] = make_float2(sum.m, sum.l);
+    __syncthreads();  // the block is one row: its warps come here together
+    if (w != 0) return;
+    float2 v[W];
+    float4 y[W];
 #pragma unroll
-    for (int e = 0; e < V / 2; ++e) dst[word0 + 32 * e] = pack2<F16>(acc[e].x * inv, acc[e].y * inv);
-    if (write_lse) a.lse[row] = sees ? kLn2 * (m + log2f(l)) : -CUDART_INF_F;
+    for (int i = 0; i < W; ++i) {
+        v[i] = s_ml[i];
+        y[i] = s_o[i][lane];
+    }
+    Sum all;
+    all.add<W>(v, y, W);
+    if (mine) to.put<F16, TREE>(r, c, all, len, c == 0);
 }
 
 template <int D, bool F16, bool TREE>
@@ -540,25 +584,29 @@ cudaError_t launch_warps(const Args &a, cudaStream_t s) {
 
 template <int D, bool F16, bool TREE>
 cudaError_t launch_as(const Args &a, cudaStream_t s) {
-    const bool wide = is_wide(a.n_tok * a.group);
-    const cudaError_t e = wide ? launch_decode_wide(a, s) : launch_warps<D, F16, TREE>(a, s);
+    const int rows = a.n_tok * a.group;
+    const Kind kind = kind_of(rows, D, TREE);
+    const cudaError_t e = kind != kFew ? launch_decode_wide(a, s) : launch_warps<D, F16, TREE>(a, s);
     if (e != cudaSuccess) return e;
-    // The join: 8 warps on every 64 columns of a row where a row has many parts (few
-    // triples for the blocks), else a warp per row.
-    const int64_t rows = a.t_total * a.h_q;
-    const Layout L = layout(a.n_tok * a.group, spec(wide, D), D, a.n_seqs);
-    const bool many = kBlocks >= (int64_t)16 * a.n_seqs * a.h_kv * L.blocks_of_rows;
+    const Spec sp = spec(kind, D);
+    const Layout L = layout(rows, sp, D, (int64_t)a.n_seqs * a.h_kv);
+    const int64_t triples = (int64_t)a.n_seqs * a.h_kv * L.blocks_of_rows;
+    const bool many = kBlocks >= 16 * triples;
+    char *const ws = static_cast<char *>(a.ws);
+    const Join w = {reinterpret_cast<const Parts *>(ws), reinterpret_cast<const float2 *>(ws + L.ml),
+                    reinterpret_cast<const float4 *>(ws + L.o), L.part_rows, sp.block_rows, L.blocks_of_rows,
+                    (L.part_rows + kJoinRows<D> - 1) / kJoinRows<D>};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = many ? dim3((unsigned)rows, D / 64) : dim3((unsigned)((rows + 7) / 8));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = many ? dim3((unsigned)(a.t_total * a.h_q), (D + 127) / 128) : dim3((unsigned)(triples * w.groups));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 8, TREE>, a, wide)
-                : cudaLaunchKernelEx(&cfg, join_kernel<D, F16, 1, TREE>, a, wide);
+    return many ? cudaLaunchKernelEx(&cfg, join_many_kernel<D, F16, TREE>, a, w)
+                : cudaLaunchKernelEx(&cfg, join_kernel<D, F16, TREE>, a, w);
 }
 
 template <int D, bool F16>
@@ -568,9 +616,9 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 
 }  // namespace
 
-size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok) {
+size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok, bool tree) {
     const int rows = n_tok * (h_q / h_kv);
-    return layout(rows, spec(is_wide(rows), d), d, n_seqs).total;
+    return layout(rows, spec(kind_of(rows, d, tree), d), d, (int64_t)n_seqs * h_kv).total;
 }
 
 cudaError_t launch_decode(const Args &a, cudaStream_t s) {

@@ -26,25 +26,40 @@ struct Spec {
 // the first (25 sequences of d = 256 42.3, 39.4, 37.3 us; 64 sequences 120.8, 120.8, 121.6; 96 of
 // d = 128 119.5, 119.7, 121.5); 3, 4 and 6 for the second (16 draft tokens 39.8, 38.5, 38.6; 50
 // sequences of d = 128 47.2, 47.6, 47.8; 52 of d = 64 30.3, 29.9, 30.5).
-__host__ __device__ constexpr Spec spec(bool wide, int d) {
-    return wide ? Spec{128, 64, 1, 4} : Spec{kWarpRows, 16, 8, 1024 / d};
+enum Kind { kFew = 0, kWide = 1, kPaired = 2 };
+__host__ __device__ constexpr Spec spec(Kind kind, int d) {
+    return kind == kFew ? Spec{kWarpRows, 16, 8, 1024 / d} : Spec{kind == kPaired ? 256 : 128, 64, 1, 4};
 }
-inline bool is_wide(int rows) { return rows > kWarpRows; }
+// Trees of more than 128 rows of up to 128 values: two blocks of rows read the keys and values together.
+// (The O of two blocks of d = 256 would leave no TMEM for their S.)
+__host__ __device__ inline Kind kind_of(int rows, int d, bool tree) {
+    return rows <= kWarpRows ? kFew : tree && rows > 128 && d <= 128 ? kPaired : kWide;
+}
 
-// Workspace: place of every sequence's first triple on the line ([n_seqs + 1], the last
-// one the total), then per worker two parts (its first and its last, cut, triple): per
-// row m and l, then O.
+// Where the parts of a triple's rows are, for the join.
+struct __align__(16) Parts {
+    int w0, w1;     // first and last worker
+    int count;      // parts to join; 1: the worker wrote the rows themselves
+    int packed;     // whether the first part is its worker's second; w0 in its block; workers of a block
+    __device__ __forceinline__ int64_t row(int i, int part_rows) const {  // of part i's first row
+        const int wk = i == 0 ? w0 : i == count - 1 ? w1 : w0 - (packed >> 1 & 15) + i * (packed >> 5);
+        return (int64_t)(2 * wk + (i == 0 ? packed & 1 : 0)) * part_rows;
+    }
+};
+
+// Workspace: per triple its parts' places, then per worker two parts (its first and its last, cut,
+// triple): per row m and l, then O.
 struct Layout {
     int blocks_of_rows, part_rows, workers;
     size_t ml, o, total;
 };
-__host__ __device__ inline Layout layout(int rows, const Spec &sp, int d, int n_seqs) {
+__host__ __device__ inline Layout layout(int rows, const Spec &sp, int d, int64_t heads) {  // of all sequences
     Layout L;
     L.blocks_of_rows = (rows + sp.block_rows - 1) / sp.block_rows;
     L.part_rows = rows < sp.block_rows ? rows : sp.block_rows;
     L.workers = kBlocks * sp.workers;
     const size_t parts = (size_t)L.workers * 2 * L.part_rows;
-    L.ml = ((size_t)(n_seqs + 1) * 8 + 15) / 16 * 16;
+    L.ml = (size_t)heads * L.blocks_of_rows * sizeof(Parts);
     L.o = L.ml + (parts * 8 + 15) / 16 * 16;
     L.total = L.o + parts * d * 4;
     return L;
@@ -76,6 +91,20 @@ struct Cut {
         return (int)(place < longer ? quotient(place, each + 1) : rest + quotient(place - longer, each));
     }
 };
+
+// Left by one thread of the worker of a triple's first tiles.  A worker's part is its first where its own
+// start is not before the triple's: so all parts but perhaps the first one's.  All but the last worker's
+// part are joined within their blocks: the parts are those of the first such worker of every block, and
+// the last worker's.  (Found by the join's threads, each for its row, it took them 500 instructions.)
+__device__ __forceinline__ void leave_parts(const Args &a, const Spec &sp, const Layout &L, const Cut &cut, int me, int s,
+                                            int h, int rb, int64_t seg0, int64_t tiles) {
+    Parts p;
+    p.w0 = me;
+    p.w1 = cut.part_of(seg0 + sp.lead + tiles - 1);
+    p.count = p.w1 == me ? 1 : (p.w1 - 1) / cut.per_block - me / cut.per_block + 2;
+    p.packed = (cut.start(me) >= seg0 ? 0 : 1) | me % cut.per_block << 1 | cut.per_block << 5;
+    static_cast<Parts *>(a.ws)[((int64_t)s * a.h_kv + h) * L.blocks_of_rows + rb] = p;
+}
 
 // The part of one triple that falls to a worker.
 struct Triple {
@@ -119,7 +148,7 @@ struct Walk {
 // The line's scan by a whole block of THREADS: THREADS sequences at a time, an exclusive
 // sum of their places; the first pass finds the total, the second where each of the
 // block's WORKERS starts (one pass of sums does both where there are up to THREADS
-// sequences).  Block 0 leaves the sequences' places in the workspace for the join.
+// sequences).
 template <int THREADS, int WORKERS>
 struct Line {
     int64_t scan[THREADS + 1];
@@ -130,7 +159,6 @@ struct Line {
     __device__ __forceinline__ int64_t place(const Args &a, const Spec &sp, int blocks_of_rows) {
         const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
         const int64_t per_seq = (int64_t)a.h_kv * blocks_of_rows;
-        int64_t *const line = reinterpret_cast<int64_t *>(a.ws);
         int64_t total = 0;
         const int chunks = (a.n_seqs + THREADS - 1) / THREADS;
         if (tid < WORKERS) seq[tid] = -1;
@@ -180,10 +208,6 @@ struct Line {
                             seq[tid] = s0 + lo;
                             base[tid] = scan[lo];
                         }
-                    }
-                    if (blockIdx.x == 0) {
-                        if (tid < m) line[s0 + tid] = scan[tid];
-                        if (tid == 0 && c == chunks - 1) line[a.n_seqs] = sum;
                     }
                 }
             }

@@ -14,10 +14,17 @@
 //            has; the copies themselves report a stage full when they land, and the MMA warp
 //            orders them before its reads (reported by the copying threads two stages from
 //            the ring's end instead, 60% of the stages sat landed and unreported: 47 us).
-//   Q        three warps, one triple ahead of need where Q's place is free.
+//   Q        three warps, a triple ahead of need where a place for Q is free.
 //   MMAs     one warp: S of the next tile before P V of this one.
-//   P, O     one warpgroup, a row per thread: P of every tile, and O at a triple's end.
+//   P, O     a warpgroup per block of rows, a row per thread: P of every tile, and O at a triple's end.
 // All roles run over the triples' ends, so the loads never stop.
+//
+// Trees of more than 128 rows (64 nodes, 4 query heads of a key/value head) would read their keys and
+// values, and pay for their loads, once per block of rows.  Up to d = 128 TMEM holds O and two S tiles of
+// two blocks, so a worker takes both (B = 2), the products block by block, so that one's P is made
+// while the other's run: 16 trees of 64 nodes, contexts up to 16,384, d = 128, 32 / 8 heads: 124 us with a
+// block a worker, 113 with two, 107 with two places for Q.  The tensor pipe and the shared memory it reads
+// (Q again for every 64 tokens) bound it: 1,770 clocks a tile, of which HBM would need 1,370.
 //
 // P is rounded to 16 bits.  A second product with what bf16's rounding left, as in
 // gdr_attn_decode.cu, would halve o's squared error and take 10% longer (16 draft tokens of 32
@@ -38,48 +45,52 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
 constexpr int kRows = 128, kTile = 64;
-constexpr uint32_t kColsS = 256;  // TMEM: O at 0, S tiles at 256 and 320
+constexpr uint32_t kColsS = 256;  // TMEM: O at 0 (and 128), S tiles at 256 and 320 (and 384 and 448)
 
-template <int D>
+// B: blocks of rows that a worker takes at once.
+template <int D, int B>
 struct Shape {
+    static_assert(B == 1 || (B == 2 && D <= 128), "O's columns");
+    static constexpr int THREADS = B * 128 + 256;
     static constexpr uint32_t Q_BLOCK = kRows * 128;  // 64 columns
     static constexpr uint32_t Q_BYTES = Q_BLOCK * (D / 64);
     static constexpr uint32_t BOX = kTile * 128;      // 64 tokens, 64 columns
     static constexpr uint32_t STAGE = BOX * (D / 64);
-    static constexpr int STAGES = D == 256 ? 5 : 8;
+    static constexpr int STAGES = D == 256 ? 5 : D == 128 && B == 2 ? 6 : 8;
+    static constexpr int QS = D == 256 ? 1 : 2;  // places for Q, where shared memory has them
     // Rows of a tile that one of the four loading warps copies: 32, two warps for K and two for
     // V, or 16 of either, so that a stage's copies are all on their way sooner.  32 pays waits,
     // arrivals and page ids of a stage half as often, 16 suits few stages: 32 against 16, d = 64
     // 32.3 / 38.1 us, d = 128 63.8 / 70.7, d = 256 42.2 / 38.7.
     static constexpr int LOAD_ROWS = D == 256 ? 16 : 32;
-    static constexpr uint32_t OFF_RING = Q_BYTES;
+    static constexpr uint32_t OFF_RING = QS * B * Q_BYTES;
     static constexpr uint32_t OFF_BAR = OFF_RING + STAGES * STAGE;
-    static constexpr uint32_t OFF_WORDS = OFF_BAR + 8 * 32;  // TMEM address, flag
+    static constexpr uint32_t OFF_WORDS = OFF_BAR + 8 * 34;  // TMEM address, flag
     static constexpr uint32_t BYTES = OFF_WORDS + 16;
     // at least 116 KiB, so that one block has the SM (and its TMEM) to itself
     static constexpr uint32_t SMEM = BYTES < 116 * 1024 ? 116 * 1024 : BYTES;
 };
 enum Bar {
-    kQFull = 0,
-    kQEmpty = 1,
-    kKvFull = 2,               // [stages]
+    kQFull = 0,                // [places]
+    kQEmpty = 2,               // [places]
+    kKvFull = 4,               // [stages]
     kKvEmpty = kKvFull + 8,    // [stages]
-    kSFull = kKvEmpty + 8,     // [2]
-    kPFull = kSFull + 2,       // [2]
-    kPvDone = kPFull + 2,      // [2]
-    kODone = kPvDone + 2,
+    kSFull = kKvEmpty + 8,     // [B][2]
+    kPFull = kSFull + 4,       // [B][2]
+    kPvDone = kPFull + 4,      // [B][2]
+    kODone = kPvDone + 4,
     kOFree = kODone + 1,
     kBars = kOFree + 1,
 };
-static_assert(kBars <= 32, "barrier words");
+static_assert(kBars <= 34, "barrier words");
 
-template <int D, bool F16, bool TREE>
-__global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant__ Args a) {
-    using Sh = Shape<D>;
-    constexpr Spec sp = spec(true, D);
-    static_assert(sp.tile == kTile && sp.block_rows == kRows, "the line's units");
+template <int D, bool F16, bool TREE, int B>
+__global__ void __launch_bounds__((Shape<D, B>::THREADS), 1) wide_kernel(const __grid_constant__ Args a) {
+    using Sh = Shape<D, B>;
+    constexpr int kThreads = Sh::THREADS, kLoads = 4 * B, kMmas = kLoads + 4;  // the roles' first warps
+    constexpr Spec sp = spec(B == 2 ? kPaired : kWide, D);
+    static_assert(sp.tile == kTile && sp.block_rows == B * kRows, "the line's units");
     constexpr int N = Sh::STAGES, CPR = D / 8;
     extern __shared__ __align__(1024) uint8_t smem[];
     // the line's scan comes before the ring's first use
@@ -94,28 +105,30 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
-        mbar_init(bar(kQFull), 96);
-        mbar_init(bar(kQEmpty), 1);
+        for (int i = 0; i < Sh::QS; ++i) {
+            mbar_init(bar(kQFull + i), 96);
+            mbar_init(bar(kQEmpty + i), 1);
+        }
         for (int i = 0; i < N; ++i) {
             mbar_init(bar(kKvFull + i), Sh::LOAD_ROWS == 32 ? 64 : 128);
             mbar_init(bar(kKvEmpty + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2 * B; ++i) {
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), 4);
             mbar_init(bar(kPvDone + i), 1);
         }
         mbar_init(bar(kODone), 1);
-        mbar_init(bar(kOFree), 4);
+        mbar_init(bar(kOFree), 4 * B);
         *s_found = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == kMmas) {
         tmem_alloc(smem_u32(s_tmem), 512);
         tmem_relinquish();
     }
     const int rows = a.n_tok * a.group;
-    const Layout L = layout(rows, sp, D, a.n_seqs);
+    const Layout L = layout(rows, sp, D, (int64_t)a.n_seqs * a.h_kv);
     const Cut cut(s_line.place(a, sp, L.blocks_of_rows), 1);
     int me;
     Walk walk = s_line.walk(cut, 0, me);
@@ -135,10 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     auto value_stage = [](uint32_t g) { return 2 * g + 2; };
     Triple t;
 
-    if (warp < 4) {
+    if (warp < kLoads) {
         // ---- P and O; a thread is a row
-        const int row = tid;
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        const int row = tid, blk = warp >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + blk * 128;
+        const uint32_t s_lanes = lanes + kColsS;  // block 1's S tiles are 128 columns behind block 0's, too
         const float sc = softmax_scale(a.scale);
         float2 *const ml_parts = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + L.ml);
         float *const o_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + L.o);
@@ -146,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         tree::Masks nodes;
         int nodes_of = -1;  // the sequence whose tree they are
         for (int it = 0; ok && walk.next(a, sp, L.blocks_of_rows, t); ++it) {
-            const int r = t.rb * kRows + row;
+            const int r = t.rb * sp.block_rows + row;
             const bool live = r < rows;
             const int j = r / a.group, hq = t.h * a.group + r - j * a.group;
             const int tree0 = t.len - a.n_tok;  // a tree's first slot
@@ -163,14 +177,14 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                 if (!live) mask = 0;
             }
             const bool any = TREE ? mask != 0 : seen > 0;  // the row sees something
-            const bool work = t.rb * kRows + warp * 32 < rows;  // some row of the warp is live
+            const bool work = t.rb * sp.block_rows + warp * 32 < rows;  // some row of the warp is live
             float m = -CUDART_INF_F, l = 0.f;
             for (int tile = t.tile0; tile < t.tile1; ++tile, ++g) {
                 const int st = g & 1;
-                if (!wait(kSFull + st, g >> 1)) break;
+                if (!wait(kSFull + 2 * blk + st, g >> 1)) break;
                 if (work) {
                     tc_fence_after_sync();
-                    const uint32_t s_at = lanes + kColsS + st * kTile;
+                    const uint32_t s_at = s_lanes + st * kTile;
                     uint32_t x[64];
                     pair::tmem_load32_start(s_at, x);
                     pair::tmem_load32_start(s_at + 32, x + 32);
@@ -204,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     const float ref = m == -CUDART_INF_F ? 0.f : m;  // nothing visible yet: p = 2^-inf
                     const float f = m_old == m ? 1.f : fast_exp2(m_old - ref);
                     if (tile > t.tile0 && __any_sync(0xffffffffu, f != 1.f)) {
-                        if (!wait(kPvDone + ((g - 1) & 1), (g - 1) >> 1)) break;
+                        if (!wait(kPvDone + 2 * blk + ((g - 1) & 1), (g - 1) >> 1)) break;
                         tc_fence_after_sync();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
                     tc_fence_before_sync();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kPFull + st));
+                if (lane == 0) mbar_arrive(bar(kPFull + 2 * blk + st));
             }
             if (!ok || !wait(kODone, it)) break;
             tc_fence_after_sync();
@@ -247,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             }
             // O, whole or as a part
             const bool whole = t.tile0 == 0 && t.tile1 == t.tiles;
+            if (row == 0 && t.tile0 == 0) leave_parts(a, sp, L, cut, me, t.s, t.h, t.rb, t.seg0, t.tiles);
             const bool patch = *s_found != 0;
             const int64_t tok = (int64_t)t.s * a.n_tok + j;
             const int64_t part = ((int64_t)me * 2 + (cut.start(me) >= t.seg0 ? 0 : 1)) * L.part_rows + row;
@@ -343,10 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
             }
             __syncwarp();
         }
-    } else if (warp < 8) {
+    } else if (warp < kMmas) {
         // ---- K and V: a warp's lanes hold the offsets of its rows of a tile
         constexpr int R = Sh::LOAD_ROWS;
-        const int w = (warp - 4) & (64 / R - 1);
+        const int w = (warp - kLoads) & (64 / R - 1);
         auto clean = [&](uint32_t st) {  // the values this thread copied, landed
             auto piece = [&](int x) {
                 const int row = w * R + x % (R / 4) * 4 + (lane >> 3);
@@ -442,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         };
         if constexpr (R == 32) {
             Tiles x = begin();
-            while (load(x, warp >= 6)) {}
+            while (load(x, warp >= kLoads + 2)) {}
         } else {
             Tiles k = begin(), v = begin();
             load(k, false);
@@ -452,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         }
         cp_async_commit();
         cp_async_wait<0>();
-    } else if (warp == 8) {
+    } else if (warp == kMmas) {
         // ---- MMAs: the whole warp walks the tiles, one elected lane issues
         const bool issue = elect_one();
         const uint32_t negate = a.scale < 0.f ? 1u << 13 : 0u;  // x = |sc| (-Q) K^T
@@ -467,71 +482,102 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
         kt.tile0 = kt.tile1 = 0;
         int k_tile = 0, k_it = -1;
         bool k_more = true;
-        auto score = [&] {
+        // S of the next tile: whether there is one (Q and its keys are waited for), the product for a
+        // block of rows, and the step to the tile after.
+        auto keys = [&] {
             if (k_tile == kt.tile1) {
                 k_more = k_walk.next(a, sp, L.blocks_of_rows, kt);
-                if (!k_more || !wait(kQFull, ++k_it)) return;
+                if (!k_more) return false;
+                ++k_it;
+                if (!wait(kQFull + k_it % Sh::QS, k_it / Sh::QS)) return false;
                 k_tile = kt.tile0;
             }
-            const uint32_t i = key_stage(gs), st = i % N;
-            if (!wait(kKvFull + st, i / N)) return;
+            const uint32_t i = key_stage(gs);
+            if (!wait(kKvFull + i % N, i / N)) return false;
             fence_proxy_async_smem();  // copies by other threads, before the MMAs read them
             tc_fence_after_sync();
+            return true;
+        };
+        auto score = [&](int b) {
+            const uint32_t st = key_stage(gs) % N;
+            const uint64_t qd = q0 + ((k_it % Sh::QS * (B * Sh::Q_BYTES) + b * Sh::Q_BYTES) >> 4);
             const uint64_t kd = k0 + (uint64_t)(st * (Sh::STAGE >> 4));
-            const uint32_t d = tmem + kColsS + (gs & 1) * kTile;
+            const uint32_t d = tmem + kColsS + b * 128 + (gs & 1) * kTile;
             if (issue) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_bf16(d, q0 + (((k >> 2) * Sh::Q_BLOCK + (k & 3) * 32) >> 4),
+                    mma_bf16(d, qd + (((k >> 2) * Sh::Q_BLOCK + (k & 3) * 32) >> 4),
                              kd + (((k >> 2) * Sh::BOX + (k & 3) * 32) >> 4), id_s, k > 0);
-                mma_commit(bar(kKvEmpty + st));
-                mma_commit(bar(kSFull + (gs & 1)));
-                if (k_tile == kt.tile1 - 1) mma_commit(bar(kQEmpty));
+                mma_commit(bar(kSFull + 2 * b + (gs & 1)));
+                if (b == B - 1) {
+                    mma_commit(bar(kKvEmpty + st));
+                    if (k_tile == kt.tile1 - 1) mma_commit(bar(kQEmpty + k_it % Sh::QS));
+                }
             }
             __syncwarp();
+        };
+        auto scored = [&] {
             ++k_tile;
             ++gs;
         };
 #pragma unroll 1
-        for (int x = 0; x < 2 && k_more && ok; ++x) score();
+        for (int x = 0; x < 2 && keys(); ++x) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) score(b);
+            scored();
+        }
         for (int it = 0; ok && walk.next(a, sp, L.blocks_of_rows, t); ++it) {
             for (int tile = t.tile0; ok && tile < t.tile1; ++tile) {
-                if (g > 0 && k_more) score();  // over P of the tile before, whose P V is issued
+                const bool ahead = g > 0 && k_more && keys();
                 if (!ok) break;
                 const uint32_t i = value_stage(g), st = i % N;
-                if (tile == t.tile0 && it > 0 && !wait(kOFree, it - 1)) break;
-                if (!wait(kKvFull + st, i / N) || !wait(kPFull + (g & 1), g >> 1)) break;
-                fence_proxy_async_smem();
-                tc_fence_after_sync();
                 const uint64_t vd = v0 + (uint64_t)(st * (Sh::STAGE >> 4));
                 const uint32_t p = tmem + kColsS + (g & 1) * kTile;
-                if (issue) {
+                // block by block, so that one's P is made while the other's products run
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        pair::mma_ts_one(tmem, p + k * 8, vd + ((k * 16 * 128) >> 4), id_o, tile > t.tile0 || k > 0);
-                    mma_commit(bar(kKvEmpty + st));
-                    mma_commit(bar(kPvDone + (g & 1)));
-                    if (tile == t.tile1 - 1) mma_commit(bar(kODone));
+                for (int b = 0; b < B; ++b) {
+                    if (ahead) score(b);  // over P of the tile before, whose P V is issued
+                    if (b == 0) {
+                        if (tile == t.tile0 && it > 0 && !wait(kOFree, it - 1)) break;
+                        if (!wait(kKvFull + st, i / N)) break;
+                    }
+                    if (!wait(kPFull + 2 * b + (g & 1), g >> 1)) break;
+                    fence_proxy_async_smem();
+                    tc_fence_after_sync();
+                    if (issue) {
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            pair::mma_ts_one(tmem + b * 128, p + b * 128 + k * 8, vd + ((k * 16 * 128) >> 4), id_o,
+                                             tile > t.tile0 || k > 0);
+                        mma_commit(bar(kPvDone + 2 * b + (g & 1)));
+                        if (b == B - 1) {
+                            mma_commit(bar(kKvEmpty + st));
+                            if (tile == t.tile1 - 1) mma_commit(bar(kODone));
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
+                if (ahead) scored();
                 ++g;
             }
         }
     } else {
         // ---- Q: row r of the block at its place in the operand tile; rows past the last are left
-        const int w = warp - 9;
+        const int w = warp - kMmas - 1;
         for (int it = 0; ok && walk.next(a, sp, L.blocks_of_rows, t); ++it) {
-            if (it > 0 && !wait(kQEmpty, it - 1)) break;
-            const int live = min(kRows, rows - t.rb * kRows);
+            const int z = it % Sh::QS;
+            if (it >= Sh::QS && !wait(kQEmpty + z, it / Sh::QS - 1)) break;
+            const int live = min(sp.block_rows, rows - t.rb * sp.block_rows);
             constexpr int RPI = 32 / CPR;
             for (int row = w * RPI + lane / CPR; row < live; row += 3 * RPI) {
-                const int r = t.rb * kRows + row, j = r / a.group;
+                const int r = t.rb * sp.block_rows + row, j = r / a.group;
                 const int64_t tok = (int64_t)t.s * a.n_tok + j;
                 const int chunk = lane % CPR;
-                cp_async16(base + (chunk >> 3) * Sh::Q_BLOCK + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
+                cp_async16(base + (z * B + (row >> 7)) * Sh::Q_BYTES + (chunk >> 3) * Sh::Q_BLOCK + (row & 127) * 128 + (((chunk & 7) ^ (row & 7)) << 4),
                            a.q.p + tok * a.q.ts + (int64_t)(t.h * a.group + r - j * a.group) * a.q.hs + chunk * 8, 16u);
             }
-            cp_async_arrive(bar(kQFull));
+            cp_async_arrive(bar(kQFull + z));
             __syncwarp();
         }
         cp_async_commit();
@@ -547,21 +593,26 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == kMmas) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool F16, bool TREE>
+template <int D, bool F16, bool TREE, int B>
 cudaError_t launch_as(const Args &a, cudaStream_t s) {
     static SmemOptIn opt_in;
-    const cudaError_t e = opt_in.set(reinterpret_cast<const void *>(wide_kernel<D, F16, TREE>), (int)Shape<D>::SMEM);
+    using Sh = Shape<D, B>;
+    const cudaError_t e = opt_in.set(reinterpret_cast<const void *>(wide_kernel<D, F16, TREE, B>), (int)Sh::SMEM);
     if (e != cudaSuccess) return e;
-    wide_kernel<D, F16, TREE><<<kBlocks, kThreads, Shape<D>::SMEM, s>>>(a);
+    wide_kernel<D, F16, TREE, B><<<kBlocks, Sh::THREADS, Sh::SMEM, s>>>(a);
     return cudaGetLastError();
 }
 
 template <int D, bool F16>
 cudaError_t launch(const Args &a, cudaStream_t s) {
-    return a.parents ? launch_as<D, F16, true>(a, s) : launch_as<D, F16, false>(a, s);
+    if (!a.parents) return launch_as<D, F16, false, 1>(a, s);
+    if constexpr (D <= 128) {
+        if (kind_of(a.n_tok * a.group, D, true) == kPaired) return launch_as<D, F16, true, 2>(a, s);
+    }
+    return launch_as<D, F16, true, 1>(a, s);
 }
 
 }  // namespace
