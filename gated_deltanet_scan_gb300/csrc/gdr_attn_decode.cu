@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
         };
 #pragma unroll
         for (int i = 0; i < Sh::SLOTS - 1; ++i) issue(i);
+        if (tile0 == 0 && lane == 0) leave_parts(a, sp, L, cut, me, s, h, tr.rb, seg0, tiles);
 
         // Q: rows lane / 4 and + 8 of this warp's 16, as MMA fragments
         uint32_t qf[KS][4];
@@ -347,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const __grid_consta
                 for (int n = 0; n < NT; ++n) acc[n][2 * i] = acc[n][2 * i + 1] = 0.f;
             }
         }
-        if (tile0 == 0 && lane == 0) leave_parts(a, sp, L, cut, me, s, h, tr.rb, seg0, tiles);
         if (tile0 == 0 && tile1 == tiles) {  // the worker saw the whole triple
 #pragma unroll
             for (int i = 0; i < 2; ++i) {

@@ -261,7 +261,6 @@ __global__ void __launch_bounds__((Shape<D, B>::THREADS), 1) wide_kernel(const _
             }
             // O, whole or as a part
             const bool whole = t.tile0 == 0 && t.tile1 == t.tiles;
-            if (row == 0 && t.tile0 == 0) leave_parts(a, sp, L, cut, me, t.s, t.h, t.rb, t.seg0, t.tiles);
             const bool patch = *s_found != 0;
             const int64_t tok = (int64_t)t.s * a.n_tok + j;
             const int64_t part = ((int64_t)me * 2 + (cut.start(me) >= t.seg0 ? 0 : 1)) * L.part_rows + row;
@@ -578,6 +577,7 @@ __global__ void __launch_bounds__((Shape<D, B>::THREADS), 1) wide_kernel(const _
                            a.q.p + tok * a.q.ts + (int64_t)(t.h * a.group + r - j * a.group) * a.q.hs + chunk * 8, 16u);
             }
             cp_async_arrive(bar(kQFull + z));
+            if (w == 0 && lane == 0 && t.tile0 == 0) leave_parts(a, sp, L, cut, me, t.s, t.h, t.rb, t.seg0, t.tiles);
             __syncwarp();
         }
         cp_async_commit();
