@@ -9,6 +9,7 @@ if the compiled library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -463,11 +464,15 @@ def _attn_init():
     return _attn_types
 
 
+_attn_struct = functools.lru_cache(maxsize=256)(gdr_attn_dims)  # read only; making one takes 0.4 us
+_rule_struct = functools.lru_cache(maxsize=256)(gdr_dims)
+
+
 def _attn_dims(h_q: int, h_kv: int, d: int, dtype, scale) -> gdr_attn_dims:
     code = (_attn_types or _attn_init())[0].get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    return gdr_attn_dims(h_q, h_kv, d, code, d ** -0.5 if scale is None else scale)
+    return _attn_struct(h_q, h_kv, d, code, d ** -0.5 if scale is None else scale)
 
 
 def _attn_stream(stream, dev: int):
@@ -736,6 +741,14 @@ def gdr_attn_commit_tree(k_cache, v_cache, page_table, kv_lens, parents, last, l
         raise GdrError(st, "gdr_attn_commit_tree")
 
 
+def _tree_dims(h_qk: int, h_v: int, d_k: int, d_v: int, dtype, out_dtype, scale, flags: int) -> gdr_dims:
+    codes = (_attn_types or _attn_init())[0]
+    io, out = codes.get(dtype), codes.get(out_dtype)
+    if io in (None, GDR_F16) or out in (None, GDR_F16):
+        raise TypeError(f"unsupported dtypes {dtype} and {out_dtype}")
+    return _rule_struct(h_qk, h_v, d_k, d_v, 64, io, out, scale, flags)
+
+
 def gdr_verify_tree(q, k, v, g, beta, state, o, parents, *, deltas=None, scale: float = 1.0, qk_l2norm: bool = False,
                     beta_logits: bool = False, stream=None) -> None:
     """The rule along every path of each sequence's tree of up to 64 drafted tokens, from its
@@ -743,13 +756,13 @@ def gdr_verify_tree(q, k, v, g, beta, state, o, parents, *, deltas=None, scale: 
     [n, n_tok]; q, k [n * n_tok, H_qk, d]; v, o [n * n_tok, H_v, d]; g, beta [n * n_tok, H_v]
     fp32; state [n, H_v, d, d] fp32; ``deltas`` (fp32, shaped like v) receives the corrections
     that gdr_verify_tree_commit takes."""
-    qs, vs = tuple(q.shape), tuple(v.shape)
-    if len(qs) != 3 or len(vs) != 3 or state.dim() != 4:
+    qs, vs, ss = q.shape, v.shape, state.shape
+    if len(qs) != 3 or len(vs) != 3 or len(ss) != 4:
         raise ValueError("q must be [T, H_qk, d], v [T, H_v, d] and state [n, H_v, d, d]")
-    n, T, hv, d = state.shape[0], qs[0], vs[1], qs[2]
-    dims = make_dims(q, v, o, 64, scale, flags_of(qk_l2norm, beta_logits))
+    (T, h_qk, d), hv, n = qs, vs[1], ss[0]
+    dims = _tree_dims(h_qk, hv, d, vs[2], q.dtype, o.dtype, scale, flags_of(qk_l2norm, beta_logits))
     dev = q.get_device()
-    types = _attn_types or _attn_init()
+    types = _attn_types
     n_tok = _tree_rows(parents, n, T)
     f32 = types[2]
     st = (_lib or lib()).gdr_verify_tree(
@@ -768,16 +781,17 @@ def gdr_verify_tree_commit(k, g, deltas, state, parents, last, *, qk_l2norm: boo
     as gdr_verify_tree took and wrote them."""
     if k.dim() != 3 or state.dim() != 4:
         raise ValueError("k must be [T, H_qk, d] and state [n, H_v, d, d]")
-    (n, hv, d, _), T = state.shape, k.shape[0]
-    dims = gdr_dims(h_qk=k.shape[1], h_v=hv, d_k=d, d_v=d, chunk=64, in_dtype=_dtype_code(k), out_dtype=GDR_F32,
-                    scale=1.0, flags=flags_of(qk_l2norm))
+    n, hv, d, _ = state.shape
+    T, h_qk, _ = ks = k.shape
+    dims = _tree_dims(h_qk, hv, d, d, k.dtype, state.dtype, 1.0, flags_of(qk_l2norm))
     dev = state.get_device()
-    types = _attn_types or _attn_init()
     n_tok = _tree_rows(parents, n, T)
-    i32, f32 = types[1], types[2]
+    i32, f32 = _attn_types[1], _attn_types[2]
+    if ks[2] != d:
+        raise ValueError(f"k must have shape {(T, h_qk, d)}")
     st = (_lib or lib()).gdr_verify_tree_commit(
         dims, n, n_tok, _plain(parents, (n, n_tok), i32, dev, "parents"), _plain(last, (n,), i32, dev, "last"),
-        _plain(k, (T, k.shape[1], d), k.dtype, dev, "k"), _plain(g, (T, hv), f32, dev, "g"),
+        _plain(k, ks, k.dtype, dev, "k"), _plain(g, (T, hv), f32, dev, "g"),
         _plain(deltas, (T, hv, d), f32, dev, "deltas"), _plain(state, (n, hv, d, d), f32, dev, "state"),
         _attn_stream(stream, dev))
     if st != GDR_OK:
