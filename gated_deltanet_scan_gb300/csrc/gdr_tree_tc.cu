@@ -234,13 +234,23 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int from = to[x] & 31;
-                const bool high = to[x] & 32;
-                const uint64_t u0 = tree::shfl64(mask[0], from), u1 = tree::shfl64(mask[1], from);
-                const int t0 = __shfl_sync(0xffffffffu, to[0], from), t1 = __shfl_sync(0xffffffffu, to[1], from);
-                const double s0 = __shfl_sync(0xffffffffu, sum[0], from), s1 = __shfl_sync(0xffffffffu, sum[1], from);
-                up[x] = high ? u1 : u0;
-                next[x] = high ? t1 : t0;
-                more[x] = high ? s1 : s0;
+                up[x] = tree::shfl64(mask[0], from);
+                next[x] = __shfl_sync(0xffffffffu, to[0], from);
+                more[x] = __shfl_sync(0xffffffffu, sum[0], from);
+                if (n <= 32) {  // the upper rows are no nodes
+                    up[1] = 0;
+                    next[1] = -2;
+                    more[1] = 0.0;
+                    break;
+                }
+                const uint64_t u1 = tree::shfl64(mask[1], from);
+                const int t1 = __shfl_sync(0xffffffffu, to[1], from);
+                const double s1 = __shfl_sync(0xffffffffu, sum[1], from);
+                if (to[x] & 32) {
+                    up[x] = u1;
+                    next[x] = t1;
+                    more[x] = s1;
+                }
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -291,7 +301,7 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
             }
         }
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; 32 * x < n; ++x) {
             const int j = lane + 32 * x;
             const double y = x ? sum[1] : sum[0];
             const float hi = (float)y, lo = (float)(y - (double)hi), logit = x ? b[1] : b[0];
@@ -355,10 +365,26 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
             attn::cp_async_wait<0>();
             fence_proxy_async_smem();
             tc_fence_before_sync();
+            named_sync(ID, N);
+        }
+        // -- the Gram products, before what the MMAs' warp makes of K and Q; then |q| and the paths' lists
+        ++grams;
+        if (warp == 4) {
+            tc_fence_after_sync();
+            if (elect_one()) {
+                const uint64_t at = smem_desc_sw128(base + kq * Sh::KQ, 0, 1024);
+                const uint32_t id = idesc_bf16_f32(128, nr, 0, 0);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t x = at + (((k >> 2) * Sh::BLOCK + (k & 3) * 32) >> 4);
+                    mma_bf16(s.tmem + Sh::GRAM, x, x, id, k > 0);
+                }
+                mma_commit(bar(kGram));
+                if (it.new_kq) mbar_arrive(bar(kKqFull + kq));
+            }
+            __syncwarp();
         }
         if (!wait_all(kTables + (i & 1), i >> 1)) return false;
-        if (it.new_kq && tid == 0) mbar_arrive(bar(kKqFull + kq));
-        // -- the Gram products, |q|, the paths' lists
         if (it.new_tree) {
             entries = s.entries[z];
             deepest = s.deepest[z];
@@ -370,21 +396,6 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
             if (more) next = items.next(a);
         }
         {
-            ++grams;
-            if (warp == 4) {
-                tc_fence_after_sync();
-                if (elect_one()) {
-                    const uint64_t at = smem_desc_sw128(base + kq * Sh::KQ, 0, 1024);
-                    const uint32_t id = idesc_bf16_f32(128, nr, 0, 0);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t x = at + (((k >> 2) * Sh::BLOCK + (k & 3) * 32) >> 4);
-                        mma_bf16(s.tmem + Sh::GRAM, x, x, id, k > 0);
-                    }
-                    mma_commit(bar(kGram));
-                }
-                __syncwarp();
-            }
             if (it.new_tree && tid < n && s.mask[z][tid]) {
                 const uint64_t mask = s.mask[z][tid], below = (1ull << tid) - 1;
                 const int d = __popcll(mask) - 1, at = s.start[z][tid];
@@ -480,12 +491,14 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
             const float2 raw = s_np[e];
             const float kk = s.rk[t] * s.rk[j] * raw.x, qk = s.rq[t] * s.rk[j] * raw.y;
             {
-                const float y = tree::decay(s.sum[i & 1][t], s.sum[i & 1][j]);
-                s_np[e] = make_float2(s.beta[i & 1][t] * y * kk, y * qk);
+                const float y = tree::decay(s.sum[i & 1][t], s.sum[i & 1][j]), nji = s.beta[i & 1][t] * y * kk;
+                s_np[e] = make_float2(nji, y * qk);
+                s_t[e] = -nji;  // T of blocks of two levels
             }
             if (two) {
-                const float y = tree::decay(s.sum[i1 & 1][t], s.sum[i1 & 1][j]);
-                s_np[e + kSecondHead] = make_float2(s.beta[i1 & 1][t] * y * kk, y * qk);
+                const float y = tree::decay(s.sum[i1 & 1][t], s.sum[i1 & 1][j]), nji = s.beta[i1 & 1][t] * y * kk;
+                s_np[e + kSecondHead] = make_float2(nji, y * qk);
+                s_t[e + kSecondHead] = -nji;
             }
         }
         named_sync(ID, N);
@@ -495,7 +508,7 @@ __device__ __forceinline__ bool factors(const Args &a, uint8_t *smem, Tables &s)
         }
         // -- T, joining blocks of b levels: entry (t, j), t in an odd block and j in the even one above it
 #pragma unroll 1
-        for (int k = 0, x0 = 0, x1; 1 << k <= deepest; ++k, x0 = x1) {
+        for (int k = 1, x0 = __popcll(s.plane[z][0]), x1; 1 << k <= deepest; ++k, x0 = x1) {
             const int b = 1 << k;
             x1 = x0 + __popcll(s.plane[z][k]) * b;
             // Y = N + N T, over the rest of the even block; it lies where W will

@@ -80,12 +80,11 @@ class Model:
             tree += new_tree
             if new_kq:
                 self.kq[kq] = i
-            if two:
-                yield from self.wait("factors", "Tables", (i + 1) & 1, (i + 1) >> 1)
-            yield from self.wait("factors", "Tables", i & 1, i >> 1)
-            if new_kq:
                 self.arrive("KqFull", kq)
                 yield
+            yield from self.wait("factors", "Tables", i & 1, i >> 1)
+            if two:
+                yield from self.wait("factors", "Tables", (i + 1) & 1, (i + 1) >> 1)
             both = (i, i + 1) if two else (i,)
             for j in both:
                 check(self.tree[tree & 3] == tree and self.tables[j & 1] == j, "tables", j)
