@@ -22,8 +22,8 @@
 // may be the inputs.
 //
 // Of a tree of drafted tokens a node's position is that of its path's end, and its slot the
-// row's: the warp finds the tree's masks (gdr_tree.cuh) once per sequence, while its first
-// vectors are on their way, and |A_j| - 1 is the node's depth.
+// row's: the warp walks up from its row while its first vectors are on their way (32 trees of 64 rows,
+// 48 heads of 128: 16.4 us; with the masks of whole trees, which other kernels need, 16.8).
 #include "gdr_attn_common.cuh"
 #include "gdr_internal.h"
 #include "gdr_tree.cuh"
@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
     const int even = (int)(a.t_total / a.n_seqs);  // tokens per sequence without cu
     int s = a.cu ? find_seq_warp(a.cu, a.n_seqs, first, lane) : (int)(first / even);
 
-    tree::Masks nodes;
-    int nodes_of = -1;  // the sequence whose tree they are
+    int2 parents = make_int2(-2, -2);
+    int parents_of = -1;  // the sequence whose they are
 
     for (int64_t t = first; t < last; ++t) {
         int64_t t0, t1;
@@ -128,12 +128,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(PAIR))
         int64_t pos = known ? (int64_t)a.kv_lens[s] - (t1 - t) : -1;
         int64_t turned_by = pos;  // the position the angles go by
         if constexpr (TREE) {
-            if (s != nodes_of) {
-                nodes_of = s;
-                nodes = tree::masks(a.parents + t0, even, lane);
-                if (nodes.bad) record_invalid(a.err);
+            if (s != parents_of) {
+                parents_of = s;
+                parents = tree::load_parents(a.parents + t0, even, lane);
             }
-            const int j = (int)(t - t0), depth = __popcll(tree::mask_of(nodes, j)) - 1;
+            const int j = (int)(t - t0);
+            bool bad;
+            const int depth = tree::depth_of(parents, j, bad);
+            if (bad) record_invalid(a.err);
             known = depth >= 0;  // the row is a node
             turned_by = pos - j + depth;
             if (pos < j) pos = -1;  // fewer tokens than the tree has rows

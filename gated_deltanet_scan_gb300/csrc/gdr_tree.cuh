@@ -118,6 +118,24 @@ __device__ __forceinline__ uint64_t mask_of(const Masks &m, int j) {
     return j & 32 ? a1 : a0;
 }
 
+// Ancestors of row j, or -1 where it is no node; `bad`: one of them, or the row, has a parent that cannot be
+// one.  By a whole warp, a step per ancestor.
+__device__ __forceinline__ int depth_of(int2 parents, int j, bool &bad) {
+    int at = j;
+    bad = false;
+#pragma unroll 1
+    for (int depth = 0;; ++depth) {
+        const int lo = __shfl_sync(0xffffffffu, parents.x, at & 31), hi = __shfl_sync(0xffffffffu, parents.y, at & 31);
+        const int up = at & 32 ? hi : lo;
+        if (up == -1) return depth;
+        if (up < 0 || up >= at) {
+            bad = up != -2 || depth > 0;
+            return -1;
+        }
+        at = up;
+    }
+}
+
 // 32 bits of what a node sees from slot `rel` on, relative to the tree's first slot: all
 // before the tree, then its mask.
 __device__ __forceinline__ uint32_t sees32(uint64_t mask, int rel) {
