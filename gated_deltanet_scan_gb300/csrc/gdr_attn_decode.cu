@@ -503,6 +503,16 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     const float2 *const ml = w.ml + lr;
     const float4 *const po = w.o + (int64_t)lr * TPR + c;
     Sum sum;
+    if (parts.count == 2) {  // kept short: a batch's rows mostly come here
+        const int64_t at0 = parts.row(0, w.part_rows), at1 = (int64_t)parts.w1 * (2 * w.part_rows);
+        const float2 v0 = __ldcg(ml + at0), v1 = __ldcg(ml + at1);
+        const float4 y0 = __ldcg(po + at0 * TPR), y1 = __ldcg(po + at1 * TPR);
+        const float2 v[2] = {v0, v1};
+        const float4 y[2] = {y0, y1};
+        sum.add<2>(v, y, 2);
+        to.put<F16, TREE>(r0 + lr, c, sum, len, c == 0);
+        return;
+    }
 #pragma unroll 1
     for (int i = 0; i < parts.count; i += 2 * kAtOnce) {
         float2 v[2][kAtOnce];
