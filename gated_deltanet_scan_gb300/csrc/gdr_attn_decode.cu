@@ -458,14 +458,15 @@ struct Join {
     const float2 *ml;
     const float4 *o;
     int part_rows, block_rows, blocks_of_rows;
-    int groups;  // blocks of threads of a triple
+    uint32_t per_group;  // 2^32 / group, rounded up (rows and groups are below 2^14)
 };
 struct Joined {  // where a row's result goes
     const Args &a;
+    uint32_t per_group;
     int s, h;
     template <bool F16, bool TREE>
     __device__ __forceinline__ void put(int r, int c, const Sum &sum, int64_t len, bool with_lse) const {
-        const int j = r / a.group, hq = h * a.group + r - j * a.group;
+        const int j = a.group == 1 ? r : (int)__umulhi((uint32_t)r, per_group), hq = h * a.group + r - j * a.group;
         const int64_t t = (int64_t)s * a.n_tok + j;
         const bool sees = len > 0 && (TREE || len - a.n_tok + j + 1 > 0);  // a tree's rows that are no nodes have l = 0
         reinterpret_cast<uint2 *>(a.o.p + t * a.o.ts + hq * a.o.hs)[c] =
@@ -484,12 +485,11 @@ template <int D, bool F16, bool TREE>
 __global__ void __launch_bounds__(kJoinThreads, 4)
     join_kernel(const __grid_constant__ Args a, const __grid_constant__ Join w) {
     constexpr int TPR = D / 4;
-    const uint32_t triple = blockIdx.x / (uint32_t)w.groups, group = blockIdx.x - triple * w.groups;
-    const uint32_t head = triple / (uint32_t)w.blocks_of_rows;
-    Joined to{a, (int)(head / (uint32_t)a.h_kv), 0};
+    const uint32_t head = blockIdx.x, triple = head * w.blocks_of_rows + blockIdx.y;
+    Joined to{a, w.per_group, (int)(head / (uint32_t)a.h_kv), 0};
     to.h = (int)(head - (uint32_t)to.s * a.h_kv);
-    const int r0 = (int)(triple - head * w.blocks_of_rows) * w.block_rows, c = threadIdx.x % TPR;
-    const int lr = (int)group * kJoinRows<D> + threadIdx.x / TPR;
+    const int r0 = (int)blockIdx.y * w.block_rows, c = threadIdx.x % TPR;
+    const int lr = (int)blockIdx.z * kJoinRows<D> + threadIdx.x / TPR;
     const bool live = lr < min(w.part_rows, a.n_tok * a.group - r0);
     const int64_t len = length_of(a, to.s);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     const bool mine = c < D / 4;  // d = 64: half of the lanes
     const uint32_t rows = (uint32_t)a.n_tok * a.group, head = blockIdx.x / rows;
     const int r = (int)(blockIdx.x - head * rows), rb = r / j.block_rows, lr = r - rb * j.block_rows;
-    Joined to{a, (int)(head / (uint32_t)a.h_kv), 0};
+    Joined to{a, j.per_group, (int)(head / (uint32_t)a.h_kv), 0};
     to.h = (int)(head - (uint32_t)to.s * a.h_kv);
     const int64_t len = length_of(a, to.s);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -605,12 +605,12 @@ cudaError_t launch_as(const Args &a, cudaStream_t s) {
     char *const ws = static_cast<char *>(a.ws);
     const Join w = {reinterpret_cast<const Parts *>(ws), reinterpret_cast<const float2 *>(ws + L.ml),
                     reinterpret_cast<const float4 *>(ws + L.o), L.part_rows, sp.block_rows, L.blocks_of_rows,
-                    (L.part_rows + kJoinRows<D> - 1) / kJoinRows<D>};
+                    (uint32_t)((0x100000000ull + a.group - 1) / a.group)};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = many ? dim3((unsigned)(a.t_total * a.h_q), (D + 127) / 128) : dim3((unsigned)(triples * w.groups));
+    cfg.gridDim = many ? dim3((unsigned)(a.t_total * a.h_q), (D + 127) / 128) : dim3((unsigned)(a.n_seqs * a.h_kv), L.blocks_of_rows, (L.part_rows + kJoinRows<D> - 1) / kJoinRows<D>);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = &attr;
