@@ -5,10 +5,17 @@
 // verify block, which leaves the state after its last token and a snapshot, moves three
 // times that): a tree has no last token.
 //
-// tree_kernel is the plain one, in fp32 on CUDA cores: a block of 256 threads has one
-// (sequence, V head, 32 columns), its queries and keys as floats and its 32 columns of the
-// state in shared memory, a column per lane.
+// tree_kernel, for fp32 inputs, is fp32 on CUDA cores: a block has a (sequence, V head), or 32 of its columns
+// where there are few, with its queries and keys in shared memory, in whose rows R and e^G S_0^T q take their
+// places.  A warp has 16 columns and every so many rows, a thread four columns of an eighth of the state's
+// rows in registers, so that a 16-byte load of a key serves 16 FMAs; the eight sums of a thread go round to one
+// a lane in seven shuffles.  N and P are made for the paths' entries, and nodes come after their ancestors, so
+// two lanes of a column go through the rows in order, four at once, with no barrier of the block.
+// Bound by issue slots (64% of them; the FMAs of S_0^T [K; Q] alone would take 16,400 clocks a pair of 64
+// nodes and d = 128, of 70,000): 64 trees of 64 nodes, 32 heads: 506 us, 16 of them 152, chains 274, 8 of 41
+// nodes 51, one of 24 15.4 (level by level, 32 columns a block: 2,300, 599, 1,432, 137 and 16.5).
 #include "gdr_attn.h"
+#include "gdr_attn_mma.cuh"
 #include "gdr_attn_ptx.cuh"
 #include "gdr_tree_rule.cuh"
 #include "tc_ptx.cuh"
@@ -17,43 +24,58 @@ namespace gdr {
 namespace {
 
 constexpr int NT = 256;
-constexpr int BV = 32;
 
-template <int D>
-struct Shape {
-    static constexpr int LDK = D + 4;
-    // floats, for n rows: state, K, Q, corrections, outputs, N and P
-    static size_t bytes(int n) { return 4 * (size_t)(D * BV + 2 * n * LDK + 2 * n * BV + 2 * n * n); }
-};
+// For n rows: K (then R, then U), Q (then e^G S_0^T q), N and P, the paths (of at most n (n + 1) / 2 entries).
+size_t tree_bytes(int n, int d) { return 4 * (size_t)(2 * n * d) + 9 * (size_t)(n * (n + 1) / 2); }
 
-template <int D>
-__global__ void __launch_bounds__(NT) tree_kernel(const __grid_constant__ Args a, int32_t *err) {
-    using Sh = Shape<D>;
+// p[0] = the sum over lanes of p[i], where i is made of the lane's bits from UNIT on: in 2 HALF - 1 shuffles.
+template <int HALF, int UNIT>
+__device__ __forceinline__ void sums_to_lanes(float *p, int lane) {
+#pragma unroll
+    for (int m = HALF; m > 0; m >>= 1) {
+        const bool upper = lane & UNIT * m;
+#pragma unroll
+        for (int e = 0; e < m; ++e)
+            p[e] = (upper ? p[m + e] : p[e]) + __shfl_xor_sync(0xffffffffu, upper ? p[e] : p[m + e], UNIT * m);
+    }
+}
+
+// C: columns of a block.
+template <int D, int C>
+__global__ void __launch_bounds__(NT, D == 128 ? 2 : D == 64 ? 3 : 4) tree_kernel(const __grid_constant__ Args a, int32_t *err) {
+    constexpr int W = NT / 32, Q4 = D / 4;
+    constexpr int AT_ONCE = 4, GROUPS = W / (C / 16), STEP = AT_ONCE * GROUPS;  // rows of a warp's step, of the block's
     extern __shared__ __align__(16) float smem[];
     __shared__ tree::Nodes s;
     const int n = a.fixed_len;
-    float *const sS = smem, *const sK = sS + D * BV, *const sQ = sK + n * Sh::LDK, *const sU = sQ + n * Sh::LDK,
-                 *const sO = sU + n * BV;
-    float2 *const sNP = reinterpret_cast<float2 *>(sO + n * BV);
-    constexpr int ncb = D / BV;
-    const int cb = blockIdx.x % ncb, h = blockIdx.x / ncb % a.h_v, seq = blockIdx.x / (ncb * a.h_v);
-    const int hq = h / (a.h_v / a.h_qk), col0 = cb * BV;
+    float *const sK = smem, *const sQ = sK + n * D;
+    float2 *const sNP = reinterpret_cast<float2 *>(sQ + n * D);
+    uint8_t *const sPath = reinterpret_cast<uint8_t *>(sNP + n * (n + 1) / 2);
+    const int pair = blockIdx.x / (D / C), col0 = blockIdx.x % (D / C) * C;
+    const int h = pair % a.h_v, seq = pair / a.h_v, hq = h / (a.h_v / a.h_qk);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row0 = (int64_t)seq * n;
-    const float *const state = a.state + ((int64_t)seq * a.h_v + h) * D * D + col0;
-
-    for (int e = tid; e < D * (BV / 4); e += NT)
-        reinterpret_cast<float4 *>(sS)[e] = *reinterpret_cast<const float4 *>(state + e / (BV / 4) * D + e % (BV / 4) * 4);
-    if (warp == 0) tree::load_nodes(s, a, seq, h, err, cb == 0 && h == 0);
-    for (int e = tid; e < n * D; e += NT) {
-        const int t = e / D, x = e % D;
-        sK[t * Sh::LDK + x] = load_in(a.k, ((row0 + t) * a.h_qk + hq) * D + x, a.in_bf16);
-        sQ[t * Sh::LDK + x] = load_in(a.q, ((row0 + t) * a.h_qk + hq) * D + x, a.in_bf16);
+    for (int e = tid; e < n * Q4; e += NT) {
+        const int t = e / Q4, x = e % Q4;
+        const int64_t from = ((row0 + t) * a.h_qk + hq) * D + 4 * x;
+        attn::cp_async16(tc::smem_u32(sK + 4 * e), static_cast<const float *>(a.k) + from, 16u);
+        attn::cp_async16(tc::smem_u32(sQ + 4 * e), static_cast<const float *>(a.q) + from, 16u);
     }
+    attn::cp_async_commit();
+    const int eighth = lane >> 2, col = warp % (C / 16) * 16 + (lane & 3) * 4;  // of the block's
+    float4 state[D / 32][4];
+    const float *const from = a.state + ((int64_t)seq * a.h_v + h) * D * D + 4 * eighth * D + col0 + col;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) state[i][e] = *reinterpret_cast<const float4 *>(from + (32 * i + e) * D);
+    }
+    if (warp == 0) tree::load_nodes(s, a, seq, h, err, h == 0 && col0 == 0);
+    attn::cp_async_wait<0>();
     __syncthreads();
     if (a.qk_norm) {
-        for (int r = warp; r < 2 * n; r += NT / 32) {
-            float *const x = sK + r * Sh::LDK;  // Q's rows follow K's
+        for (int r = warp; r < 2 * n; r += W) {
+            float *const x = sK + r * D;  // Q's rows follow K's
             float sq = 0.f;
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) sq = fmaf(x[lane + 32 * e], x[lane + 32 * e], sq);
@@ -61,49 +83,170 @@ __global__ void __launch_bounds__(NT) tree_kernel(const __grid_constant__ Args a
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) x[lane + 32 * e] *= f;
         }
-        __syncthreads();
     }
-    // S^T k and S^T q: a column per lane, rows warp, warp + 8, ...
-    for (int t0 = warp; t0 < n; t0 += 32) {
-        float ks[4] = {0.f, 0.f, 0.f, 0.f}, qs[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int x = 0; x < D; x += 4) {
-            float v[4];
+    if (tid < n) {
+        int at = s.start[tid];
+        for (uint64_t up = s.mask[tid]; up; up &= up - 1) sPath[at++] = (uint8_t)(__ffsll((long long)up) - 1);
+    }
+    __syncthreads();
+    // N and P, a row per warp, eight of its entries at a time: their 16 sums over the lanes go round to one a
+    // pair of lanes in 16 shuffles (N's in the lower half of the warp)
+    constexpr int V = D / 32;
+    for (int t = warp; t < n; t += W) {
+        const int at = s.start[t], count = s.start[t + 1] - at;
+        float k[V], q[V];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = sS[(x + e) * BV + lane];
+        for (int x = 0; x < V; ++x) {
+            k[x] = sK[t * D + lane + 32 * x];
+            q[x] = sQ[t * D + lane + 32 * x];
+        }
+#pragma unroll 1
+        for (int r0 = 0; r0 < count; r0 += 8) {
+            float p[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = min(t0 + 8 * i, n - 1);
-                const float4 k = *reinterpret_cast<const float4 *>(sK + t * Sh::LDK + x);
-                const float4 q = *reinterpret_cast<const float4 *>(sQ + t * Sh::LDK + x);
-                ks[i] = fmaf(k.x, v[0], fmaf(k.y, v[1], fmaf(k.z, v[2], fmaf(k.w, v[3], ks[i]))));
-                qs[i] = fmaf(q.x, v[0], fmaf(q.y, v[1], fmaf(q.z, v[2], fmaf(q.w, v[3], qs[i]))));
+            for (int e = 0; e < 8; ++e) {
+                const float *const y = sK + sPath[at + min(r0 + e, count - 1)] * D + lane;
+                p[e] = p[8 + e] = 0.f;
+#pragma unroll
+                for (int x = 0; x < V; ++x) {
+                    p[e] = fmaf(k[x], y[32 * x], p[e]);
+                    p[8 + e] = fmaf(q[x], y[32 * x], p[8 + e]);
+                }
+            }
+            sums_to_lanes<8, 2>(p, lane);
+            p[0] += __shfl_xor_sync(0xffffffffu, p[0], 1);
+            const int r = r0 + (lane >> 1 & 7);
+            if ((lane & 1) == 0 && r < count) {
+                const float f = tree::decay(s.sum[t], s.sum[sPath[at + r]]);
+                reinterpret_cast<float *>(sNP + at + r)[lane >> 4] = (lane < 16 ? s.beta[t] : 1.f) * f * p[0];
+            }
+        }
+    }
+    // R and e^G S_0^T q
+    const bool is_q = lane & 16;  // the sum that goes to this lane, and its column
+    const int own = col + (lane >> 2 & 2) + (lane >> 2 & 1);
+    float v[AT_ONCE];
+    auto load_v = [&](int t0) {
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            v[u] = 0.f;
+            if (!is_q && t0 + u < n) v[u] = static_cast<const float *>(a.v)[((row0 + t0 + u) * a.h_v + h) * D + col0 + own];
+        }
+    };
+    const int first = warp / (C / 16) * AT_ONCE;
+    load_v(first);
+#pragma unroll 1
+    for (int step = 0; step < n; step += STEP) {
+        const int t0 = step + first;
+        float z[AT_ONCE];
+#pragma unroll
+        for (int u0 = 0; u0 < AT_ONCE; u0 += 2) {
+            float p[2][8] = {};
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int at = min(t0 + u0 + u, n - 1) * D + 32 * i + 4 * eighth;
+                    const float4 k = *reinterpret_cast<const float4 *>(sK + at), q = *reinterpret_cast<const float4 *>(sQ + at);
+                    const float kx[4] = {k.x, k.y, k.z, k.w}, qx[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 w = state[i][e];
+                        p[u][0] = fmaf(kx[e], w.x, p[u][0]);
+                        p[u][1] = fmaf(kx[e], w.y, p[u][1]);
+                        p[u][2] = fmaf(kx[e], w.z, p[u][2]);
+                        p[u][3] = fmaf(kx[e], w.w, p[u][3]);
+                        p[u][4] = fmaf(qx[e], w.x, p[u][4]);
+                        p[u][5] = fmaf(qx[e], w.y, p[u][5]);
+                        p[u][6] = fmaf(qx[e], w.z, p[u][6]);
+                        p[u][7] = fmaf(qx[e], w.w, p[u][7]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                sums_to_lanes<4, 4>(p[u], lane);
+                z[u0 + u] = p[u][0];
+            }
+        }
+        __syncthreads();  // all warps have read these rows
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const int t = t0 + u;
+            if (t >= n) break;
+            const float x = s.grown[t] * z[u];
+            (is_q ? sQ : sK)[t * D + own] = is_q ? x : s.beta[t] * (v[u] - x);
+        }
+        load_v(t0 + STEP);
+    }
+    __syncthreads();
+    // u and o, some rows at once: two lanes a column sum every other ancestor each of those before these
+    // rows, then the rows' own ancestors among them, the last of their lists, are added in order
+    constexpr int G = 4;
+    if (tid >= 2 * C) return;
+    const int c = tid >> 1, half = tid & 1;
+    const int64_t out = (row0 * a.h_v + h) * D + col0 + c, step = (int64_t)a.h_v * D;
+#pragma unroll 1
+    for (int t0 = 0; t0 < n; t0 += G) {
+        float u[G], o[G];
+        int at[G], before[G], most = 0;
+        uint32_t among[G];
+#pragma unroll
+        for (int x = 0; x < G; ++x) {
+            const uint64_t mask = t0 + x < n ? s.mask[t0 + x] : 0;
+            u[x] = o[x] = 0.f;
+            at[x] = s.start[min(t0 + x, n)];
+            before[x] = __popcll(mask & ((1ull << t0) - 1));
+            among[x] = (uint32_t)(mask >> t0);
+            most = max(most, before[x]);
+        }
+#pragma unroll 2
+        for (int r = half; r < most; r += 2) {
+#pragma unroll
+            for (int x = 0; x < G; ++x) {
+                const bool there = r < before[x];  // without branches, so that all rows' loads are on their way
+                const int e = there ? at[x] + r : 0, i = there ? sPath[e] : 0;
+                const float2 np = sNP[e];
+                const float y = there ? sK[i * D + c] : 0.f;
+                u[x] = fmaf(there ? -np.x : 0.f, y, u[x]);
+                o[x] = fmaf(there ? np.y : 0.f, y, o[x]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 8 * i;
-            if (t >= n) break;
-            const float v = load_in(a.v, ((row0 + t) * a.h_v + h) * D + col0 + lane, a.in_bf16);
-            sU[t * BV + lane] = s.beta[t] * (v - s.grown[t] * ks[i]);
-            sO[t * BV + lane] = s.grown[t] * qs[i];
+        for (int x = 0; x < G; ++x) {
+            const int t = min(t0 + x, n - 1);
+            u[x] += __shfl_xor_sync(0xffffffffu, u[x], 1);
+            o[x] += __shfl_xor_sync(0xffffffffu, o[x], 1);
+            u[x] += sK[t * D + c];
+            o[x] += sQ[t * D + c];
+        }
+        __syncwarp();  // the rows' R are read
+#pragma unroll
+        for (int x = 0; x < G; ++x) {
+            int r = at[x] + before[x];
+#pragma unroll
+            for (int y = 0; y < x; ++y) {
+                if (among[x] >> y & 1) {
+                    const float2 np = sNP[r++];
+                    u[x] = fmaf(-np.x, u[y], u[x]);
+                    o[x] = fmaf(np.y, u[y], o[x]);
+                }
+            }
+            const bool node = among[x] >> x & 1;
+            o[x] = node ? a.scale * fmaf(sNP[r].y, u[x], o[x]) : 0.f;
+            u[x] = node ? u[x] : 0.f;
+            if (node && half == 0) sK[(t0 + x) * D + c] = u[x];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < G; ++x) {
+            if (t0 + x >= n) break;
+            if (half == 0)
+                store_out(a.o, out + (t0 + x) * step, o[x], a.out_bf16);
+            else if (a.deltas)
+                a.deltas[out + (t0 + x) * step] = u[x];
         }
     }
-    // N and P where there is a path
-    for (int e = tid; e < n * n; e += NT) {
-        const int t = e / n, i = e - t * n;
-        if (!(s.mask[t] >> i & 1)) continue;
-        float kk = 0.f, qk = 0.f;
-        for (int x = 0; x < D; x += 4) {
-            const float4 k = *reinterpret_cast<const float4 *>(sK + t * Sh::LDK + x);
-            const float4 q = *reinterpret_cast<const float4 *>(sQ + t * Sh::LDK + x);
-            const float4 y = *reinterpret_cast<const float4 *>(sK + i * Sh::LDK + x);
-            kk = fmaf(k.x, y.x, fmaf(k.y, y.y, fmaf(k.z, y.z, fmaf(k.w, y.w, kk))));
-            qk = fmaf(q.x, y.x, fmaf(q.y, y.y, fmaf(q.z, y.z, fmaf(q.w, y.w, qk))));
-        }
-        const float f = tree::decay(s.sum[t], s.sum[i]);
-        sNP[e] = make_float2(s.beta[t] * f * kk, f * qk);
-    }
-    tree::sweep<BV, NT, BV>(s, sU, sO, sNP, n, a, row0, h, col0);
 }
 
 // --- commit: S = e^{G_a} S + sum_{i in A_a} e^{G_a - G_i} k_i u_i^T ------------------------------
@@ -313,16 +456,17 @@ __global__ void __launch_bounds__(NT) tree_commit_kernel(const __grid_constant__
     if (!ok) __syncthreads();
 }
 
-template <int D>
+template <int D, int C>
 cudaError_t launch_plain(const Args &a, int32_t *err, cudaStream_t s) {
-    const size_t bytes = Shape<D>::bytes(a.fixed_len);
     static attn::SmemOptIn opt_in;
     const cudaError_t e =
-        opt_in.set(reinterpret_cast<const void *>(tree_kernel<D>), (int)Shape<D>::bytes(tree::kMaxNodes));
+        opt_in.set(reinterpret_cast<const void *>(tree_kernel<D, C>), (int)tree_bytes(tree::kMaxNodes, D));
     if (e != cudaSuccess) return e;
-    tree_kernel<D><<<(unsigned)((int64_t)a.n_seqs * a.h_v * (D / BV)), NT, bytes, s>>>(a, err);
+    tree_kernel<D, C><<<(unsigned)((int64_t)a.n_seqs * a.h_v * (D / C)), NT, tree_bytes(a.fixed_len, D), s>>>(a, err);
     return cudaGetLastError();
 }
+// (Sequence, V head) pairs up to which four blocks share one of d = 128: as many as are resident at once.
+constexpr int64_t kFewPairs = 2 * 152 / 4;
 
 // States up to which the kernel of a few rows a block commits them.  Measured on 32-node trees, us, rows
 // against whole states: 32 states of d = 128 4.4 / 5.8, 64 4.8 / 6.1, 128 6.1 / 6.1, 256 9.4 / 8.0,
@@ -348,9 +492,9 @@ cudaError_t launch_commit_as(const Args &a, int32_t *err, cudaStream_t s) {
 
 cudaError_t launch_tree(const Args &a, int32_t *err, cudaStream_t s) {
     if (a.in_bf16) return launch_tree_tc(a, err, s);
-    if (a.d == 32) return launch_plain<32>(a, err, s);
-    if (a.d == 64) return launch_plain<64>(a, err, s);
-    return launch_plain<128>(a, err, s);
+    if (a.d == 32) return launch_plain<32, 32>(a, err, s);
+    if (a.d == 64) return launch_plain<64, 64>(a, err, s);
+    return (int64_t)a.n_seqs * a.h_v <= kFewPairs ? launch_plain<128, 32>(a, err, s) : launch_plain<128, 128>(a, err, s);
 }
 
 cudaError_t launch_tree_commit(const Args &a, int32_t *err, cudaStream_t s) {

@@ -18,12 +18,10 @@ namespace tree {
 // A sequence's tree and gates of one V head, in shared memory.
 struct Nodes {
     uint64_t mask[kMaxNodes];
-    float2 sum[kMaxNodes];  // G_j as the sum of two floats
+    float2 sum[kMaxNodes];   // G_j as the sum of two floats
     float grown[kMaxNodes];  // e^{G_j}
     float beta[kMaxNodes];
-    uint8_t order[kMaxNodes];      // the nodes level by level
-    uint8_t start[kMaxNodes + 1];  // where a level starts among them
-    int levels;
+    uint16_t start[kMaxNodes + 1];  // where the list of a node's path starts
 };
 
 // e^{G_t - G_i}.  Sums of 64 gates reach -100 and more, where a float is 2^-18 coarse; their
@@ -49,97 +47,25 @@ __device__ __forceinline__ void load_nodes(Nodes &s, const Args &a, int seq, int
     }
     const Masks m = masks<true>(load_parents(a.parents + row0, n, lane), n, lane, sum);
     if (lead && m.bad) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
-    int depth[2], deepest = 0;
+    int at = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int j = lane + 32 * i;
-        depth[i] = __popcll(m.a[i]);
-        deepest = max(deepest, depth[i]);
+        const int j = lane + 32 * i, length = __popcll(m.a[i]);
         const float hi = (float)sum[i], lo = (float)(sum[i] - (double)hi);
         s.mask[j] = m.a[i];
         s.sum[j] = make_float2(hi, lo);
         s.grown[j] = expf(hi) * (1.f + lo);
         s.beta[j] = a.beta_logits ? 1.f / (1.f + expf(-b[i])) : b[i];
-    }
-    deepest = __reduce_max_sync(0xffffffffu, deepest);
-    int at = 0;
-    const uint32_t below = (1u << lane) - 1u;
-    for (int d = 1; d <= deepest; ++d) {
-        const uint32_t b0 = __ballot_sync(0xffffffffu, depth[0] == d), b1 = __ballot_sync(0xffffffffu, depth[1] == d);
-        if (lane == 0) s.start[d - 1] = (uint8_t)at;
-        if (depth[0] == d) s.order[at + __popc(b0 & below)] = (uint8_t)lane;
-        if (depth[1] == d) s.order[at + __popc(b0) + __popc(b1 & below)] = (uint8_t)(lane + 32);
-        at += __popc(b0) + __popc(b1);
-    }
-    if (lane == 0) {
-        s.start[deepest] = (uint8_t)at;
-        s.levels = deepest;
-    }
-}
-
-// The corrections and outputs, level by level: the nodes of a level depend on none of each
-// other, so the block's threads take COLS columns of THREADS / COLS of them at a time, and a
-// tree of a few levels has a few dependent steps whatever it holds.  Only a node's ancestors
-// are looked at: what the others hold (infinities, NaNs) cannot reach it.
-//   su   [n][LD] in: beta_j (v_j - e^{G_j} S_0^T k_j); out: u_j
-//   so   [n][LD] e^{G_j} S_0^T q_j
-//   np   [n][ld_np] N and P
-// Starts and ends with a barrier of the block.
-template <int COLS, int THREADS, int LD>
-__device__ __forceinline__ void sweep(const Nodes &s, float *su, const float *so, const float2 *np, int ld_np,
-                                      const Args &a, int64_t row0, int h, int col0) {
-    constexpr int AT_ONCE = THREADS / COLS;
-    const int c = threadIdx.x % COLS, w = threadIdx.x / COLS, n = a.fixed_len;
-    auto store = [&](int t, float o, float u) {
-        const int64_t at = ((row0 + t) * a.h_v + h) * a.d + col0 + c;
-        store_out(a.o, at, o, a.out_bf16);
-        if (a.deltas) a.deltas[at] = u;
-    };
-    for (int t = w; t < n; t += AT_ONCE)
-        if (s.mask[t] == 0) store(t, 0.f, 0.f);
-    __syncthreads();
-    for (int level = 0; level < s.levels; ++level) {
-        const int end = s.start[level + 1];
-        for (int x = s.start[level] + w; x < end; x += AT_ONCE) {
-            const int t = s.order[x];
-            const float2 *const row = np + t * ld_np;
-            float u = su[t * LD + c], o = so[t * LD + c];
-            uint64_t up = s.mask[t] & ~(1ull << t);
-            int left = __popcll(up);
-            auto next = [&] {
-                const int i = __ffsll((long long)up) - 1;
-                up &= up - 1;
-                return i;
-            };
-            for (; left >= 4; left -= 4) {
-                int i[4];
-                float2 f[4];
-                float v[4];
+        int upto = length;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) i[e] = next();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[e] = row[i[e]];
-                    v[e] = su[i[e] * LD + c];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    u = fmaf(-f[e].x, v[e], u);
-                    o = fmaf(f[e].y, v[e], o);
-                }
-            }
-            for (; left > 0; --left) {
-                const int i = next();
-                const float2 f = row[i];
-                const float v = su[i * LD + c];
-                u = fmaf(-f.x, v, u);
-                o = fmaf(f.y, v, o);
-            }
-            su[t * LD + c] = u;
-            store(t, a.scale * fmaf(row[t].y, u, o), u);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
         }
-        __syncthreads();
+        s.start[j] = (uint16_t)(at + upto - length);
+        at += __shfl_sync(0xffffffffu, upto, 31);
     }
+    if (lane == 0) s.start[kMaxNodes] = (uint16_t)at;
 }
 
 }  // namespace tree
