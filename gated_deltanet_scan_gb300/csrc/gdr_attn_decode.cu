@@ -22,6 +22,11 @@
 // programmatic dependent launch, joins the blocks' parts from the workspace; always in
 // the order of the tokens.
 //
+// Of a tree of drafted tokens (TREE) a row sees what is before the tree and its own path: the worker makes the
+// masks of the tree's nodes (gdr_tree.cuh) when it comes to the sequence, and in the tiles that hold the tree
+// a score is selected by its bit.  A row that is no node takes the tokens before the tree with the others
+// and is undone at the end: its row of the products costs nothing.
+//
 // P enters P V in 16 bits (its sum l does not): that is the only rounding between the
 // inputs and the output's own.  fp16 holds 11 bits of a weight.  bf16 holds 8, which added
 // as much error as the output's own rounding (64 sequences of d = 256: 0.00226 of o's rms

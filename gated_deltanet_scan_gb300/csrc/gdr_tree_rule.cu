@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(NT, D == 128 ? 2 : D == 64 ? 3 : 4) tree_kerne
 // how many bytes of states an SM has on their way meanwhile.  tree_commit_kernel, for batches,
 // has a block of 256 threads per (sequence, V head) and brings its whole state into shared
 // memory with bulk copies, 192 KiB an SM.  tree_commit_rows_kernel, for a few, has ROWS rows of a
-// state in registers, so that one sequence spreads over the GPU.
+// state in registers, so that one sequence spreads over the GPU.  64 trees of 64 nodes, 32 heads of 128: 49.6 us,
+// 82% of the measured bandwidth; one tree of 24 6.2 us (its bytes would take 0.6).
 
 // The accepted path of a sequence for one V head, by a warp: its nodes in rising order and their
 // weights e^{G_a - G_i}.  Returns their number; `grown` is e^{G_a}.

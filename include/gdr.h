@@ -448,9 +448,11 @@ gdr_status gdr_verify_commit(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok
  *   state  [n_seqs][H_v][d_k][d_v]
  *   deltas NULL, or fp32 [n_seqs * n_tok][H_v][d_v] that receives the corrections u_j
  * Rows of o and deltas that are no nodes are set to zero.  dims->chunk has no effect;
- * dims->flags as everywhere.  Products are exact in the inputs' values and summed in fp32,
- * whatever the kernel (the state's values enter tensor-core products in three bf16 parts,
- * which hold all their 24 bits); the sums of g are fp64.  n_seqs * H_v is below 2^28
+ * dims->flags as everywhere.  Everything between the inputs and o's own rounding is held to
+ * fp32: what enters a tensor-core product enters as three bf16 parts (24 bits), of whose nine
+ * products the six that reach 2^-24 are summed in fp32; the sums of g are fp64.  A gate of
+ * minus infinity forgets the path before it (all gates below -10^4 count as -10^4).  An
+ * infinite or NaN value of v or of the state stays in its column, and in the nodes whose path it is on.  n_seqs * H_v is below 2^28
  * (GDR_ERR_UNSUPPORTED otherwise); n_seqs = 0 is a no-op, whatever the pointers are.
  */
 gdr_status gdr_verify_tree(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents, const void *q,
