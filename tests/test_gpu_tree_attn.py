@@ -233,6 +233,36 @@ def test_attend_again_on_another_stream_and_in_a_graph(h_q, n_tok):
     no_error()
 
 
+@pytest.mark.parametrize("h_q,n_tok", [(2, 3), (8, 24), (8, 60)])
+def test_attend_on_two_streams_and_by_two_graphs_of_one_workspace(h_q, n_tok):
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(28)
+    cs = [Paged(rng, lens, 32, 2, 64, "bf16") for lens in ([900, 70, 0, 333], [64, 1500])]
+    qs = [randn(rng, (len(c.lens) * n_tok, h_q, 64), "bf16") for c in cs]
+    trees = [parents_of(trees_of(rng, len(c.lens), n_tok)) for c in cs]
+    want = [attend(c, q, p) for c, q, p in zip(cs, qs, trees)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[attend(c, q, p, stream=s) for c, q, p, s in zip(cs, qs, trees, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for pairs in got:
+        assert all(torch.equal(x, y) for a, b in zip(pairs, want) for x, y in zip(a, b))
+    size = max(gdr.gdr_attn_decode_tree_workspace_bytes(q, c.k, p) for c, q, p in zip(cs, qs, trees))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    outs, graphs = [nan_like(q.shape, q.dtype) for q in qs], []
+    for c, q, p, o in zip(cs, qs, trees, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            gdr.gdr_attn_decode_tree(q, c.k, c.v, c.table, c.kv_lens, o, p, workspace=ws)
+    for _ in range(3):
+        for o, g in zip(outs, graphs):
+            o.fill_(NAN)
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w[0]) for o, w in zip(outs, want))
+    no_error()
+
+
 @pytest.mark.parametrize("h_q,n_tok", [(1, 9), (4, 24), (4, 60)])
 def test_attend_bad_trees_lengths_and_pages_are_recorded(h_q, n_tok):
     torch = gu.require_gpu()
@@ -452,6 +482,11 @@ def test_compact_records_what_it_leaves_out():
     for n in (7, 1, -1, top + 1, -(1 << 31), (1 << 31) - 1):
         assert run([6, -1], lens=[n, 30]) == (gdr.GDR_ERR_INVALID_ARG, [n, 22]) and torch.equal(c.k, k0), n
     assert run([-1, -1], lens=[0, 30]) == (gdr.GDR_OK, [0, 22])
+    run([6, 7])
+    moved = c.k.clone()
+    c.k.copy_(k0), c.v.copy_(v0)
+    gdr.gdr_attn_commit_tree(c.k, c.v, c.table, ints(c.lens), parents_of([tree, tree]), ints([6, 7]))  # no lengths
+    assert torch.equal(c.k, moved)
     for page in (-1, c.k.shape[0], 1 << 30):
         kept = c.table.clone()
         c.table[0, 4] = page  # of the slots 32 .. 39

@@ -141,6 +141,32 @@ def test_more_pairs_than_blocks(h_qk, h_v, n_seqs, n_tok, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("h_qk,h_v,n_seqs,n_tok", [(2, 4, 19, 7), (4, 8, 10, 24), (8, 8, 24, 12), (1, 4, 40, 64)])
+def test_more_pairs_than_blocks_of_128_columns(h_qk, h_v, n_seqs, n_tok, dtype):
+    """76 pairs and more: fp32 kernels on either side of it, and more than a bf16 block each."""
+    gu.require_gpu()
+    rng = np.random.default_rng(n_seqs + n_tok)
+    kinds = ("deep", "holes", "draft", "chain", "padded")
+    b = Batch(rng, [tr.make(rng, n_tok, kinds[s % len(kinds)]) for s in range(n_seqs)], h_qk, h_v, 128, dtype)
+    _, u = b.check()
+    b.check_settle(u, [int(rng.choice(np.r_[-1, np.flatnonzero(r)])) for r in b.real])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_streams_at_once(dtype):
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(13)
+    b = Batch(rng, [tr.make(rng, 40, kind) for kind in ("draft", "chain", "forest") * 4], 4, 8, 128, dtype)
+    o, u = b.run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    out = [[b.run(stream=s) for s in streams] for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, o) and torch.equal(y, u) for pair in out for x, y in pair)
+    no_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("scale", [1.0, 128 ** -0.5, -0.3, 0.0])
 def test_flags_scales_and_bf16_outputs(scale, dtype):
     gu.require_gpu()
