@@ -600,12 +600,13 @@ cudaError_t launch_warps(const Args &a, cudaStream_t s) {
 template <int D, bool F16, bool TREE>
 cudaError_t launch_as(const Args &a, cudaStream_t s) {
     const int rows = a.n_tok * a.group;
-    const Kind kind = kind_of(rows, D, TREE);
+    const int64_t heads = (int64_t)a.n_seqs * a.h_kv;
+    const Kind kind = kind_of(rows, D, TREE, heads);
     const cudaError_t e = kind != kFew ? launch_decode_wide(a, s) : launch_warps<D, F16, TREE>(a, s);
     if (e != cudaSuccess) return e;
     const Spec sp = spec(kind, D);
-    const Layout L = layout(rows, sp, D, (int64_t)a.n_seqs * a.h_kv);
-    const int64_t triples = (int64_t)a.n_seqs * a.h_kv * L.blocks_of_rows;
+    const Layout L = layout(rows, sp, D, heads);
+    const int64_t triples = heads * L.blocks_of_rows;
     const bool many = kBlocks >= 16 * triples;
     char *const ws = static_cast<char *>(a.ws);
     const Join w = {reinterpret_cast<const Parts *>(ws), reinterpret_cast<const float2 *>(ws + L.ml),
@@ -633,7 +634,8 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 
 size_t decode_workspace_bytes(int h_q, int h_kv, int d, int n_seqs, int n_tok, bool tree) {
     const int rows = n_tok * (h_q / h_kv);
-    return layout(rows, spec(kind_of(rows, d, tree), d), d, (int64_t)n_seqs * h_kv).total;
+    const int64_t heads = (int64_t)n_seqs * h_kv;
+    return layout(rows, spec(kind_of(rows, d, tree, heads), d), d, heads).total;
 }
 
 cudaError_t launch_decode(const Args &a, cudaStream_t s) {

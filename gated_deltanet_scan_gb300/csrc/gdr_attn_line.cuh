@@ -30,10 +30,15 @@ enum Kind { kFew = 0, kWide = 1, kPaired = 2 };
 __host__ __device__ constexpr Spec spec(Kind kind, int d) {
     return kind == kFew ? Spec{kWarpRows, 16, 8, 1024 / d} : Spec{kind == kPaired ? 256 : 128, 64, 1, 4};
 }
-// Trees of more than 128 rows of up to 128 values: two blocks of rows read the keys and values together.
-// (The O of two blocks of d = 256 would leave no TMEM for their S.)
-__host__ __device__ inline Kind kind_of(int rows, int d, bool tree) {
-    return rows <= kWarpRows ? kFew : tree && rows > 128 && d <= 128 ? kPaired : kWide;
+// Of the rows of a key/value head, of so many heads of all sequences.  Trees of more than 128 rows of up to 128
+// values, more blocks of rows than workers: two of them read the keys and values together.  (The O of two
+// blocks of d = 256 would leave no TMEM for their S.)  Fewer have more to lose by parts of twice the rows.
+// d = 128, 256 rows, 4 heads a sequence, us apart / together: 32 sequences of up to 8,000 tokens 82.6 / 77.5, of
+// 1,000 43.2 / 44.0; 16 53.1 / 50.8 and 28.9 / 34.9; 8 of 16,000 45.9 / 45.1, of 4,000 28.9 / 32.9; one 16.4 / 20.5.
+inline Kind kind_of(int rows, int d, bool tree, int64_t heads) {
+    return rows <= kWarpRows                                                                ? kFew
+           : tree && rows > 128 && d <= 128 && (int64_t)((rows + 127) / 128) * heads > kBlocks ? kPaired
+                                                                                              : kWide;
 }
 
 // Where the parts of a triple's rows are, for the join.

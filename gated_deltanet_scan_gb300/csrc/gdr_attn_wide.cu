@@ -21,7 +21,7 @@
 //
 // Trees of more than 128 rows (64 nodes, 4 query heads of a key/value head) would read their keys and
 // values, and pay for their loads, once per block of rows.  Up to d = 128 TMEM holds O and two S tiles of
-// two blocks, so a worker takes both (B = 2), the products block by block, so that one's P is made
+// two blocks, so a worker takes both (B = 2, where there are enough of them: kind_of), the products block by block, so that one's P is made
 // while the other's run: 16 trees of 64 nodes, contexts up to 16,384, d = 128, 32 / 8 heads: 124 us with a
 // block a worker, 113 with two, 107 with two places for Q.  The tensor pipe and the shared memory it reads
 // (Q again for every 64 tokens) bound it: 1,770 clocks a tile, of which HBM would need 1,370.
@@ -610,7 +610,7 @@ template <int D, bool F16>
 cudaError_t launch(const Args &a, cudaStream_t s) {
     if (!a.parents) return launch_as<D, F16, false, 1>(a, s);
     if constexpr (D <= 128) {
-        if (kind_of(a.n_tok * a.group, D, true) == kPaired) return launch_as<D, F16, true, 2>(a, s);
+        if (kind_of(a.n_tok * a.group, D, true, (int64_t)a.n_seqs * a.h_kv) == kPaired) return launch_as<D, F16, true, 2>(a, s);
     }
     return launch_as<D, F16, true, 1>(a, s);
 }

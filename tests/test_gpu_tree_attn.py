@@ -103,6 +103,52 @@ def test_attend_many_sequences(h_q, n_tok, n):
     check_attend(c, randn(rng, (n * n_tok, h_q, 64), "f16", 2.0), trees_of(rng, n, n_tok), "f16")
 
 
+# more than 128 rows of d <= 128, and more blocks of rows than the kernel has workers: two blocks a worker
+TOGETHER = [(128, 4, 1, 48, 33, 80), (64, 12, 3, 64, 16, 27), (128, 10, 2, 27, 64, 40), (128, 16, 1, 64, 48, 21), (64, 5, 1, 40, 5, 90)]
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("d,h_q,h_kv,n_tok,page,n", TOGETHER)
+def test_attend_blocks_of_rows_together(d, h_q, h_kv, n_tok, page, n, dtype):
+    gu.require_gpu()
+    rng = np.random.default_rng(d + n)
+    lens = [int(x) if x >= n_tok else 0 for x in rng.integers(n_tok // 2, n_tok + 90, n)]
+    lens[3], lens[n - 1] = 1500, n_tok
+    c = Paged(rng, lens, page, h_kv, d, dtype, by_head=bool(n & 1), stale=NAN)
+    check_attend(c, randn(rng, (n * n_tok, h_q, d), dtype, 2.0), trees_of(rng, n, n_tok), dtype)
+
+
+@pytest.mark.parametrize("d,h_q,n_tok,n", [(128, 4, 40, 90), (64, 4, 64, 80)])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_attend_blocks_of_rows_together_see_their_paths_only(d, h_q, n_tok, n, bad):
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(29)
+    trees = trees_of(rng, n, n_tok, ("forest", "binary", "deep"))
+    parents = parents_of(trees)
+    c = Paged(rng, [n_tok + int(x) for x in rng.integers(0, 100, n)], 32, 1, d, "bf16")
+    q = randn(rng, (n * n_tok, h_q, d), "bf16")
+    clean, lse = attend(c, q, parents)
+    again, lse2 = attend(c, q, parents)
+    assert torch.equal(clean, again) and torch.equal(lse, lse2)
+    hit = torch.zeros(d, dtype=torch.bool, device="cuda")
+    hit[1::3] = True
+    for s, j in ((0, 0), (7, n_tok // 2), (n - 1, 5)):
+        under = torch.zeros(n * n_tok, dtype=torch.bool, device="cuda")
+        under[s * n_tok:(s + 1) * n_tok] = torch.from_numpy(below(trees[s], j)).cuda()
+        p = c.lens[s] - n_tok + j
+        at = (int(c.table_np[s, p // 32]), p % 32)
+        kept = c.k[at].clone(), c.v[at].clone()
+        c.v[at[0], at[1], :, 1::3] = bad
+        o, _ = attend(c, q, parents)
+        assert torch.equal(o[~under], clean[~under]), (s, j)
+        assert torch.all(~torch.isfinite(o[under][..., hit])) and torch.all(torch.isfinite(o[under][..., ~hit])), (s, j)
+        c.k[at] = bad
+        o, _ = attend(c, q, parents)
+        assert torch.equal(o[~under], clean[~under]), (s, j)
+        c.k[at], c.v[at] = kept
+    no_error()
+
+
 @pytest.mark.parametrize("d,h_q,n_tok", [(256, 1, 9), (128, 4, 24), (64, 8, 64)])
 def test_attend_long_sequence_is_split_and_joined(d, h_q, n_tok):
     gu.require_gpu()
@@ -112,7 +158,7 @@ def test_attend_long_sequence_is_split_and_joined(d, h_q, n_tok):
 
 
 @pytest.mark.parametrize("dtype", DT)
-# the same kernels on the same cuts: the same bits (over 128 rows of d <= 128 a tree's are cut otherwise)
+# the same kernels on the same cuts: the same bits (many trees of more than 128 rows are cut otherwise)
 @pytest.mark.parametrize("d,h_q,n_tok", [(128, 1, 16), (256, 4, 16), (64, 2, 5), (128, 8, 16), (256, 16, 16)])
 def test_attend_a_chain_is_decode(d, h_q, n_tok, dtype):
     torch = gu.require_gpu()
