@@ -530,12 +530,11 @@ def _cache_of(shape, strides, k_cache, v_cache, page_table, n_seqs: int, dtype, 
         raise ValueError("the caches' last dimension must be contiguous")
     if page_table.dtype != _attn_types[1]:
         raise TypeError("page_table must be int32")
-    if page_table.dim() != 2:
+    table = page_table.shape
+    if len(table) != 2 or table[0] != n_seqs:
         raise ValueError(f"page_table must have shape ({n_seqs}, max_pages)")
-    n, width = page_table.shape
+    n, width = table
     rs, cs = page_table.stride()
-    if n != n_seqs:
-        raise ValueError(f"page_table must have shape ({n_seqs}, max_pages)")
     if cs != 1 and width > 1:
         raise ValueError("page_table's rows must be contiguous")
     if k_cache.get_device() != dev or v_cache.get_device() != dev or page_table.get_device() != dev:
@@ -675,12 +674,13 @@ def _decode(q, k_cache, v_cache, page_table, kv_lens, o, n_tok, parents, scale, 
 
 # --- trees of drafted tokens ------------------------------------------------------
 
-def _tree_rows(parents, n: int, rows: int) -> int:
-    """Rows of each of n trees; ``rows`` is what the tensors have."""
-    if parents.dim() != 2 or parents.shape[0] != n:
+def _tree_rows(parents, n: int, rows: Optional[int]) -> int:
+    """Rows of each of n trees; ``rows`` is what the tensors have, if any."""
+    shape = parents.shape
+    if len(shape) != 2 or shape[0] != n:
         raise ValueError(f"parents must have shape ({n}, n_tok)")
-    n_tok = parents.shape[1]
-    if rows != n * n_tok:
+    n_tok = shape[1]
+    if rows is not None and rows != n * n_tok:
         raise ValueError(f"the tensors must have n * n_tok = {n * n_tok} rows, not {rows}")
     return n_tok
 
@@ -731,7 +731,7 @@ def gdr_attn_commit_tree(k_cache, v_cache, page_table, kv_lens, parents, last, l
     dtype, dev = k_cache.dtype, k_cache.get_device()
     dims = _attn_dims(h_kv, h_kv, d, dtype, 1.0)
     i32, n = _attn_types[1], kv_lens.shape[0]
-    n_tok = _tree_rows(parents, n, n * parents.shape[-1])
+    n_tok = _tree_rows(parents, n, None)
     st = (_lib or lib()).gdr_attn_commit_tree(
         dims, n, n_tok, _plain(parents, (n, n_tok), i32, dev, "parents"), _plain(last, (n,), i32, dev, "last"), layers,
         stride, _cache_of(shape, strides, k_cache, v_cache, page_table, n, dtype, dev),
