@@ -536,16 +536,17 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     to.put<F16, TREE>(r0 + lr, c, sum, len, c == 0);
 }
 
-// The same where rows have many parts (few triples for the blocks): eight warps share the parts of
-// one row's 128 columns.
+// The same where rows have many parts (few triples for the blocks): eight warps share the parts of a row.
+// (Blocks of 128 columns, twice as many at d = 256, do not all fit the GPU at once: one tree of 24 rows, 16 heads,
+// whole: 20.4 us; 18.5 so.)
 template <int D, bool F16, bool TREE>
 __global__ void __launch_bounds__(kJoinThreads)
     join_many_kernel(const __grid_constant__ Args a, const __grid_constant__ Join j) {
-    constexpr int W = kJoinThreads / 32;
-    __shared__ float4 s_o[W][32];
+    constexpr int W = kJoinThreads / 32, V = D > 128 ? D / 128 : 1;  // a lane's pieces of four columns
+    __shared__ float4 s_o[V][W][32];
     __shared__ float2 s_ml[W];
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.y * 32 + lane;
-    const bool mine = c < D / 4;  // d = 64: half of the lanes
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool mine = lane < D / 4;  // d = 64: half of the lanes
     const uint32_t rows = (uint32_t)a.n_tok * a.group, head = blockIdx.x / rows;
     const int r = (int)(blockIdx.x - head * rows), rb = r / j.block_rows, lr = r - rb * j.block_rows;
     Joined to{a, j.per_group, (int)(head / (uint32_t)a.h_kv), 0};
@@ -553,39 +554,42 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int64_t len = length_of(a, to.s);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (len == 0) {
-        if (w == 0 && mine) to.put<F16, TREE>(r, c, Sum(), 0, c == 0);
+        if (w < V && mine) to.put<F16, TREE>(r, 32 * w + lane, Sum(), 0, w == 0 && lane == 0);
         return;
     }
     const Parts parts = j.triples[(int64_t)head * j.blocks_of_rows + rb];
     if (parts.count == 1) return;
-    Sum sum;
+    Sum sum[V];
 #pragma unroll 1
     for (int i = w; i < parts.count; i += W * kAtOnce) {
         float2 v[kAtOnce];
-        float4 y[kAtOnce];
+        float4 y[V][kAtOnce];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
             if (u > 0 && i + u * W >= parts.count) break;
             const int64_t at = parts.row(i + u * W, j.part_rows) + lr;
             v[u] = __ldcg(j.ml + at);
-            y[u] = __ldcg(j.o + at * (D / 4) + (mine ? c : 0));
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e][u] = __ldcg(j.o + at * (D / 4) + 32 * e + (mine ? lane : 0));
         }
-        sum.add<kAtOnce>(v, y, (parts.count - i + W - 1) / W);
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[e].add<kAtOnce>(v, y[e], (parts.count - i + W - 1) / W);
     }
-    s_o[w][lane] = sum.o;
-    if (lane == 0) s_ml[w] = make_float2(sum.m, sum.l);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_o[e][w][lane] = sum[e].o;
+    if (lane == 0) s_ml[w] = make_float2(sum[0].m, sum[0].l);
     __syncthreads();  // the block is one row: its warps come here together
-    if (w != 0) return;
+    if (w >= V) return;
     float2 v[W];
     float4 y[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         v[i] = s_ml[i];
-        y[i] = s_o[i][lane];
+        y[i] = s_o[w][i][lane];
     }
     Sum all;
     all.add<W>(v, y, W);
-    if (mine) to.put<F16, TREE>(r, c, all, len, c == 0);
+    if (mine) to.put<F16, TREE>(r, 32 * w + lane, all, len, w == 0 && lane == 0);
 }
 
 template <int D, bool F16, bool TREE>
@@ -616,7 +620,7 @@ cudaError_t launch_as(const Args &a, cudaStream_t s) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = many ? dim3((unsigned)(a.t_total * a.h_q), (D + 127) / 128) : dim3((unsigned)(a.n_seqs * a.h_kv), L.blocks_of_rows, (L.part_rows + kJoinRows<D> - 1) / kJoinRows<D>);
+    cfg.gridDim = many ? dim3((unsigned)(a.t_total * a.h_q)) : dim3((unsigned)(a.n_seqs * a.h_kv), L.blocks_of_rows, (L.part_rows + kJoinRows<D> - 1) / kJoinRows<D>);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = &attr;
