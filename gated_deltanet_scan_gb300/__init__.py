@@ -464,7 +464,9 @@ def _attn_init():
     return _attn_types
 
 
-_attn_struct = functools.lru_cache(maxsize=256)(gdr_attn_dims)  # read only; making one takes 0.4 us
+# Read only; making one takes 0.4 us.  They are kept by value: a scale enters as a float, since a tensor's own key would
+# be its identity, whatever it holds by now.
+_attn_struct = functools.lru_cache(maxsize=256)(gdr_attn_dims)
 _rule_struct = functools.lru_cache(maxsize=256)(gdr_dims)
 
 
@@ -472,7 +474,7 @@ def _attn_dims(h_q: int, h_kv: int, d: int, dtype, scale) -> gdr_attn_dims:
     code = (_attn_types or _attn_init())[0].get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    return _attn_struct(h_q, h_kv, d, code, d ** -0.5 if scale is None else scale)
+    return _attn_struct(h_q, h_kv, d, code, d ** -0.5 if scale is None else float(scale))
 
 
 def _attn_stream(stream, dev: int):
@@ -746,7 +748,7 @@ def _tree_dims(h_qk: int, h_v: int, d_k: int, d_v: int, dtype, out_dtype, scale,
     io, out = codes.get(dtype), codes.get(out_dtype)
     if io in (None, GDR_F16) or out in (None, GDR_F16):
         raise TypeError(f"unsupported dtypes {dtype} and {out_dtype}")
-    return _rule_struct(h_qk, h_v, d_k, d_v, 64, io, out, scale, flags)
+    return _rule_struct(h_qk, h_v, d_k, d_v, 64, io, out, float(scale), flags)
 
 
 def gdr_verify_tree(q, k, v, g, beta, state, o, parents, *, deltas=None, scale: float = 1.0, qk_l2norm: bool = False,
