@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const __grid_constant
         uint64_t path = tree::mask_of(nodes, last & 63);
         if (last < 0 || last >= a.n_tok || !inside) path = 0;
         const int count = __popcll(path);
-        // a sequence of no tokens and nothing accepted is not in the batch
-        const bool bad = nodes.bad || last < -1 || (last >= 0 && count == 0) || (!inside && len != 0);
+        // a sequence of no tokens is not in the batch, whatever its tree and last node hold
+        const bool bad = len != 0 && (nodes.bad || last < -1 || (last >= 0 && count == 0) || !inside);
         if (bad && blockIdx.y == 0) record_invalid(a.err);
         auto offset = [&](int64_t p) -> int64_t {
             const int pg = (int)((uint32_t)p / (uint32_t)a.cache.page_size);

@@ -664,9 +664,10 @@ size_t gdr_attn_decode_tree_workspace_bytes(const gdr_attn_dims *dims, int32_t n
  *   lens_out      NULL, or DEVICE int32 [n_seqs]: the new lengths, base + |A_last| (kv_lens[s]
  *                 itself where that is 0 or out of range); must not overlap kv_lens
  * dims->h_q, dtype and scale have no effect on the result.  A sequence with kv_lens[s] = 0 is
- * not in the batch; one in 1 .. n_tok - 1 or beyond max_pages * page_size is left as it is and
- * recorded.  Rows whose page id is out of range are left out and recorded.  Slots of a tree
- * must not be shared between sequences.
+ * not in the batch (its parents and last[s] may hold anything; its new length is 0); one in
+ * 1 .. n_tok - 1 or beyond max_pages * page_size is left as it is and recorded.  Rows whose
+ * page id is out of range are left out and recorded.  Slots of a tree must not be shared
+ * between sequences.
  */
 gdr_status gdr_attn_commit_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents,
                                 const int32_t *last, int32_t n_layers, int64_t layer_stride, const gdr_kv_cache *cache,

@@ -1,0 +1,42 @@
+"""Tree operators on the GPU at the edges of what their documentation allows."""
+
+import numpy as np
+import pytest
+
+import gated_deltanet_scan_gb300 as gdr
+from tests import gpu_util as gu
+from tests.test_gpu_attn import Paged, ints, no_error
+from tests.test_gpu_tree_attn import parents_of
+
+pytestmark = pytest.mark.gpu
+
+TREE = [-1, -1, 1, 0, 2, -2, 4, 3]
+
+
+@pytest.mark.parametrize("layers", [0, 3])
+@pytest.mark.parametrize("stale,last", [
+    ([-1, 0, 1, 2, 3, 4, 5, 6], 7), ([-2] * 8, 3), ([9, -7, 1 << 30, 3, 4, 5, -(1 << 31), 7], -1), (TREE, 1 << 30), (TREE, -9),
+])
+def test_compaction_of_a_batch_with_empty_places(stale, last, layers):
+    """A sequence of no tokens is not in the batch: whatever its parents and last node hold, nothing is recorded, its
+    new length is 0, and the others' rows move as they do without it."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(61)
+    c = Paged(rng, [40, 24, 30], 8, 2, 64, "bf16")
+    if layers:
+        c.k, c.v = (torch.stack([x + i for i in range(layers)]) for x in (c.k, c.v))
+    k0, v0 = c.k.clone(), c.v.clone()
+
+    def run(lens, trees, nodes):
+        c.k.copy_(k0), c.v.copy_(v0)
+        out = ints([-9] * 3)
+        gdr.gdr_attn_commit_tree(c.k, c.v, c.table, ints(lens), parents_of(trees), ints(nodes), out)
+        torch.cuda.synchronize()
+        return c.k.clone(), c.v.clone(), out.tolist()
+
+    want = run([40, 24, 30], [TREE, TREE, TREE], [6, -1, 7])
+    no_error()
+    got = run([40, 0, 30], [TREE, stale, TREE], [6, last, 7])
+    no_error()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and got[2] == [36, 0, 25]
+    assert not torch.equal(got[0], k0)
