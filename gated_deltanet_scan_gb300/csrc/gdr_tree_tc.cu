@@ -713,9 +713,11 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
     }
     __syncwarp();
     load_values(items.at);
+    // A wait may give up for one warp and not for another: they leave at a vote, never between two.
+    bool ok = true;
 #pragma unroll 1
     for (int i = 0, q = 0; i < pairs; ++i) {
-        bool ok = i == 0 || wait_warp(bar(kFirst), i - 1);
+        ok = (i == 0 || wait_warp(bar(kFirst), i - 1)) && ok;
         tc_fence_after_sync();
 #pragma unroll 1
         for (int k = 0; k < PER; ++k, ++q) {
@@ -744,12 +746,12 @@ __device__ __forceinline__ bool states(const Args &a, uint8_t *smem, Tables &s) 
         if (lane == 0) mbar_arrive(bar(kParts));
         // its values, once the rows are done with those of the pair before
         if (i > 0) {
-            if (!wait_warp(bar(kRParts), i - 1)) return false;
-            load_values(items.at + i);
+            ok = wait_warp(bar(kRParts), i - 1) && ok;
+            if (ok) load_values(items.at + i);
         }
     }
     attn::cp_async_wait<0>();
-    return true;
+    return ok;
 }
 
 // ---- the rows' warps -------------------------------------------------------------------------------
