@@ -716,13 +716,15 @@ def gdr_attn_commit_tree(k_cache, v_cache, page_table, kv_lens, parents, last, l
     """Move every tree's accepted path, which ends in node ``last`` (int32 [n], -1: none), to
     the front of the tree's slots (see gdr_attn_commit_tree in include/gdr.h).  k_cache,
     v_cache [n_pages, page_size, H_kv, d], or [layers, n_pages, page_size, H_kv, d] for all
-    layers at once; lens_out int32 [n] (not kv_lens itself) receives the new lengths."""
+    layers at once; lens_out int32 [n] (not kv_lens or last itself) receives the new lengths."""
     shape, strides = k_cache.shape, k_cache.stride()
     if len(shape) == 4:
         layers, stride = 1, 0
     elif len(shape) == 5:
         layers, stride = shape[0], strides[0] if shape[0] > 1 else 0
         if layers == 0:
+            if lens_out is not None:
+                raise ValueError("without layers there is nothing that gives lens_out")
             return
         shape, strides = shape[1:], strides[1:]
     else:

@@ -240,8 +240,10 @@ gdr_status gdr_attn_commit_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32
     if (n_seqs == 0) return GDR_OK;
     if (!aligned(parents, 4) || !aligned(last, 4) || !aligned(kv_lens, 4) || (lens_out && !aligned(lens_out, 4)))
         return GDR_ERR_INVALID_ARG;
-    // other blocks read a sequence's length while one writes its new one
-    if (lens_out && lens_out < kv_lens + n_seqs && kv_lens < lens_out + n_seqs) return GDR_ERR_INVALID_ARG;
+    // other blocks read a sequence's length, last node and parents while one writes its new length
+    auto over = [&](const int32_t *x, int64_t n) { return lens_out < x + n && x < lens_out + n_seqs; };
+    if (lens_out && (over(kv_lens, n_seqs) || over(last, n_seqs) || over(parents, (int64_t)n_seqs * n_tok)))
+        return GDR_ERR_INVALID_ARG;
     st = check_cache(cache);
     if (st != GDR_OK) return st;
     if (!stride_ok(layer_stride) || !out_cache_ok(cache, dims->h_kv, dims->d)) return GDR_ERR_INVALID_ARG;

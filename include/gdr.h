@@ -446,7 +446,8 @@ gdr_status gdr_verify_commit(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok
  *
  *   q, k [n_seqs * n_tok][H_qk][d_k]; v, o [n_seqs * n_tok][H_v][d_v]; g, beta [n_seqs * n_tok][H_v]
  *   state  [n_seqs][H_v][d_k][d_v]
- *   deltas NULL, or fp32 [n_seqs * n_tok][H_v][d_v] that receives the corrections u_j
+ *   deltas NULL, or fp32 [n_seqs * n_tok][H_v][d_v] that receives the corrections u_j; like o, it
+ *          must not overlap an input
  * Rows of o and deltas that are no nodes are set to zero.  dims->chunk has no effect;
  * dims->flags as everywhere.  Everything between the inputs and o's own rounding is held to
  * fp32: what enters a tensor-core product enters as three bf16 parts (24 bits), of whose nine
@@ -662,7 +663,8 @@ size_t gdr_attn_decode_tree_workspace_bytes(const gdr_attn_dims *dims, int32_t n
  *                 (layer_stride: a multiple of 8, not negative, below 2^38)
  *   cache         layer 0's; one page table for all layers
  *   lens_out      NULL, or DEVICE int32 [n_seqs]: the new lengths, base + |A_last| (kv_lens[s]
- *                 itself where that is 0 or out of range); must not overlap kv_lens
+ *                 itself where that is 0 or out of range); must not overlap kv_lens, last or parents
+ *                 (GDR_ERR_INVALID_ARG)
  * dims->h_q, dtype and scale have no effect on the result.  A sequence with kv_lens[s] = 0 is
  * not in the batch (its parents and last[s] may hold anything; its new length is 0); one in
  * 1 .. n_tok - 1 or beyond max_pages * page_size is left as it is and recorded.  Rows whose
