@@ -88,7 +88,7 @@ gdr_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GDR_OK : GDR_ERR
 
 bool aligned4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Trees of drafted tokens: at most 64 rows each, and a grid of 8 blocks per (sequence, V head).
+// Trees of drafted tokens: at most 64 rows each, and at most 4 blocks per (sequence, V head) in a grid.
 gdr_status check_tree(const gdr_dims *d, int32_t n_seqs, int32_t n_tok) {
     const gdr_status st = check_dims(d);
     if (st != GDR_OK) return st;

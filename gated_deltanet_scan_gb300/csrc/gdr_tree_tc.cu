@@ -23,14 +23,17 @@
 //            size d, and the state is the operand that lives in TMEM
 //   rows     (warps 0 .. 15) R and e^G S_0^T q are made from X in place, and [U; O]^T is what they are
 //            plus R^T [T - I; W]^T, inner size n, R's parts in TMEM too.  Neither the state nor R passes
-//            through shared memory.  Of the nine products of parts, the six that reach 2^-24 are made,
-//            smallest first.
+//            through shared memory.  Of the nine products of parts six are made, smallest first: cutting leaves
+//            a middle part under 2^-7 and a low one under 2^-15 of the value, so the three that are left out are
+//            together under 2^-21 of a product.  What the accumulators cut after every 16 products weighs more:
+//            o and u are 1.5 to 3.9 * 10^-7 of their norm off 64 bits.
 //   MMAs     (warp 30) both products: an issuing thread stands still while the tensor pipe is full.
 //
 // Bound by the chain X, R, U and O of a pair, 9,500 clocks at 64 nodes, and as long by the factors' of two
 // heads (18,000); everything else is done while the pairs before go through it, and HBM would need 5,600. 64
-// trees of 64 nodes with 32 heads: 96 us, 290 MB at 45% of the measured bandwidth (floor 49.6; an fp32
-// kernel level by level took 2,222). 8 of 41 nodes 21.5 us (4.6), one of 24 12.4 (0.5): there the first
+// trees of 64 nodes with 32 heads: 96 us; their 336 MB (294 of it DRAM traffic, the rest is still in L2 when
+// the kernel ends) would take 49.6, so 52% of the measured bandwidth (an fp32 kernel level by level took 2,222).
+// 8 of 41 nodes 22 us (4.6), one of 24 12.5 (0.5): there the first
 // pair of a block takes 15,000 to 25,000 clocks, a quarter of them instructions that come from memory.
 //
 // A node's rows of T and W are zero but at its ancestors, and zero times an infinity or NaN would
@@ -40,7 +43,12 @@
 // Every role's code runs once a pair or two, and the first pair waits for all of it to come from
 // memory: it is kept small, in loops where registers allow.
 //
-// d < 128 leaves lanes (and warps) idle.
+// Deep paths cost more: the joins and W are sums over lists in shared memory, cubic in a path's length, and a
+// pair of more than half of all possible entries goes through them alone. 64 chains of 64: 438 us, 16 of them 133,
+// one 44; 64 chains of 32 105, of 24 87.
+//
+// d < 128 leaves lanes (and warps) idle, and the factors, which then bound it, as they are: 64 trees of 64 nodes
+// take 87 us at d = 64 (floor 20), 82 at d = 32 (8.8), one of 24 12.3 at either.
 #include "gdr_attn.h"
 #include "gdr_attn_mma.cuh"
 #include "gdr_attn_ptx.cuh"

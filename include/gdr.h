@@ -449,12 +449,16 @@ gdr_status gdr_verify_commit(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok
  *   deltas NULL, or fp32 [n_seqs * n_tok][H_v][d_v] that receives the corrections u_j; like o, it
  *          must not overlap an input
  * Rows of o and deltas that are no nodes are set to zero.  dims->chunk has no effect;
- * dims->flags as everywhere.  Everything between the inputs and o's own rounding is held to
- * fp32: what enters a tensor-core product enters as three bf16 parts (24 bits), of whose nine
- * products the six that reach 2^-24 are summed in fp32; the sums of g are fp64.  A gate of
- * minus infinity forgets the path before it (all gates below -10^4 count as -10^4).  An
- * infinite or NaN value of v or of the state stays in its column, and in the nodes whose path it is on.  n_seqs * H_v is below 2^28
- * (GDR_ERR_UNSUPPORTED otherwise); n_seqs = 0 is a no-op, whatever the pointers are.
+ * dims->flags as everywhere.  Everything between the inputs and o's own rounding is held in
+ * fp32, the sums of g in fp64.  With bf16 inputs the large products are made on tensor cores:
+ * what enters one of them enters as three bf16 parts (24 bits); of the nine products of two
+ * such values the three smallest are left out, together under 2^-21 of the product and of its
+ * sign; and the fp32 accumulators cut what they add.  So fp32 o and u are off by 1.5 to 3.9 *
+ * 10^-7 of their norm there, and by 0.6 to 1.3 * 10^-7 with fp32 inputs, which take fp32 sums
+ * on CUDA cores.  A gate of minus infinity forgets the path before it (all gates below -10^4
+ * count as -10^4).  An infinite or NaN value of v or of the state stays in its column, and in
+ * the nodes whose path it is on.  n_seqs * H_v is below 2^28 (GDR_ERR_UNSUPPORTED otherwise);
+ * n_seqs = 0 is a no-op, whatever the pointers are.
  */
 gdr_status gdr_verify_tree(const gdr_dims *dims, int32_t n_seqs, int32_t n_tok, const int32_t *parents, const void *q,
                            const void *k, const void *v, const float *g, const float *beta, const float *state,
