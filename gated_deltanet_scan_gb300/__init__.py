@@ -698,7 +698,8 @@ def gdr_attn_append_tree(q, k, v, q_out, k_out, k_cache, v_cache, page_table, kv
 
 
 def gdr_attn_decode_tree_workspace_bytes(q, k_cache, parents) -> int:
-    """Device scratch bytes gdr_attn_decode_tree needs."""
+    """Device scratch bytes gdr_attn_decode_tree needs for these shapes (see include/gdr.h): fewer tokens may need
+    more, so a buffer kept for trees of several sizes has the largest of their bytes."""
     dims = _attn_dims(q.shape[1], k_cache.shape[2], k_cache.shape[3], q.dtype, None)
     return int(lib().gdr_attn_decode_tree_workspace_bytes(dims, *parents.shape))
 

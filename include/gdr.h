@@ -653,7 +653,12 @@ gdr_status gdr_attn_decode_tree(const gdr_attn_dims *dims, int32_t n_seqs, int32
                                 const gdr_rows *q, const gdr_kv_cache *cache, const int32_t *kv_lens, const gdr_rows *o,
                                 float *lse, void *workspace, size_t workspace_bytes, gdr_stream_t stream);
 
-/* Bytes of workspace gdr_attn_decode_tree needs (0 for invalid dims).  Depends on the shapes only. */
+/*
+ * Bytes of workspace gdr_attn_decode_tree needs (0 for invalid dims).  Depends on the shapes
+ * only.  It grows with n_seqs but not always with n_tok: up to 16 rows of a key/value head
+ * (n_tok h_q / h_kv) are shared among more workers than 17 are, so 4 tokens may need more than
+ * 24.  A buffer kept for trees of several sizes has the largest of their sizes' bytes.
+ */
 size_t gdr_attn_decode_tree_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok);
 
 /*

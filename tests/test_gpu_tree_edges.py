@@ -5,8 +5,9 @@ import pytest
 
 import gated_deltanet_scan_gb300 as gdr
 from tests import gpu_util as gu
-from tests.test_gpu_attn import Paged, ints, no_error
-from tests.test_gpu_tree_attn import parents_of
+from tests import tree_ref as tr
+from tests.test_gpu_attn import Paged, ints, no_error, randn
+from tests.test_gpu_tree_attn import attend, parents_of
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,26 @@ def test_compaction_of_a_batch_with_empty_places(stale, last, layers):
     no_error()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and got[2] == [36, 0, 25]
     assert not torch.equal(got[0], k0)
+
+
+def test_one_workspace_for_trees_of_several_sizes():
+    """The bytes do not grow with every token of a tree: a buffer of the largest of the sizes' bytes serves them all."""
+    torch = gu.require_gpu()
+    rng = np.random.default_rng(62)
+    c = Paged(rng, [700, 64, 0, 3000], 16, 2, 128, "bf16")
+    sizes = (24, 4, 5, 1, 17, 64, 16)
+    calls = []
+    for n_tok in sizes:
+        parents = parents_of([tr.make(rng, n_tok, kind) for kind in ("draft", "chain", "holes", "forest")])
+        calls.append((randn(rng, (4 * n_tok, 8, 128), "bf16"), parents))
+    need = [gdr.gdr_attn_decode_tree_workspace_bytes(q, c.k, p) for q, p in calls]
+    assert need[1] > need[0]
+    ws = torch.full((max(need),), 255, dtype=torch.uint8, device="cuda")
+    for (q, p), size in zip(calls, need):
+        want, lse = attend(c, q, p)
+        got, lse2 = attend(c, q, p, workspace=ws)
+        assert torch.equal(got, want) and torch.equal(lse, lse2)
+        attend(c, q, p, workspace=ws[:size])
+        with pytest.raises(gdr.GdrError):
+            attend(c, q, p, workspace=ws[:size - 1])
+    no_error()
