@@ -221,74 +221,18 @@ __device__ __forceinline__ bool gates(const Args &a, int32_t *err, Tables &s) {
     for (int i = 0;; ++i) {
         // the buffers are free once the factors have used them two pairs ago
         if (i >= 2 && !wait_warp(bar(kTabFree + (i & 1)), i - 2 >> 1)) return false;
-        // masks and sums of the gates along the paths by pointer jumping (gdr_tree.cuh); sums in doubles,
-        // since their differences enter exponentials
-        int to[2] = {parents.x, parents.y};
-        uint64_t mask[2];
-        double sum[2];
-        bool bad = false;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int j = lane + 32 * x;
-            if (to[x] < -2 || to[x] >= j) {
-                bad = bad || j < n;
-                to[x] = -2;
-            }
-            mask[x] = to[x] != -2 ? 1ull << j : 0;
-            sum[x] = to[x] != -2 ? tree::gate(g[x]) : 0.0;
-        }
-#pragma unroll 1
-        for (int step = 1; step < n; step <<= 1) {
-            uint64_t up[2];
-            int next[2];
-            double more[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int from = to[x] & 31;
-                up[x] = tree::shfl64(mask[0], from);
-                next[x] = __shfl_sync(0xffffffffu, to[0], from);
-                more[x] = __shfl_sync(0xffffffffu, sum[0], from);
-                if (n <= 32) {  // the upper rows are no nodes
-                    up[1] = 0;
-                    next[1] = -2;
-                    more[1] = 0.0;
-                    break;
-                }
-                const uint64_t u1 = tree::shfl64(mask[1], from);
-                const int t1 = __shfl_sync(0xffffffffu, to[1], from);
-                const double s1 = __shfl_sync(0xffffffffu, sum[1], from);
-                if (to[x] & 32) {
-                    up[x] = u1;
-                    next[x] = t1;
-                    more[x] = s1;
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (to[x] >= 0) {
-                    mask[x] |= up[x];
-                    sum[x] += more[x];
-                    to[x] = next[x];
-                }
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            if (mask[x] != 0 && to[x] == -2) {  // a path that ends in a row that is no node
-                bad = true;
-                mask[x] = 0;
-                sum[x] = 0.0;
-            }
-        }
+        // masks and sums of the gates along the paths; sums in doubles, since their differences enter exponentials
+        double sum[2] = {tree::gate(g[0]), tree::gate(g[1])};
+        const tree::Masks m = tree::masks<true>(parents, n, lane, sum);
         if (it.new_tree) {
             const int z = ++trees & 3;
-            if (bad) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
-            const uint32_t real[2] = {__ballot_sync(0xffffffffu, mask[0] != 0), __ballot_sync(0xffffffffu, mask[1] != 0)};
+            if (m.bad) atomicCAS(err, 0, (int32_t)GDR_ERR_INVALID_ARG);
+            const uint32_t real[2] = {__ballot_sync(0xffffffffu, m.a[0] != 0), __ballot_sync(0xffffffffu, m.a[1] != 0)};
             int length[2], at = 0;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                s.mask[z][lane + 32 * x] = mask[x];
-                length[x] = __popcll(mask[x]);
+                s.mask[z][lane + 32 * x] = m.a[x];
+                length[x] = __popcll(m.a[x]);
                 int upto = length[x];
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
