@@ -3,7 +3,8 @@
 Random weights, head shapes of the 9B model the library was written for (rule: 16 QK and 32 V heads of 128;
 attention: 16 query and 4 key/value heads of 256, rotation over 64 of them).  Two prompts of different lengths are
 prefilled as one packed batch; then both sequences decode token by token from the rule's states and the paged cache,
-and last a block of draft tokens goes through attention at once.
+and last a block of draft tokens goes through attention at once.  A second run verifies trees of drafted tokens in all
+layers and accepts a path of each.
 
     python examples/hybrid_decode.py
 """
@@ -60,6 +61,17 @@ class RuleLayer:
                                       beta_logits=True)
         return x + o.view(x.shape[0], -1).to(torch.bfloat16) @ self.out
 
+    def tree(self, x, parents):
+        """Every node of a tree per sequence; what accept() takes.  The states stay."""
+        q, k, v, g, b, z = self.inputs(x)
+        o, deltas = (torch.empty(v.shape, dtype=torch.float32, device="cuda") for _ in range(2))
+        gdr.gdr_verify_tree(q, k, v, g, b, self.state, o, parents, deltas=deltas, qk_l2norm=True, beta_logits=True)
+        gdr.gdr_gated_rmsnorm(o, z, self.weight, o)
+        return x + o.view(x.shape[0], -1).to(torch.bfloat16) @ self.out, (k, g, deltas)
+
+    def accept(self, kept, parents, last):
+        gdr.gdr_verify_tree_commit(*kept, self.state, parents, last, qk_l2norm=True)
+
 
 class AttentionLayer:
     """x + out(attention(rotated q, rotated k, v)), keys and values in a paged cache."""
@@ -86,6 +98,22 @@ class AttentionLayer:
         else:  # the last n_tok tokens of every sequence
             gdr.gdr_attn_decode(q, self.k_cache, self.v_cache, self.table, self.kv_lens, o, n_tok)
         return x + o.view(x.shape[0], -1) @ self.out
+
+    def tree(self, x, parents):
+        """Every node of a tree per sequence, in the slots after the sequence's tokens."""
+        qkv = (norm(x) @ self.qkv).view(-1, ATT_Q + 2 * ATT_KV, ATT_D)
+        q, k, v = qkv.split([ATT_Q, ATT_KV, ATT_KV], dim=1)
+        self.kv_lens += parents.shape[1]
+        gdr.gdr_attn_append_tree(q, k, v, q, None, self.k_cache, self.v_cache, self.table, self.kv_lens, self.inv_freq,
+                                 parents)
+        o = torch.empty(x.shape[0], ATT_Q, ATT_D, dtype=torch.bfloat16, device="cuda")
+        gdr.gdr_attn_decode_tree(q, self.k_cache, self.v_cache, self.table, self.kv_lens, o, parents)
+        return x + o.view(x.shape[0], -1) @ self.out
+
+    def accept(self, parents, last):
+        new = torch.empty_like(self.kv_lens)  # other sequences' blocks still read the lengths
+        gdr.gdr_attn_commit_tree(self.k_cache, self.v_cache, self.table, self.kv_lens, parents, last, new)
+        self.kv_lens = new
 
 
 def run(lengths=(300, 77), steps=8, draft=4, seed=0):
@@ -128,8 +156,52 @@ def run(lengths=(300, 77), steps=8, draft=4, seed=0):
     return torch.cat([t for g in got for t in g]), whole
 
 
+def run_tree(lengths=(300, 77), seed=0):
+    """Outputs of the accepted nodes of a drafted tree per sequence, by sequence, and of the same tokens decoded one
+    after another; and the lengths both leave in the cache."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    trees = [[-1, 0, 0, 1, 3, 2, 3], [-1, -1, 1, 2, -2, -2, -2]]  # the second has three rows that are no nodes
+    paths = [[0, 1, 3, 6], [1, 2, 3]]  # accepted
+    n, n_tok = len(trees), len(trees[0])
+    parents = torch.tensor(trees, dtype=torch.int32, device="cuda")
+    last = torch.tensor([p[-1] for p in paths], dtype=torch.int32, device="cuda")
+    rules, att = [RuleLayer(gen, n) for _ in range(3)], AttentionLayer(gen, n, max(lengths) + n_tok)
+    x = torch.randn(sum(lengths), WIDTH, generator=gen, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, lengths[0], sum(lengths)], dtype=torch.int32, device="cuda")
+    for layer in rules + [att]:
+        x = layer(x, cu)
+    before = [layer.state.clone() for layer in rules], att.kv_lens.clone()
+
+    drafted = torch.randn(n * n_tok, WIDTH, generator=gen, device="cuda").to(torch.bfloat16)
+    x, kept = drafted, []
+    for layer in rules:
+        x, k = layer.tree(x, parents)
+        kept.append(k)
+    tree = att.tree(x, parents)
+    for layer, k in zip(rules, kept):  # once the nodes' outputs are judged
+        layer.accept(k, parents, last)
+    att.accept(parents, last)
+    lens = att.kv_lens
+
+    one = []
+    for s, path in enumerate(paths):
+        for layer, state in zip(rules, before[0]):
+            layer.state = state.clone()
+        att.kv_lens = before[1].clone()
+        for j in path:  # the other sequence takes the same token, and is not looked at
+            x = drafted[s * n_tok + j].expand(n, -1)
+            for layer in rules + [att]:
+                x = layer(x, None)
+            one.append(x[s])
+    return (torch.stack([tree[s * n_tok + j] for s, path in enumerate(paths) for j in path]), torch.stack(one),
+            lens.tolist(), [m + len(path) for m, path in zip(lengths, paths)])
+
+
 if __name__ == "__main__":
     tokens, whole = run()
     print(f"{tokens.shape[0]} rows; step by step against one prefill: "
           f"largest difference {(tokens.float() - whole.float()).abs().max().item():.3g} "
           f"of {whole.float().abs().max().item():.3g}")
+    tokens, one, lens, _ = run_tree()
+    print(f"{tokens.shape[0]} accepted nodes of two trees: one after another "
+          f"{(tokens.float() - one.float()).abs().max().item():.3g} off, lengths {lens}")

@@ -64,3 +64,18 @@ def test_one_workspace_for_trees_of_several_sizes():
         with pytest.raises(gdr.GdrError):
             attend(c, q, p, workspace=ws[:size - 1])
     no_error()
+
+
+def test_example_verifies_and_accepts_trees():
+    import importlib.util
+    import os
+
+    torch = gu.require_gpu()
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_decode.py")
+    spec = importlib.util.spec_from_file_location("hybrid_decode", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    tokens, one, lens, want = mod.run_tree(lengths=(130, 61))
+    no_error()
+    assert lens == want and tokens.shape == one.shape == (7, mod.WIDTH)
+    assert torch.isfinite(tokens).all() and torch.isfinite(one).all()
