@@ -33,8 +33,13 @@ __host__ __device__ constexpr Spec spec(Kind kind, int d) {
 // Of the rows of a key/value head, of so many heads of all sequences.  Trees of more than 128 rows of up to 128
 // values, more blocks of rows than workers: two of them read the keys and values together.  (The O of two
 // blocks of d = 256 would leave no TMEM for their S.)  Fewer have more to lose by parts of twice the rows.
-// d = 128, 256 rows, 4 heads a sequence, us apart / together: 32 sequences of up to 8,000 tokens 82.6 / 77.5, of
-// 1,000 43.2 / 44.0; 16 53.1 / 50.8 and 28.9 / 34.9; 8 of 16,000 45.9 / 45.1, of 4,000 28.9 / 32.9; one 16.4 / 20.5.
+// fp16, us apart / together, every sequence of 1,000, 2,000 and 8,000 tokens (lengths are not known on the host):
+//   256 rows, d = 128: 80 heads 39.0 / 41.2, 53.3 / 53.3, 136.8 / 115.5; 96 43.1 / 44.7, 61.4 / 59.4, 159.9 / 133.2;
+//     128 51.4 / 51.2, 75.8 / 69.7, 206.6 / 169.3; 512 151 / 135, 242 / 204, 765 / 595
+//   256 rows, d = 64: 80 heads 30.0 / 30.5, 43.1 / 39.1, 114.7 / 89.6; 512 117 / 94, 193 / 150, 643 / 467
+//   160 rows, d = 128: 80 heads 34.9 / 35.0, 49.5 / 47.0, 133.2 / 110.0; 512 139 / 118, 235 / 189, 757 / 580
+// With fewer heads than that: 64 heads of 1,000 28.9 / 34.9, of up to 8,000 53.1 / 50.8; 32 of 4,000 28.9 / 32.9, of
+// 16,000 45.9 / 45.1; 4 of 1,500 16.4 / 20.5.
 inline Kind kind_of(int rows, int d, bool tree, int64_t heads) {
     return rows <= kWarpRows                                                                ? kFew
            : tree && rows > 128 && d <= 128 && (int64_t)((rows + 127) / 128) * heads > kBlocks ? kPaired

@@ -23,10 +23,15 @@
 // values, and pay for their loads, once per block of rows.  Up to d = 128 TMEM holds O and two S tiles of
 // two blocks, so a worker takes both (B = 2, where there are enough of them: kind_of), the products block by block, so that one's P is made
 // while the other's run: 16 trees of 64 nodes, contexts up to 16,384, d = 128, 32 / 8 heads: 124 us with a
-// block a worker, 113 with two, 107 with two places for Q.  The tensor pipe and the shared memory it reads
-// (Q again for every 64 tokens) bound it: 1,770 clocks a tile, of which HBM would need 1,370.
+// block a worker, 113 with two, 107 with two places for Q, 98 with today's join.  While tiles run, the tensor
+// pipe and the shared memory it reads (Q again for every 64 tokens) bound it: 1,770 clocks a tile, of which HBM
+// would need 1,370.  But a worker's 47 tiles are 42 of the kernel's 87 us, and its tensor pipe works 28% of them:
+// the others are its start, one or two changes of triple (256 rows of Q in, O out) and parts of up to 256 rows
+// (40 MB written and read again), how much of each is not measured.
 //
-// P is rounded to 16 bits.  A second product with what bf16's rounding left, as in
+// P is rounded to its type, fp16's 11 bits or bf16's 8: o is up to 2.8 * 10^-4 or 2.3 * 10^-3 of its norm off 64
+// bits, of which its own rounding makes 2.1 * 10^-4 and 1.7 * 10^-3.  A chain as a tree has the bits of gdr_attn_decode where
+// both take this kernel on the same cuts.  A second product with what bf16's rounding left, as in
 // gdr_attn_decode.cu, would halve o's squared error and take 10% longer (16 draft tokens of 32
 // sequences of 2,000, d = 128: 77.6 against 69.5 us; 8 of 512 to 8,192, d = 256: 39.4 / 38.6).
 //

@@ -12,8 +12,11 @@
 // a lane in seven shuffles.  N and P are made for the paths' entries, and nodes come after their ancestors, so
 // two lanes of a column go through the rows in order, four at once, with no barrier of the block.
 // Bound by issue slots (64% of them; the FMAs of S_0^T [K; Q] alone would take 16,400 clocks a pair of 64
-// nodes and d = 128, of 70,000): 64 trees of 64 nodes, 32 heads: 506 us, 16 of them 152, chains 274, 8 of 41
-// nodes 51, one of 24 15.4 (level by level, 32 columns a block: 2,300, 599, 1,432, 137 and 16.5).
+// nodes and d = 128, of 70,000): 64 trees of 64 nodes, 32 heads: 506 us, 16 of them 152, 16 chains 274 (64 938), 8
+// trees of 41 nodes 51, one of 24 15.4 (level by level, 32 columns a block: 2,300, 599, 1,432, 137 and 16.5).  At
+// d = 64 and 32 64 trees of 64 take 225 and 135 us, one of 24 15.5 and 14.0.  It stays on CUDA cores: the tensor-core
+// kernel takes K and Q as one bf16 part; three of each would be twice the products that make X and three times the
+// operand tiles, for which its shared memory, as it is laid out, has no room.
 #include "gdr_attn.h"
 #include "gdr_attn_mma.cuh"
 #include "gdr_attn_ptx.cuh"
