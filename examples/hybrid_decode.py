@@ -178,7 +178,7 @@ def run_tree(lengths=(300, 77), seed=0):
         x, k = layer.tree(x, parents)
         kept.append(k)
     tree = att.tree(x, parents)
-    for layer, k in zip(rules, kept):  # once the nodes' outputs are judged
+    for layer, k in zip(rules, kept):  # once a path of each is chosen
         layer.accept(k, parents, last)
     att.accept(parents, last)
     lens = att.kv_lens

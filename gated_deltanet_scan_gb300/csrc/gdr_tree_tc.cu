@@ -33,7 +33,7 @@
 // heads (18,000); everything else is done while the pairs before go through it, and HBM would need 5,600. 64
 // trees of 64 nodes with 32 heads: 96 us; their 336 MB (294 of it DRAM traffic, the rest is still in L2 when
 // the kernel ends) would take 49.6, so 52% of the measured bandwidth (an fp32 kernel level by level took 2,222).
-// 8 of 41 nodes 22 us (4.6), one of 24 12.5 (0.5): there the first
+// 8 of 41 nodes 20.8 us (4.6), one of 24 12.4 (0.5): there the first
 // pair of a block takes 15,000 to 25,000 clocks, a quarter of them instructions that come from memory.
 //
 // A node's rows of T and W are zero but at its ancestors, and zero times an infinity or NaN would

@@ -627,7 +627,8 @@ gdr_status gdr_attn_decode(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_
                            const gdr_kv_cache *cache, const int32_t *kv_lens, const gdr_rows *o, float *lse,
                            void *workspace, size_t workspace_bytes, gdr_stream_t stream);
 
-/* Bytes of workspace gdr_attn_decode needs (0 for invalid dims).  Depends on the shapes only. */
+/* Bytes of workspace gdr_attn_decode needs (0 for invalid dims).  Depends on the shapes only;
+ * fewer tokens may need more (see gdr_attn_decode_tree_workspace_bytes). */
 size_t gdr_attn_decode_workspace_bytes(const gdr_attn_dims *dims, int32_t n_seqs, int32_t n_tok);
 
 /*
